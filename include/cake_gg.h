@@ -104,11 +104,13 @@ typedef enum {
     CAKE_GG_ERR_CUDA = 6,         /* a CUDA runtime/driver call failed                      */
     CAKE_GG_ERR_BAD_OFFSETS = 7,  /* device-detected: offsets not 0-based, decreasing or > M_max */
     CAKE_GG_ERR_TIMEOUT = 8,      /* device-detected: a bounded wait inside the kernel expired */
-    CAKE_GG_ERR_SCRATCH_LIMIT = 9 /* the problem needs more scratch than cake_gg_wgrad_noalloc's fixed maximum */
+    CAKE_GG_ERR_SCRATCH_LIMIT = 9,/* the problem needs more scratch than cake_gg_wgrad_noalloc's fixed maximum */
+    CAKE_GG_ERR_BAD_ROWS = 10     /* device-detected: a row index of the 8-bit products outside [0, T) */
 } cake_gg_status_t;
 
 typedef enum { CAKE_GG_FWD = 0, CAKE_GG_DGRAD = 1, CAKE_GG_WGRAD = 2 } cake_gg_pass_t;
-typedef enum { CAKE_GG_BF16 = 0, CAKE_GG_FP32 = 1 } cake_gg_dtype_t;
+/* CAKE_GG_INT8: the 8-bit products' tokens only (cake_gg_i8_plan's x_dtype). */
+typedef enum { CAKE_GG_BF16 = 0, CAKE_GG_FP32 = 1, CAKE_GG_INT8 = 2 } cake_gg_dtype_t;
 
 /* Plan: a caller-owned plain struct filled by cake_gg_plan(); nothing to free.
  * The first block holds the problem as given; the second holds the choices
@@ -276,8 +278,83 @@ int cake_gg_router_plan(cake_gg_router_plan_t *rp, int64_t T, int32_t R, int32_t
 int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const float *W, float *Y,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- 8-bit integer products with scales per token and channel -------------
+ *
+ * A quantised linear layer in serving: dense (E = 1), or grouped by expert
+ * with ragged sizes and rows routed from tokens by index.  (No page of the
+ * sources the passes above cite has a counterpart.)
+ *
+ *   Y[m, n] = (sum_k q[r(m), k] W[e(m), n, k]) * ws[e(m), n] * xs[r(m)]
+ *
+ * W [E, N, K] int8 with a scale ws [E, N] per output channel; q [T, K] int8
+ * with a scale xs [T] per token; e(m) the expert that owns row m by offsets
+ * [E + 1] (as in the passes above; null when E = 1: it owns every row), r(m) =
+ * rows[m], or m where rows is null.  All row-major, dense, all 256 values of
+ * a byte allowed.  Rows at or past offsets[E] of Y are never written, and an
+ * expert without rows reads no weights.  Sums of the few-row path are exact
+ * 32-bit integers; one rounding to FP32 and two multiplications follow, then
+ * one rounding to BF16 for BF16 output.  The same call gives the same bits on
+ * every run and under every max_sms.
+ *
+ * X is q itself (x_dtype CAKE_GG_INT8, xs given), or BF16 / FP32 activations
+ * (xs null) that the call quantises row by row first:
+ *
+ *   h = x, or with CAKE_GG_ACT_SILU_MUL  h = g / (1 + exp(-g)) * u  of rows
+ *       x[t] = [g | u] of 2 K values (what stands between the two products
+ *       of a gated expert layer)
+ *   a = max_k |h|,  xs = a / 127,  q = round(h * (127 / a)), ties to even,
+ *
+ * in FP32.  A row whose a is below 2^-120 counts as zero (xs = 0, q = 0); one
+ * that holds a NaN or an infinity gets xs = NaN, q = 0, so its products are
+ * NaN.  Weights are quantised the same way: cake_gg_i8_quant over W's rows. */
+typedef enum { CAKE_GG_ACT_NONE = 0, CAKE_GG_ACT_SILU_MUL = 1 } cake_gg_act_t;
+typedef enum { CAKE_GG_I8_ROWS = 0 } cake_gg_i8_path_t;
+
+typedef struct cake_gg_i8_plan {
+    int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
+    int32_t E;               /* experts, 1 .. 1024                                  */
+    int64_t M_max;           /* rows of Y (0 .. 2^31 - 1)                           */
+    int64_t T;               /* rows of X (= M_max without rows)                    */
+    int32_t N;               /* output channels, a multiple of 8                    */
+    int32_t K;               /* reduction length, a multiple of 16, below 2^17      */
+    int32_t x_dtype;         /* cake_gg_dtype_t: CAKE_GG_INT8, _BF16 or _FP32       */
+    int32_t act;             /* cake_gg_act_t (CAKE_GG_ACT_NONE for int8 X)         */
+    int32_t out_dtype;       /* CAKE_GG_BF16 or CAKE_GG_FP32                        */
+    int32_t max_sms;         /* cap on persistent CTAs; 0 = every SM of the device  */
+    /* chosen by cake_gg_i8_plan() */
+    int32_t path;            /* cake_gg_i8_path_t                                   */
+    int32_t reserved;
+    uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
+    uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
+} cake_gg_i8_plan_t;
+
+/* Fill *plan.  Pure host arithmetic.  CAKE_GG_ERR_INVALID_ARG for sizes out of
+ * range, T < 1 with rows to compute, an activation with int8 X;
+ * CAKE_GG_ERR_UNSUPPORTED for other types; CAKE_GG_ERR_ALIGNMENT unless N is a
+ * multiple of 8 and K of 16; CAKE_GG_ERR_OVERFLOW for K >= 2^17 or a size
+ * product past 64 bits. */
+int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K,
+                    int x_dtype, int act, int out_dtype, int32_t max_sms);
+
+/* The product.  X, W, Y, workspace: device pointers, 16-byte aligned; xs, ws,
+ * rows, offsets 4-byte aligned.  The workspace is plan->workspace_bytes,
+ * zero-filled once after allocation.  Enqueues one or two kernels on `stream`;
+ * allocates nothing, never synchronises.  Host-detected errors return
+ * non-zero and enqueue nothing; offsets that the device finds invalid
+ * (CAKE_GG_ERR_BAD_OFFSETS) and a row index outside [0, T)
+ * (CAKE_GG_ERR_BAD_ROWS; nothing is read through it) land in the workspace's
+ * status word. */
+int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *xs, const int32_t *rows,
+                    const int8_t *W, const float *ws, void *Y, const int32_t *offsets, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Quantise the rows of X [T, K] (BF16 or FP32; [T, 2 K] with
+ * CAKE_GG_ACT_SILU_MUL) into Xq [T, K] and xs [T], as above.  One kernel. */
+int cake_gg_i8_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, int8_t *Xq, float *xs,
+                     void *stream);
+
 /* Synchronise `stream`, return the status word of `workspace` (CAKE_GG_OK,
- * or the first _BAD_OFFSETS / _TIMEOUT recorded by a call since the last
+ * or the first _BAD_OFFSETS / _TIMEOUT / _BAD_ROWS recorded by a call since the last
  * check) and reset it to CAKE_GG_OK; CAKE_GG_ERR_CUDA if a CUDA call failed. */
 int cake_gg_check_status(const void *workspace, void *stream);
 

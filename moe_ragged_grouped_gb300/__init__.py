@@ -8,5 +8,5 @@ entry points; ``workloads`` draws seeded synthetic inputs.
 from . import cake_gg, workloads  # noqa: F401
 from .cake_gg import (  # noqa: F401
     cake_gg_check_status, cake_gg_dgrad, cake_gg_fwd, cake_gg_plan, cake_gg_strerror,
-    cake_gg_tile_walk, cake_gg_wgrad, grouped_gemm,
+    cake_gg_tile_walk, cake_gg_wgrad, grouped_gemm, int8_gemm, quantize_rows,
 )

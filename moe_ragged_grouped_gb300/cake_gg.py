@@ -27,18 +27,23 @@ CAKE_GG_ERR_CUDA = 6
 CAKE_GG_ERR_BAD_OFFSETS = 7
 CAKE_GG_ERR_TIMEOUT = 8
 CAKE_GG_ERR_SCRATCH_LIMIT = 9
+CAKE_GG_ERR_BAD_ROWS = 10
 CAKE_GG_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 CAKE_GG_FWD, CAKE_GG_DGRAD, CAKE_GG_WGRAD = 0, 1, 2
-CAKE_GG_BF16, CAKE_GG_FP32 = 0, 1
+CAKE_GG_BF16, CAKE_GG_FP32, CAKE_GG_INT8 = 0, 1, 2
+CAKE_GG_ACT_NONE, CAKE_GG_ACT_SILU_MUL = 0, 1
 CAKE_GG_DEBUG_DROP_FIRST_LOAD = 1
 
 PASSES = {"fwd": CAKE_GG_FWD, "dgrad": CAKE_GG_DGRAD, "wgrad": CAKE_GG_WGRAD}
 DTYPES = {"bf16": CAKE_GG_BF16, "fp32": CAKE_GG_FP32}
+I8_X_DTYPES = {**DTYPES, "int8": CAKE_GG_INT8}
+I8_ACTS = {None: CAKE_GG_ACT_NONE, "silu_mul": CAKE_GG_ACT_SILU_MUL}
 
 EXPORTED = ["cake_gg_plan", "cake_gg_fwd", "cake_gg_dgrad", "cake_gg_wgrad",
             "cake_gg_check_status", "cake_gg_strerror", "cake_gg_tile_walk", "cake_gg_corun_spinner",
-            "cake_gg_router_plan", "cake_gg_router_fp32"]
+            "cake_gg_router_plan", "cake_gg_router_fp32",
+            "cake_gg_i8_plan", "cake_gg_i8_gemm", "cake_gg_i8_quant"]
 
 
 class CakeGGPlan(ctypes.Structure):
@@ -90,6 +95,29 @@ class CakeGGRouterPlan(ctypes.Structure):
     ]
 
 
+class CakeGGI8Plan(ctypes.Structure):
+    """Mirror of cake_gg_i8_plan_t (same field order, same C layout)."""
+    _fields_ = [
+        ("abi_version", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("M_max", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("max_sms", ctypes.c_int32),
+        ("path", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("timeout_ns", ctypes.c_uint64),
+        ("workspace_bytes", ctypes.c_uint64),
+    ]
+
+    def as_dict(self):
+        return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
+
+
 class CakeGGError(RuntimeError):
     def __init__(self, code, where):
         super().__init__(f"{where}: {cake_gg_strerror(code)} (status {code})")
@@ -133,6 +161,13 @@ def load_library(path: str = LIB_PATH):
     lib.cake_gg_router_plan.restype = ctypes.c_int
     lib.cake_gg_router_fp32.argtypes = [rplan_p, vp, vp, vp, vp, sz, vp]
     lib.cake_gg_router_fp32.restype = ctypes.c_int
+    i8plan_p = ctypes.POINTER(CakeGGI8Plan)
+    lib.cake_gg_i8_plan.argtypes = [i8plan_p, i32, i64, i64, i32, i32, ctypes.c_int, ctypes.c_int, ctypes.c_int, i32]
+    lib.cake_gg_i8_plan.restype = ctypes.c_int
+    lib.cake_gg_i8_gemm.argtypes = [i8plan_p, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.cake_gg_i8_gemm.restype = ctypes.c_int
+    lib.cake_gg_i8_quant.argtypes = [vp, ctypes.c_int, ctypes.c_int, i64, i32, vp, vp, vp]
+    lib.cake_gg_i8_quant.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -269,6 +304,37 @@ def cake_gg_router_fp32(rp, X, W, Y, workspace, workspace_bytes=None, stream=Non
     return load_library().cake_gg_router_fp32(ctypes.byref(rp), _ptr(X), _ptr(W), _ptr(Y), _ptr(workspace), nb, s)
 
 
+def _i8_x_code(d):
+    return I8_X_DTYPES[d] if isinstance(d, str) else int(d)
+
+
+def _act_code(a):
+    return I8_ACTS[a] if a is None or isinstance(a, str) else int(a)
+
+
+def cake_gg_i8_plan(E, M_max, T, N, K, x_dtype="bf16", act=None, out_dtype="bf16", max_sms=0) -> CakeGGI8Plan:
+    """cake_gg_i8_plan(): plan of an 8-bit product of M_max rows from T tokens; raises on error."""
+    plan = CakeGGI8Plan()
+    rc = load_library().cake_gg_i8_plan(ctypes.byref(plan), int(E), int(M_max), int(T), int(N), int(K),
+                                        _i8_x_code(x_dtype), _act_code(act), _dtype_code(out_dtype), int(max_sms))
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_i8_plan")
+    return plan
+
+
+def cake_gg_i8_gemm(plan, X, xs, rows, W, ws, Y, offsets, workspace, workspace_bytes=None, stream=None) -> int:
+    """cake_gg_i8_gemm(): the 8-bit product; returns the status code."""
+    nb = int(workspace.numel() * workspace.element_size()) if workspace_bytes is None else int(workspace_bytes)
+    return load_library().cake_gg_i8_gemm(ctypes.byref(plan), _ptr(X), _ptr(xs), _ptr(rows), _ptr(W), _ptr(ws), _ptr(Y),
+                                          _ptr(offsets), _ptr(workspace), nb, _stream(stream, W))
+
+
+def cake_gg_i8_quant(X, x_dtype, act, T, K, Xq, xs, stream=None) -> int:
+    """cake_gg_i8_quant(): rows of X to 8-bit rows and scales; returns the status code."""
+    return load_library().cake_gg_i8_quant(_ptr(X), _i8_x_code(x_dtype), _act_code(act), int(T), int(K), _ptr(Xq),
+                                           _ptr(xs), _stream(stream, X))
+
+
 # ---------------------------------------------------------------- tensor-level helpers
 
 
@@ -344,4 +410,108 @@ def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=Non
         st = cake_gg_check_status(workspace, stream)
         if st != CAKE_GG_OK:
             raise CakeGGError(st, "cake_gg_router_fp32 (device status)")
+    return out
+
+
+def _i8_x_name(X):
+    import torch
+    name = {torch.int8: "int8", torch.bfloat16: "bf16", torch.float32: "fp32"}.get(X.dtype)
+    if name is None:
+        raise TypeError(f"X is {X.dtype}: int8, bfloat16 or float32 are taken")
+    return name
+
+
+def _need(tensor, name, dtype, shape, device):
+    """A dense CUDA tensor of this type and shape on `device`."""
+    if tensor.dtype != dtype:
+        raise TypeError(f"{name} is {tensor.dtype}: {dtype} is needed")
+    if tuple(tensor.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(tensor.shape)}: {shape} is needed")
+    if tensor.device != device:
+        raise ValueError(f"{name} is on {tensor.device}: the weights are on {device}")
+    if not tensor.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def quantize_rows(X, act=None, out=None, scale=None, stream=None):
+    """Rows of X [T, K] (bf16 or fp32) as 8-bit integers [T, K] and FP32 scales [T].
+
+    ``act="silu_mul"`` takes X [T, 2 K] = [g | u] and quantises silu(g) * u.
+    The scale of a row is its largest magnitude / 127; integers are rounded to
+    nearest, ties to even.  A row that holds a NaN or an infinity gets the scale
+    NaN and zeros, one whose values are all below 2^-120 the scale 0 and zeros.
+    Quantising W.reshape(E * N, K) gives int8_gemm's weights.
+    """
+    import torch
+    name = _i8_x_name(X)
+    if X.dim() != 2 or (act is not None and X.shape[1] % 2 != 0):
+        raise ValueError("X is [T, K], or [T, 2 K] with an activation")
+    T, K = int(X.shape[0]), int(X.shape[1]) // (1 if act is None else 2)
+    _need(X, "X", X.dtype, tuple(X.shape), X.device)
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.int8, device=X.device)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=X.device)
+    _need(out, "out", torch.int8, (T, K), X.device)
+    _need(scale, "scale", torch.float32, (T,), X.device)
+    rc = cake_gg_i8_quant(X, name, act, T, K, out, scale, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_i8_quant")
+    return out, scale
+
+
+def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="bf16", max_sms=0, out=None,
+              plan=None, workspace=None, stream=None, check=True):
+    """Product of 8-bit rows and weights with a scale per token and per channel.
+
+        Y[m, n] = (sum_k q[r, k] W[e, n, k]) * ws[e, n] * xs[r]
+
+    W [E, N, K] int8 and ws [E, N] fp32 (dense: [N, K] and [N]); expert e owns
+    the rows [offsets[e], offsets[e+1]) of Y (int32 [E + 1]; none for dense);
+    r = rows[m] (int32 [M], the token that row m was routed from) or m itself.
+    X is the tokens: int8 [T, K] with their scales xs [T], or bf16 / fp32
+    [T, K] quantised on the way ([T, 2 K] with act="silu_mul", see
+    quantize_rows).  Rows >= offsets[E] of Y are left as allocated.  Output and
+    workspace are allocated through torch when not given.
+    """
+    import torch
+    name = _i8_x_name(X)
+    if W.dim() not in (2, 3) or X.dim() != 2:
+        raise ValueError("X is [T, K] and W [N, K] or [E, N, K]")
+    E = int(W.shape[0]) if W.dim() == 3 else 1
+    N, K = int(W.shape[-2]), int(W.shape[-1])
+    T = int(X.shape[0])
+    M = T if rows is None else int(rows.shape[0])
+    device = W.device
+    _need(W, "W", torch.int8, tuple(W.shape), device)
+    _need(X, "X", X.dtype, (T, K if act is None else 2 * K), device)
+    _need(ws, "ws", torch.float32, tuple(W.shape[:-1]), device)
+    if (xs is None) == (name == "int8"):
+        raise ValueError("xs comes with int8 X, and only with it")
+    if xs is not None:
+        _need(xs, "xs", torch.float32, (T,), device)
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, (E + 1,), device)
+    elif W.dim() == 3 and E != 1:
+        raise ValueError("W of several experts comes with offsets")
+    if rows is not None:
+        _need(rows, "rows", torch.int32, (M,), device)
+    if plan is None:
+        plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
+    elif (plan.E, plan.M_max, plan.T, plan.N, plan.K, plan.x_dtype, plan.act, plan.out_dtype) != (
+            E, M, T, N, K, I8_X_DTYPES[name], _act_code(act), _dtype_code(out_dtype)):
+        raise ValueError("the plan is another problem's")
+    if out is None:
+        out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=device)
+    else:
+        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), device)
+    if workspace is None:
+        workspace = make_workspace(plan, device)
+    rc = cake_gg_i8_gemm(plan, X, xs, rows, W, ws, out, offsets, workspace, stream=stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_i8_gemm")
+    if check:
+        st = cake_gg_check_status(workspace, stream)
+        if st != CAKE_GG_OK:
+            raise CakeGGError(st, "cake_gg_i8_gemm (device status)")
     return out

@@ -694,6 +694,14 @@ int run(const cake_gg_plan_t *plan, int mode, const void *opA, const void *opB, 
 
 namespace cakegg {
 
+int device_sms(int *sms)
+{
+    DevInfo dev;
+    const int rc = device_info(&dev);
+    if (rc == CAKE_GG_OK) *sms = dev.sms;
+    return rc;
+}
+
 int router_plan(cake_gg_plan_t *plan, int64_t T, int32_t R, int32_t K, int32_t max_sms)
 {
     std::memset(plan, 0, sizeof(*plan));
@@ -825,6 +833,7 @@ const char *cake_gg_strerror(int code)
     case CAKE_GG_ERR_TIMEOUT: return "a bounded wait inside the kernel expired";
     case CAKE_GG_ERR_SCRATCH_LIMIT:
         return "problem needs more scratch than the no-allocation entry point's fixed maximum";
+    case CAKE_GG_ERR_BAD_ROWS: return "device found a row index outside the tokens";
     default: return "unknown status";
     }
 }
