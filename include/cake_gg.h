@@ -291,9 +291,10 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
  * [E + 1] (as in the passes above; null when E = 1: it owns every row), r(m) =
  * rows[m], or m where rows is null.  All row-major, dense, all 256 values of
  * a byte allowed.  Rows at or past offsets[E] of Y are never written, and an
- * expert without rows reads no weights.  Sums of the few-row path are exact
- * 32-bit integers; one rounding to FP32 and two multiplications follow, then
- * one rounding to BF16 for BF16 output.  The same call gives the same bits on
+ * expert without rows reads no weights.  Sums are exact 32-bit integers (few
+ * rows) or FP32 sums of exact products (tensor cores: exact too while their
+ * magnitude stays below 2^24); two FP32 multiplications follow, by ws and then
+ * xs, and one rounding for BF16 output.  The same call gives the same bits on
  * every run and under every max_sms.
  *
  * X is q itself (x_dtype CAKE_GG_INT8, xs given), or BF16 / FP32 activations
@@ -308,7 +309,10 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
  * that holds a NaN or an infinity gets xs = NaN, q = 0, so its products are
  * NaN.  Weights are quantised the same way: cake_gg_i8_quant over W's rows. */
 typedef enum { CAKE_GG_ACT_NONE = 0, CAKE_GG_ACT_SILU_MUL = 1 } cake_gg_act_t;
-typedef enum { CAKE_GG_I8_ROWS = 0 } cake_gg_i8_path_t;
+typedef enum {
+    CAKE_GG_I8_ROWS = 0,     /* few rows: 32-bit integer dot products              */
+    CAKE_GG_I8_MMA = 1       /* tensor cores: FP16 operands, FP32 sums             */
+} cake_gg_i8_path_t;
 
 typedef struct cake_gg_i8_plan {
     int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
@@ -322,8 +326,14 @@ typedef struct cake_gg_i8_plan {
     int32_t out_dtype;       /* CAKE_GG_BF16 or CAKE_GG_FP32                        */
     int32_t max_sms;         /* cap on persistent CTAs; 0 = every SM of the device  */
     /* chosen by cake_gg_i8_plan() */
-    int32_t path;            /* cake_gg_i8_path_t                                   */
-    int32_t reserved;
+    int32_t path;            /* cake_gg_i8_path_t; the rest is the tensor-core path's: */
+    int32_t pair;            /* 2: two CTAs compute 256 channels as one MMA, else 1 */
+    int32_t tile_rows;       /* rows of a tile at most (16 .. 256)                  */
+    int32_t acc_bufs;        /* accumulators in tensor memory (1 or 2)              */
+    int32_t slots;           /* widened weight tiles in tensor memory               */
+    int32_t stages;          /* shared-memory ring depth                            */
+    int32_t splits;          /* CTAs of a cluster that share a tile's reduction     */
+    int32_t debug_flags;     /* test-only fault injection; 0 in normal use          */
     uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
     uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
 } cake_gg_i8_plan_t;

@@ -15,6 +15,7 @@
 #include "../../include/cake_gg.h"
 #include "cake_gg_launch.h"
 #include "cake_gg_sched.h"
+#include "cake_gg_int8.h"
 
 using namespace cakegg;
 
@@ -700,6 +701,25 @@ int device_sms(int *sms)
     const int rc = device_info(&dev);
     if (rc == CAKE_GG_OK) *sms = dev.sms;
     return rc;
+}
+
+int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box)
+{
+    const int rc = get_encoder();
+    if (rc != CAKE_GG_OK) return rc;
+    cuuint64_t gdim[5], gstride[4];
+    cuuint32_t bx[5], estride[5];
+    for (int i = 0; i < rank; ++i) {
+        gdim[i] = dims[i];
+        bx[i] = box[i];
+        estride[i] = 1;
+        if (i > 0) gstride[i - 1] = strides[i - 1];
+    }
+    const CUresult r = g_encode(m, type, cuuint32_t(rank), const_cast<void *>(base), gdim, gstride, bx, estride,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
 int router_plan(cake_gg_plan_t *plan, int64_t T, int32_t R, int32_t K, int32_t max_sms)

@@ -26,6 +26,7 @@ namespace {
 
 constexpr uint64_t kHeader = 256;              // status word at byte 0
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kStagesMost = 12, kSlotsMost = 8;
 constexpr int32_t kMaxExperts = 1024;
 constexpr int32_t kMaxK = (1 << 17) - 16;      // |sum of K products| <= 2^14 K stays below 2^31
 
@@ -44,7 +45,9 @@ bool pdl_enabled()
     return !(v && std::atoi(v) == 0);
 }
 
-// Workspace: header | token scales [T] | 8-bit tokens [T, K].
+// Workspace: header | token scales [T] (activations only) | the tokens as the
+// path reads them: FP16 integers [T, K] for the tensor cores, 8-bit ones for
+// the few-row path (activations only).
 struct Layout {
     uint64_t scales, tokens, total;
 };
@@ -52,10 +55,11 @@ struct Layout {
 Layout layout(const cake_gg_i8_plan_t &pl)
 {
     Layout L;
-    const bool pass = pl.x_dtype != CAKE_GG_INT8;
+    const bool ready = pl.x_dtype == CAKE_GG_INT8;
+    const uint64_t size = pl.path == CAKE_GG_I8_MMA ? 2 : ready ? 0 : 1;
     L.scales = kHeader;
-    L.tokens = L.scales + (pass ? align_up(uint64_t(pl.T) * 4, 256) : 0);
-    L.total = L.tokens + (pass ? align_up(uint64_t(pl.T) * uint64_t(pl.K), 256) : 0);
+    L.tokens = L.scales + (ready ? 0 : align_up(uint64_t(pl.T) * 4, 256));
+    L.total = L.tokens + align_up(uint64_t(pl.T) * uint64_t(pl.K) * size, 256);
     return L;
 }
 
@@ -98,6 +102,25 @@ __device__ __forceinline__ void row8(const XT *row, int32_t K, int k, float (&v)
     }
 }
 
+// Eight integers of a row as bytes, or as the FP16 operands of the tensor cores.
+__device__ __forceinline__ void store8(int8_t *out, const float (&v)[8])
+{
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i / 4] |= uint32_t(__float2int_rn(v[i]) & 0xff) << (8 * (i % 4));
+    *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store8(__half *out, const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // One block per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
 // rest again (from L2).  |h| is compared by its bit pattern, so a NaN or an
@@ -106,9 +129,9 @@ __device__ __forceinline__ void row8(const XT *row, int32_t K, int k, float (&v)
 // zero (127 / a would not be finite).
 constexpr int kHeld = 2;
 
-template <typename XT, bool ACT>
+template <typename XT, bool ACT, typename QT>
 __global__ void __launch_bounds__(1024)
-    i8_quant_kernel(const XT *__restrict__ X, int32_t K, int8_t *__restrict__ Q, float *__restrict__ S)
+    i8_quant_kernel(const XT *__restrict__ X, int32_t K, QT *__restrict__ Q, float *__restrict__ S)
 {
     __shared__ uint32_t warp_max[32];
     grid_dependency_wait();
@@ -142,15 +165,12 @@ __global__ void __launch_bounds__(1024)
     const bool finite = m < 0x7f800000u, tiny = a < 0x1p-120f;
     const float inv = finite && !tiny ? 127.0f / a : 0.0f;
     if (threadIdx.x == 0) S[t] = !finite ? __uint_as_float(0x7fc00000u) : tiny ? 0.0f : a / 127.0f;
-    int8_t *out = Q + t * int64_t(K);
+    QT *out = Q + t * int64_t(K);
     auto emit = [&](const float (&v)[8], int k) {
-        uint32_t w[2] = {0, 0};
+        float r[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int q = finite ? __float2int_rn(v[i] * inv) : 0;
-            w[i / 4] |= uint32_t(q & 0xff) << (8 * (i % 4));
-        }
-        *reinterpret_cast<uint2 *>(out + k) = make_uint2(w[0], w[1]);
+        for (int i = 0; i < 8; ++i) r[i] = finite ? rintf(v[i] * inv) : 0.0f;
+        store8(out + k, r);
     };
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
@@ -164,33 +184,72 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-int launch_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, int8_t *Q, float *S, cudaStream_t stream)
+// 8-bit tokens as FP16 integers, 16 values a thread.
+__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ X, __half *__restrict__ Q, int64_t n16)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n16) return;
+    const uint4 w = reinterpret_cast<const uint4 *>(X)[i];
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = float(int8_t(u[h * 2 + j / 4] >> (8 * (j % 4))));
+        store8(Q + i * 16 + h * 8, v);
+    }
+}
+
+// A kernel of the token pass: a programmatic dependent of the stream's
+// previous kernel (it waits for it before it reads anything), and only then
+// lets the product start, whose early reads of weights and offsets are thus
+// ordered after everything before this call.
+cudaLaunchConfig_t pass_config(int64_t blocks, int threads, cudaLaunchAttribute *attr, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    int threads = int(align_up((uint64_t(K) / 8 + kHeld - 1) / kHeld, 32));
-    if (threads > 1024) threads = 1024;
-    cfg.gridDim = dim3(unsigned(T), 1, 1);
+    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.stream = stream;
     if (pdl_enabled()) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr->val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const bool silu = act == CAKE_GG_ACT_SILU_MUL;
-    cudaError_t err;
-    if (x_dtype == CAKE_GG_BF16) {
-        const uint16_t *x = static_cast<const uint16_t *>(X);
-        err = silu ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<uint16_t, true>, x, K, Q, S)
-                   : cudaLaunchKernelEx(&cfg, i8_quant_kernel<uint16_t, false>, x, K, Q, S);
-    } else {
-        const float *x = static_cast<const float *>(X);
-        err = silu ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<float, true>, x, K, Q, S)
-                   : cudaLaunchKernelEx(&cfg, i8_quant_kernel<float, false>, x, K, Q, S);
-    }
+    return cfg;
+}
+
+template <typename XT, typename QT>
+cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q, float *S, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    int threads = int(align_up((uint64_t(K) / 8 + kHeld - 1) / kHeld, 32));
+    if (threads > 1024) threads = 1024;
+    const cudaLaunchConfig_t cfg = pass_config(T, threads, &attr, stream);
+    const XT *x = static_cast<const XT *>(X);
+    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, true, QT>, x, K, Q, S)
+                                       : cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, false, QT>, x, K, Q, S);
+}
+
+template <typename QT>
+int launch_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, QT *Q, float *S, cudaStream_t stream)
+{
+    const cudaError_t err = x_dtype == CAKE_GG_BF16 ? launch_quant_as<uint16_t>(X, act, T, K, Q, S, stream)
+                                                    : launch_quant_as<float>(X, act, T, K, Q, S, stream);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+int launch_expand(const void *X, int64_t T, int32_t K, __half *Q, cudaStream_t stream)
+{
+    const int64_t n16 = T * (K / 16), blocks = (n16 + 255) / 256;
+    if (blocks > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pass_config(blocks, 256, &attr, stream);
+    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, static_cast<const int8_t *>(X), Q, n16) == cudaSuccess
+               ? CAKE_GG_OK
+               : CAKE_GG_ERR_CUDA;
 }
 
 // The problem's own checks, shared by the plan and the call.
@@ -210,6 +269,75 @@ int check_problem(int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K, int
         !mul_ok(uint64_t(M_max), uint64_t(N) * 4u, &t))
         return CAKE_GG_ERR_OVERFLOW;
     return CAKE_GG_OK;
+}
+
+int env_int(const char *name, int dflt)
+{
+    const char *v = std::getenv(name);
+    return v && *v ? std::atoi(v) : dflt;
+}
+
+// Tensor memory (512 columns of a CTA) left beside the accumulators, in slots
+// of 64 columns, and the ring depth that fits beside the rest of shared memory.
+int slots_for(int nt, int bufs)
+{
+    const int n = (512 - bufs * (nt < 32 ? 32 : nt)) / 64;
+    return n > kSlotsMost ? kSlotsMost : n;
+}
+
+int stages_for(int pair, int nt, int splits, int E)
+{
+    int s = kStagesMost;
+    while (s > 2 && i8_mma_smem(pair, nt, s, splits, E) > kI8SmemLimit) --s;
+    return s;
+}
+
+// Shape of the tensor-core path.  Rows of a tile: what an expert is expected to
+// have (twice the average where rows are routed), in powers of two up to 128;
+// above that pairs of CTAs take 256 channels x 192 rows.
+void choose_mma(cake_gg_i8_plan_t *pl)
+{
+    const int64_t busy = pl->M_max < pl->E ? pl->M_max : pl->E;
+    const int64_t est = pl->E == 1 ? pl->M_max : 2 * ((pl->M_max + busy - 1) / (busy > 0 ? busy : 1));
+    pl->path = CAKE_GG_I8_MMA;
+    pl->pair = 1;
+    pl->tile_rows = est <= 16 ? 16 : est <= 32 ? 32 : est <= 64 ? 64 : 128;
+    pl->acc_bufs = 2;
+    pl->splits = 1;
+    if (est > 256) {
+        pl->pair = 2;
+        pl->tile_rows = 192;
+    }
+    pl->pair = env_int("CAKE_GG_I8_PAIR", pl->pair) == 2 ? 2 : 1;
+    const int nt = env_int("CAKE_GG_I8_ROWS_PER_TILE", pl->tile_rows);
+    if (nt >= 16 && nt <= 256 && nt % 16 == 0) pl->tile_rows = nt;
+    pl->acc_bufs = env_int("CAKE_GG_I8_BUFS", pl->tile_rows > 192 ? 1 : pl->acc_bufs) == 1 ? 1 : 2;
+    const int64_t tiles = (pl->M_max / pl->tile_rows + busy) * ((pl->N + 127) / 128);
+    if (pl->pair == 1 && pl->tile_rows <= 64) {
+        const int n_kb = (pl->K + 127) / 128;
+        for (int s = 8; s > 1; s /= 2)
+            if (tiles * s <= 152 && n_kb >= 4 * s) {
+                pl->splits = s;
+                break;
+            }
+    }
+    const int sp = env_int("CAKE_GG_I8_SPLITS", pl->splits);
+    if (sp >= 1 && sp <= 8 && pl->pair == 1) pl->splits = sp;
+    pl->slots = slots_for(pl->tile_rows, pl->acc_bufs);
+    pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
+}
+
+// What the tensor-core kernel can run.
+bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
+{
+    const int per_cta = pl.pair == 2 ? pl.tile_rows / 2 : pl.tile_rows;
+    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 16 * pl.pair && pl.tile_rows <= 256 &&
+           pl.tile_rows % (16 * pl.pair) == 0 && (per_cta < 64 || per_cta % 32 == 0) &&
+           (pl.tile_rows == 16 || pl.tile_rows % 32 == 0) && (pl.acc_bufs == 1 || pl.acc_bufs == 2) &&
+           pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
+           pl.slots <= slots_for(pl.tile_rows, pl.acc_bufs) && pl.splits >= 1 && pl.splits <= 8 &&
+           (pl.splits == 1 || pl.pair == 1) &&
+           i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }
 
 }  // namespace
@@ -234,7 +362,11 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
     plan->act = act;
     plan->out_dtype = out_dtype;
     plan->max_sms = max_sms;
-    plan->path = CAKE_GG_I8_ROWS;
+    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8RowChunk ? CAKE_GG_I8_ROWS : CAKE_GG_I8_MMA);
+    if (path == CAKE_GG_I8_MMA) {
+        choose_mma(plan);
+        if (!mma_plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
+    }
     plan->timeout_ns = kTimeoutNs;
     plan->workspace_bytes = layout(*plan).total;
     return CAKE_GG_OK;
@@ -262,7 +394,8 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     const cake_gg_i8_plan_t &pl = *plan;
     int rc = check_problem(pl.E, pl.M_max, pl.T, pl.N, pl.K, pl.x_dtype, pl.act, pl.out_dtype);
     if (rc != CAKE_GG_OK) return rc;
-    if (pl.path != CAKE_GG_I8_ROWS || pl.max_sms < 0) return CAKE_GG_ERR_INVALID_ARG;
+    if ((pl.path != CAKE_GG_I8_ROWS && (pl.path != CAKE_GG_I8_MMA || !mma_plan_ok(pl))) || pl.max_sms < 0)
+        return CAKE_GG_ERR_INVALID_ARG;
     const bool ready = pl.x_dtype == CAKE_GG_INT8;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))
         return CAKE_GG_ERR_INVALID_ARG;
@@ -278,14 +411,17 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
 
     uint8_t *base = static_cast<uint8_t *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int8_t *q = static_cast<const int8_t *>(X);
+    const bool mma = pl.path == CAKE_GG_I8_MMA;
+    void *tokens = base + L.tokens;
     if (!ready) {
-        int8_t *Xq = reinterpret_cast<int8_t *>(base + L.tokens);
         float *scales = reinterpret_cast<float *>(base + L.scales);
-        if ((rc = launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, Xq, scales, s)) != CAKE_GG_OK) return rc;
-        q = Xq;
+        rc = mma ? launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<__half *>(tokens), scales, s)
+                 : launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<int8_t *>(tokens), scales, s);
         xs = scales;
+    } else if (mma) {
+        rc = launch_expand(X, pl.T, pl.K, static_cast<__half *>(tokens), s);
     }
+    if (rc != CAKE_GG_OK) return rc;
     I8Params p{};
     p.offsets = offsets;
     p.rows = rows;
@@ -300,9 +436,21 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     p.N = pl.N;
     p.K = pl.K;
     p.out_f32 = pl.out_dtype == CAKE_GG_FP32;
-    p.early = ready ? 0 : 1;
+    p.early = !ready || mma ? 1 : 0;
     p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
-    return launch_i8_rows(p, q, pdl_enabled(), s) == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+    if (!mma)
+        return launch_i8_rows(p, static_cast<const int8_t *>(ready ? X : tokens), pdl_enabled(), s) == cudaSuccess
+                   ? CAKE_GG_OK
+                   : CAKE_GG_ERR_CUDA;
+    I8MmaParams m{};
+    m.b = p;
+    m.nt = pl.tile_rows;
+    m.stages = pl.stages;
+    m.slots = pl.slots;
+    m.bufs = pl.acc_bufs;
+    m.splits = pl.splits;
+    m.debug_flags = pl.debug_flags;
+    return launch_i8_mma(m, tokens, pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl_enabled(), s);
 }
 
 }  // extern "C"

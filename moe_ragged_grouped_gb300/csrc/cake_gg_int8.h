@@ -14,6 +14,10 @@ namespace cakegg {
 
 // (cake_gg_capi.cu) checks that the current device is sm_103 and gives its SM count
 int device_sms(int *sms);
+// (cake_gg_capi.cu) tensor map of a dense tensor, dims[0] contiguous, byte strides of
+// dims 1 .. given, 128-byte swizzled boxes, zero fill outside the tensor
+int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box);
 
 // One call of the products, as every kernel sees it.
 //   Y[m, n] = (sum_k q[r(m), k] W[e(m), n, k]) * ws[e(m), n] * xs[r(m)]
@@ -36,6 +40,26 @@ struct I8Params {
 constexpr int32_t kI8StatusBadOffsets = CAKE_GG_ERR_BAD_OFFSETS;
 constexpr int32_t kI8StatusBadRows = CAKE_GG_ERR_BAD_ROWS;
 constexpr int32_t kI8StatusTimeout = CAKE_GG_ERR_TIMEOUT;
+
+// The tensor-core path's own numbers.
+struct I8MmaParams {
+    I8Params b;
+    int32_t nt;               // rows of a tile at most
+    int32_t stages;           // shared-memory ring depth
+    int32_t slots;            // widened weight tiles in tensor memory
+    int32_t bufs;             // accumulators (1 or 2)
+    int32_t splits;           // CTAs that share a tile's reduction (one cluster; 1 = none)
+    int32_t debug_flags;
+    int32_t n_ct, n_kb, box;  // (set by the launch) channel tiles, stages of a tile, rows of a copy box
+};
+
+constexpr size_t kI8SmemLimit = 232448;   // opt-in dynamic shared memory per CTA (227 KB)
+
+// Dynamic shared memory of a CTA.
+size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E);
+
+// Tensor-core path: `tokens` are FP16 integers [T, K].  Returns a cake_gg_status_t.
+int launch_i8_mma(const I8MmaParams &p, const void *tokens, int pair, int sms, bool pdl, cudaStream_t stream);
 
 constexpr int kI8RowChunk = 8;   // rows of one expert that the row kernel computes together
 

@@ -1,0 +1,637 @@
+// cake_gg_int8_mma.cu -- the 8-bit integer products on the tensor cores.
+//
+//   Y[m, n] = (sum_k q[r(m), k] W[e(m), n, k]) * ws[e(m), n] * xs[r(m)]
+//
+// sm_103a multiplies 8-bit integers slowly, but every 8-bit integer is exact in
+// FP16, every product of two exact in FP32 and so is every sum below 2^24: the
+// products run at the FP16 tensor rate and the weights stay 8-bit in memory.
+//
+// A tile is 128 channels (256 for a pair of CTAs) x up to nt rows of one
+// expert, computed transposed: D[channel, row] += W q^T.  The weights are the
+// MMA's A operand, which may come from tensor memory: 8-bit tiles arrive in
+// shared memory by TMA, converter warps widen them to FP16 and write them to
+// tensor memory, so the widened weights cost no shared memory bandwidth.  The
+// rows are the B operand: FP16 integers in shared memory (written by the token
+// pass), loaded by TMA, row by row through `rows` where they are routed.  B's
+// width follows the rows the tile really has, so a ragged end costs its own
+// size only.
+//
+// Roles of a CTA (448 threads): warp 0 copies, warp 1 issues MMAs, warps 2-5
+// scale and store, warps 6-13 convert (two groups on alternate stages).
+#include "cake_gg_int8.h"
+#include "cake_gg_ptx.cuh"
+
+namespace cakegg {
+namespace {
+
+constexpr int kThreads = 448;
+constexpr int kConvWarp0 = 6;
+constexpr int kKB = 128;                     // reduction length of a stage
+constexpr uint32_t kWBytes = 128 * kKB;      // 8-bit weight tile of a stage
+constexpr int kStagesMax = 12;
+constexpr int kSlotsMax = 8;
+constexpr uint32_t kSlotCols = kKB / 2;      // tensor memory columns of a widened weight tile
+constexpr uint64_t kDrainNs = 20000000ull;
+
+struct __align__(16) Ctrl {
+    uint64_t full[kStagesMax], empty[kStagesMax];     // stage: copies landed / MMAs done
+    uint64_t conv[kSlotsMax], aempty[kSlotsMax];      // slot: weights widened / MMAs done
+    uint64_t tfull[2], tempty[2];                     // accumulator: complete / stored
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t bad;
+    int32_t total;                                    // row tiles of all experts
+};
+
+__device__ __forceinline__ bool aborted(Ctrl *c) { return *reinterpret_cast<volatile int32_t *>(&c->abort_flag) != 0; }
+
+// Bounded wait on one mbarrier phase by every lane of a warp; warp-uniform
+// verdict (false: it ran out, or another role gave up).
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctrl *c, const I8Params &p)
+{
+    auto poll = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    bool ok = poll();
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (true) {
+            for (int i = 0; i < 32 && !ok; ++i) ok = poll();
+            if (ok || aborted(c)) break;
+            if (global_timer_ns() - t0 > p.timeout_ns) {
+                *reinterpret_cast<volatile int32_t *>(&c->abort_flag) = 1;
+                atomicCAS(p.status, 0, kI8StatusTimeout);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > kDrainNs) return;
+}
+
+// Four rows of a tensor (box one row high) to consecutive 128-byte rows.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                            const int32_t (&r)[4])
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Four 8-bit integers (a 32-bit word) as two packed pairs of FP16: with its
+// sign bit flipped a byte is b + 128, and as the low byte of the FP16 pattern
+// 0x6400 (1024, one unit in the last place) it reads 1024 + 128 + b.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));   // 1152 each
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+// FP32 accumulators, FP16 operands (A and B format fields 0), both K-major.
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t M, uint32_t N)
+{
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// A place in a ring and the parity of its current round.  A wait for the
+// opposite parity passes at once in the first round: the ring starts free.
+struct Turn {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int n)
+    {
+        if (++at == n) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void back(int n)
+    {
+        if (at-- == 0) {
+            at = n - 1;
+            parity ^= 1u;
+        }
+    }
+};
+
+struct Tile {
+    int e, ct;            // expert, channel tile
+    int32_t m0, rows, end;   // first row, rows in the tile, end of the expert's rows
+};
+
+__device__ __forceinline__ Tile decode(int64_t u, const I8MmaParams &p, const int32_t *off, const int32_t *pref)
+{
+    Tile t;
+    t.ct = int(u % p.n_ct);
+    const int32_t g = int32_t(u / p.n_ct);
+    int lo = 0, hi = p.b.E;      // pref[lo] <= g < pref[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pref[mid] <= g) lo = mid;
+        else hi = mid;
+    }
+    t.e = lo;
+    t.m0 = off[lo] + (g - pref[lo]) * p.nt;
+    t.end = off[lo + 1];
+    t.rows = min(p.nt, t.end - t.m0);
+    return t;
+}
+
+template <int PAIR, bool OUT_F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    i8_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
+                  const I8MmaParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    const uint32_t x_rows = uint32_t(p.nt / PAIR);               // B rows of this CTA in a stage
+    const uint32_t stage_bytes = kWBytes + x_rows * 256u;
+    uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
+    float *recv = reinterpret_cast<float *>(after);              // split: [split][column][128]
+    after += p.splits > 1 ? size_t(p.nt + p.splits) * 512u : 0;
+    Ctrl *c = reinterpret_cast<Ctrl *>(after);
+    float *xs_tile = reinterpret_cast<float *>(c + 1);           // [2][nt]
+    int32_t *off = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);
+    int32_t *pref = off + p.b.E + 1;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = p.b.E;
+    const int rank = PAIR == 2 || p.splits > 1 ? int(cluster_ctarank()) : 0;
+    const int half = PAIR == 2 ? rank : 0;
+    const bool leader = half == 0;
+
+    // ---- set-up: TMEM, barriers, offsets and the prefix of their row tiles ----
+    if (tid == 0) {
+        c->abort_flag = 0;
+        c->bad = 0;
+        tma_prefetch_desc(&mapW);
+        tma_prefetch_desc(&mapX);
+    }
+    if (warp == 1) {
+        tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
+        tmem_relinquish<PAIR>();
+    }
+    if (tid == 64) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&c->full[s]), 1);
+            mbar_init(smem_u32(&c->empty[s]), 1);
+        }
+        for (int a = 0; a < p.slots; ++a) {
+            mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);         // the group's warps, of both CTAs
+            mbar_init(smem_u32(&c->aempty[a]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c->tfull[b]), 1);
+            mbar_init(smem_u32(&c->tempty[b]), 4u * PAIR);       // storing warps, of both CTAs
+        }
+        mbar_init(smem_u32(&c->drain), 1);
+        fence_barrier_init();
+    }
+    if (!p.b.early) grid_dependency_wait();
+    grid_launch_dependents();
+    __syncthreads();                                             // c->bad is zero
+    for (int i = tid; i <= E; i += kThreads) off[i] = p.b.offsets ? p.b.offsets[i] : (i ? int32_t(p.b.M) : 0);
+    __syncthreads();
+    if (warp == 0) {
+        // lane l sums the row tiles of its run of experts, then the runs are scanned
+        const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+        int32_t sum = 0;
+        bool bad = lane == 0 && off[0] != 0;
+        for (int e = e0; e < e1; ++e) {
+            const int32_t n = off[e + 1] - off[e];
+            bad |= off[e + 1] < off[e] || int64_t(off[e + 1]) > p.b.M;
+            sum += n > 0 ? (n - 1) / p.nt + 1 : 0;
+        }
+        int32_t inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        int32_t at = inc - sum;
+        for (int e = e0; e < e1; ++e) {
+            const int32_t n = off[e + 1] - off[e];
+            pref[e] = at;
+            at += n > 0 ? (n - 1) / p.nt + 1 : 0;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 31) {
+            pref[E] = inc;
+            c->total = bad ? 0 : inc;
+            if (bad) atomicCAS(p.b.status, 0, kI8StatusBadOffsets);
+        }
+    }
+    if (PAIR == 2 || p.splits > 1) cluster_sync_all();           // peers' barriers are ready
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = c->tmem_base;
+    const uint32_t d_stride = uint32_t(p.nt < 32 ? 32 : p.nt);
+    const uint32_t slots0 = tmem + d_stride * uint32_t(p.bufs);
+
+    // Units: channel tile fastest, so that concurrent CTAs share an expert's
+    // rows and all of its weights stay in L2 between its row tiles.  A split
+    // cluster takes one unit, each of its CTAs a part of the reduction.
+    const int64_t units = int64_t(c->total) * p.n_ct;
+    const int64_t unit0 = blockIdx.x / (PAIR * p.splits);
+    const int64_t step = p.splits > 1 ? units + 1 : int64_t(gridDim.x / PAIR);
+    const int kb0 = p.splits > 1 ? p.n_kb * rank / p.splits : 0;
+    const int kb1 = p.splits > 1 ? p.n_kb * (rank + 1) / p.splits : p.n_kb;
+    constexpr int kNAlign = 16 * PAIR;
+    const uint16_t pair_mask = 3;
+
+    if (warp == 0) {
+        // ======================= copies =======================
+        const bool routed = p.b.rows != nullptr;
+        Turn st;
+        int issued = 0;       // stages filled, up to the ring's depth
+        bool ok = true, first = true;
+        for (int64_t u = unit0; ok && u < units; u += step) {
+            const Tile t = decode(u, p, off, pref);
+            const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
+            const int32_t mb = t.m0 + half * n_half;
+            const int n_box = (n_half + p.box - 1) / p.box;
+            const uint32_t bytes = kWBytes + 256u * uint32_t(routed ? n_half : n_box * p.box);
+            int32_t ids[2][4];
+            if (routed) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int32_t m = mb + (lane + 32 * i) * 4 + r;
+                        const int32_t id = (lane + 32 * i) * 4 < n_half && m < t.end ? p.b.rows[m] : 0;
+                        ids[i][r] = id >= 0 && id < p.b.T ? id : 0;     // (reported where it is scaled)
+                    }
+            }
+            auto load_w = [&](int kb, int s) {
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&c->full[s]);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0 && s == 0))
+                        tma_load_3d(ring + uint32_t(s) * stage_bytes, &mapW, bar, kb * kKB, (t.ct * PAIR + half) * 128, t.e);
+                }
+                __syncwarp();
+            };
+            auto load_x = [&](int kb, int s) {
+                const uint32_t bar = smem_u32(&c->full[s]), dst = ring + uint32_t(s) * stage_bytes + kWBytes;
+                if (routed) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int g = lane + 32 * i;
+                        if (g * 4 < n_half) {
+                            tma_gather4(dst + uint32_t(g) * 512u, &mapX, bar, kb * kKB, ids[i]);
+                            tma_gather4(dst + x_rows * 128u + uint32_t(g) * 512u, &mapX, bar, kb * kKB + 64, ids[i]);
+                        }
+                    }
+                } else if (lane < 2 * n_box) {
+                    const uint32_t chunk = uint32_t(lane) & 1u, b = uint32_t(lane) >> 1;
+                    tma_load_2d(dst + chunk * x_rows * 128u + b * uint32_t(p.box) * 128u, &mapX, bar,
+                                kb * kKB + int(chunk) * 64, mb + int(b) * p.box);
+                }
+            };
+            int kb = kb0;
+            if (first) {
+                // the weights of the first stages do not wait for the tokens
+                const int n = min(p.stages, kb1 - kb0);
+                for (int i = 0; i < n; ++i) load_w(kb0 + i, i);
+                grid_dependency_wait();
+                for (int i = 0; i < n; ++i) load_x(kb0 + i, i);
+                for (int i = 0; i < n; ++i) st.next(p.stages);
+                kb += n;
+                issued = n;
+                first = false;
+            }
+            for (; kb < kb1; ++kb) {
+                if (!warp_wait<false>(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b)) {
+                    ok = false;
+                    break;
+                }
+                load_w(kb, st.at);
+                load_x(kb, st.at);
+                st.next(p.stages);
+                if (issued < p.stages) ++issued;
+            }
+        }
+        if (first) grid_dependency_wait();
+        __syncwarp();
+        if (!ok || aborted(c)) {
+            // the copies in flight land before the CTA leaves
+            if (lane == 0)
+                for (int i = 0; i < issued; ++i) {
+                    st.back(p.stages);
+                    drain_wait(smem_u32(&c->full[st.at]), st.parity);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ======================= MMAs (the even CTA of a pair) =======================
+        Turn st, sl, acc;
+        bool ok = true, any = false;
+        if (leader) {
+            for (int64_t u = unit0; ok && u < units; u += step) {
+                const Tile t = decode(u, p, off, pref);
+                const uint32_t n = uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign);
+                const uint32_t idesc = idesc_f16(128u * PAIR, n);
+                const int buf = acc.at;
+                if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p.b)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + uint32_t(buf) * d_stride;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const int s = st.at, a = sl.at;
+                    // the converters of both CTAs saw their stage's copies land
+                    if (!warp_wait<PAIR == 2>(smem_u32(&c->conv[a]), sl.parity, c, p.b)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        tc_fence_after_sync();
+                        const uint32_t xb = ring + uint32_t(s) * stage_bytes + kWBytes;
+                        const uint64_t b0 = smem_desc_sw128(xb, 16, 1024), b1 = smem_desc_sw128(xb + x_rows * 128u, 16, 1024);
+                        const uint32_t at = slots0 + uint32_t(a) * kSlotCols;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            umma_bf16_ta<PAIR>(d, at + uint32_t(k) * 8u, (k < 4 ? b0 : b1) + uint64_t(k & 3) * 2u, idesc,
+                                               kb > kb0 || k > 0 ? 1u : 0u);
+                        if (PAIR == 2) {
+                            umma_commit_mc<2>(smem_u32(&c->empty[s]), pair_mask);
+                            umma_commit_mc<2>(smem_u32(&c->aempty[a]), pair_mask);
+                            if (kb + 1 == kb1) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
+                        } else {
+                            umma_commit<1>(smem_u32(&c->empty[s]));
+                            umma_commit<1>(smem_u32(&c->aempty[a]));
+                            if (kb + 1 == kb1) umma_commit<1>(smem_u32(&c->tfull[buf]));
+                        }
+                    }
+                    any = true;
+                    __syncwarp();
+                    st.next(p.stages);
+                    sl.next(p.slots);
+                }
+                acc.next(p.bufs);
+            }
+            if (!ok && any && lane == 0) {
+                umma_commit<PAIR>(smem_u32(&c->drain));
+                drain_wait(smem_u32(&c->drain), 0);
+            }
+        }
+        grid_dependency_wait();
+        __syncwarp();
+    } else if (warp < kConvWarp0) {
+        // ======================= scales and stores =======================
+        grid_dependency_wait();                                  // the token scales
+        const int q = warp & 3;                                  // tensor memory lanes 32 q ..
+        Turn acc, xb;
+        for (int64_t u = unit0; u < units; u += step) {
+            const Tile t = decode(u, p, off, pref);
+            float *xs = xs_tile + xb.at * p.nt;
+            for (int j = tid - 64; j < t.rows; j += 128) {
+                int64_t r = t.m0 + j;
+                if (p.b.rows) r = p.b.rows[r];
+                const bool bad = r < 0 || r >= p.b.T;
+                if (bad) atomicCAS(p.b.status, 0, kI8StatusBadRows);
+                xs[j] = bad ? 0.0f : p.b.xs[r];
+            }
+            const int n = (t.ct * PAIR + half) * 128 + q * 32 + lane;
+            const bool ch_ok = n < p.b.N;
+            const float ws = ch_ok ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
+            const int buf = acc.at;
+            const bool ok = warp_wait<false>(smem_u32(&c->tfull[buf]), acc.parity, c, p.b);
+            // the scales are in (their buffer is rewritten two tiles on, after the
+            // barrier between), and the four warps go on or give up together
+            if (!named_bar_and(1, 128, ok)) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + uint32_t(buf) * d_stride + (uint32_t(q * 32) << 16);
+            const int per = (t.rows + p.splits - 1) / p.splits;  // split: columns that a CTA sums
+            int owner = 0, mine = 0;
+            for (int c0 = 0; c0 < t.rows; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(d + uint32_t(c0), r);
+                tmem_ld_wait();
+                if (p.splits > 1) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < t.rows) {
+                            st_cluster_f32(map_to_cta(smem_u32(recv + (rank * per + mine) * 128 + q * 32 + lane), uint32_t(owner)),
+                                           __uint_as_float(r[j]));
+                            if (++mine == per) {
+                                mine = 0;
+                                ++owner;
+                            }
+                        }
+                    continue;
+                }
+                const int64_t y0 = (int64_t(t.m0) + c0) * p.b.N + n;
+                if (OUT_F32) {
+                    float *y = static_cast<float *>(p.b.Y) + y0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < t.rows && ch_ok) y[int64_t(j) * p.b.N] = __uint_as_float(r[j]) * ws * xs[c0 + j];
+                } else {
+                    // neighbouring lanes hold neighbouring channels: of two rows the even
+                    // lane stores the first row's pair, the odd lane the second's
+                    uint16_t *y = static_cast<uint16_t *>(p.b.Y) + y0 - (lane & 1);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float a = __uint_as_float(r[j]) * ws * xs[min(c0 + j, p.nt - 1)];
+                        const float b = __uint_as_float(r[j + 1]) * ws * xs[min(c0 + j + 1, p.nt - 1)];
+                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+                        const int row = j + (lane & 1);
+                        if (c0 + row < t.rows && ch_ok)
+                            *reinterpret_cast<uint32_t *>(y + int64_t(row) * p.b.N) =
+                                lane & 1 ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(smem_u32(&c->tempty[buf]));
+                else mbar_arrive_cluster(map_to_cta(smem_u32(&c->tempty[buf]), 0));
+            }
+            acc.next(p.bufs);
+            xb.next(2);
+        }
+    } else {
+        // ======================= weights to FP16 =======================
+        const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
+        const int row = q * 32 + lane;
+        const int64_t mine = unit0 < units ? (units - unit0 - 1) / step + 1 : 0;
+        const int64_t total = mine * (kb1 - kb0);
+        Turn st, sl;
+        for (int64_t it = 0; it < total; ++it, st.next(p.stages), sl.next(p.slots)) {
+            if (int(it & 1) != group) continue;
+            const int s = st.at, a = sl.at;
+            if (!warp_wait<false>(smem_u32(&c->full[s]), st.parity, c, p.b)) break;
+            if (!warp_wait<false>(smem_u32(&c->aempty[a]), sl.parity ^ 1u, c, p.b)) break;
+            const uint8_t *src = ring_ptr + size_t(s) * stage_bytes + row * 128;
+            const uint32_t dst = slots0 + uint32_t(a) * kSlotCols + (uint32_t(q * 32) << 16);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[32];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + (((h * 4 + v) ^ (row & 7)) << 4));
+                    widen4(w.x, f[v * 8], f[v * 8 + 1]);
+                    widen4(w.y, f[v * 8 + 2], f[v * 8 + 3]);
+                    widen4(w.z, f[v * 8 + 4], f[v * 8 + 5]);
+                    widen4(w.w, f[v * 8 + 6], f[v * 8 + 7]);
+                }
+                tmem_st_32x32b_x32(dst + uint32_t(h) * 32u, f);
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(smem_u32(&c->conv[a]));
+                else mbar_arrive_cluster(map_to_cta(smem_u32(&c->conv[a]), 0));
+            }
+        }
+        grid_dependency_wait();
+        __syncwarp();
+    }
+
+    if (PAIR == 1 && p.splits > 1) {
+        // every part of this CTA's columns has arrived: sum them in split order
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && warp < kConvWarp0 && unit0 < units && !aborted(c)) {
+            const Tile t = decode(unit0, p, off, pref);
+            const int per = (t.rows + p.splits - 1) / p.splits;
+            const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
+            if (n < p.b.N) {
+                const float ws = p.b.ws[int64_t(t.e) * p.b.N + n];
+                for (int j = 0; j < per && rank * per + j < t.rows; ++j) {
+                    float sum = recv[j * 128 + row];
+                    for (int s = 1; s < p.splits; ++s) sum += recv[(s * per + j) * 128 + row];
+                    const int m = rank * per + j;
+                    const float v = sum * ws * xs_tile[m];
+                    const int64_t at = (int64_t(t.m0) + m) * p.b.N + n;
+                    if (OUT_F32) static_cast<float *>(p.b.Y)[at] = v;
+                    else static_cast<uint16_t *>(p.b.Y)[at] = uint16_t(pack_bf16x2(v, 0.0f) & 0xffffu);
+                }
+            }
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1 && PAIR == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem, 512u);
+    }
+    if (PAIR == 2) {
+        // no CTA leaves while its peer may still use its memory or barriers
+        cluster_sync_all();
+        if (warp == 1) {
+            tc_fence_after_sync();
+            tmem_dealloc<2>(tmem, 512u);
+        }
+    }
+}
+
+template <int PAIR, bool OUT_F32>
+cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaParams &p, int grid, bool pdl,
+                   cudaStream_t stream)
+{
+    auto kern = i8_mma_kernel<PAIR, OUT_F32>;
+    static bool raised[64] = {};   // the opt-in limit is raised once per device
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!raised[dev]) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kI8SmemLimit));
+        if (err != cudaSuccess) return err;
+        raised[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    const int cluster = PAIR * p.splits;
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = unsigned(cluster);
+        attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = 1;
+    }
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = i8_mma_smem(PAIR, p.nt, p.stages, p.splits, p.b.E);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(na);
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
+}
+
+}  // namespace
+
+size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
+{
+    return 1024 + size_t(stages) * (kWBytes + size_t(nt / pair) * 256) +
+           (splits > 1 ? size_t(nt + splits) * 512 : 0) + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
+}
+
+int launch_i8_mma(const I8MmaParams &p0, const void *tokens, int pair, int sms, bool pdl, cudaStream_t stream)
+{
+    I8MmaParams p = p0;
+    p.n_ct = (p.b.N + 128 * pair - 1) / (128 * pair);
+    p.n_kb = (p.b.K + kKB - 1) / kKB;
+    p.box = p.nt / pair >= 64 ? 32 : 16;
+    CUtensorMap mw, mx;
+    const uint64_t dw[3] = {uint64_t(p.b.K), uint64_t(p.b.N), uint64_t(p.b.E)};
+    const uint64_t sw[2] = {uint64_t(p.b.K), uint64_t(p.b.N) * uint64_t(p.b.K)};
+    const uint32_t bw[3] = {uint32_t(kKB), 128, 1};
+    int rc = encode_tiled(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.b.W, dw, sw, bw);
+    if (rc != CAKE_GG_OK) return rc;
+    const uint64_t dx[2] = {uint64_t(p.b.K), uint64_t(p.b.T)};
+    const uint64_t sx[1] = {uint64_t(p.b.K) * 2};
+    const uint32_t bx[2] = {64, p.b.rows ? 1u : uint32_t(p.box)};
+    rc = encode_tiled(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, tokens, dx, sx, bx);
+    if (rc != CAKE_GG_OK) return rc;
+
+    // row tiles at most: a whole one per nt rows and a last one per expert with rows
+    const int64_t bound = (p.b.M / p.nt + (p.b.M < p.b.E ? p.b.M : p.b.E)) * int64_t(p.n_ct);
+    int64_t grid;
+    if (p.splits > 1) {
+        grid = bound * p.splits;                       // one cluster per unit
+        if (grid > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    } else {
+        grid = sms / pair < bound ? sms / pair : bound;
+        grid = (grid < 1 ? 1 : grid) * pair;
+    }
+    cudaError_t err;
+    if (pair == 2)
+        err = p.b.out_f32 ? launch<2, true>(mw, mx, p, int(grid), pdl, stream)
+                          : launch<2, false>(mw, mx, p, int(grid), pdl, stream);
+    else
+        err = p.b.out_f32 ? launch<1, true>(mw, mx, p, int(grid), pdl, stream)
+                          : launch<1, false>(mw, mx, p, int(grid), pdl, stream);
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+}  // namespace cakegg

@@ -308,3 +308,48 @@ def test_no_rows():
     assert gg.int8_gemm(x, W, ws).shape == (0, 16)
     q, s = gg.quantize_rows(x)
     assert q.shape == (0, 32) and s.shape == (0,)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A dropped copy: the bounded waits end, the status says so, the next call is right again."""
+    import torch
+    rng = np.random.default_rng(2)
+    M, N, K = 700, 264, 1040
+    q, W, xs, ws = _ints((M, K), rng), _ints((N, K), rng), _scales(M, rng), _scales(N, rng)
+    for rows in (64, M):
+        plan = gg.cake_gg_i8_plan(1, rows, rows, N, K, "int8", None, "fp32")
+        work = gg.make_workspace(plan, "cuda")
+        out = torch.empty((rows, N), device="cuda")
+        plan.debug_flags, plan.timeout_ns = gg.CAKE_GG_DEBUG_DROP_FIRST_LOAD, 50_000_000
+        with pytest.raises(gg.CakeGGError) as err:
+            gg.int8_gemm(q[:rows], W, ws, xs=xs[:rows], out_dtype="fp32", out=out, plan=plan, workspace=work)
+        assert err.value.code == gg.CAKE_GG_ERR_TIMEOUT
+        plan.debug_flags, plan.timeout_ns = 0, 2_000_000_000
+        gg.int8_gemm(q[:rows], W, ws, xs=xs[:rows], out_dtype="fp32", out=out, plan=plan, workspace=work)
+        _close(out, _want(q[:rows], xs[:rows], W[None], ws[None], [rows]), "fp32")
+
+
+@pytest.mark.parametrize("env", [
+    dict(PAIR="1", ROWS_PER_TILE="16", SPLITS="1"), dict(PAIR="1", ROWS_PER_TILE="32", SPLITS="3"),
+    dict(PAIR="1", ROWS_PER_TILE="64", SPLITS="8"), dict(PAIR="1", ROWS_PER_TILE="128", SPLITS="1"),
+    dict(PAIR="1", ROWS_PER_TILE="256", SPLITS="1"), dict(PAIR="2", ROWS_PER_TILE="64", SPLITS="1"),
+    dict(PAIR="2", ROWS_PER_TILE="128", SPLITS="1"), dict(PAIR="2", ROWS_PER_TILE="192", SPLITS="1"),
+    dict(PAIR="2", ROWS_PER_TILE="256", SPLITS="1"),
+], ids=lambda e: "-".join(e.values()))
+@pytest.mark.parametrize("routed", [False, True])
+def test_every_tile_shape(env, routed, monkeypatch):
+    """Each shape of tile on the same ragged rows, with one CTA or pair and with all."""
+    import torch
+    for k, v in dict(env, PATH="1").items():
+        monkeypatch.setenv("CAKE_GG_I8_" + k, v)
+    rng = np.random.default_rng(4)
+    sizes, N, K = [5, 0, 290, 1, 0, 33, 64, 17], 392, 1200
+    E, M = len(sizes), sum(sizes)
+    T = 77 if routed else M
+    q, W, xs, ws = _ints((T, K), rng), _ints((E, N, K), rng), _scales(T, rng), _scales((E, N), rng)
+    rows = torch.from_numpy(rng.integers(0, T, size=M).astype(np.int32)).cuda() if routed else None
+    want = _want(q, xs, W, ws, sizes, rows)
+    for out_dtype in ("fp32", "bf16"):
+        for cap in (0, 2):
+            got = gg.int8_gemm(q, W, ws, xs=xs, offsets=_offsets(sizes), rows=rows, out_dtype=out_dtype, max_sms=cap)
+            _close(got, want, out_dtype)
