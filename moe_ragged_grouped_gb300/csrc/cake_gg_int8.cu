@@ -323,8 +323,9 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     }
     const int sp = env_int("CAKE_GG_I8_SPLITS", pl->splits);
     if (sp >= 1 && sp <= 8 && pl->pair == 1) pl->splits = sp;
-    pl->slots = slots_for(pl->tile_rows, pl->acc_bufs);
     pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
+    pl->slots = slots_for(pl->tile_rows, pl->acc_bufs);
+    if (pl->slots > pl->stages) pl->slots = pl->stages;
 }
 
 // What the tensor-core kernel can run.
@@ -332,10 +333,10 @@ bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
 {
     const int per_cta = pl.pair == 2 ? pl.tile_rows / 2 : pl.tile_rows;
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 16 * pl.pair && pl.tile_rows <= 256 &&
-           pl.tile_rows % (16 * pl.pair) == 0 && (per_cta < 64 || per_cta % 32 == 0) &&
+           pl.tile_rows % (16 * pl.pair) == 0 && per_cta <= 128 &&
            (pl.tile_rows == 16 || pl.tile_rows % 32 == 0) && (pl.acc_bufs == 1 || pl.acc_bufs == 2) &&
            pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
-           pl.slots <= slots_for(pl.tile_rows, pl.acc_bufs) && pl.splits >= 1 && pl.splits <= 8 &&
+           pl.slots <= pl.stages && pl.slots <= slots_for(pl.tile_rows, pl.acc_bufs) && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) &&
            i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }
@@ -450,7 +451,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     m.bufs = pl.acc_bufs;
     m.splits = pl.splits;
     m.debug_flags = pl.debug_flags;
-    return launch_i8_mma(m, tokens, pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl_enabled(), s);
+    return launch_i8_mma(m, static_cast<const uint16_t *>(tokens), pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl_enabled(), s);
 }
 
 }  // extern "C"

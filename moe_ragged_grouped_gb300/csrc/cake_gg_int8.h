@@ -50,7 +50,7 @@ struct I8MmaParams {
     int32_t bufs;             // accumulators (1 or 2)
     int32_t splits;           // CTAs that share a tile's reduction (one cluster; 1 = none)
     int32_t debug_flags;
-    int32_t n_ct, n_kb, box;  // (set by the launch) channel tiles, stages of a tile, rows of a copy box
+    int32_t n_ct, n_kb, box;  // (set by the launch) channel tiles, stages of a tile, rows of a copy
 };
 
 constexpr size_t kI8SmemLimit = 232448;   // opt-in dynamic shared memory per CTA (227 KB)
@@ -58,8 +58,8 @@ constexpr size_t kI8SmemLimit = 232448;   // opt-in dynamic shared memory per CT
 // Dynamic shared memory of a CTA.
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E);
 
-// Tensor-core path: `tokens` are FP16 integers [T, K].  Returns a cake_gg_status_t.
-int launch_i8_mma(const I8MmaParams &p, const void *tokens, int pair, int sms, bool pdl, cudaStream_t stream);
+// Tensor-core path: q [T, K] as FP16 integers.  Returns a cake_gg_status_t.
+int launch_i8_mma(const I8MmaParams &p, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream);
 
 constexpr int kI8RowChunk = 8;   // rows of one expert that the row kernel computes together
 

@@ -11,31 +11,36 @@
 // MMA's A operand, which may come from tensor memory: 8-bit tiles arrive in
 // shared memory by TMA, converter warps widen them to FP16 and write them to
 // tensor memory, so the widened weights cost no shared memory bandwidth.  The
-// rows are the B operand: FP16 integers in shared memory (written by the token
-// pass), loaded by TMA, row by row through `rows` where they are routed.  B's
-// width follows the rows the tile really has, so a ragged end costs its own
-// size only.
+// rows are the B operand, FP16 integers that the token pass wrote: TMA copies
+// them, or, where they are routed, gather warps do, row by row through `rows`.
+// (Widening the rows here as well, from 8-bit ones, took twice the time: the
+// converters' integer instructions then bound the kernel.)  B's width follows
+// the rows the tile really has, so a ragged end costs its own size only.
 //
-// Roles of a CTA (448 threads): warp 0 copies, warp 1 issues MMAs, warps 2-5
-// scale and store, warps 6-13 convert (two groups on alternate stages).
+// Roles of a CTA: warp 0 copies, warp 1 issues MMAs, warps 2-5 scale and store,
+// warps 6-13 convert (two groups on alternate stages), warps 14-17 gather
+// (launched for routed rows only).
 #include "cake_gg_int8.h"
 #include "cake_gg_ptx.cuh"
 
 namespace cakegg {
 namespace {
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 448, kThreadsRouted = kThreads + 128;
 constexpr int kConvWarp0 = 6;
 constexpr int kKB = 128;                     // reduction length of a stage
 constexpr uint32_t kWBytes = 128 * kKB;      // 8-bit weight tile of a stage
 constexpr int kStagesMax = 12;
 constexpr int kSlotsMax = 8;
+constexpr int kGatherWarp0 = 14;
+constexpr int kRowsPerCta = 128;             // B rows of a CTA at most
+constexpr uint32_t kStageOut = 4 * 32 * 64;  // BF16 output: 32 rows x 32 channels per storing warp
 constexpr uint32_t kSlotCols = kKB / 2;      // tensor memory columns of a widened weight tile
 constexpr uint64_t kDrainNs = 20000000ull;
 
 struct __align__(16) Ctrl {
     uint64_t full[kStagesMax], empty[kStagesMax];     // stage: copies landed / MMAs done
-    uint64_t conv[kSlotsMax], aempty[kSlotsMax];      // slot: weights widened / MMAs done
+    uint64_t conv[kSlotsMax];                         // slot: weights widened
     uint64_t tfull[2], tempty[2];                     // accumulator: complete / stored
     uint64_t drain;
     uint32_t tmem_base;
@@ -48,15 +53,15 @@ __device__ __forceinline__ bool aborted(Ctrl *c) { return *reinterpret_cast<vola
 
 // Bounded wait on one mbarrier phase by every lane of a warp; warp-uniform
 // verdict (false: it ran out, or another role gave up).
-template <bool CLUSTER>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctrl *c, const I8Params &p)
 {
-    auto poll = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    bool ok = poll();
+    bool ok = mbar_try_wait(bar, parity);
+    // (the global timer is slow to read: a wait that is soon over never asks it)
+    for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
     if (!ok) {
         const uint64_t t0 = global_timer_ns();
         while (true) {
-            for (int i = 0; i < 32 && !ok; ++i) ok = poll();
+            for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
             if (ok || aborted(c)) break;
             if (global_timer_ns() - t0 > p.timeout_ns) {
                 *reinterpret_cast<volatile int32_t *>(&c->abort_flag) = 1;
@@ -75,15 +80,26 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
         if (global_timer_ns() - t0 > kDrainNs) return;
 }
 
-// Four rows of a tensor (box one row high) to consecutive 128-byte rows.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
-                                            const int32_t (&r)[4])
+// One lane of a converged warp.  (The MMA's descriptors then stay in uniform
+// registers: under a test of the lane number each of the eight issues of a
+// stage took 70 clocks, a stage 960; elected, 281.)
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-        : "memory");
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// 16 bytes from global to shared memory, zeros where `in` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// Arrive on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
@@ -130,32 +146,48 @@ struct Turn {
 };
 
 struct Tile {
-    int e, ct;            // expert, channel tile
-    int32_t m0, rows, end;   // first row, rows in the tile, end of the expert's rows
+    int e, ct;                // expert, channel tile
+    int32_t m0, rows, end;    // first row, rows in the tile, end of the expert's rows
 };
 
-__device__ __forceinline__ Tile decode(int64_t u, const I8MmaParams &p, const int32_t *off, const int32_t *pref)
-{
-    Tile t;
-    t.ct = int(u % p.n_ct);
-    const int32_t g = int32_t(u / p.n_ct);
-    int lo = 0, hi = p.b.E;      // pref[lo] <= g < pref[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (pref[mid] <= g) lo = mid;
-        else hi = mid;
+// The units of a CTA (pair), a fixed stride over (row tile, channel tile) with
+// the channel tile fastest: concurrent CTAs share an expert's rows, and its
+// weights stay in L2 between its row tiles.
+struct Walk {
+    int32_t g, ct, e, dg, dct, n_ct;
+    __device__ __forceinline__ Walk(uint32_t first, uint32_t step, int32_t n) : e(0), n_ct(n)
+    {
+        g = int32_t(first / uint32_t(n));
+        ct = int32_t(first % uint32_t(n));
+        dg = int32_t(step / uint32_t(n));
+        dct = int32_t(step % uint32_t(n));
     }
-    t.e = lo;
-    t.m0 = off[lo] + (g - pref[lo]) * p.nt;
-    t.end = off[lo + 1];
-    t.rows = min(p.nt, t.end - t.m0);
-    return t;
-}
+    __device__ __forceinline__ void next()
+    {
+        g += dg;
+        ct += dct;
+        if (ct >= n_ct) {
+            ct -= n_ct;
+            ++g;
+        }
+    }
+    __device__ __forceinline__ Tile tile(int nt, const int32_t *off, const int32_t *pref)
+    {
+        while (pref[e + 1] <= g) ++e;
+        Tile t;
+        t.ct = ct;
+        t.e = e;
+        t.m0 = off[e] + (g - pref[e]) * nt;
+        t.end = off[e + 1];
+        t.rows = min(nt, t.end - t.m0);
+        return t;
+    }
+};
 
 template <int PAIR, bool OUT_F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsRouted, 1)
     i8_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
-                  const I8MmaParams p)
+                  const uint16_t *__restrict__ q16, const I8MmaParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -165,6 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
     float *recv = reinterpret_cast<float *>(after);              // split: [split][column][128]
     after += p.splits > 1 ? size_t(p.nt + p.splits) * 512u : 0;
+    uint8_t *out_tile = after;                                   // [warp][row][32 channels] BF16
+    after += OUT_F32 ? 0 : kStageOut;
     Ctrl *c = reinterpret_cast<Ctrl *>(after);
     float *xs_tile = reinterpret_cast<float *>(c + 1);           // [2][nt]
     int32_t *off = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);
@@ -181,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c->abort_flag = 0;
         c->bad = 0;
         tma_prefetch_desc(&mapW);
-        tma_prefetch_desc(&mapX);
+        if (!p.b.rows) tma_prefetch_desc(&mapX);
     }
     if (warp == 1) {
         tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
@@ -189,12 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 64) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(smem_u32(&c->full[s]), 1);
+            mbar_init(smem_u32(&c->full[s]), p.b.rows ? 1u + 128u : 1u);   // the copies' arming, every gathering thread
             mbar_init(smem_u32(&c->empty[s]), 1);
         }
         for (int a = 0; a < p.slots; ++a) {
             mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);         // the group's warps, of both CTAs
-            mbar_init(smem_u32(&c->aempty[a]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c->tfull[b]), 1);
@@ -206,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!p.b.early) grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();                                             // c->bad is zero
-    for (int i = tid; i <= E; i += kThreads) off[i] = p.b.offsets ? p.b.offsets[i] : (i ? int32_t(p.b.M) : 0);
+    for (int i = tid; i <= E; i += int(blockDim.x)) off[i] = p.b.offsets ? p.b.offsets[i] : (i ? int32_t(p.b.M) : 0);
     __syncthreads();
     if (warp == 0) {
         // lane l sums the row tiles of its run of experts, then the runs are scanned
@@ -245,12 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t d_stride = uint32_t(p.nt < 32 ? 32 : p.nt);
     const uint32_t slots0 = tmem + d_stride * uint32_t(p.bufs);
 
-    // Units: channel tile fastest, so that concurrent CTAs share an expert's
-    // rows and all of its weights stay in L2 between its row tiles.  A split
-    // cluster takes one unit, each of its CTAs a part of the reduction.
-    const int64_t units = int64_t(c->total) * p.n_ct;
-    const int64_t unit0 = blockIdx.x / (PAIR * p.splits);
-    const int64_t step = p.splits > 1 ? units + 1 : int64_t(gridDim.x / PAIR);
+    // A split cluster takes one unit, each of its CTAs a part of the reduction.
+    const uint32_t unit0 = blockIdx.x / uint32_t(PAIR * p.splits);
+    const uint32_t step = p.splits > 1 ? uint32_t(p.n_ct) : gridDim.x / PAIR;
+    const int32_t tiles = p.splits > 1 ? min(c->total, int32_t(unit0 / uint32_t(p.n_ct)) + 1) : c->total;
     const int kb0 = p.splits > 1 ? p.n_kb * rank / p.splits : 0;
     const int kb1 = p.splits > 1 ? p.n_kb * (rank + 1) / p.splits : p.n_kb;
     constexpr int kNAlign = 16 * PAIR;
@@ -258,78 +289,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ======================= copies =======================
-        const bool routed = p.b.rows != nullptr;
         Turn st;
         int issued = 0;       // stages filled, up to the ring's depth
-        bool ok = true, first = true;
-        for (int64_t u = unit0; ok && u < units; u += step) {
-            const Tile t = decode(u, p, off, pref);
+        bool ok = true;
+        const bool boxes = p.b.rows == nullptr;
+        bool waited = false;
+        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
             const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
             const int32_t mb = t.m0 + half * n_half;
-            const int n_box = (n_half + p.box - 1) / p.box;
-            const uint32_t bytes = kWBytes + 256u * uint32_t(routed ? n_half : n_box * p.box);
-            int32_t ids[2][4];
-            if (routed) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int32_t m = mb + (lane + 32 * i) * 4 + r;
-                        const int32_t id = (lane + 32 * i) * 4 < n_half && m < t.end ? p.b.rows[m] : 0;
-                        ids[i][r] = id >= 0 && id < p.b.T ? id : 0;     // (reported where it is scaled)
-                    }
-            }
-            auto load_w = [&](int kb, int s) {
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&c->full[s]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0 && s == 0))
-                        tma_load_3d(ring + uint32_t(s) * stage_bytes, &mapW, bar, kb * kKB, (t.ct * PAIR + half) * 128, t.e);
-                }
-                __syncwarp();
+            const int n_box = boxes ? (n_half + p.box - 1) / p.box : 0;
+            const uint32_t bytes = kWBytes + 256u * uint32_t(n_box * p.box);
+            auto copy_w = [&](int kb, int s) {
+                const uint32_t bar = smem_u32(&c->full[s]);
+                mbar_arrive_expect_tx(bar, bytes);
+                if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0 && s == 0))
+                    tma_load_3d(ring + uint32_t(s) * stage_bytes, &mapW, bar, kb * kKB, (t.ct * PAIR + half) * 128, t.e);
             };
-            auto load_x = [&](int kb, int s) {
+            auto copy_x = [&](int kb, int s) {
                 const uint32_t bar = smem_u32(&c->full[s]), dst = ring + uint32_t(s) * stage_bytes + kWBytes;
-                if (routed) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int g = lane + 32 * i;
-                        if (g * 4 < n_half) {
-                            tma_gather4(dst + uint32_t(g) * 512u, &mapX, bar, kb * kKB, ids[i]);
-                            tma_gather4(dst + x_rows * 128u + uint32_t(g) * 512u, &mapX, bar, kb * kKB + 64, ids[i]);
-                        }
-                    }
-                } else if (lane < 2 * n_box) {
-                    const uint32_t chunk = uint32_t(lane) & 1u, b = uint32_t(lane) >> 1;
-                    tma_load_2d(dst + chunk * x_rows * 128u + b * uint32_t(p.box) * 128u, &mapX, bar,
-                                kb * kKB + int(chunk) * 64, mb + int(b) * p.box);
+                for (int b = 0; b < n_box; ++b) {
+                    tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, mb + b * p.box);
+                    tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, mb + b * p.box);
                 }
             };
             int kb = kb0;
-            if (first) {
-                // the weights of the first stages do not wait for the tokens
+            if (!waited) {
+                // the weights of the first stages do not wait for the token pass
                 const int n = min(p.stages, kb1 - kb0);
-                for (int i = 0; i < n; ++i) load_w(kb0 + i, i);
+                if (elect_one())
+                    for (int i = 0; i < n; ++i) copy_w(kb0 + i, i);
+                __syncwarp();
                 grid_dependency_wait();
-                for (int i = 0; i < n; ++i) load_x(kb0 + i, i);
+                waited = true;
+                if (elect_one())
+                    for (int i = 0; i < n; ++i) copy_x(kb0 + i, i);
+                __syncwarp();
                 for (int i = 0; i < n; ++i) st.next(p.stages);
                 kb += n;
                 issued = n;
-                first = false;
             }
             for (; kb < kb1; ++kb) {
-                if (!warp_wait<false>(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b)) {
+                if (!warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b)) {
                     ok = false;
                     break;
                 }
-                load_w(kb, st.at);
-                load_x(kb, st.at);
+                if (elect_one()) {
+                    copy_w(kb, st.at);
+                    copy_x(kb, st.at);
+                }
+                __syncwarp();
                 st.next(p.stages);
                 if (issued < p.stages) ++issued;
             }
         }
-        if (first) grid_dependency_wait();
-        __syncwarp();
+        if (!waited) grid_dependency_wait();
         if (!ok || aborted(c)) {
             // the copies in flight land before the CTA leaves
             if (lane == 0)
@@ -344,12 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Turn st, sl, acc;
         bool ok = true, any = false;
         if (leader) {
-            for (int64_t u = unit0; ok && u < units; u += step) {
-                const Tile t = decode(u, p, off, pref);
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
                 const uint32_t n = uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign);
                 const uint32_t idesc = idesc_f16(128u * PAIR, n);
                 const int buf = acc.at;
-                if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p.b)) {
+                if (!warp_wait(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p.b)) {
                     ok = false;
                     break;
                 }
@@ -358,11 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const int s = st.at, a = sl.at;
                     // the converters of both CTAs saw their stage's copies land
-                    if (!warp_wait<PAIR == 2>(smem_u32(&c->conv[a]), sl.parity, c, p.b)) {
+                    if (!warp_wait(smem_u32(&c->conv[a]), sl.parity, c, p.b)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
+                    if (elect_one()) {
                         tc_fence_after_sync();
                         const uint32_t xb = ring + uint32_t(s) * stage_bytes + kWBytes;
                         const uint64_t b0 = smem_desc_sw128(xb, 16, 1024), b1 = smem_desc_sw128(xb + x_rows * 128u, 16, 1024);
@@ -373,11 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                kb > kb0 || k > 0 ? 1u : 0u);
                         if (PAIR == 2) {
                             umma_commit_mc<2>(smem_u32(&c->empty[s]), pair_mask);
-                            umma_commit_mc<2>(smem_u32(&c->aempty[a]), pair_mask);
                             if (kb + 1 == kb1) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
                         } else {
                             umma_commit<1>(smem_u32(&c->empty[s]));
-                            umma_commit<1>(smem_u32(&c->aempty[a]));
                             if (kb + 1 == kb1) umma_commit<1>(smem_u32(&c->tfull[buf]));
                         }
                     }
@@ -400,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         grid_dependency_wait();                                  // the token scales
         const int q = warp & 3;                                  // tensor memory lanes 32 q ..
         Turn acc, xb;
-        for (int64_t u = unit0; u < units; u += step) {
-            const Tile t = decode(u, p, off, pref);
+        for (Walk w(unit0, step, p.n_ct); w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
             float *xs = xs_tile + xb.at * p.nt;
             for (int j = tid - 64; j < t.rows; j += 128) {
                 int64_t r = t.m0 + j;
@@ -414,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ch_ok = n < p.b.N;
             const float ws = ch_ok ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
             const int buf = acc.at;
-            const bool ok = warp_wait<false>(smem_u32(&c->tfull[buf]), acc.parity, c, p.b);
+            const bool ok = warp_wait(smem_u32(&c->tfull[buf]), acc.parity, c, p.b);
             // the scales are in (their buffer is rewritten two tiles on, after the
             // barrier between), and the four warps go on or give up together
             if (!named_bar_and(1, 128, ok)) break;
@@ -439,74 +451,144 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     continue;
                 }
-                const int64_t y0 = (int64_t(t.m0) + c0) * p.b.N + n;
                 if (OUT_F32) {
+                    const int64_t y0 = (int64_t(t.m0) + c0) * p.b.N + n;
                     float *y = static_cast<float *>(p.b.Y) + y0;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c0 + j < t.rows && ch_ok) y[int64_t(j) * p.b.N] = __uint_as_float(r[j]) * ws * xs[c0 + j];
                 } else {
-                    // neighbouring lanes hold neighbouring channels: of two rows the even
-                    // lane stores the first row's pair, the odd lane the second's
-                    uint16_t *y = static_cast<uint16_t *>(p.b.Y) + y0 - (lane & 1);
+                    // through shared memory, transposed: a lane writes its channel of 32
+                    // rows, then stores 16 bytes of a row's 32 channels
+                    uint8_t *tile = out_tile + q * (kStageOut / 4);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float a = __uint_as_float(r[j]) * ws * xs[min(c0 + j, p.nt - 1)];
-                        const float b = __uint_as_float(r[j + 1]) * ws * xs[min(c0 + j + 1, p.nt - 1)];
-                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-                        const int row = j + (lane & 1);
-                        if (c0 + row < t.rows && ch_ok)
-                            *reinterpret_cast<uint32_t *>(y + int64_t(row) * p.b.N) =
-                                lane & 1 ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 x4 = *reinterpret_cast<const float4 *>(xs + c0 + j);
+                        const uint32_t a = pack_bf16x2(__uint_as_float(r[j]) * ws * x4.x, __uint_as_float(r[j + 1]) * ws * x4.y);
+                        const uint32_t b = pack_bf16x2(__uint_as_float(r[j + 2]) * ws * x4.z, __uint_as_float(r[j + 3]) * ws * x4.w);
+                        uint16_t *dst = reinterpret_cast<uint16_t *>(tile + j * 64) + lane;
+                        dst[0] = uint16_t(a & 0xffffu);
+                        dst[32] = uint16_t(a >> 16);
+                        dst[64] = uint16_t(b & 0xffffu);
+                        dst[96] = uint16_t(b >> 16);
                     }
+                    __syncwarp();
+                    const int piece = lane & 3, n8 = n - lane + piece * 8;
+                    uint16_t *y = static_cast<uint16_t *>(p.b.Y) + (int64_t(t.m0) + c0) * p.b.N + n8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = (lane >> 2) + 8 * i;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * 64 + piece * 16);
+                        if (c0 + row < t.rows && n8 < p.b.N) *reinterpret_cast<uint4 *>(y + int64_t(row) * p.b.N) = v;
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
                 if (leader) mbar_arrive(smem_u32(&c->tempty[buf]));
-                else mbar_arrive_cluster(map_to_cta(smem_u32(&c->tempty[buf]), 0));
+                else mbar_arrive_remote(map_to_cta(smem_u32(&c->tempty[buf]), 0));
             }
             acc.next(p.bufs);
             xb.next(2);
         }
-    } else {
+    } else if (warp < kGatherWarp0) {
         // ======================= weights to FP16 =======================
         const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
-        const int row = q * 32 + lane;
-        const int64_t mine = unit0 < units ? (units - unit0 - 1) / step + 1 : 0;
-        const int64_t total = mine * (kb1 - kb0);
-        Turn st, sl;
-        for (int64_t it = 0; it < total; ++it, st.next(p.stages), sl.next(p.slots)) {
-            if (int(it & 1) != group) continue;
-            const int s = st.at, a = sl.at;
-            if (!warp_wait<false>(smem_u32(&c->full[s]), st.parity, c, p.b)) break;
-            if (!warp_wait<false>(smem_u32(&c->aempty[a]), sl.parity ^ 1u, c, p.b)) break;
-            const uint8_t *src = ring_ptr + size_t(s) * stage_bytes + row * 128;
-            const uint32_t dst = slots0 + uint32_t(a) * kSlotCols + (uint32_t(q * 32) << 16);
-            tc_fence_after_sync();
+        const int row = q * 32 + lane;                           // weight row = tensor memory lane
+        const int n_kb = kb1 - kb0;
+        // A slot is free once the MMAs of the stage that last used it, `slots` before
+        // this one, are done: that stage's `empty` says so (slots <= stages).
+        Turn st, sl, last;
+        if (group) st.next(p.stages), sl.next(p.slots);
+        int it = group, kb = group;
+        bool ok = true;
+        Walk w(unit0, step, p.n_ct);
+        while (ok) {
+            while (kb >= n_kb) {
+                kb -= n_kb;
+                w.next();
+            }
+            if (w.g >= tiles) break;
+            ok = warp_wait(smem_u32(&c->full[st.at]), st.parity, c, p.b);
+            if (!ok) break;
+            const uint8_t *src = ring_ptr + size_t(st.at) * stage_bytes + row * 128;
+            const uint32_t dst = slots0 + uint32_t(sl.at) * kSlotCols + (uint32_t(q * 32) << 16);
+            // (gathered rows were written through the generic proxy)
+            if (p.b.rows) fence_proxy_async_smem();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t f[32];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + (((h * 4 + v) ^ (row & 7)) << 4));
-                    widen4(w.x, f[v * 8], f[v * 8 + 1]);
-                    widen4(w.y, f[v * 8 + 2], f[v * 8 + 3]);
-                    widen4(w.z, f[v * 8 + 4], f[v * 8 + 5]);
-                    widen4(w.w, f[v * 8 + 6], f[v * 8 + 7]);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (((h * 4 + v) ^ (row & 7)) << 4));
+                    widen4(x.x, f[v * 8], f[v * 8 + 1]);
+                    widen4(x.y, f[v * 8 + 2], f[v * 8 + 3]);
+                    widen4(x.z, f[v * 8 + 4], f[v * 8 + 5]);
+                    widen4(x.w, f[v * 8 + 6], f[v * 8 + 7]);
                 }
-                tmem_st_32x32b_x32(dst + uint32_t(h) * 32u, f);
+                if (h == 0 && it >= p.slots) {
+                    if (it > p.slots) last.next(p.stages);
+                    if (it > p.slots + 1) last.next(p.stages);
+                    ok = warp_wait(smem_u32(&c->empty[last.at]), last.parity, c, p.b);
+                    tc_fence_after_sync();
+                }
+                if (ok) tmem_st_32x32b_x32(dst + uint32_t(h) * 32u, f);
             }
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                if (leader) mbar_arrive(smem_u32(&c->conv[a]));
-                else mbar_arrive_cluster(map_to_cta(smem_u32(&c->conv[a]), 0));
+            if (ok && lane == 0) {
+                // (default semantics: what the MMA reads is complete and fenced; a
+                // release at cluster scope cost a tenth of the whole product)
+                if (leader) mbar_arrive(smem_u32(&c->conv[sl.at]));
+                else mbar_arrive_remote(map_to_cta(smem_u32(&c->conv[sl.at]), 0));
             }
+            st.next(p.stages), st.next(p.stages);
+            sl.next(p.slots), sl.next(p.slots);
+            it += 2;
+            kb += 2;
         }
         grid_dependency_wait();
+        __syncwarp();
+    } else {
+        // ======================= routed rows =======================
+        // 16 lanes copy the 256 bytes of a row that a stage holds; a warp copies two
+        // rows at once, the four warps 8.
+        const int gt = tid - kGatherWarp0 * 32;
+        const int b_row = gt >> 4, piece = gt & 15;
+        const uint32_t at = kWBytes + uint32_t(piece >> 3) * x_rows * 128u + uint32_t(b_row) * 128u +
+                            (uint32_t((piece & 7) ^ (b_row & 7)) << 4);
+        Turn st;
+        bool ok = true;
+        grid_dependency_wait();                                  // the tokens
+        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
+            const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
+            const int32_t mb = t.m0 + half * n_half + b_row;
+            int32_t id[kRowsPerCta / 8];                         // -1: a row past the tile's end, zeros
+#pragma unroll
+            for (int i = 0; i < kRowsPerCta / 8; ++i) {
+                id[i] = 8 * i < n_half && mb + 8 * i < t.end ? p.b.rows[mb + 8 * i] : -1;
+                if (id[i] >= p.b.T) id[i] = -1;                  // (reported where it is scaled)
+            }
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
+                if (!ok) break;
+                const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + at;
+                const int k = kb * kKB + piece * 8;
+#pragma unroll
+                for (int i = 0; i < kRowsPerCta / 8; ++i)
+                    if (8 * i < n_half) {
+                        const bool in = id[i] >= 0 && k < p.b.K;
+                        cp_async16(dst + uint32_t(i) * 1024u, q16 + (in ? int64_t(id[i]) * p.b.K + k : 0), in);
+                    }
+                cp_async_arrive(smem_u32(&c->full[st.at]));
+                st.next(p.stages);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
 
@@ -514,8 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every part of this CTA's columns has arrived: sum them in split order
         __syncwarp();
         cluster_sync_all();
-        if (warp >= 2 && warp < kConvWarp0 && unit0 < units && !aborted(c)) {
-            const Tile t = decode(unit0, p, off, pref);
+        Walk w(unit0, step, p.n_ct);
+        if (warp >= 2 && warp < kConvWarp0 && w.g < tiles && !aborted(c)) {
+            const Tile t = w.tile(p.nt, off, pref);
             const int per = (t.rows + p.splits - 1) / p.splits;
             const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
             if (n < p.b.N) {
@@ -551,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int PAIR, bool OUT_F32>
-cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaParams &p, int grid, bool pdl,
+cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const uint16_t *q, const I8MmaParams &p, int grid, bool pdl,
                    cudaStream_t stream)
 {
     auto kern = i8_mma_kernel<PAIR, OUT_F32>;
@@ -580,12 +663,12 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaPara
         attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }
     cfg.gridDim = dim3(unsigned(grid), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(p.b.rows ? kThreadsRouted : kThreads, 1, 1);
     cfg.dynamicSmemBytes = i8_mma_smem(PAIR, p.nt, p.stages, p.splits, p.b.E);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = unsigned(na);
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, q, p);
 }
 
 }  // namespace
@@ -593,25 +676,26 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaPara
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
     return 1024 + size_t(stages) * (kWBytes + size_t(nt / pair) * 256) +
-           (splits > 1 ? size_t(nt + splits) * 512 : 0) + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
+           (splits > 1 ? size_t(nt + splits) * 512 : 0) + kStageOut + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
-int launch_i8_mma(const I8MmaParams &p0, const void *tokens, int pair, int sms, bool pdl, cudaStream_t stream)
+int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream)
 {
     I8MmaParams p = p0;
     p.n_ct = (p.b.N + 128 * pair - 1) / (128 * pair);
     p.n_kb = (p.b.K + kKB - 1) / kKB;
-    p.box = p.nt / pair >= 64 ? 32 : 16;
+    p.box = p.nt / pair % 32 == 0 ? 32 : 16;
     CUtensorMap mw, mx;
     const uint64_t dw[3] = {uint64_t(p.b.K), uint64_t(p.b.N), uint64_t(p.b.E)};
     const uint64_t sw[2] = {uint64_t(p.b.K), uint64_t(p.b.N) * uint64_t(p.b.K)};
     const uint32_t bw[3] = {uint32_t(kKB), 128, 1};
     int rc = encode_tiled(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.b.W, dw, sw, bw);
     if (rc != CAKE_GG_OK) return rc;
+
     const uint64_t dx[2] = {uint64_t(p.b.K), uint64_t(p.b.T)};
     const uint64_t sx[1] = {uint64_t(p.b.K) * 2};
-    const uint32_t bx[2] = {64, p.b.rows ? 1u : uint32_t(p.box)};
-    rc = encode_tiled(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, tokens, dx, sx, bx);
+    const uint32_t bx[2] = {64, uint32_t(p.box)};
+    rc = encode_tiled(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, dx, sx, bx);
     if (rc != CAKE_GG_OK) return rc;
 
     // row tiles at most: a whole one per nt rows and a last one per expert with rows
@@ -626,11 +710,11 @@ int launch_i8_mma(const I8MmaParams &p0, const void *tokens, int pair, int sms, 
     }
     cudaError_t err;
     if (pair == 2)
-        err = p.b.out_f32 ? launch<2, true>(mw, mx, p, int(grid), pdl, stream)
-                          : launch<2, false>(mw, mx, p, int(grid), pdl, stream);
+        err = p.b.out_f32 ? launch<2, true>(mw, mx, q, p, int(grid), pdl, stream)
+                          : launch<2, false>(mw, mx, q, p, int(grid), pdl, stream);
     else
-        err = p.b.out_f32 ? launch<1, true>(mw, mx, p, int(grid), pdl, stream)
-                          : launch<1, false>(mw, mx, p, int(grid), pdl, stream);
+        err = p.b.out_f32 ? launch<1, true>(mw, mx, q, p, int(grid), pdl, stream)
+                          : launch<1, false>(mw, mx, q, p, int(grid), pdl, stream);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
