@@ -186,6 +186,19 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream(index):
+    """The current stream's handle on a device (a few times cheaper than through a Stream object, where torch allows)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
 def _stream(stream, *tensors):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
@@ -321,6 +334,9 @@ def _act_code(a):
 def cake_gg_i8_plan(E, M_max, T, N, K, x_dtype="bf16", act=None, out_dtype="bf16", max_sms=0) -> CakeGGI8Plan:
     """cake_gg_i8_plan(): plan of an 8-bit product of M_max rows from T tokens; raises on error."""
     plan = CakeGGI8Plan()
+    # the problem as int8_gemm compares it (a changed field is the library's to refuse)
+    plan.problem = (int(E), int(M_max), int(T), int(N), int(K), _i8_x_code(x_dtype), _act_code(act),
+                    _dtype_code(out_dtype))
     rc = load_library().cake_gg_i8_plan(ctypes.byref(plan), int(E), int(M_max), int(T), int(N), int(K),
                                         _i8_x_code(x_dtype), _act_code(act), _dtype_code(out_dtype), int(max_sms))
     if rc != CAKE_GG_OK:
@@ -421,14 +437,21 @@ def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=Non
 
 def _i8_x_name(X):
     import torch
-    name = {torch.int8: "int8", torch.bfloat16: "bf16", torch.float32: "fp32"}.get(X.dtype)
-    if name is None:
-        raise TypeError(f"X is {X.dtype}: int8, bfloat16 or float32 are taken")
-    return name
+    dtype = X.dtype
+    if dtype is torch.bfloat16:
+        return "bf16"
+    if dtype is torch.int8:
+        return "int8"
+    if dtype is torch.float32:
+        return "fp32"
+    raise TypeError(f"X is {dtype}: int8, bfloat16 or float32 are taken")
 
 
 def _need(tensor, name, dtype, shape, device):
-    """A dense CUDA tensor of this type and shape on `device`."""
+    """A dense tensor of this type and shape on `device` (the common case is tested first, in few calls)."""
+    if (tensor.dtype is dtype and tensor.shape == shape and tensor.get_device() == device.index
+            and tensor.is_contiguous()):
+        return
     if tensor.dtype != dtype:
         raise TypeError(f"{name} is {tensor.dtype}: {dtype} is needed")
     if tuple(tensor.shape) != shape:
@@ -482,30 +505,30 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     """
     import torch
     name = _i8_x_name(X)
-    if W.dim() not in (2, 3) or X.dim() != 2:
+    x_shape, w_shape = X.shape, W.shape
+    if len(w_shape) not in (2, 3) or len(x_shape) != 2:
         raise ValueError("X is [T, K] and W [N, K] or [E, N, K]")
-    E = int(W.shape[0]) if W.dim() == 3 else 1
-    N, K = int(W.shape[-2]), int(W.shape[-1])
-    T = int(X.shape[0])
-    M = T if rows is None else int(rows.shape[0])
+    E = w_shape[0] if len(w_shape) == 3 else 1
+    N, K = w_shape[-2], w_shape[-1]
+    T = x_shape[0]
+    M = T if rows is None else rows.shape[0]
     device = W.device
-    _need(W, "W", torch.int8, tuple(W.shape), device)
+    _need(W, "W", torch.int8, w_shape, device)
     _need(X, "X", X.dtype, (T, K if act is None else 2 * K), device)
-    _need(ws, "ws", torch.float32, tuple(W.shape[:-1]), device)
+    _need(ws, "ws", torch.float32, w_shape[:-1], device)
     if (xs is None) == (name == "int8"):
         raise ValueError("xs comes with int8 X, and only with it")
     if xs is not None:
         _need(xs, "xs", torch.float32, (T,), device)
     if offsets is not None:
         _need(offsets, "offsets", torch.int32, (E + 1,), device)
-    elif W.dim() == 3 and E != 1:
+    elif E != 1:
         raise ValueError("W of several experts comes with offsets")
     if rows is not None:
         _need(rows, "rows", torch.int32, (M,), device)
     if plan is None:
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
-    elif (plan.E, plan.M_max, plan.T, plan.N, plan.K, plan.x_dtype, plan.act, plan.out_dtype) != (
-            E, M, T, N, K, I8_X_DTYPES[name], _act_code(act), _dtype_code(out_dtype)):
+    elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], _act_code(act), _dtype_code(out_dtype)):
         raise ValueError("the plan is another problem's")
     if out is None:
         out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=device)
@@ -513,6 +536,8 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         _need(out, "out", _torch_out_dtype(out_dtype), (M, N), device)
     if workspace is None:
         workspace = make_workspace(plan, device)
+    if stream is None and device.type == "cuda":
+        stream = _current_stream(device.index)
     rc = cake_gg_i8_gemm(plan, X, xs, rows, W, ws, out, offsets, workspace, stream=stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_i8_gemm")

@@ -13,11 +13,11 @@
 #include <cstdlib>
 #include <cstring>
 
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "cake_gg_int8.h"
+#include "cake_gg_int8_quant.cuh"
 #include "cake_gg_ptx.cuh"
 
 using namespace cakegg;
@@ -67,50 +67,8 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // ---------------------------------------------------------------- token pass
 
-template <typename XT>
-__device__ __forceinline__ void load8(const XT *p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t *p, float (&v)[8])
-{
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8])
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-// Eight values of a row, the gate applied: silu(g) * u = g / (1 + e^-g) * u.
-// (g = -inf gives NaN, as the formula does; a large negative g gives 0.)
-template <typename XT, bool ACT>
-__device__ __forceinline__ void row8(const XT *row, int32_t K, int k, float (&v)[8])
-{
-    load8(row + k, v);
-    if (ACT) {
-        float u[8];
-        load8(row + K + k, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
-    }
-}
-
-// Eight integers of a row as bytes, or as the FP16 operands of the tensor cores.
-__device__ __forceinline__ void store8(int8_t *out, const float (&v)[8])
-{
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 4] |= uint32_t(__float2int_rn(v[i]) & 0xff) << (8 * (i % 4));
-    *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void store8(__half *out, const float (&v)[8])
+// Eight integers as the FP16 operands of the tensor cores.
+__device__ __forceinline__ uint4 halves8(const float (&v)[8])
 {
     uint32_t w[4];
 #pragma unroll
@@ -118,15 +76,23 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8])
         const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(int8_t *out, const float (&v)[8], const RowScale &s)
+{
+    *reinterpret_cast<uint2 *>(out) = bytes8(v, s);
+}
+__device__ __forceinline__ void store8(__half *out, const float (&v)[8], const RowScale &s)
+{
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = s.integer(v[i]);
+    *reinterpret_cast<uint4 *>(out) = halves8(r);
 }
 
 // One block per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
-// rest again (from L2).  |h| is compared by its bit pattern, so a NaN or an
-// infinity wins the maximum: such a row gets the scale NaN and zero integers
-// (its products are NaN).  A row whose largest value is below 2^-120 counts as
-// zero (127 / a would not be finite).
+// rest again (from L2).
 constexpr int kHeld = 2;
 
 template <typename XT, bool ACT, typename QT>
@@ -146,41 +112,31 @@ __global__ void __launch_bounds__(1024)
         const int k = int(threadIdx.x) * 8 + j * stride;
         if (k < K) {
             row8<XT, ACT>(row, K, k, held[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(held[j][i]) & 0x7fffffffu);
+            m = max_bits(held[j], m);
         }
     }
     for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < K; k += stride) {
         float v[8];
         row8<XT, ACT>(row, K, k, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        m = max_bits(v, m);
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();
     m = threadIdx.x % 32 < blockDim.x / 32 ? warp_max[threadIdx.x % 32] : 0;
     m = __reduce_max_sync(0xffffffffu, m);
-    const float a = __uint_as_float(m);
-    const bool finite = m < 0x7f800000u, tiny = a < 0x1p-120f;
-    const float inv = finite && !tiny ? 127.0f / a : 0.0f;
-    if (threadIdx.x == 0) S[t] = !finite ? __uint_as_float(0x7fc00000u) : tiny ? 0.0f : a / 127.0f;
+    const RowScale rs(m);
+    if (threadIdx.x == 0) S[t] = rs.scale;
     QT *out = Q + t * int64_t(K);
-    auto emit = [&](const float (&v)[8], int k) {
-        float r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = finite ? rintf(v[i] * inv) : 0.0f;
-        store8(out + k, r);
-    };
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int k = int(threadIdx.x) * 8 + j * stride;
-        if (k < K) emit(held[j], k);
+        if (k < K) store8(out + k, held[j], rs);
     }
     for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < K; k += stride) {
         float v[8];
         row8<XT, ACT>(row, K, k, v);
-        emit(v, k);
+        store8(out + k, v, rs);
     }
 }
 
@@ -198,7 +154,7 @@ __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = float(int8_t(u[h * 2 + j / 4] >> (8 * (j % 4))));
-        store8(Q + i * 16 + h * 8, v);
+        *reinterpret_cast<uint4 *>(Q + i * 16 + h * 8) = halves8(v);
     }
 }
 
@@ -298,13 +254,13 @@ int stages_for(int pair, int nt, int splits, int E)
 void choose_mma(cake_gg_i8_plan_t *pl)
 {
     const int64_t busy = pl->M_max < pl->E ? pl->M_max : pl->E;
-    const int64_t est = pl->E == 1 ? pl->M_max : 2 * ((pl->M_max + busy - 1) / (busy > 0 ? busy : 1));
+    const int64_t est = pl->E == 1 ? pl->M_max : 4 * ((pl->M_max + busy - 1) / (busy > 0 ? busy : 1));
     pl->path = CAKE_GG_I8_MMA;
     pl->pair = 1;
     pl->tile_rows = est <= 16 ? 16 : est <= 32 ? 32 : est <= 64 ? 64 : 128;
     pl->acc_bufs = 2;
     pl->splits = 1;
-    if (est > 256) {
+    if (est > 512 || (pl->E == 1 && est > 256)) {
         pl->pair = 2;
         pl->tile_rows = 192;
     }
@@ -363,7 +319,7 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
     plan->act = act;
     plan->out_dtype = out_dtype;
     plan->max_sms = max_sms;
-    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8RowChunk ? CAKE_GG_I8_ROWS : CAKE_GG_I8_MMA);
+    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8FewRows ? CAKE_GG_I8_ROWS : CAKE_GG_I8_MMA);
     if (path == CAKE_GG_I8_MMA) {
         choose_mma(plan);
         if (!mma_plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
@@ -412,17 +368,6 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
 
     uint8_t *base = static_cast<uint8_t *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool mma = pl.path == CAKE_GG_I8_MMA;
-    void *tokens = base + L.tokens;
-    if (!ready) {
-        float *scales = reinterpret_cast<float *>(base + L.scales);
-        rc = mma ? launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<__half *>(tokens), scales, s)
-                 : launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<int8_t *>(tokens), scales, s);
-        xs = scales;
-    } else if (mma) {
-        rc = launch_expand(X, pl.T, pl.K, static_cast<__half *>(tokens), s);
-    }
-    if (rc != CAKE_GG_OK) return rc;
     I8Params p{};
     p.offsets = offsets;
     p.rows = rows;
@@ -437,12 +382,24 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     p.N = pl.N;
     p.K = pl.K;
     p.out_f32 = pl.out_dtype == CAKE_GG_FP32;
-    p.early = !ready || mma ? 1 : 0;
     p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
-    if (!mma)
-        return launch_i8_rows(p, static_cast<const int8_t *>(ready ? X : tokens), pdl_enabled(), s) == cudaSuccess
-                   ? CAKE_GG_OK
-                   : CAKE_GG_ERR_CUDA;
+    const bool mma = pl.path == CAKE_GG_I8_MMA, pdl = pdl_enabled();
+    auto status = [](cudaError_t err) { return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA; };
+    if (!mma && (ready || i8_rows_fused(p))) return status(launch_i8_rows(p, X, pl.x_dtype, pl.act, pdl, s));
+
+    // the token pass, then the product
+    void *tokens = base + L.tokens;
+    if (!ready) {
+        float *scales = reinterpret_cast<float *>(base + L.scales);
+        rc = mma ? launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<__half *>(tokens), scales, s)
+                 : launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<int8_t *>(tokens), scales, s);
+        p.xs = scales;
+    } else {
+        rc = launch_expand(X, pl.T, pl.K, static_cast<__half *>(tokens), s);
+    }
+    if (rc != CAKE_GG_OK) return rc;
+    p.early = 1;
+    if (!mma) return status(launch_i8_rows(p, tokens, CAKE_GG_INT8, CAKE_GG_ACT_NONE, pdl, s));
     I8MmaParams m{};
     m.b = p;
     m.nt = pl.tile_rows;
@@ -451,7 +408,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     m.bufs = pl.acc_bufs;
     m.splits = pl.splits;
     m.debug_flags = pl.debug_flags;
-    return launch_i8_mma(m, static_cast<const uint16_t *>(tokens), pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl_enabled(), s);
+    return launch_i8_mma(m, static_cast<const uint16_t *>(tokens), pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl, s);
 }
 
 }  // extern "C"

@@ -4,13 +4,20 @@
 //
 // With a handful of rows per expert every weight byte is used a handful of
 // times, so the weights' bytes bound the time.  Each warp owns C channels of
-// one expert and up to 8 of its rows; its lanes walk K in 16-byte vectors, so
+// one expert and up to R of its rows; its lanes walk K in 16-byte vectors, so
 // a warp load covers 512 contiguous bytes of a weight row, and U * C loads are
 // in flight per lane before the first is used.  Products are summed four at a
 // time in 32-bit integers (exact: K < 2^17 keeps |sum| below 2^31), so the
-// order of the sums is free and a row's K can be divided over the warps of a
+// order of the sums is free and a row's K can be divided over S warps of a
 // block; the result is rounded once, at the end.
+//
+// Activations of one or two rows over few weights (up to 32 MB) are quantised by
+// every block for itself, into shared memory, while its first weights are on
+// the way: called one by one, a launch less is worth more (4096 -> 4096, one
+// token: 8.6 against 10.9 us).  Over more weights the token pass comes first:
+// every block repeats the quantising (4 x 6144 -> 4096: 18.5 against 17.5 us).
 #include "cake_gg_int8.h"
+#include "cake_gg_int8_quant.cuh"
 #include "cake_gg_ptx.cuh"
 
 namespace cakegg {
@@ -18,6 +25,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kC = 4;              // channels of a warp
+constexpr int kU = 2;              // vectors of each in flight per lane
+constexpr int kFusedBytes = 32768; // rows quantised in shared memory at most
+constexpr int64_t kFusedWeights = 32 << 20;
 
 // 16 weight bytes, read once: not kept in L1.
 __device__ __forceinline__ uint4 ld_weights(const int8_t *p)
@@ -43,90 +54,54 @@ __device__ __forceinline__ void store_out(const I8Params &p, int64_t at, float v
     else static_cast<uint16_t *>(p.Y)[at] = uint16_t(pack_bf16x2(v, 0.0f) & 0xffffu);
 }
 
-// Rows [m, m + n_rows) of expert e against the block's channels.  R >= n_rows
-// rows are computed (a missing one repeats the first and is not stored).
-template <int R, int C, int U>
-__device__ __forceinline__ void row_chunk(const I8Params &p, const int8_t *__restrict__ q, int e, int64_t m,
-                                          int n_rows, int block_c, int S, int *part)
+// The block's R rows of activations (null: none) as bytes in shared memory and
+// their scales.  (The second reading comes from L1; held in registers between
+// the two the values cost more in occupancy: 18.5 against 20.8 us for one token
+// through 4 of 32 experts 6144 -> 4096.)
+template <int R, typename XT, bool ACT>
+__device__ __forceinline__ void quantise_rows(const XT *const (&x)[R], int32_t K, int8_t *q, float *scale, uint32_t (*top)[kWarps])
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ks = warp % S, groups = kWarps / S;
-    const int n0 = (block_c * groups + warp / S) * C;
-    const int nv = p.K / 16;                 // 16-byte vectors of a row
-    const int step = 32 * S;
-    const bool live = n0 < p.N;              // N is a multiple of 8, so all C channels are
-    const int8_t *w = p.W + (int64_t(e) * p.N + (live ? n0 : 0)) * p.K;
-
-    int acc[R][C];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[r][c] = 0;
-
-    const int8_t *x[R];
-    bool ready = false;
-    for (int v0 = ks * 32 + lane; __any_sync(0xffffffffu, live && v0 < nv); v0 += U * step) {
-        uint4 wv[U][C];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int v = v0 + u * step;
-                wv[u][c] = live && v < nv ? ld_weights(w + int64_t(c) * p.K + int64_t(v) * 16) : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < R; ++r) {
+        uint32_t m = 0;
+        if (x[r])
+            for (int k = int(threadIdx.x) * 8; k < K; k += kThreads * 8) {
+                float v[8];
+                row8<XT, ACT>(x[r], K, k, v);
+                m = max_bits(v, m);
             }
-        if (!ready) {
-            // the tokens are complete once the grid before this one is
-            grid_dependency_wait();
-            ready = true;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                int64_t t = m + (r < n_rows ? r : 0);
-                if (p.rows) t = p.rows[t];
-                x[r] = q + (t >= 0 && t < p.T ? t : 0) * int64_t(p.K);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = v0 + u * step < nv ? v0 + u * step : 0;   // past the end: weights are zero
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint4 xv = *reinterpret_cast<const uint4 *>(x[r] + int64_t(v) * 16);
-#pragma unroll
-                for (int c = 0; c < C; ++c) acc[r][c] = dot16(wv[u][c], xv, acc[r][c]);
-            }
-        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (threadIdx.x % 32 == 0) top[r][threadIdx.x / 32] = m;
     }
-    grid_dependency_wait();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int s = __reduce_add_sync(0xffffffffu, acc[r][c]);
-            if (lane == 0) part[warp * (R * C) + r * C + c] = s;
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < groups * R * C; i += kThreads) {
-        const int g = i / (R * C), r = i / C % R, c = i % C;
-        const int n = (block_c * groups + g) * C + c;
-        if (r >= n_rows || n >= p.N) continue;
-        int sum = 0;
-        for (int k = 0; k < S; ++k) sum += part[(g * S + k) * (R * C) + r * C + c];
-        int64_t t = m + r;
-        if (p.rows) t = p.rows[t];
-        if (t < 0 || t >= p.T) {
-            atomicCAS(p.status, 0, kI8StatusBadRows);
-            continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        uint32_t m = top[r][0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = max(m, top[r][w]);
+        const RowScale s(m);
+        if (threadIdx.x == 0) scale[r] = s.scale;
+        for (int k = int(threadIdx.x) * 8; k < K; k += kThreads * 8) {
+            float v[8] = {};
+            if (x[r]) row8<XT, ACT>(x[r], K, k, v);
+            *reinterpret_cast<uint2 *>(q + int64_t(r) * K + k) = bytes8(v, s);
         }
-        store_out(p, (m + r) * int64_t(p.N) + n, float(sum) * p.ws[int64_t(e) * p.N + n] * p.xs[t]);
     }
+    __syncthreads();
 }
 
+// XT: int8_t (X holds the quantised tokens), uint16_t (BF16) or float.
 // blockIdx.x = row * blocks_n + channel block.  The block whose row starts a
-// chunk of its expert's rows computes the chunk; the others leave.
+// run of R of its expert's rows computes the run; the others leave.
+template <int R, typename XT, bool ACT>
 __global__ void __launch_bounds__(kThreads)
-    i8_rows_kernel(const I8Params p, const int8_t *__restrict__ q, int blocks_n, int S)
+    i8_rows_kernel(const I8Params p, const XT *__restrict__ X, int blocks_n, int S)
 {
-    __shared__ int part[kWarps * 32];
+    constexpr bool kFused = sizeof(XT) > 1;
+    extern __shared__ __align__(16) int8_t q_smem[];   // fused: [R][K]
+    __shared__ int part[kWarps * R * kC];
+    __shared__ uint32_t top[R][kWarps];
+    __shared__ float scale[R];
     __shared__ int found[4];   // expert, its first row, its end, offsets invalid
     if (!p.early) grid_dependency_wait();
     grid_launch_dependents();
@@ -151,30 +126,106 @@ __global__ void __launch_bounds__(kThreads)
         }
     __syncthreads();
     const int e = found[0];
-    if (found[3] || e < 0 || (m - found[1]) % kI8RowChunk != 0) {
+    if (found[3] || e < 0 || (m - found[1]) % R != 0) {
         grid_dependency_wait();
         if (found[3] && threadIdx.x == 0) atomicCAS(p.status, 0, kI8StatusBadOffsets);
         return;
     }
-    const int n = int(found[2] - m < kI8RowChunk ? found[2] - m : kI8RowChunk);
-    if (n == 1) row_chunk<1, 2, 4>(p, q, e, m, n, block_c, S, part);
-    else if (n == 2) row_chunk<2, 2, 4>(p, q, e, m, n, block_c, S, part);
-    else if (n <= 4) row_chunk<4, 2, 4>(p, q, e, m, n, block_c, S, part);
-    else row_chunk<8, 2, 4>(p, q, e, m, n, block_c, S, part);
+    const int n_rows = int(found[2] - m < R ? found[2] - m : R);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ks = warp % S, groups = kWarps / S;
+    const int n0 = (block_c * groups + warp / S) * kC;
+    const int nv = p.K / 16;                 // 16-byte vectors of a row
+    const int step = 32 * S;
+    const bool live = n0 < p.N;              // N is a multiple of 8, so all C channels are
+    const int8_t *w = p.W + (int64_t(e) * p.N + (live ? n0 : 0)) * p.K;
+    uint4 wv[kU][kC];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int v = v0 + u * step;
+                wv[u][c] = live && v < nv ? ld_weights(w + int64_t(c) * p.K + int64_t(v) * 16) : make_uint4(0, 0, 0, 0);
+            }
+    };
+    const int first = ks * 32 + lane;
+    load(first);
+
+    // the tokens are complete once the grid before this one is
+    grid_dependency_wait();
+    const int8_t *x[R];
+    const XT *row[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        int64_t t = m + (r < n_rows ? r : 0);
+        if (p.rows) t = p.rows[t];
+        const bool in = t >= 0 && t < p.T;                       // (others: reported where they are scaled)
+        row[r] = r < n_rows && in ? X + t * (ACT ? 2 : 1) * int64_t(p.K) : kFused ? nullptr : X;
+        x[r] = kFused ? q_smem + int64_t(r) * p.K : reinterpret_cast<const int8_t *>(row[r]);
+    }
+    if constexpr (kFused) quantise_rows<R, XT, ACT>(row, p.K, q_smem, scale, top);
+
+    int acc[R][kC];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) acc[r][c] = 0;
+    for (int v0 = first; __any_sync(0xffffffffu, live && v0 < nv);) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int v = v0 + u * step < nv ? v0 + u * step : 0;   // past the end: weights are zero
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint4 xv = *reinterpret_cast<const uint4 *>(x[r] + int64_t(v) * 16);
+#pragma unroll
+                for (int c = 0; c < kC; ++c) acc[r][c] = dot16(wv[u][c], xv, acc[r][c]);
+            }
+        }
+        v0 += kU * step;
+        load(v0);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int s = __reduce_add_sync(0xffffffffu, acc[r][c]);
+            if (lane == 0) part[warp * (R * kC) + r * kC + c] = s;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < groups * R * kC; i += kThreads) {
+        const int g = i / (R * kC), r = i / kC % R, c = i % kC;
+        const int n = (block_c * groups + g) * kC + c;
+        if (r >= n_rows || n >= p.N) continue;
+        int sum = 0;
+        for (int k = 0; k < S; ++k) sum += part[(g * S + k) * (R * kC) + r * kC + c];
+        int64_t t = m + r;
+        if (p.rows) t = p.rows[t];
+        if (t < 0 || t >= p.T) {
+            atomicCAS(p.status, 0, kI8StatusBadRows);
+            continue;
+        }
+        store_out(p, (m + r) * int64_t(p.N) + n, float(sum) * p.ws[int64_t(e) * p.N + n] * (kFused ? scale[r] : p.xs[t]));
+    }
 }
 
-}  // namespace
-
-cudaError_t launch_i8_rows(const I8Params &p, const int8_t *q, bool pdl, cudaStream_t stream)
+template <int R, typename XT, bool ACT>
+cudaError_t launch(const I8Params &p, const void *X, bool pdl, cudaStream_t stream)
 {
-    const int S = 1, C = 2;
-    const int blocks_n = (p.N + kWarps / S * C - 1) / (kWarps / S * C);
+    // K is divided over S warps until about 4096 warps share the weights (27 a
+    // multiprocessor), as long as each has a vector of every lane
+    int S = 1;
+    while (S < kWarps && p.M / R * (p.N / kC) * S < 4096 && 512 * S < p.K) S *= 2;
+    const int per_block = kWarps / S * kC;
+    const int blocks_n = (p.N + per_block - 1) / per_block;
     const int64_t blocks = p.M * blocks_n;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(unsigned(blocks), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(XT) > 1 ? size_t(R) * size_t(p.K) : 0;
     cfg.stream = stream;
     if (pdl) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -182,7 +233,48 @@ cudaError_t launch_i8_rows(const I8Params &p, const int8_t *q, bool pdl, cudaStr
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, i8_rows_kernel, p, q, blocks_n, S);
+    return cudaLaunchKernelEx(&cfg, i8_rows_kernel<R, XT, ACT>, p, static_cast<const XT *>(X), blocks_n, S);
+}
+
+// Rows of an expert that a block takes: all that there can be where rows are
+// dense.  Where few rows meet many experts nearly every expert has one row (and
+// a token never meets an expert twice), and the kernels for fewer rows hold
+// more loads in flight; a second row of an expert is another block.
+int run_rows(const I8Params &p)
+{
+    const int64_t most = p.rows && p.E > 1 && p.T < p.M ? p.T : p.M;
+    if (most <= 1 || (p.E > 1 && p.E >= 4 * p.M)) return 1;
+    if (most <= 2 || (p.E > 1 && p.E >= p.M)) return 2;
+    return most <= 4 ? 4 : 8;
+}
+
+template <typename XT, bool ACT>
+cudaError_t launch_fused(const I8Params &p, const void *X, bool pdl, cudaStream_t stream)
+{
+    return run_rows(p) == 1 ? launch<1, XT, ACT>(p, X, pdl, stream) : launch<2, XT, ACT>(p, X, pdl, stream);
+}
+
+}  // namespace
+
+bool i8_rows_fused(const I8Params &p)
+{
+    const int64_t bytes = int64_t(p.M < p.E ? p.M : p.E) * p.N * p.K;
+    return bytes <= kFusedWeights && run_rows(p) <= 2 && int64_t(run_rows(p)) * p.K <= kFusedBytes;
+}
+
+cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream)
+{
+    const bool silu = act == CAKE_GG_ACT_SILU_MUL;
+    if (x_dtype == CAKE_GG_BF16)
+        return silu ? launch_fused<uint16_t, true>(p, X, pdl, stream) : launch_fused<uint16_t, false>(p, X, pdl, stream);
+    if (x_dtype == CAKE_GG_FP32)
+        return silu ? launch_fused<float, true>(p, X, pdl, stream) : launch_fused<float, false>(p, X, pdl, stream);
+    switch (run_rows(p)) {
+    case 1: return launch<1, int8_t, false>(p, X, pdl, stream);
+    case 2: return launch<2, int8_t, false>(p, X, pdl, stream);
+    case 4: return launch<4, int8_t, false>(p, X, pdl, stream);
+    default: return launch<8, int8_t, false>(p, X, pdl, stream);
+    }
 }
 
 }  // namespace cakegg
