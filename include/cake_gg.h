@@ -311,7 +311,8 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
 typedef enum { CAKE_GG_ACT_NONE = 0, CAKE_GG_ACT_SILU_MUL = 1 } cake_gg_act_t;
 typedef enum {
     CAKE_GG_I8_ROWS = 0,     /* few rows: 32-bit integer dot products              */
-    CAKE_GG_I8_MMA = 1       /* tensor cores: FP16 operands, FP32 sums             */
+    CAKE_GG_I8_MMA = 1,      /* tensor cores: FP16 operands, FP32 sums             */
+    CAKE_GG_I8_WARPS = 2     /* a few dozen rows: the same from warps' registers   */
 } cake_gg_i8_path_t;
 
 typedef struct cake_gg_i8_plan {

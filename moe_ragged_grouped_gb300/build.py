@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libcake_gg.so")
 
 SOURCES = ["cake_gg_capi.cu", "cake_gg_fwd.cu", "cake_gg_dgrad.cu", "cake_gg_wgrad.cu", "cake_gg_router.cu",
-           "cake_gg_int8.cu", "cake_gg_int8_rows.cu", "cake_gg_int8_mma.cu"]
+           "cake_gg_int8.cu", "cake_gg_int8_rows.cu", "cake_gg_int8_mma.cu", "cake_gg_int8_warps.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                 "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -248,31 +248,42 @@ int stages_for(int pair, int nt, int splits, int E)
     return s;
 }
 
-// Shape of the tensor-core path.  Rows of a tile: what an expert is expected to
-// have (twice the average where rows are routed), in powers of two up to 128;
-// above that pairs of CTAs take 256 channels x 192 rows.
+// Shape of the tensor-core path: a rule on the rows that an expert is expected to
+// have.
+//  - Long: pairs of CTAs, 256 channels x 192 rows with two accumulators (16384 x
+//    4096 -> 4096: 305 us; 256 rows with one accumulator, stored between tiles:
+//    355 us), but 256 rows where they are gathered, whose copies weigh more per
+//    row (8192 tokens through 4 of 32 experts 6144 -> 4096: 1014 against 1083 us).
+//  - Else single CTAs, 128 channels x the next power of two from 32 (16 rows and
+//    more tiles: 158 against 139 us for 64 tokens through 4 of 32 experts): of
+//    the rows there are, or of four times the average where experts share them.
+//  - Few tiles: clusters of up to 8 CTAs divide the reduction while all of them
+//    run at once and each keeps two stages (33 x 4096 -> 5120: 12.5 us, 16.5
+//    undivided).
 void choose_mma(cake_gg_i8_plan_t *pl)
 {
     const int64_t busy = pl->M_max < pl->E ? pl->M_max : pl->E;
     const int64_t est = pl->E == 1 ? pl->M_max : 4 * ((pl->M_max + busy - 1) / (busy > 0 ? busy : 1));
+    const bool routed = pl->E > 1 && pl->T != pl->M_max;   // (rows need not be given where T = M)
     pl->path = CAKE_GG_I8_MMA;
     pl->pair = 1;
-    pl->tile_rows = est <= 16 ? 16 : est <= 32 ? 32 : est <= 64 ? 64 : 128;
+    pl->tile_rows = est <= 32 ? 32 : est <= 64 ? 64 : 128;
     pl->acc_bufs = 2;
     pl->splits = 1;
     if (est > 512 || (pl->E == 1 && est > 256)) {
         pl->pair = 2;
-        pl->tile_rows = 192;
+        pl->tile_rows = routed ? 256 : 192;
     }
     pl->pair = env_int("CAKE_GG_I8_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_I8_ROWS_PER_TILE", pl->tile_rows);
     if (nt >= 16 && nt <= 256 && nt % 16 == 0) pl->tile_rows = nt;
     pl->acc_bufs = env_int("CAKE_GG_I8_BUFS", pl->tile_rows > 192 ? 1 : pl->acc_bufs) == 1 ? 1 : 2;
-    const int64_t tiles = (pl->M_max / pl->tile_rows + busy) * ((pl->N + 127) / 128);
+    const int64_t tiles = (pl->E == 1 ? (pl->M_max + pl->tile_rows - 1) / pl->tile_rows : pl->M_max / pl->tile_rows + busy) *
+                          ((pl->N + 127) / 128);
     if (pl->pair == 1 && pl->tile_rows <= 64) {
         const int n_kb = (pl->K + 127) / 128;
-        for (int s = 8; s > 1; s /= 2)
-            if (tiles * s <= 152 && n_kb >= 4 * s) {
+        for (int s = 8; s > 1; --s)
+            if (tiles * s <= 152 && n_kb >= 2 * s) {
                 pl->splits = s;
                 break;
             }
@@ -319,11 +330,20 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
     plan->act = act;
     plan->out_dtype = out_dtype;
     plan->max_sms = max_sms;
-    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8FewRows ? CAKE_GG_I8_ROWS : CAKE_GG_I8_MMA);
+    // Up to 8 rows: integer dot products.  Up to 16 over at most 32 MB of weights:
+    // products from warps' registers, whose start costs less (16 x 4096 -> 5120:
+    // 10.6 against 15.6 us; x 8192 -> 8192: 24.5 against 27.6; 33 x 4096 -> 5120: 28
+    // against 12.5).  Else the tensor cores.
+    const int64_t weights = (M_max < E ? M_max : E) * int64_t(N) * K;
+    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8FewRows ? CAKE_GG_I8_ROWS
+                                                : M_max <= 16 && weights <= (32 << 20) ? CAKE_GG_I8_WARPS
+                                                                                       : CAKE_GG_I8_MMA);
+    plan->path = path;
     if (path == CAKE_GG_I8_MMA) {
         choose_mma(plan);
         if (!mma_plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
     }
+    if (path == CAKE_GG_I8_WARPS) plan->tile_rows = env_int("CAKE_GG_I8_ROWS_PER_TILE", M_max <= 16 ? 16 : M_max <= 32 ? 32 : M_max <= 48 ? 48 : 64);
     plan->timeout_ns = kTimeoutNs;
     plan->workspace_bytes = layout(*plan).total;
     return CAKE_GG_OK;
@@ -351,7 +371,10 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     const cake_gg_i8_plan_t &pl = *plan;
     int rc = check_problem(pl.E, pl.M_max, pl.T, pl.N, pl.K, pl.x_dtype, pl.act, pl.out_dtype);
     if (rc != CAKE_GG_OK) return rc;
-    if ((pl.path != CAKE_GG_I8_ROWS && (pl.path != CAKE_GG_I8_MMA || !mma_plan_ok(pl))) || pl.max_sms < 0)
+    const bool warps = pl.path == CAKE_GG_I8_WARPS;
+    if (pl.max_sms < 0 || (pl.path != CAKE_GG_I8_ROWS && !warps && pl.path != CAKE_GG_I8_MMA) ||
+        (pl.path == CAKE_GG_I8_MMA && !mma_plan_ok(pl)) ||
+        (warps && (pl.tile_rows < 16 || pl.tile_rows > 64 || pl.tile_rows % 16 != 0)))
         return CAKE_GG_ERR_INVALID_ARG;
     const bool ready = pl.x_dtype == CAKE_GG_INT8;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))
@@ -385,7 +408,10 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
     const bool mma = pl.path == CAKE_GG_I8_MMA, pdl = pdl_enabled();
     auto status = [](cudaError_t err) { return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA; };
-    if (!mma && (ready || i8_rows_fused(p))) return status(launch_i8_rows(p, X, pl.x_dtype, pl.act, pdl, s));
+    if (warps && ready)
+        return status(launch_i8_warps(p, static_cast<const int8_t *>(X), pl.tile_rows, pdl, s));
+    if (pl.path == CAKE_GG_I8_ROWS && (ready || i8_rows_fused(p)))
+        return status(launch_i8_rows(p, X, pl.x_dtype, pl.act, pdl, s));
 
     // the token pass, then the product
     void *tokens = base + L.tokens;
@@ -399,6 +425,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     }
     if (rc != CAKE_GG_OK) return rc;
     p.early = 1;
+    if (warps) return status(launch_i8_warps(p, static_cast<const int8_t *>(tokens), pl.tile_rows, pdl, s));
     if (!mma) return status(launch_i8_rows(p, tokens, CAKE_GG_INT8, CAKE_GG_ACT_NONE, pdl, s));
     I8MmaParams m{};
     m.b = p;

@@ -70,4 +70,8 @@ constexpr int kI8FewRows = 8;   // rows of a call that the few-row path takes
 bool i8_rows_fused(const I8Params &p);
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream);
 
+// A few dozen rows: warp-level products from registers, runs of 16, 32, 48 or 64
+// of an expert's rows; q [T, K].
+cudaError_t launch_i8_warps(const I8Params &p, const int8_t *q, int rows, bool pdl, cudaStream_t stream);
+
 }  // namespace cakegg

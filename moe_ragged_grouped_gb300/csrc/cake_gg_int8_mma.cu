@@ -21,6 +21,7 @@
 // warps 6-13 convert (two groups on alternate stages), warps 14-17 gather
 // (launched for routed rows only).
 #include "cake_gg_int8.h"
+#include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
 
 namespace cakegg {
@@ -34,7 +35,7 @@ constexpr int kStagesMax = 12;
 constexpr int kSlotsMax = 8;
 constexpr int kGatherWarp0 = 14;
 constexpr int kRowsPerCta = 128;             // B rows of a CTA at most
-constexpr uint32_t kStageOut = 4 * 32 * 64;  // BF16 output: 32 rows x 32 channels per storing warp
+constexpr uint32_t kOutTile = 32 * 32 * 4;   // 32 rows x 32 channels of output, per storing warp
 constexpr uint32_t kSlotCols = kKB / 2;      // tensor memory columns of a widened weight tile
 constexpr uint64_t kDrainNs = 20000000ull;
 
@@ -102,22 +103,6 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// Four 8-bit integers (a 32-bit word) as two packed pairs of FP16: with its
-// sign bit flipped a byte is b + 128, and as the low byte of the FP16 pattern
-// 0x6400 (1024, one unit in the last place) it reads 1024 + 128 + b.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    w ^= 0x80808080u;
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));   // 1152 each
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-}
-
 // FP32 accumulators, FP16 operands (A and B format fields 0), both K-major.
 __device__ __forceinline__ uint32_t idesc_f16(uint32_t M, uint32_t N)
 {
@@ -144,6 +129,18 @@ struct Turn {
         }
     }
 };
+
+// A split tile's rows are summed by the CTAs of its cluster, each its share, in
+// whole fours; what a CTA receives (a row of it padded by 16 bytes: no bank
+// conflicts).
+__host__ __device__ constexpr int split_columns(int rows, int splits)
+{
+    return ((rows + 3) / 4 + splits - 1) / splits * 4;
+}
+__host__ __device__ constexpr size_t split_bytes(int nt, int splits)
+{
+    return size_t(splits) * 128 * size_t(split_columns(nt, splits) + 4) * sizeof(float);
+}
 
 struct Tile {
     int e, ct;                // expert, channel tile
@@ -195,10 +192,10 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     const uint32_t x_rows = uint32_t(p.nt / PAIR);               // B rows of this CTA in a stage
     const uint32_t stage_bytes = kWBytes + x_rows * 256u;
     uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
-    float *recv = reinterpret_cast<float *>(after);              // split: [split][column][128]
-    after += p.splits > 1 ? size_t(p.nt + p.splits) * 512u : 0;
-    uint8_t *out_tile = after;                                   // [warp][row][32 channels] BF16
-    after += OUT_F32 ? 0 : kStageOut;
+    float *recv = reinterpret_cast<float *>(after);              // split: [split][channel][columns + 4]
+    after += p.splits > 1 ? split_bytes(p.nt, p.splits) : 0;
+    uint8_t *out_tile = after;                                   // [warp][row][32 channels]
+    after += 4 * kOutTile;
     Ctrl *c = reinterpret_cast<Ctrl *>(after);
     float *xs_tile = reinterpret_cast<float *>(c + 1);           // [2][nt]
     int32_t *off = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);
@@ -370,27 +367,23 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                 tc_fence_after_sync();
                 const uint32_t d = tmem + uint32_t(buf) * d_stride;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    const int s = st.at, a = sl.at;
                     // the converters of both CTAs saw their stage's copies land
-                    if (!warp_wait(smem_u32(&c->conv[a]), sl.parity, c, p.b)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(smem_u32(&c->conv[sl.at]), sl.parity, c, p.b);
+                    if (!ok) break;
                     if (elect_one()) {
                         tc_fence_after_sync();
-                        const uint32_t xb = ring + uint32_t(s) * stage_bytes + kWBytes;
+                        const uint32_t xb = ring + uint32_t(st.at) * stage_bytes + kWBytes;
                         const uint64_t b0 = smem_desc_sw128(xb, 16, 1024), b1 = smem_desc_sw128(xb + x_rows * 128u, 16, 1024);
-                        const uint32_t at = slots0 + uint32_t(a) * kSlotCols;
+                        const uint32_t at = slots0 + uint32_t(sl.at) * kSlotCols;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             umma_bf16_ta<PAIR>(d, at + uint32_t(k) * 8u, (k < 4 ? b0 : b1) + uint64_t(k & 3) * 2u, idesc,
                                                kb > kb0 || k > 0 ? 1u : 0u);
-                        if (PAIR == 2) {
-                            umma_commit_mc<2>(smem_u32(&c->empty[s]), pair_mask);
-                            if (kb + 1 == kb1) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
-                        } else {
-                            umma_commit<1>(smem_u32(&c->empty[s]));
-                            if (kb + 1 == kb1) umma_commit<1>(smem_u32(&c->tfull[buf]));
+                        if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->empty[st.at]), pair_mask);
+                        else umma_commit<1>(smem_u32(&c->empty[st.at]));
+                        if (kb + 1 == kb1) {
+                            if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
+                            else umma_commit<1>(smem_u32(&c->tfull[buf]));
                         }
                     }
                     any = true;
@@ -432,57 +425,54 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             if (!named_bar_and(1, 128, ok)) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + uint32_t(buf) * d_stride + (uint32_t(q * 32) << 16);
-            const int per = (t.rows + p.splits - 1) / p.splits;  // split: columns that a CTA sums
-            int owner = 0, mine = 0;
+            const int per = split_columns(t.rows, p.splits);
+            uint8_t *tile = out_tile + q * kOutTile;
             for (int c0 = 0; c0 < t.rows; c0 += 32) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(d + uint32_t(c0), r);
                 tmem_ld_wait();
                 if (p.splits > 1) {
+                    // four columns at a time to the CTA that sums them
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 32; j += 4)
                         if (c0 + j < t.rows) {
-                            st_cluster_f32(map_to_cta(smem_u32(recv + (rank * per + mine) * 128 + q * 32 + lane), uint32_t(owner)),
-                                           __uint_as_float(r[j]));
-                            if (++mine == per) {
-                                mine = 0;
-                                ++owner;
-                            }
+                            const int owner = (c0 + j) / per, col = c0 + j - owner * per;
+                            float *to = recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4) + col;
+                            st_cluster_v4(map_to_cta(smem_u32(to), uint32_t(owner)),
+                                          make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                                                      __uint_as_float(r[j + 3])));
                         }
                     continue;
                 }
-                if (OUT_F32) {
-                    const int64_t y0 = (int64_t(t.m0) + c0) * p.b.N + n;
-                    float *y = static_cast<float *>(p.b.Y) + y0;
+                // through shared memory, transposed: a lane writes its channel of 32
+                // rows, then stores 16 bytes of a row's channels at a time
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < t.rows && ch_ok) y[int64_t(j) * p.b.N] = __uint_as_float(r[j]) * ws * xs[c0 + j];
-                } else {
-                    // through shared memory, transposed: a lane writes its channel of 32
-                    // rows, then stores 16 bytes of a row's 32 channels
-                    uint8_t *tile = out_tile + q * (kStageOut / 4);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 x4 = *reinterpret_cast<const float4 *>(xs + c0 + j);
-                        const uint32_t a = pack_bf16x2(__uint_as_float(r[j]) * ws * x4.x, __uint_as_float(r[j + 1]) * ws * x4.y);
-                        const uint32_t b = pack_bf16x2(__uint_as_float(r[j + 2]) * ws * x4.z, __uint_as_float(r[j + 3]) * ws * x4.w);
-                        uint16_t *dst = reinterpret_cast<uint16_t *>(tile + j * 64) + lane;
-                        dst[0] = uint16_t(a & 0xffffu);
-                        dst[32] = uint16_t(a >> 16);
-                        dst[64] = uint16_t(b & 0xffffu);
-                        dst[96] = uint16_t(b >> 16);
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 x4 = *reinterpret_cast<const float4 *>(xs + c0 + j);
+                    const float v[4] = {__uint_as_float(r[j]) * ws * x4.x, __uint_as_float(r[j + 1]) * ws * x4.y,
+                                        __uint_as_float(r[j + 2]) * ws * x4.z, __uint_as_float(r[j + 3]) * ws * x4.w};
+                    if (OUT_F32) {
+                        float *dst = reinterpret_cast<float *>(tile) + j * 32 + lane;
+                        dst[0] = v[0], dst[32] = v[1], dst[64] = v[2], dst[96] = v[3];
+                    } else {
+                        const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+                        uint16_t *dst = reinterpret_cast<uint16_t *>(tile) + j * 32 + lane;
+                        dst[0] = uint16_t(a & 0xffffu), dst[32] = uint16_t(a >> 16);
+                        dst[64] = uint16_t(b & 0xffffu), dst[96] = uint16_t(b >> 16);
                     }
-                    __syncwarp();
-                    const int piece = lane & 3, n8 = n - lane + piece * 8;
-                    uint16_t *y = static_cast<uint16_t *>(p.b.Y) + (int64_t(t.m0) + c0) * p.b.N + n8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = (lane >> 2) + 8 * i;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * 64 + piece * 16);
-                        if (c0 + row < t.rows && n8 < p.b.N) *reinterpret_cast<uint4 *>(y + int64_t(row) * p.b.N) = v;
-                    }
-                    __syncwarp();
                 }
+                __syncwarp();
+                constexpr int kSize = OUT_F32 ? 4 : 2, kPieces = 2 * kSize, kPer = 16 / kSize;   // 16-byte pieces of a row
+                const int piece = lane % kPieces, nv = n - lane + piece * kPer;
+                uint8_t *y = static_cast<uint8_t *>(p.b.Y) + ((int64_t(t.m0) + c0) * p.b.N + nv) * kSize;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int row = lane / kPieces + i * (32 / kPieces);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * (32 * kSize) + piece * 16);
+                    if (c0 + row < t.rows && nv < p.b.N)
+                        *reinterpret_cast<uint4 *>(y + int64_t(row) * p.b.N * kSize) = v;
+                }
+                __syncwarp();
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -505,41 +495,43 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         int it = group, kb = group;
         bool ok = true;
         Walk w(unit0, step, p.n_ct);
-        while (ok) {
+        auto widen = [&](const uint8_t *src, int h, uint32_t (&f)[32]) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + (((h * 4 + v) ^ (row & 7)) << 4));
+                widen4(x.x, f[v * 8], f[v * 8 + 1]);
+                widen4(x.y, f[v * 8 + 2], f[v * 8 + 3]);
+                widen4(x.z, f[v * 8 + 4], f[v * 8 + 5]);
+                widen4(x.w, f[v * 8 + 6], f[v * 8 + 7]);
+            }
+        };
+        while (true) {
             while (kb >= n_kb) {
                 kb -= n_kb;
                 w.next();
             }
             if (w.g >= tiles) break;
-            ok = warp_wait(smem_u32(&c->full[st.at]), st.parity, c, p.b);
-            if (!ok) break;
+            if (!warp_wait(smem_u32(&c->full[st.at]), st.parity, c, p.b)) break;
             const uint8_t *src = ring_ptr + size_t(st.at) * stage_bytes + row * 128;
-            const uint32_t dst = slots0 + uint32_t(sl.at) * kSlotCols + (uint32_t(q * 32) << 16);
             // (gathered rows were written through the generic proxy)
             if (p.b.rows) fence_proxy_async_smem();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t f[32];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (((h * 4 + v) ^ (row & 7)) << 4));
-                    widen4(x.x, f[v * 8], f[v * 8 + 1]);
-                    widen4(x.y, f[v * 8 + 2], f[v * 8 + 3]);
-                    widen4(x.z, f[v * 8 + 4], f[v * 8 + 5]);
-                    widen4(x.w, f[v * 8 + 6], f[v * 8 + 7]);
-                }
-                if (h == 0 && it >= p.slots) {
-                    if (it > p.slots) last.next(p.stages);
-                    if (it > p.slots + 1) last.next(p.stages);
-                    ok = warp_wait(smem_u32(&c->empty[last.at]), last.parity, c, p.b);
-                    tc_fence_after_sync();
-                }
-                if (ok) tmem_st_32x32b_x32(dst + uint32_t(h) * 32u, f);
+            const uint32_t dst = slots0 + uint32_t(sl.at) * kSlotCols + (uint32_t(q * 32) << 16);
+            uint32_t f[32];
+            widen(src, 0, f);
+            if (it >= p.slots) {
+                if (it > p.slots) last.next(p.stages);
+                if (it > p.slots + 1) last.next(p.stages);
+                if (!warp_wait(smem_u32(&c->empty[last.at]), last.parity, c, p.b)) break;
+                tc_fence_after_sync();
             }
+            tmem_st_32x32b_x32(dst, f);
+            uint32_t g[32];
+            widen(src, 1, g);
+            tmem_st_32x32b_x32(dst + 32u, g);
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (ok && lane == 0) {
+            if (lane == 0) {
                 // (default semantics: what the MMA reads is complete and fenced; a
                 // release at cluster scope cost a tenth of the whole product)
                 if (leader) mbar_arrive(smem_u32(&c->conv[sl.at]));
@@ -599,19 +591,25 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         Walk w(unit0, step, p.n_ct);
         if (warp >= 2 && warp < kConvWarp0 && w.g < tiles && !aborted(c)) {
             const Tile t = w.tile(p.nt, off, pref);
-            const int per = (t.rows + p.splits - 1) / p.splits;
+            const int per = split_columns(t.rows, p.splits);
             const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
-            if (n < p.b.N) {
-                const float ws = p.b.ws[int64_t(t.e) * p.b.N + n];
-                for (int j = 0; j < per && rank * per + j < t.rows; ++j) {
-                    float sum = recv[j * 128 + row];
-                    for (int s = 1; s < p.splits; ++s) sum += recv[(s * per + j) * 128 + row];
-                    const int m = rank * per + j;
-                    const float v = sum * ws * xs_tile[m];
-                    const int64_t at = (int64_t(t.m0) + m) * p.b.N + n;
-                    if (OUT_F32) static_cast<float *>(p.b.Y)[at] = v;
-                    else static_cast<uint16_t *>(p.b.Y)[at] = uint16_t(pack_bf16x2(v, 0.0f) & 0xffffu);
+            const float ws = n < p.b.N ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
+            const int m0 = rank * per;
+            for (int j = 0; j < per && m0 + j < t.rows; j += 4) {
+                float4 sum = *reinterpret_cast<const float4 *>(recv + size_t(row) * (per + 4) + j);
+                for (int v = 1; v < p.splits; ++v) {
+                    const float4 o = *reinterpret_cast<const float4 *>(recv + (size_t(v) * 128 + row) * (per + 4) + j);
+                    sum.x += o.x, sum.y += o.y, sum.z += o.z, sum.w += o.w;
                 }
+                const float4 x4 = *reinterpret_cast<const float4 *>(xs_tile + m0 + j);
+                const float v[4] = {sum.x * ws * x4.x, sum.y * ws * x4.y, sum.z * ws * x4.z, sum.w * ws * x4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (m0 + j + i < t.rows && n < p.b.N) {
+                        const int64_t at = (int64_t(t.m0) + m0 + j + i) * p.b.N + n;
+                        if (OUT_F32) static_cast<float *>(p.b.Y)[at] = v[i];
+                        else static_cast<uint16_t *>(p.b.Y)[at] = uint16_t(pack_bf16x2(v[i], 0.0f) & 0xffffu);
+                    }
             }
         }
     }
@@ -676,7 +674,7 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const uint16_t 
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
     return 1024 + size_t(stages) * (kWBytes + size_t(nt / pair) * 256) +
-           (splits > 1 ? size_t(nt + splits) * 512 : 0) + kStageOut + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
+           (splits > 1 ? split_bytes(nt, splits) : 0) + 4 * kOutTile + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
 int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream)
@@ -699,7 +697,8 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
     if (rc != CAKE_GG_OK) return rc;
 
     // row tiles at most: a whole one per nt rows and a last one per expert with rows
-    const int64_t bound = (p.b.M / p.nt + (p.b.M < p.b.E ? p.b.M : p.b.E)) * int64_t(p.n_ct);
+    const int64_t tiles = p.b.E == 1 ? (p.b.M + p.nt - 1) / p.nt : p.b.M / p.nt + (p.b.M < p.b.E ? p.b.M : p.b.E);
+    const int64_t bound = tiles * p.n_ct;
     int64_t grid;
     if (p.splits > 1) {
         grid = bound * p.splits;                       // one cluster per unit

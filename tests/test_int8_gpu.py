@@ -330,6 +330,8 @@ def test_a_wait_that_runs_out_is_reported():
 
 
 @pytest.mark.parametrize("env", [
+    dict(PATH="0"), dict(PATH="2", ROWS_PER_TILE="16"), dict(PATH="2", ROWS_PER_TILE="32"),
+    dict(PATH="2", ROWS_PER_TILE="48"), dict(PATH="2", ROWS_PER_TILE="64"),
     dict(PAIR="1", ROWS_PER_TILE="16", SPLITS="1"), dict(PAIR="1", ROWS_PER_TILE="32", SPLITS="3"),
     dict(PAIR="1", ROWS_PER_TILE="64", SPLITS="8"), dict(PAIR="1", ROWS_PER_TILE="128", SPLITS="1"),
     dict(PAIR="2", ROWS_PER_TILE="64", SPLITS="1"),
@@ -340,7 +342,7 @@ def test_a_wait_that_runs_out_is_reported():
 def test_every_tile_shape(env, routed, monkeypatch):
     """Each shape of tile on the same ragged rows, with one CTA or pair and with all."""
     import torch
-    for k, v in dict(env, PATH="1").items():
+    for k, v in dict(dict(PATH="1"), **env).items():
         monkeypatch.setenv("CAKE_GG_I8_" + k, v)
     rng = np.random.default_rng(4)
     sizes, N, K = [5, 0, 290, 1, 0, 33, 64, 17], 392, 1200
