@@ -91,16 +91,15 @@ __device__ __forceinline__ bool elect_one()
     return e != 0;
 }
 
-// 16 bytes from global to shared memory, zeros where `in` is false.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
+// Four rows of a tensor (its box one row high) to consecutive 128-byte rows.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t r0,
+                                            int32_t r1, int32_t r2, int32_t r3)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-
-// Arrive on `bar` when this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
 }
 
 // FP32 accumulators, FP16 operands (A and B format fields 0), both K-major.
@@ -184,7 +183,7 @@ struct Walk {
 template <int PAIR, bool OUT_F32>
 __global__ void __launch_bounds__(kThreadsRouted, 1)
     i8_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
-                  const uint16_t *__restrict__ q16, const I8MmaParams p)
+                  const I8MmaParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         c->abort_flag = 0;
         c->bad = 0;
         tma_prefetch_desc(&mapW);
-        if (!p.b.rows) tma_prefetch_desc(&mapX);
+        tma_prefetch_desc(&mapX);
     }
     if (warp == 1) {
         tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     }
     if (tid == 64) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(smem_u32(&c->full[s]), p.b.rows ? 1u + 128u : 1u);   // the copies' arming, every gathering thread
+            mbar_init(smem_u32(&c->full[s]), 1);
             mbar_init(smem_u32(&c->empty[s]), 1);
         }
         for (int a = 0; a < p.slots; ++a) {
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
             const int32_t mb = t.m0 + half * n_half;
             const int n_box = boxes ? (n_half + p.box - 1) / p.box : 0;
-            const uint32_t bytes = kWBytes + 256u * uint32_t(n_box * p.box);
+            const uint32_t bytes = kWBytes + 256u * uint32_t(boxes ? n_box * p.box : n_half);
             auto copy_w = [&](int kb, int s) {
                 const uint32_t bar = smem_u32(&c->full[s]);
                 mbar_arrive_expect_tx(bar, bytes);
@@ -513,8 +512,6 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             if (w.g >= tiles) break;
             if (!warp_wait(smem_u32(&c->full[st.at]), st.parity, c, p.b)) break;
             const uint8_t *src = ring_ptr + size_t(st.at) * stage_bytes + row * 128;
-            // (gathered rows were written through the generic proxy)
-            if (p.b.rows) fence_proxy_async_smem();
             const uint32_t dst = slots0 + uint32_t(sl.at) * kSlotCols + (uint32_t(q * 32) << 16);
             uint32_t f[32];
             widen(src, 0, f);
@@ -546,41 +543,43 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         __syncwarp();
     } else {
         // ======================= routed rows =======================
-        // 16 lanes copy the 256 bytes of a row that a stage holds; a warp copies two
-        // rows at once, the four warps 8.
-        const int gt = tid - kGatherWarp0 * 32;
-        const int b_row = gt >> 4, piece = gt & 15;
-        const uint32_t at = kWBytes + uint32_t(piece >> 3) * x_rows * 128u + uint32_t(b_row) * 128u +
-                            (uint32_t((piece & 7) ^ (b_row & 7)) << 4);
+        // Four rows at a time, fours v, v + 4, .. of this CTA's B tile by warp v; lane
+        // l knows the token of row l % 4 of the warp's four l / 4.  (The bytes are
+        // armed with the weights'.)
+        const int v = warp - kGatherWarp0;
         Turn st;
         bool ok = true;
         grid_dependency_wait();                                  // the tokens
         for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
             const Tile t = w.tile(p.nt, off, pref);
             const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
-            const int32_t mb = t.m0 + half * n_half + b_row;
-            int32_t id[kRowsPerCta / 8];                         // -1: a row past the tile's end, zeros
+            const int row = (lane >> 2) * 16 + v * 4 + (lane & 3);
+            const int32_t m = t.m0 + half * n_half + row;
+            int32_t token = row < n_half && m < t.end ? p.b.rows[m] : 0;
+            if (token < 0 || token >= p.b.T) token = 0;          // (reported where it is scaled)
+            int32_t id[32];
 #pragma unroll
-            for (int i = 0; i < kRowsPerCta / 8; ++i) {
-                id[i] = 8 * i < n_half && mb + 8 * i < t.end ? p.b.rows[mb + 8 * i] : -1;
-                if (id[i] >= p.b.T) id[i] = -1;                  // (reported where it is scaled)
-            }
+            for (int i = 0; i < 32; ++i) id[i] = __shfl_sync(0xffffffffu, token, i);
+            const int fours = n_half / 16;                       // (n_half is a multiple of 16)
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
                 if (!ok) break;
-                const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + at;
-                const int k = kb * kKB + piece * 8;
+                if (elect_one()) {
+                    const uint32_t bar = smem_u32(&c->full[st.at]);
+                    const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(v) * 512u;
 #pragma unroll
-                for (int i = 0; i < kRowsPerCta / 8; ++i)
-                    if (8 * i < n_half) {
-                        const bool in = id[i] >= 0 && k < p.b.K;
-                        cp_async16(dst + uint32_t(i) * 1024u, q16 + (in ? int64_t(id[i]) * p.b.K + k : 0), in);
-                    }
-                cp_async_arrive(smem_u32(&c->full[st.at]));
+                    for (int i = 0; i < 8; ++i)
+                        if (i < fours) {
+                            tma_gather4(dst + uint32_t(i) * 2048u, &mapX, bar, kb * kKB, id[4 * i], id[4 * i + 1], id[4 * i + 2],
+                                        id[4 * i + 3]);
+                            tma_gather4(dst + x_rows * 128u + uint32_t(i) * 2048u, &mapX, bar, kb * kKB + 64, id[4 * i],
+                                        id[4 * i + 1], id[4 * i + 2], id[4 * i + 3]);
+                        }
+                }
+                __syncwarp();
                 st.next(p.stages);
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
 
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
 }
 
 template <int PAIR, bool OUT_F32>
-cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const uint16_t *q, const I8MmaParams &p, int grid, bool pdl,
+cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaParams &p, int grid, bool pdl,
                    cudaStream_t stream)
 {
     auto kern = i8_mma_kernel<PAIR, OUT_F32>;
@@ -666,7 +665,7 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const uint16_t 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = unsigned(na);
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, q, p);
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
 }
 
 }  // namespace
@@ -692,7 +691,7 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
 
     const uint64_t dx[2] = {uint64_t(p.b.K), uint64_t(p.b.T)};
     const uint64_t sx[1] = {uint64_t(p.b.K) * 2};
-    const uint32_t bx[2] = {64, uint32_t(p.box)};
+    const uint32_t bx[2] = {64, p.b.rows ? 1u : uint32_t(p.box)};   // (gathered four rows at a time)
     rc = encode_tiled(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, dx, sx, bx);
     if (rc != CAKE_GG_OK) return rc;
 
@@ -709,11 +708,11 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
     }
     cudaError_t err;
     if (pair == 2)
-        err = p.b.out_f32 ? launch<2, true>(mw, mx, q, p, int(grid), pdl, stream)
-                          : launch<2, false>(mw, mx, q, p, int(grid), pdl, stream);
+        err = p.b.out_f32 ? launch<2, true>(mw, mx, p, int(grid), pdl, stream)
+                          : launch<2, false>(mw, mx, p, int(grid), pdl, stream);
     else
-        err = p.b.out_f32 ? launch<1, true>(mw, mx, q, p, int(grid), pdl, stream)
-                          : launch<1, false>(mw, mx, q, p, int(grid), pdl, stream);
+        err = p.b.out_f32 ? launch<1, true>(mw, mx, p, int(grid), pdl, stream)
+                          : launch<1, false>(mw, mx, p, int(grid), pdl, stream);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
