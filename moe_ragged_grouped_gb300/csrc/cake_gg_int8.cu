@@ -272,7 +272,7 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     pl->splits = 1;
     if (est > 512 || (pl->E == 1 && est > 256)) {
         pl->pair = 2;
-        pl->tile_rows = routed ? 256 : 192;
+        pl->tile_rows = 192;
     }
     pl->pair = env_int("CAKE_GG_I8_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_I8_ROWS_PER_TILE", pl->tile_rows);

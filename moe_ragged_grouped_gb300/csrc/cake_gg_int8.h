@@ -50,7 +50,9 @@ struct I8MmaParams {
     int32_t bufs;             // accumulators (1 or 2)
     int32_t splits;           // CTAs that share a tile's reduction (one cluster; 1 = none)
     int32_t debug_flags;
-    int32_t n_ct, n_kb, box;  // (set by the launch) channel tiles, stages of a tile, rows of a copy
+    // (set by the launch) channel tiles, stages of a tile, rows of a copy, 2^32 / (nt / 16) rounded up
+    int32_t n_ct, n_kb, box;
+    uint32_t div_nt;
 };
 
 constexpr size_t kI8SmemLimit = 232448;   // opt-in dynamic shared memory per CTA (227 KB)

@@ -17,9 +17,11 @@
 // converters' integer instructions then bound the kernel.)  B's width follows
 // the rows the tile really has, so a ragged end costs its own size only.
 //
-// Roles of a CTA: warp 0 copies, warp 1 issues MMAs, warps 2-5 scale and store,
-// warps 6-13 convert (two groups on alternate stages), warps 14-17 gather
-// (launched for routed rows only).
+// Roles of a CTA: warp 0 copies weights, warp 1 issues MMAs, warps 2-5 scale and
+// store, warps 6-13 convert (two groups on alternate stages), warp 14 copies
+// rows, or, where they are routed, warps 14-17 gather them, two on every other
+// stage (the first issue of a batch of copies takes a few hundred clocks: all
+// four on every stage were late).
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
@@ -27,13 +29,14 @@
 namespace cakegg {
 namespace {
 
-constexpr int kThreads = 448, kThreadsRouted = kThreads + 128;
+constexpr int kThreads = 480, kThreadsRouted = 576;
 constexpr int kConvWarp0 = 6;
 constexpr int kKB = 128;                     // reduction length of a stage
 constexpr uint32_t kWBytes = 128 * kKB;      // 8-bit weight tile of a stage
 constexpr int kStagesMax = 12;
 constexpr int kSlotsMax = 8;
-constexpr int kGatherWarp0 = 14;
+constexpr int kRowsWarp0 = 14;
+constexpr int kGatherWarps = 4;
 constexpr int kRowsPerCta = 128;             // B rows of a CTA at most
 constexpr uint32_t kOutTile = 32 * 32 * 4;   // 32 rows x 32 channels of output, per storing warp
 constexpr uint32_t kSlotCols = kKB / 2;      // tensor memory columns of a widened weight tile
@@ -46,7 +49,6 @@ struct __align__(16) Ctrl {
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort_flag;
-    int32_t bad;
     int32_t total;                                    // row tiles of all experts
 };
 
@@ -74,6 +76,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctrl *c
     return __all_sync(0xffffffffu, ok);
 }
 
+// A copy phase in flight lands before the CTA leaves (bounded).
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
 {
     const uint64_t t0 = global_timer_ns();
@@ -128,6 +131,34 @@ struct Turn {
         }
     }
 };
+
+// After an abort: the copies into this warp's last `issued` stages, `every` apart
+// before `st`, land before the CTA leaves.  (A phase that lacks the other
+// warp's part runs into the limit, by when the copies have long landed.)
+__device__ __forceinline__ void drain_stages(Turn st, int issued, int every, int lane, int stages, Ctrl *c)
+{
+    if (lane != 0) return;
+    for (int i = 0; i < issued; ++i) {
+        for (int k = 0; k < every; ++k) st.back(stages);
+        drain_wait(smem_u32(&c->full[st.at]), st.parity);
+    }
+}
+
+// Row tiles of n rows: n / nt rounded up, by a multiplication (nt = 16 k, k <= 16;
+// exact for n < 2^31).
+__device__ __forceinline__ int32_t row_tiles(int32_t n, const I8MmaParams &p)
+{
+    if (n <= 0) return 0;
+    const uint32_t t = (uint32_t(n) + 15u) >> 4;                 // (n + nt - 1) / nt = (t + k - 1) / k
+    return int32_t(p.nt == 16 ? t : __umulhi(t + uint32_t(p.nt >> 4) - 1u, p.div_nt));
+}
+
+__device__ __forceinline__ int4 lds_i4(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
 // A split tile's rows are summed by the CTAs of its cluster, each its share, in
 // whole fours; what a CTA receives (a row of it padded by 16 bytes: no bank
@@ -197,7 +228,8 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     after += 4 * kOutTile;
     Ctrl *c = reinterpret_cast<Ctrl *>(after);
     float *xs_tile = reinterpret_cast<float *>(c + 1);           // [2][nt]
-    int32_t *off = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);
+    int32_t *row_ids = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);   // [gathering warp][row]
+    int32_t *off = row_ids + kGatherWarps * kRowsPerCta / 2;
     int32_t *pref = off + p.b.E + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -207,45 +239,19 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     const bool leader = half == 0;
 
     // ---- set-up: TMEM, barriers, offsets and the prefix of their row tiles ----
-    if (tid == 0) {
-        c->abort_flag = 0;
-        c->bad = 0;
-        tma_prefetch_desc(&mapW);
-        tma_prefetch_desc(&mapX);
-    }
-    if (warp == 1) {
-        tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
-        tmem_relinquish<PAIR>();
-    }
-    if (tid == 64) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(smem_u32(&c->full[s]), 1);
-            mbar_init(smem_u32(&c->empty[s]), 1);
-        }
-        for (int a = 0; a < p.slots; ++a) {
-            mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);         // the group's warps, of both CTAs
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&c->tfull[b]), 1);
-            mbar_init(smem_u32(&c->tempty[b]), 4u * PAIR);       // storing warps, of both CTAs
-        }
-        mbar_init(smem_u32(&c->drain), 1);
-        fence_barrier_init();
-    }
     if (!p.b.early) grid_dependency_wait();
     grid_launch_dependents();
-    __syncthreads();                                             // c->bad is zero
-    for (int i = tid; i <= E; i += int(blockDim.x)) off[i] = p.b.offsets ? p.b.offsets[i] : (i ? int32_t(p.b.M) : 0);
-    __syncthreads();
     if (warp == 0) {
+        for (int i = lane; i <= E; i += 32) off[i] = p.b.offsets ? p.b.offsets[i] : (i ? int32_t(p.b.M) : 0);
+        __syncwarp();
         // lane l sums the row tiles of its run of experts, then the runs are scanned
         const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
         int32_t sum = 0;
         bool bad = lane == 0 && off[0] != 0;
         for (int e = e0; e < e1; ++e) {
             const int32_t n = off[e + 1] - off[e];
-            bad |= off[e + 1] < off[e] || int64_t(off[e + 1]) > p.b.M;
-            sum += n > 0 ? (n - 1) / p.nt + 1 : 0;
+            bad |= n < 0 || int64_t(off[e + 1]) > p.b.M;
+            sum += row_tiles(n, p);
         }
         int32_t inc = sum;
 #pragma unroll
@@ -255,9 +261,8 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         }
         int32_t at = inc - sum;
         for (int e = e0; e < e1; ++e) {
-            const int32_t n = off[e + 1] - off[e];
             pref[e] = at;
-            at += n > 0 ? (n - 1) / p.nt + 1 : 0;
+            at += row_tiles(off[e + 1] - off[e], p);
         }
         bad = __any_sync(0xffffffffu, bad);
         if (lane == 31) {
@@ -265,6 +270,25 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             c->total = bad ? 0 : inc;
             if (bad) atomicCAS(p.b.status, 0, kI8StatusBadOffsets);
         }
+    } else if (warp == 1) {
+        tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
+        tmem_relinquish<PAIR>();
+    } else if (tid == 64) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&c->full[s]), p.b.rows ? 3 : 2);  // the weights' arming and the rows'
+            mbar_init(smem_u32(&c->empty[s]), 1);
+        }
+        for (int a = 0; a < p.slots; ++a) mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);   // the group's warps, of both CTAs
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c->tfull[b]), 1);
+            mbar_init(smem_u32(&c->tempty[b]), 4u * PAIR);       // storing warps, of both CTAs
+        }
+        mbar_init(smem_u32(&c->drain), 1);
+        fence_barrier_init();
+    } else if (tid == 96) {
+        c->abort_flag = 0;
+        tma_prefetch_desc(&mapW);
+        tma_prefetch_desc(&mapX);
     }
     if (PAIR == 2 || p.splits > 1) cluster_sync_all();           // peers' barriers are ready
     tc_fence_before_sync();
@@ -281,73 +305,33 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     const int kb0 = p.splits > 1 ? p.n_kb * rank / p.splits : 0;
     const int kb1 = p.splits > 1 ? p.n_kb * (rank + 1) / p.splits : p.n_kb;
     constexpr int kNAlign = 16 * PAIR;
+    float ws_split = 0.0f;                                       // a storing thread's channel scale, for the split sum
     const uint16_t pair_mask = 3;
 
     if (warp == 0) {
-        // ======================= copies =======================
+        // ======================= weight copies =======================
+        // (these do not wait for the token pass)
         Turn st;
         int issued = 0;       // stages filled, up to the ring's depth
         bool ok = true;
-        const bool boxes = p.b.rows == nullptr;
-        bool waited = false;
         for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
             const Tile t = w.tile(p.nt, off, pref);
-            const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
-            const int32_t mb = t.m0 + half * n_half;
-            const int n_box = boxes ? (n_half + p.box - 1) / p.box : 0;
-            const uint32_t bytes = kWBytes + 256u * uint32_t(boxes ? n_box * p.box : n_half);
-            auto copy_w = [&](int kb, int s) {
-                const uint32_t bar = smem_u32(&c->full[s]);
-                mbar_arrive_expect_tx(bar, bytes);
-                if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0 && s == 0))
-                    tma_load_3d(ring + uint32_t(s) * stage_bytes, &mapW, bar, kb * kKB, (t.ct * PAIR + half) * 128, t.e);
-            };
-            auto copy_x = [&](int kb, int s) {
-                const uint32_t bar = smem_u32(&c->full[s]), dst = ring + uint32_t(s) * stage_bytes + kWBytes;
-                for (int b = 0; b < n_box; ++b) {
-                    tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, mb + b * p.box);
-                    tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, mb + b * p.box);
-                }
-            };
-            int kb = kb0;
-            if (!waited) {
-                // the weights of the first stages do not wait for the token pass
-                const int n = min(p.stages, kb1 - kb0);
-                if (elect_one())
-                    for (int i = 0; i < n; ++i) copy_w(kb0 + i, i);
-                __syncwarp();
-                grid_dependency_wait();
-                waited = true;
-                if (elect_one())
-                    for (int i = 0; i < n; ++i) copy_x(kb0 + i, i);
-                __syncwarp();
-                for (int i = 0; i < n; ++i) st.next(p.stages);
-                kb += n;
-                issued = n;
-            }
-            for (; kb < kb1; ++kb) {
-                if (!warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b)) {
-                    ok = false;
-                    break;
-                }
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
+                if (!ok) break;
                 if (elect_one()) {
-                    copy_w(kb, st.at);
-                    copy_x(kb, st.at);
+                    const uint32_t bar = smem_u32(&c->full[st.at]);
+                    mbar_arrive_expect_tx(bar, kWBytes);
+                    if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0))
+                        tma_load_3d(ring + uint32_t(st.at) * stage_bytes, &mapW, bar, kb * kKB, (t.ct * PAIR + half) * 128, t.e);
                 }
                 __syncwarp();
                 st.next(p.stages);
                 if (issued < p.stages) ++issued;
             }
         }
-        if (!waited) grid_dependency_wait();
-        if (!ok || aborted(c)) {
-            // the copies in flight land before the CTA leaves
-            if (lane == 0)
-                for (int i = 0; i < issued; ++i) {
-                    st.back(p.stages);
-                    drain_wait(smem_u32(&c->full[st.at]), st.parity);
-                }
-        }
+        grid_dependency_wait();
+        if (!ok || aborted(c)) drain_stages(st, issued, 1, lane, p.stages, c);
         __syncwarp();
     } else if (warp == 1) {
         // ======================= MMAs (the even CTA of a pair) =======================
@@ -426,6 +410,9 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             const uint32_t d = tmem + uint32_t(buf) * d_stride + (uint32_t(q * 32) << 16);
             const int per = split_columns(t.rows, p.splits);
             uint8_t *tile = out_tile + q * kOutTile;
+            int owner = 0, col = 0;                              // split: where the next columns go
+            uint32_t to = p.splits > 1 ? map_to_cta(smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4)), 0u) : 0u;
+            ws_split = ws;
             for (int c0 = 0; c0 < t.rows; c0 += 32) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(d + uint32_t(c0), r);
@@ -435,11 +422,14 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         if (c0 + j < t.rows) {
-                            const int owner = (c0 + j) / per, col = c0 + j - owner * per;
-                            float *to = recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4) + col;
-                            st_cluster_v4(map_to_cta(smem_u32(to), uint32_t(owner)),
+                            if (col == per) {
+                                col = 0;
+                                to = map_to_cta(smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4)), uint32_t(++owner));
+                            }
+                            st_cluster_v4(to + uint32_t(col) * 4u,
                                           make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
                                                       __uint_as_float(r[j + 3])));
+                            col += 4;
                         }
                     continue;
                 }
@@ -482,7 +472,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             acc.next(p.bufs);
             xb.next(2);
         }
-    } else if (warp < kGatherWarp0) {
+    } else if (warp < kRowsWarp0) {
         // ======================= weights to FP16 =======================
         const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
         const int row = q * 32 + lane;                           // weight row = tensor memory lane
@@ -542,43 +532,75 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         grid_dependency_wait();
         __syncwarp();
     } else {
-        // ======================= routed rows =======================
-        // Four rows at a time, fours v, v + 4, .. of this CTA's B tile by warp v; lane
-        // l knows the token of row l % 4 of the warp's four l / 4.  (The bytes are
-        // armed with the weights'.)
-        const int v = warp - kGatherWarp0;
+        // ======================= rows =======================
+        const int v = warp - kRowsWarp0, n_kb = kb1 - kb0;
         Turn st;
+        int issued = 0;
         bool ok = true;
         grid_dependency_wait();                                  // the tokens
-        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
-            const Tile t = w.tile(p.nt, off, pref);
-            const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
-            const int row = (lane >> 2) * 16 + v * 4 + (lane & 3);
-            const int32_t m = t.m0 + half * n_half + row;
-            int32_t token = row < n_half && m < t.end ? p.b.rows[m] : 0;
-            if (token < 0 || token >= p.b.T) token = 0;          // (reported where it is scaled)
-            int32_t id[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) id[i] = __shfl_sync(0xffffffffu, token, i);
-            const int fours = n_half / 16;                       // (n_half is a multiple of 16)
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
-                if (!ok) break;
-                if (elect_one()) {
-                    const uint32_t bar = smem_u32(&c->full[st.at]);
-                    const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(v) * 512u;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < fours) {
-                            tma_gather4(dst + uint32_t(i) * 2048u, &mapX, bar, kb * kKB, id[4 * i], id[4 * i + 1], id[4 * i + 2],
-                                        id[4 * i + 3]);
-                            tma_gather4(dst + x_rows * 128u + uint32_t(i) * 2048u, &mapX, bar, kb * kKB + 64, id[4 * i],
-                                        id[4 * i + 1], id[4 * i + 2], id[4 * i + 3]);
+        if (p.b.rows == nullptr) {
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
+                const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
+                const int n_box = (n_half + p.box - 1) / p.box;
+                const int32_t mb = t.m0 + half * n_half;
+                const uint32_t bytes = 256u * uint32_t(n_box * p.box);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t bar = smem_u32(&c->full[st.at]), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
+                        mbar_arrive_expect_tx(bar, bytes);
+                        for (int b = 0; b < n_box; ++b) {
+                            tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, mb + b * p.box);
+                            tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, mb + b * p.box);
                         }
+                    }
+                    __syncwarp();
+                    st.next(p.stages);
+                    if (issued < p.stages) ++issued;
+                }
+            }
+            if (!ok || aborted(c)) drain_stages(st, issued, 1, lane, p.stages, c);
+        } else {
+            // warps 0, 1 and 2, 3 gather alternate stages, each every other four rows
+            const int group = v >> 1, side = v & 1;
+            int32_t *mine = row_ids + v * (kRowsPerCta / 2);     // tokens of this warp's rows
+            const uint32_t ids = smem_u32(mine);
+            if (group) st.next(p.stages);
+            int kb = group;
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
+                const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
+                __syncwarp();
+                for (int i = lane; i < n_half / 2; i += 32) {
+                    const int32_t m = t.m0 + half * n_half + (i >> 2) * 8 + side * 4 + (i & 3);
+                    const int32_t id = m < t.end ? p.b.rows[m] : 0;
+                    mine[i] = id >= 0 && id < p.b.T ? id : 0;    // (reported where it is scaled)
                 }
                 __syncwarp();
-                st.next(p.stages);
+                for (; kb < n_kb; kb += 2) {
+                    ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t bar = smem_u32(&c->full[st.at]);
+                        const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(side) * 512u;
+                        const int32_t k = (kb0 + kb) * kKB;
+                        mbar_arrive_expect_tx(bar, uint32_t(n_half) * 128u);
+#pragma unroll 4
+                        for (int i = 0; i < n_half / 2; i += 4) {
+                            const int4 id = lds_i4(ids + uint32_t(i) * 4u);
+                            tma_gather4(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
+                            tma_gather4(dst + x_rows * 128u + uint32_t(i) * 256u, &mapX, bar, k + 64, id.x, id.y, id.z, id.w);
+                        }
+                    }
+                    __syncwarp();
+                    st.next(p.stages), st.next(p.stages);
+                    if (issued < p.stages) ++issued;
+                }
+                kb -= n_kb;
             }
+            if (!ok || aborted(c)) drain_stages(st, issued, 2, lane, p.stages, c);
         }
         __syncwarp();
     }
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             const Tile t = w.tile(p.nt, off, pref);
             const int per = split_columns(t.rows, p.splits);
             const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
-            const float ws = n < p.b.N ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
+            const float ws = ws_split;
             const int m0 = rank * per;
             for (int j = 0; j < per && m0 + j < t.rows; j += 4) {
                 float4 sum = *reinterpret_cast<const float4 *>(recv + size_t(row) * (per + 4) + j);
@@ -673,7 +695,8 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaPara
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
     return 1024 + size_t(stages) * (kWBytes + size_t(nt / pair) * 256) +
-           (splits > 1 ? split_bytes(nt, splits) : 0) + 4 * kOutTile + sizeof(Ctrl) + size_t(2 * nt) * 4 + size_t(2 * (E + 1)) * 4;
+           (splits > 1 ? split_bytes(nt, splits) : 0) + 4 * kOutTile + sizeof(Ctrl) + size_t(2 * nt) * 4 +
+           size_t(kGatherWarps * kRowsPerCta / 2) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
 int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream)
@@ -681,6 +704,7 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
     I8MmaParams p = p0;
     p.n_ct = (p.b.N + 128 * pair - 1) / (128 * pair);
     p.n_kb = (p.b.K + kKB - 1) / kKB;
+    p.div_nt = uint32_t((uint64_t(1) << 32) / uint32_t(p.nt / 16) + ((uint64_t(1) << 32) % uint32_t(p.nt / 16) != 0));
     p.box = p.nt / pair % 32 == 0 ? 32 : 16;
     CUtensorMap mw, mx;
     const uint64_t dw[3] = {uint64_t(p.b.K), uint64_t(p.b.N), uint64_t(p.b.E)};
