@@ -248,48 +248,73 @@ int stages_for(int pair, int nt, int splits, int E)
     return s;
 }
 
-// Shape of the tensor-core path: a rule on the rows that an expert is expected to
-// have.
-//  - Long: pairs of CTAs, 256 channels x 192 rows with two accumulators (16384 x
-//    4096 -> 4096: 305 us; 256 rows with one accumulator, stored between tiles:
-//    355 us), but 256 rows where they are gathered, whose copies weigh more per
-//    row (8192 tokens through 4 of 32 experts 6144 -> 4096: 1014 against 1083 us).
-//  - Else single CTAs, 128 channels x the next power of two from 32 (16 rows and
-//    more tiles: 158 against 139 us for 64 tokens through 4 of 32 experts): of
-//    the rows there are, or of four times the average where experts share them.
-//  - Few tiles: clusters of up to 8 CTAs divide the reduction while all of them
-//    run at once and each keeps two stages (33 x 4096 -> 5120: 12.5 us, 16.5
-//    undivided).
+// Which kernels: by the rows M and the weights that they meet.
+//  - Up to 4 rows, or up to 8 that meet mostly experts of their own over more than
+//    16 MB: integer dot products (4 x 4096 -> 4096: 8.7 us, 9.2 from warps'
+//    registers, 9.4 on the tensor cores; 8 rows in 32 experts 6144 -> 4096: 30, 52,
+//    43 us).
+//  - Up to 16 rows over at most 16 MB, up to 32 over 4 MB: warps' registers, which
+//    start at once (16 x 2048 -> 4096: 6.8 us, 8.6 on the tensor cores; 24 x 1024 ->
+//    1024: 4.7, 7.2; but 16 x 8192 -> 4096: 20.5, 12.1).
+//  - Else the tensor cores.
+int choose_path(const cake_gg_i8_plan_t &pl)
+{
+    const int64_t M = pl.M_max, weights = (M < pl.E ? M : pl.E) * int64_t(pl.N) * pl.K;
+    if (M <= 4 || (M <= 8 && weights > (16 << 20) && i8_run_rows(pl.E, M, pl.T) <= 2)) return CAKE_GG_I8_ROWS;
+    if ((M <= 16 && weights <= (16 << 20)) || (M <= 32 && weights <= (4 << 20))) return CAKE_GG_I8_WARPS;
+    return CAKE_GG_I8_MMA;
+}
+
+// Row tiles of nt rows that the call will have: exact for one expert; where E
+// share the rows, whole tiles and half a tile more for each expert that can have
+// rows, at least one each (the sizes are the device's).
+int64_t row_tiles(const cake_gg_i8_plan_t &pl, int nt)
+{
+    const int64_t whole = (pl.M_max + nt - 1) / nt;
+    if (pl.E == 1) return whole;
+    const int64_t busy = pl.M_max < pl.E ? pl.M_max : pl.E;
+    return whole + busy / 2 > busy ? whole + busy / 2 : busy;
+}
+
+// Shape of the tensor-core path, from a model of its time in nanoseconds: waves
+// of units over the multiprocessors (152, or 76 pairs), the stages of a unit,
+// the storing of the last one, and the exchange between the CTAs that share a
+// tile.  The times of a stage were measured with all multiprocessors at work
+// (12288 x 4096 -> 4096): pairs 323, 358, 368, 432, 473 ns for 64, 96, 128, 160,
+// 192 rows, single CTAs 314, 348, 382, 451 ns for 32, 64, 96, 128.  (Pairs of 256
+// rows hold one accumulator, whose storing nothing overlaps: 774 ns.)  What it
+// decides, measured with the neighbours: 3001 x 5120 -> 1000 takes 160 rows (38.6
+// us; 39.8 with 192, 48.5 with 128), 701 tokens through 2 of 8 experts 4096 ->
+// 2048 take 96 (31.5; 32.7 with 128, 35.4 with 192), 200 x 4096 -> 4096 take 64
+// (16.6; 20.5 with 192), 33 x 4096 -> 5120 divide the reduction by 3 (11.3; 14.6
+// undivided).
 void choose_mma(cake_gg_i8_plan_t *pl)
 {
-    const int64_t busy = pl->M_max < pl->E ? pl->M_max : pl->E;
-    const int64_t est = pl->E == 1 ? pl->M_max : 4 * ((pl->M_max + busy - 1) / (busy > 0 ? busy : 1));
-    const bool routed = pl->E > 1 && pl->T != pl->M_max;   // (rows need not be given where T = M)
-    pl->path = CAKE_GG_I8_MMA;
-    pl->pair = 1;
-    pl->tile_rows = est <= 32 ? 32 : est <= 64 ? 64 : 128;
-    pl->acc_bufs = 2;
-    pl->splits = 1;
-    if (est > 512 || (pl->E == 1 && est > 256)) {
-        pl->pair = 2;
-        pl->tile_rows = 192;
-    }
+    constexpr int kSms = 152;
+    const int64_t n_kb = (pl->K + 127) / 128;
+    int64_t best = -1;
+    auto consider = [&](int pair, int nt, int splits) {
+        const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
+        if (splits > 1 && (units * splits > kSms || n_kb < 2 * splits)) return;
+        const int64_t waves = (units * pair + kSms - 1) / kSms;
+        const int64_t stage = pair == 2 ? 250 + nt * 7 / 6 : 280 + nt * 11 / 10;
+        const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage + 16 * nt + (splits > 1 ? 1100 * splits : 0);
+        if (best < 0 || ns < best) {
+            best = ns;
+            pl->pair = pair;
+            pl->tile_rows = nt;
+            pl->splits = splits;
+        }
+    };
+    for (int nt = 192; nt >= 64; nt -= 32) consider(2, nt, 1);
+    for (int nt = 128; nt >= 32; nt -= 32)
+        for (int s = 1; s <= (nt <= 64 ? 8 : 1); ++s) consider(1, nt, s);
     pl->pair = env_int("CAKE_GG_I8_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_I8_ROWS_PER_TILE", pl->tile_rows);
     if (nt >= 16 && nt <= 256 && nt % 16 == 0) pl->tile_rows = nt;
-    pl->acc_bufs = env_int("CAKE_GG_I8_BUFS", pl->tile_rows > 192 ? 1 : pl->acc_bufs) == 1 ? 1 : 2;
-    const int64_t tiles = (pl->E == 1 ? (pl->M_max + pl->tile_rows - 1) / pl->tile_rows : pl->M_max / pl->tile_rows + busy) *
-                          ((pl->N + 127) / 128);
-    if (pl->pair == 1 && pl->tile_rows <= 64) {
-        const int n_kb = (pl->K + 127) / 128;
-        for (int s = 8; s > 1; --s)
-            if (tiles * s <= 152 && n_kb >= 2 * s) {
-                pl->splits = s;
-                break;
-            }
-    }
     const int sp = env_int("CAKE_GG_I8_SPLITS", pl->splits);
-    if (sp >= 1 && sp <= 8 && pl->pair == 1) pl->splits = sp;
+    pl->splits = sp >= 1 && sp <= 8 && pl->pair == 1 ? sp : 1;
+    pl->acc_bufs = env_int("CAKE_GG_I8_BUFS", pl->tile_rows > 192 ? 1 : 2) == 1 ? 1 : 2;
     pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
     pl->slots = slots_for(pl->tile_rows, pl->acc_bufs);
     if (pl->slots > pl->stages) pl->slots = pl->stages;
@@ -330,20 +355,13 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
     plan->act = act;
     plan->out_dtype = out_dtype;
     plan->max_sms = max_sms;
-    // Up to 8 rows: integer dot products.  Up to 16 over at most 32 MB of weights:
-    // products from warps' registers, whose start costs less (16 x 4096 -> 5120:
-    // 10.6 against 15.6 us; x 8192 -> 8192: 24.5 against 27.6; 33 x 4096 -> 5120: 28
-    // against 12.5).  Else the tensor cores.
-    const int64_t weights = (M_max < E ? M_max : E) * int64_t(N) * K;
-    const int path = env_int("CAKE_GG_I8_PATH", M_max <= kI8FewRows ? CAKE_GG_I8_ROWS
-                                                : M_max <= 16 && weights <= (32 << 20) ? CAKE_GG_I8_WARPS
-                                                                                       : CAKE_GG_I8_MMA);
+    const int path = env_int("CAKE_GG_I8_PATH", choose_path(*plan));
     plan->path = path;
     if (path == CAKE_GG_I8_MMA) {
         choose_mma(plan);
         if (!mma_plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
     }
-    if (path == CAKE_GG_I8_WARPS) plan->tile_rows = env_int("CAKE_GG_I8_ROWS_PER_TILE", M_max <= 16 ? 16 : M_max <= 32 ? 32 : M_max <= 48 ? 48 : 64);
+    if (path == CAKE_GG_I8_WARPS) plan->tile_rows = env_int("CAKE_GG_I8_ROWS_PER_TILE", M_max <= 16 ? 16 : 32);
     plan->timeout_ns = kTimeoutNs;
     plan->workspace_bytes = layout(*plan).total;
     return CAKE_GG_OK;
@@ -374,7 +392,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     const bool warps = pl.path == CAKE_GG_I8_WARPS;
     if (pl.max_sms < 0 || (pl.path != CAKE_GG_I8_ROWS && !warps && pl.path != CAKE_GG_I8_MMA) ||
         (pl.path == CAKE_GG_I8_MMA && !mma_plan_ok(pl)) ||
-        (warps && (pl.tile_rows < 16 || pl.tile_rows > 64 || pl.tile_rows % 16 != 0)))
+        (warps && (pl.tile_rows != 16 && pl.tile_rows != 32)))
         return CAKE_GG_ERR_INVALID_ARG;
     const bool ready = pl.x_dtype == CAKE_GG_INT8;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))

@@ -63,17 +63,16 @@ size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E);
 // Tensor-core path: q [T, K] as FP16 integers.  Returns a cake_gg_status_t.
 int launch_i8_mma(const I8MmaParams &p, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream);
 
-constexpr int kI8FewRows = 8;   // rows of a call that the few-row path takes
-
 // Few-row path: 32-bit integer dot products, weights streamed once per run of
 // an expert's rows.  X: the quantised tokens [T, K] (x_dtype CAKE_GG_INT8), or
 // activations where i8_rows_fused() says that the blocks quantise their rows
 // themselves.
 bool i8_rows_fused(const I8Params &p);
+int i8_run_rows(int32_t E, int64_t M, int64_t T);   // rows of a run: 1, 2 or 4
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream);
 
-// A few dozen rows: warp-level products from registers, runs of 16, 32, 48 or 64
-// of an expert's rows; q [T, K].
+// A few dozen rows: warp-level products from registers, runs of 16 or 32 of an
+// expert's rows; q [T, K].
 cudaError_t launch_i8_warps(const I8Params &p, const int8_t *q, int rows, bool pdl, cudaStream_t stream);
 
 }  // namespace cakegg

@@ -236,30 +236,30 @@ cudaError_t launch(const I8Params &p, const void *X, bool pdl, cudaStream_t stre
     return cudaLaunchKernelEx(&cfg, i8_rows_kernel<R, XT, ACT>, p, static_cast<const XT *>(X), blocks_n, S);
 }
 
-// Rows of an expert that a block takes: all that there can be where rows are
-// dense.  Where few rows meet many experts nearly every expert has one row (and
-// a token never meets an expert twice), and the kernels for fewer rows hold
-// more loads in flight; a second row of an expert is another block.
-int run_rows(const I8Params &p)
-{
-    const int64_t most = p.rows && p.E > 1 && p.T < p.M ? p.T : p.M;
-    if (most <= 1 || (p.E > 1 && p.E >= 4 * p.M)) return 1;
-    if (most <= 2 || (p.E > 1 && p.E >= p.M)) return 2;
-    return most <= 4 ? 4 : 8;
-}
-
 template <typename XT, bool ACT>
 cudaError_t launch_fused(const I8Params &p, const void *X, bool pdl, cudaStream_t stream)
 {
-    return run_rows(p) == 1 ? launch<1, XT, ACT>(p, X, pdl, stream) : launch<2, XT, ACT>(p, X, pdl, stream);
+    return i8_run_rows(p.E, p.M, p.T) == 1 ? launch<1, XT, ACT>(p, X, pdl, stream) : launch<2, XT, ACT>(p, X, pdl, stream);
 }
 
 }  // namespace
 
+// Rows of an expert that a block takes: all that there can be where rows are
+// dense.  Where few rows meet many experts nearly every expert has one row (and
+// a token never meets an expert twice), and the kernels for fewer rows hold
+// more loads in flight; a second row of an expert is another block.
+int i8_run_rows(int32_t E, int64_t M, int64_t T)
+{
+    const int64_t most = E > 1 && T < M ? T : M;
+    if (most <= 1 || (E > 1 && E >= 4 * M)) return 1;
+    return most <= 2 || (E > 1 && E >= M) ? 2 : 4;
+}
+
 bool i8_rows_fused(const I8Params &p)
 {
-    const int64_t bytes = int64_t(p.M < p.E ? p.M : p.E) * p.N * p.K;
-    return bytes <= kFusedWeights && run_rows(p) <= 2 && int64_t(run_rows(p)) * p.K <= kFusedBytes;
+    const int64_t bytes = (p.M < p.E ? p.M : p.E) * p.N * p.K;
+    const int run = i8_run_rows(p.E, p.M, p.T);
+    return bytes <= kFusedWeights && run <= 2 && int64_t(run) * p.K <= kFusedBytes;
 }
 
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream)
@@ -269,11 +269,10 @@ cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int ac
         return silu ? launch_fused<uint16_t, true>(p, X, pdl, stream) : launch_fused<uint16_t, false>(p, X, pdl, stream);
     if (x_dtype == CAKE_GG_FP32)
         return silu ? launch_fused<float, true>(p, X, pdl, stream) : launch_fused<float, false>(p, X, pdl, stream);
-    switch (run_rows(p)) {
+    switch (i8_run_rows(p.E, p.M, p.T)) {
     case 1: return launch<1, int8_t, false>(p, X, pdl, stream);
     case 2: return launch<2, int8_t, false>(p, X, pdl, stream);
-    case 4: return launch<4, int8_t, false>(p, X, pdl, stream);
-    default: return launch<8, int8_t, false>(p, X, pdl, stream);
+    default: return launch<4, int8_t, false>(p, X, pdl, stream);
     }
 }
 

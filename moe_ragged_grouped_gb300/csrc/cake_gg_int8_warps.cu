@@ -187,16 +187,7 @@ cudaError_t launch(const I8Params &p, const int8_t *q, bool pdl, cudaStream_t st
 {
     auto kern = i8_warps_kernel<NT>;
     constexpr size_t smem = size_t(kWarps) * 8 * NT * kPad * sizeof(float);
-    static bool raised[64] = {};   // the opt-in limit is raised once per device
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (smem > 48 * 1024 && !raised[dev]) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (err != cudaSuccess) return err;
-        raised[dev] = true;
-    }
+    static_assert(smem <= 48 * 1024, "no opt-in needed");
     const int blocks_n = (p.N + kChannels - 1) / kChannels;
     const int64_t blocks = p.M * blocks_n;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
@@ -219,13 +210,7 @@ cudaError_t launch(const I8Params &p, const int8_t *q, bool pdl, cudaStream_t st
 
 cudaError_t launch_i8_warps(const I8Params &p, const int8_t *q, int rows, bool pdl, cudaStream_t stream)
 {
-    switch (rows) {
-    case 16: return launch<2>(p, q, pdl, stream);
-    case 32: return launch<4>(p, q, pdl, stream);
-    case 48: return launch<6>(p, q, pdl, stream);
-    case 64: return launch<8>(p, q, pdl, stream);
-    default: return cudaErrorInvalidValue;
-    }
+    return rows == 16 ? launch<2>(p, q, pdl, stream) : launch<4>(p, q, pdl, stream);
 }
 
 }  // namespace cakegg

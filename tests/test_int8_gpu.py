@@ -331,7 +331,6 @@ def test_a_wait_that_runs_out_is_reported():
 
 @pytest.mark.parametrize("env", [
     dict(PATH="0"), dict(PATH="2", ROWS_PER_TILE="16"), dict(PATH="2", ROWS_PER_TILE="32"),
-    dict(PATH="2", ROWS_PER_TILE="48"), dict(PATH="2", ROWS_PER_TILE="64"),
     dict(PAIR="1", ROWS_PER_TILE="16", SPLITS="1"), dict(PAIR="1", ROWS_PER_TILE="32", SPLITS="3"),
     dict(PAIR="1", ROWS_PER_TILE="64", SPLITS="8"), dict(PAIR="1", ROWS_PER_TILE="128", SPLITS="1"),
     dict(PAIR="2", ROWS_PER_TILE="64", SPLITS="1"),
