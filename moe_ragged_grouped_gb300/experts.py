@@ -1,0 +1,114 @@
+"""A mixture-of-experts layer in serving, with 8-bit weights and tokens.
+
+    layer = Int8Experts(router, gate_up, down, top_k)
+    y = layer(x)                               # x [T, K] bf16 -> y [T, K] bf16
+
+Each token goes through the top_k experts of its router logits and their
+outputs are added with softmax weights over those:
+
+    p = softmax of the top_k of  x router^T
+    y[t] = sum_j p[t, j] * down[e_j] (silu(g) * u),   [g | u] = gate_up[e_j] x[t]
+
+The layer chains the library's calls as a server does: the FP32 router GEMM,
+the grouped 8-bit product over rows routed by index (tokens quantised once,
+gathered by expert), and the second grouped product, whose rows are gated and
+quantised on the way.  Weights are quantised per output channel when the layer
+is made.  Plans, workspaces and the products' outputs are kept per token count,
+device and stream and reused, as the workspace contract allows; y is a new
+tensor each call.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import cake_gg as gg
+
+
+class Int8Experts:
+    """Quantised experts: router [E, K] fp32, gate_up [E, 2 F, K] and down [E, K, F] bf16 or fp32 (CUDA)."""
+
+    def __init__(self, router, gate_up, down, top_k):
+        E, F2, K = gate_up.shape
+        F = F2 // 2
+        if tuple(router.shape) != (E, K) or tuple(down.shape) != (E, K, F) or F2 % 2:
+            raise ValueError("shapes: router [E, K], gate_up [E, 2 F, K], down [E, K, F]")
+        if not 1 <= top_k <= E:
+            raise ValueError("top_k is 1 .. E")
+        self.E, self.K, self.F, self.top_k = E, K, F, top_k
+        self.router = router.float().contiguous()
+        self.up_q, self.up_s = self._quantise(gate_up)
+        self.down_q, self.down_s = self._quantise(down)
+        self._kept = {}
+
+    @staticmethod
+    def _quantise(w):
+        E, N, K = w.shape
+        q, s = gg.quantize_rows(w.reshape(E * N, K).contiguous())
+        return q.view(E, N, K), s.view(E, N)
+
+    def _for(self, T, device):
+        """What a call of T tokens reuses: plans, workspaces, and the two products' outputs."""
+        key = (T, str(device), torch.cuda.current_stream(device).cuda_stream)
+        kept = self._kept.get(key)
+        if kept is None:
+            M = T * self.top_k
+            route = gg.cake_gg_router_plan(T, self.E, self.K)
+            up = gg.cake_gg_i8_plan(self.E, M, T, 2 * self.F, self.K, "bf16", None, "bf16")
+            down = gg.cake_gg_i8_plan(self.E, M, M, self.K, self.F, "bf16", "silu_mul", "fp32")
+            kept = (
+                (route, gg.make_workspace(route, device)),
+                (up, gg.make_workspace(up, device), torch.empty((M, 2 * self.F), dtype=torch.bfloat16, device=device)),
+                (down, gg.make_workspace(down, device), torch.empty((M, self.K), dtype=torch.float32, device=device)),
+            )
+            self._kept[key] = kept
+        return kept
+
+    def route(self, x):
+        """Experts [T, top_k] and weights [T, top_k] of each token."""
+        plan, work = self._for(x.shape[0], x.device)[0]
+        logits = gg.router_gemm(x.float(), self.router, plan=plan, workspace=work, check=False)
+        top, expert = torch.topk(logits, self.top_k, dim=1)
+        return expert, torch.softmax(top, dim=1)
+
+    def __call__(self, x, check=False):
+        T = x.shape[0]
+        if T == 0:
+            return torch.empty_like(x)
+        _, (up, up_work, h), (down, down_work, out) = self._for(T, x.device)
+        expert, weight = self.route(x)
+        # rows in expert order, the token of each, and where each token's rows went
+        flat = expert.reshape(-1)
+        order = torch.argsort(flat, stable=True)
+        rows = torch.div(order, self.top_k, rounding_mode="floor").to(torch.int32)
+        counts = (flat[:, None] == torch.arange(self.E, device=x.device)).sum(dim=0)
+        offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+        gg.int8_gemm(x, self.up_q, self.up_s, offsets=offsets, rows=rows, out=h, plan=up, workspace=up_work, check=check)
+        gg.int8_gemm(h, self.down_q, self.down_s, offsets=offsets, act="silu_mul", out_dtype="fp32", out=out, plan=down,
+                     workspace=down_work, check=check)
+        at = torch.empty_like(order)
+        at[order] = torch.arange(order.numel(), device=x.device)
+        return (out[at].view(T, self.top_k, self.K) * weight[:, :, None]).sum(dim=1).to(x.dtype)
+
+
+def main():
+    """Run a small layer on the GPU and compare it with the same layer in FP32 on the quantised weights."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    E, K, F, top_k = 8, 1024, 512, 2
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    layer = Int8Experts(rand(E, K) / K ** 0.5, rand(E, 2 * F, K) / K ** 0.5, rand(E, K, F) / F ** 0.5, top_k)
+    for T in (1, 16, 700):
+        x = rand(T, K).to(torch.bfloat16)
+        y = layer(x, check=True)
+        expert, weight = layer.route(x)
+        up, down = layer.up_q.float() * layer.up_s[..., None], layer.down_q.float() * layer.down_s[..., None]
+        want = torch.zeros(T, K, device="cuda")
+        for e in range(E):
+            t, j = (expert == e).nonzero(as_tuple=True)
+            gate, lin = (x[t].float() @ up[e].T).chunk(2, dim=1)
+            want[t] += weight[t, j, None] * ((torch.nn.functional.silu(gate) * lin) @ down[e].T)
+        err = float((y.float() - want).norm() / want.norm())
+        print(f"{T} tokens: relative difference from the unquantised activations {err:.4f}")
+
+
+if __name__ == "__main__":
+    main()
