@@ -94,6 +94,7 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
 // stay in registers between the maximum and the rounding; longer rows read the
 // rest again (from L2).
 constexpr int kHeld = 2;
+constexpr int64_t kFewBlocks = 304;   // two rows a multiprocessor
 
 template <typename XT, bool ACT, typename QT>
 __global__ void __launch_bounds__(1024)
@@ -181,7 +182,9 @@ template <typename XT, typename QT>
 cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q, float *S, cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
-    int threads = int(align_up((uint64_t(K) / 8 + kHeld - 1) / kHeld, 32));
+    // one vector a thread where rows are few and their latency counts, else kHeld
+    const int held = T <= kFewBlocks ? 1 : kHeld;
+    int threads = int(align_up((uint64_t(K) / 8 + held - 1) / held, 32));
     if (threads > 1024) threads = 1024;
     const cudaLaunchConfig_t cfg = pass_config(T, threads, &attr, stream);
     const XT *x = static_cast<const XT *>(X);

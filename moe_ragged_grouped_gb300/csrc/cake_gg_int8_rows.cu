@@ -152,6 +152,12 @@ __global__ void __launch_bounds__(kThreads)
     };
     const int first = ks * 32 + lane;
     load(first);
+    // while the token pass still runs the rest of the block's weights move to L2
+    // (down one token, 4 x 2048 -> 6144: 11.2 us, 12.3 without)
+    if (p.early && live && lane % 8 == 0)
+        for (int v = first + kU * step; v < nv; v += step)
+#pragma unroll
+            for (int c = 0; c < kC; ++c) prefetch_l2(w + int64_t(c) * p.K + int64_t(v) * 16);
 
     // the tokens are complete once the grid before this one is
     grid_dependency_wait();
