@@ -310,13 +310,19 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
 
     if (warp == 0) {
         // ======================= weight copies =======================
-        // (these do not wait for the token pass)
+        // The first ring of them does not wait for the token pass.  (Every role waits
+        // for the pass before its first wait with a limit, so that the limit does
+        // not count the pass.)
         Turn st;
         int issued = 0;       // stages filled, up to the ring's depth
-        bool ok = true;
+        bool ok = true, passed = false;
         for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
             const Tile t = w.tile(p.nt, off, pref);
             for (int kb = kb0; kb < kb1; ++kb) {
+                if (issued == p.stages && !passed) {
+                    grid_dependency_wait();
+                    passed = true;
+                }
                 ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
                 if (!ok) break;
                 if (elect_one()) {
@@ -335,6 +341,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ======================= MMAs (the even CTA of a pair) =======================
+        grid_dependency_wait();
         Turn st, sl, acc;
         bool ok = true, any = false;
         if (leader) {
@@ -381,7 +388,6 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                 drain_wait(smem_u32(&c->drain), 0);
             }
         }
-        grid_dependency_wait();
         __syncwarp();
     } else if (warp < kConvWarp0) {
         // ======================= scales and stores =======================
@@ -477,6 +483,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         const int q = warp & 3, group = (warp - kConvWarp0) >> 2;
         const int row = q * 32 + lane;                           // weight row = tensor memory lane
         const int n_kb = kb1 - kb0;
+        grid_dependency_wait();
         // A slot is free once the MMAs of the stage that last used it, `slots` before
         // this one, are done: that stage's `empty` says so (slots <= stages).
         Turn st, sl, last;
@@ -529,7 +536,6 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             it += 2;
             kb += 2;
         }
-        grid_dependency_wait();
         __syncwarp();
     } else {
         // ======================= rows =======================

@@ -194,6 +194,22 @@ def test_quantize_rows_that_hold_nothing_or_no_number(dtype):
     assert (y[5] == 127 * 32 * (s[5])).all()
 
 
+@pytest.mark.parametrize("T", [3, 14, 90, 700])
+def test_rows_without_numbers_stay_by_themselves(T):
+    """A row that holds a NaN or an infinity gives NaN; its neighbours in the tile are as without it."""
+    import torch
+    rng = np.random.default_rng(T)
+    N, K = 136, 400
+    W, ws = _ints((N, K), rng), _scales(N, rng)
+    x = _rows_of(T, K, torch.bfloat16, T)
+    clean = gg.int8_gemm(x, W, ws)
+    x[0, 7], x[T // 2, 0] = float("nan"), float("inf")
+    got = gg.int8_gemm(x, W, ws)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[0] = keep[T // 2] = False
+    assert torch.isnan(got[~keep]).all() and torch.equal(got[keep], clean[keep])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("act", [None, "silu_mul"])
 @pytest.mark.parametrize("sizes,T,N,K", [([1], 1, 264, 1024), ([2, 0, 5], 7, 72, 112), ([40, 0, 90, 3], 50, 136, 528),
