@@ -472,6 +472,8 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     Quantising W.reshape(E * N, K) gives int8_gemm's weights.
     """
     import torch
+    if act not in I8_ACTS:
+        raise ValueError(f"act is None or 'silu_mul', got {act!r}")
     name = _i8_x_name(X)
     if X.dim() != 2 or (act is not None and X.shape[1] % 2 != 0):
         raise ValueError("X is [T, K], or [T, 2 K] with an activation")
@@ -504,6 +506,8 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     workspace are allocated through torch when not given.
     """
     import torch
+    if act not in I8_ACTS:
+        raise ValueError(f"act is None or 'silu_mul', got {act!r}")
     name = _i8_x_name(X)
     x_shape, w_shape = X.shape, W.shape
     if len(w_shape) not in (2, 3) or len(x_shape) != 2:
@@ -528,7 +532,7 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         _need(rows, "rows", torch.int32, (M,), device)
     if plan is None:
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
-    elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], _act_code(act), _dtype_code(out_dtype)):
+    elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], I8_ACTS[act], _dtype_code(out_dtype)):
         raise ValueError("the plan is another problem's")
     if out is None:
         out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=device)
@@ -536,9 +540,16 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         _need(out, "out", _torch_out_dtype(out_dtype), (M, N), device)
     if workspace is None:
         workspace = make_workspace(plan, device)
-    if stream is None and device.type == "cuda":
-        stream = _current_stream(device.index)
-    rc = cake_gg_i8_gemm(plan, X, xs, rows, W, ws, out, offsets, workspace, stream=stream)
+    if stream is None:
+        stream = _current_stream(device.index) if device.type == "cuda" else 0
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    # (the call of cake_gg_i8_gemm() above, without its conversions: a short product's
+    # time is the host's)
+    rc = (_lib or load_library()).cake_gg_i8_gemm(
+        ctypes.byref(plan), X.data_ptr(), None if xs is None else xs.data_ptr(),
+        None if rows is None else rows.data_ptr(), W.data_ptr(), ws.data_ptr(), out.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes, stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_i8_gemm")
     if check:

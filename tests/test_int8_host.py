@@ -117,6 +117,7 @@ def test_helpers_refuse():
         (ValueError, (x, W, ws), dict(offsets=off[:2])),
         (ValueError, (x, W, ws), dict(offsets=off, act="silu_mul")),
         (ValueError, (x, W, ws), dict(offsets=off, xs=s)),
+        (ValueError, (x, W, ws), dict(offsets=off, act="gelu")),
         (ValueError, (q, W, ws), dict(offsets=off)),
         (ValueError, (q, W, ws), dict(offsets=off, xs=s[:3])),
         (ValueError, (x.T.contiguous().T, W, ws), dict(offsets=off)),
