@@ -66,6 +66,10 @@
  *     in k-blocks), CAKE_GG_STAGES, CAKE_GG_STAGING_BUFS (1 or 2),
  *     CAKE_GG_DECIDED=0 (the non-deterministic planner ignores its table of
  *     measured points where a plan rule failed the decision protocol);
+ *   read by cake_gg_i8_plan(), recorded in its plan (no result bit follows them
+ *   while a sum stays below 2^24):
+ *     CAKE_GG_I8_PATH (cake_gg_i8_path_t), CAKE_GG_I8_PAIR (1 or 2),
+ *     CAKE_GG_I8_ROWS_PER_TILE (32 .. 192), CAKE_GG_I8_SPLITS (1 .. 8);
  *   read by each compute call, changing no result:
  *     CAKE_GG_PDL=0 (no programmatic dependent launch), CAKE_GG_ROUTER_STAGGER
  *     (the router's per-unit k-order stagger, default 7, 0 = in order;
@@ -293,9 +297,10 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
  * a byte allowed.  Rows at or past offsets[E] of Y are never written, and an
  * expert without rows reads no weights.  Sums are exact 32-bit integers (few
  * rows) or FP32 sums of exact products (tensor cores: exact too while their
- * magnitude stays below 2^24); two FP32 multiplications follow, by ws and then
- * xs, and one rounding for BF16 output.  The same call gives the same bits on
- * every run and under every max_sms.
+ * magnitude stays below 2^24; bytes of 90 .. 127 without a sign, the worst there
+ * is, measured 2e-7 off at K = 4096, 4e-6 at 32768, 5e-5 at 131056); two FP32
+ * multiplications follow, by ws and then xs, and one rounding for BF16 output.
+ * The same call gives the same bits on every run and under every max_sms.
  *
  * X is q itself (x_dtype CAKE_GG_INT8, xs given), or BF16 / FP32 activations
  * (xs null) that the call quantises row by row first:
@@ -325,16 +330,18 @@ typedef struct cake_gg_i8_plan {
     int32_t x_dtype;         /* cake_gg_dtype_t: CAKE_GG_INT8, _BF16 or _FP32       */
     int32_t act;             /* cake_gg_act_t (CAKE_GG_ACT_NONE for int8 X)         */
     int32_t out_dtype;       /* CAKE_GG_BF16 or CAKE_GG_FP32                        */
-    int32_t max_sms;         /* cap on persistent CTAs; 0 = every SM of the device  */
+    int32_t max_sms;         /* cap on persistent CTAs (tensor cores, no splits);
+                                0 = every SM of the device                          */
     /* chosen by cake_gg_i8_plan() */
-    int32_t path;            /* cake_gg_i8_path_t; the rest is the tensor-core path's: */
+    int32_t path;            /* cake_gg_i8_path_t; what follows is the tensor-core
+                                path's                                              */
     int32_t pair;            /* 2: two CTAs compute 256 channels as one MMA, else 1 */
-    int32_t tile_rows;       /* rows of a tile at most (16 .. 256)                  */
-    int32_t acc_bufs;        /* accumulators in tensor memory (1 or 2)              */
+    int32_t tile_rows;       /* rows of a tile (of a block's run: warps) at most    */
     int32_t slots;           /* widened weight tiles in tensor memory               */
     int32_t stages;          /* shared-memory ring depth                            */
     int32_t splits;          /* CTAs of a cluster that share a tile's reduction     */
     int32_t debug_flags;     /* test-only fault injection; 0 in normal use          */
+    int32_t reserved;
     uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
     uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
 } cake_gg_i8_plan_t;

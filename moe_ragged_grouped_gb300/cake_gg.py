@@ -111,17 +111,17 @@ class CakeGGI8Plan(ctypes.Structure):
         ("path", ctypes.c_int32),
         ("pair", ctypes.c_int32),
         ("tile_rows", ctypes.c_int32),
-        ("acc_bufs", ctypes.c_int32),
         ("slots", ctypes.c_int32),
         ("stages", ctypes.c_int32),
         ("splits", ctypes.c_int32),
         ("debug_flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
         ("timeout_ns", ctypes.c_uint64),
         ("workspace_bytes", ctypes.c_uint64),
     ]
 
     def as_dict(self):
-        return {f[0]: getattr(self, f[0]) for f in self._fields_}
+        return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
 
 
 class CakeGGError(RuntimeError):

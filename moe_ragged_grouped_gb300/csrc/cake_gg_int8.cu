@@ -236,11 +236,11 @@ int env_int(const char *name, int dflt)
     return v && *v ? std::atoi(v) : dflt;
 }
 
-// Tensor memory (512 columns of a CTA) left beside the accumulators, in slots
+// Tensor memory (512 columns of a CTA) left beside the two accumulators, in slots
 // of 64 columns, and the ring depth that fits beside the rest of shared memory.
-int slots_for(int nt, int bufs)
+int slots_for(int nt)
 {
-    const int n = (512 - bufs * (nt < 32 ? 32 : nt)) / 64;
+    const int n = (512 - 2 * nt) / 64;
     return n > kSlotsMost ? kSlotsMost : n;
 }
 
@@ -314,24 +314,20 @@ void choose_mma(cake_gg_i8_plan_t *pl)
         for (int s = 1; s <= (nt <= 64 ? 8 : 1); ++s) consider(1, nt, s);
     pl->pair = env_int("CAKE_GG_I8_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_I8_ROWS_PER_TILE", pl->tile_rows);
-    if (nt >= 16 && nt <= 256 && nt % 16 == 0) pl->tile_rows = nt;
+    if (nt >= 32 && nt <= 192 && nt % 32 == 0) pl->tile_rows = nt;
     const int sp = env_int("CAKE_GG_I8_SPLITS", pl->splits);
     pl->splits = sp >= 1 && sp <= 8 && pl->pair == 1 ? sp : 1;
-    pl->acc_bufs = env_int("CAKE_GG_I8_BUFS", pl->tile_rows > 192 ? 1 : 2) == 1 ? 1 : 2;
     pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
-    pl->slots = slots_for(pl->tile_rows, pl->acc_bufs);
+    pl->slots = slots_for(pl->tile_rows);
     if (pl->slots > pl->stages) pl->slots = pl->stages;
 }
 
 // What the tensor-core kernel can run.
 bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
 {
-    const int per_cta = pl.pair == 2 ? pl.tile_rows / 2 : pl.tile_rows;
-    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 16 * pl.pair && pl.tile_rows <= 256 &&
-           pl.tile_rows % (16 * pl.pair) == 0 && per_cta <= 128 &&
-           (pl.tile_rows == 16 || pl.tile_rows % 32 == 0) && (pl.acc_bufs == 1 || pl.acc_bufs == 2) &&
-           pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
-           pl.slots <= pl.stages && pl.slots <= slots_for(pl.tile_rows, pl.acc_bufs) && pl.splits >= 1 && pl.splits <= 8 &&
+    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= (pl.pair == 2 ? 192 : 128) &&
+           pl.tile_rows % 32 == 0 && pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
+           pl.slots <= pl.stages && pl.slots <= slots_for(pl.tile_rows) && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) &&
            i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }
@@ -453,7 +449,6 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     m.nt = pl.tile_rows;
     m.stages = pl.stages;
     m.slots = pl.slots;
-    m.bufs = pl.acc_bufs;
     m.splits = pl.splits;
     m.debug_flags = pl.debug_flags;
     return launch_i8_mma(m, static_cast<const uint16_t *>(tokens), pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl, s);

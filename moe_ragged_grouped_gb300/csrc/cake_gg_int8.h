@@ -44,10 +44,9 @@ constexpr int32_t kI8StatusTimeout = CAKE_GG_ERR_TIMEOUT;
 // The tensor-core path's own numbers.
 struct I8MmaParams {
     I8Params b;
-    int32_t nt;               // rows of a tile at most
+    int32_t nt;               // rows of a tile at most (a multiple of 32)
     int32_t stages;           // shared-memory ring depth
     int32_t slots;            // widened weight tiles in tensor memory
-    int32_t bufs;             // accumulators (1 or 2)
     int32_t splits;           // CTAs that share a tile's reduction (one cluster; 1 = none)
     int32_t debug_flags;
     // (set by the launch) channel tiles, stages of a tile, rows of a copy, 2^32 / (nt / 16) rounded up

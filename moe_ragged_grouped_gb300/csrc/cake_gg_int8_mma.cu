@@ -144,13 +144,13 @@ __device__ __forceinline__ void drain_stages(Turn st, int issued, int every, int
     }
 }
 
-// Row tiles of n rows: n / nt rounded up, by a multiplication (nt = 16 k, k <= 16;
-// exact for n < 2^31).
+// Row tiles of n rows: n / nt rounded up, by a multiplication (nt = 16 k, 2 <= k <=
+// 12; exact for n < 2^31).
 __device__ __forceinline__ int32_t row_tiles(int32_t n, const I8MmaParams &p)
 {
     if (n <= 0) return 0;
     const uint32_t t = (uint32_t(n) + 15u) >> 4;                 // (n + nt - 1) / nt = (t + k - 1) / k
-    return int32_t(p.nt == 16 ? t : __umulhi(t + uint32_t(p.nt >> 4) - 1u, p.div_nt));
+    return int32_t(__umulhi(t + uint32_t(p.nt >> 4) - 1u, p.div_nt));
 }
 
 __device__ __forceinline__ int4 lds_i4(uint32_t addr)
@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = c->tmem_base;
-    const uint32_t d_stride = uint32_t(p.nt < 32 ? 32 : p.nt);
-    const uint32_t slots0 = tmem + d_stride * uint32_t(p.bufs);
+    const uint32_t d_stride = uint32_t(p.nt);                    // two accumulators, then the widened weights
+    const uint32_t slots0 = tmem + 2u * d_stride;
 
     // A split cluster takes one unit, each of its CTAs a part of the reduction.
     const uint32_t unit0 = blockIdx.x / uint32_t(PAIR * p.splits);
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                     st.next(p.stages);
                     sl.next(p.slots);
                 }
-                acc.next(p.bufs);
+                acc.next(2);
             }
             if (!ok && any && lane == 0) {
                 umma_commit<PAIR>(smem_u32(&c->drain));
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                 if (leader) mbar_arrive(smem_u32(&c->tempty[buf]));
                 else mbar_arrive_remote(map_to_cta(smem_u32(&c->tempty[buf]), 0));
             }
-            acc.next(p.bufs);
+            acc.next(2);
             xb.next(2);
         }
     } else if (warp < kRowsWarp0) {
