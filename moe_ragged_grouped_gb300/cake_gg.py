@@ -435,29 +435,34 @@ def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=Non
     return out
 
 
+_i8_types = None
+
+
+def _i8_torch():
+    """Names of the X types, and torch's int8, float32 and int32."""
+    global _i8_types
+    if _i8_types is None:
+        import torch
+        _i8_types = ({torch.bfloat16: "bf16", torch.float32: "fp32", torch.int8: "int8"},
+                     torch.int8, torch.float32, torch.int32)
+    return _i8_types
+
+
 def _i8_x_name(X):
-    import torch
-    dtype = X.dtype
-    if dtype is torch.bfloat16:
-        return "bf16"
-    if dtype is torch.int8:
-        return "int8"
-    if dtype is torch.float32:
-        return "fp32"
-    raise TypeError(f"X is {dtype}: int8, bfloat16 or float32 are taken")
+    name = _i8_torch()[0].get(X.dtype)
+    if name is None:
+        raise TypeError(f"X is {X.dtype}: int8, bfloat16 or float32 are taken")
+    return name
 
 
 def _need(tensor, name, dtype, shape, device):
-    """A dense tensor of this type and shape on `device` (the common case is tested first, in few calls)."""
-    if (tensor.dtype is dtype and tensor.shape == shape and tensor.get_device() == device.index
-            and tensor.is_contiguous()):
-        return
+    """A dense tensor of this type and shape on `device`."""
     if tensor.dtype != dtype:
         raise TypeError(f"{name} is {tensor.dtype}: {dtype} is needed")
-    if tuple(tensor.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(tensor.shape)}: {shape} is needed")
+    if tuple(tensor.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(tensor.shape)}: {tuple(shape)} is needed")
     if tensor.device != device:
-        raise ValueError(f"{name} is on {tensor.device}: the weights are on {device}")
+        raise ValueError(f"{name} is on {tensor.device}, not on {device}")
     if not tensor.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
 
@@ -472,9 +477,9 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     Quantising W.reshape(E * N, K) gives int8_gemm's weights.
     """
     import torch
+    name = _i8_x_name(X)
     if act not in I8_ACTS:
         raise ValueError(f"act is None or 'silu_mul', got {act!r}")
-    name = _i8_x_name(X)
     if X.dim() != 2 or (act is not None and X.shape[1] % 2 != 0):
         raise ValueError("X is [T, K], or [T, 2 K] with an activation")
     T, K = int(X.shape[0]), int(X.shape[1]) // (1 if act is None else 2)
@@ -505,10 +510,10 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     quantize_rows).  Rows >= offsets[E] of Y are left as allocated.  Output and
     workspace are allocated through torch when not given.
     """
-    import torch
+    names, i8, f32, i32 = _i8_types or _i8_torch()
+    name = names.get(X.dtype) or _i8_x_name(X)
     if act not in I8_ACTS:
         raise ValueError(f"act is None or 'silu_mul', got {act!r}")
-    name = _i8_x_name(X)
     x_shape, w_shape = X.shape, W.shape
     if len(w_shape) not in (2, 3) or len(x_shape) != 2:
         raise ValueError("X is [T, K] and W [N, K] or [E, N, K]")
@@ -516,32 +521,42 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     N, K = w_shape[-2], w_shape[-1]
     T = x_shape[0]
     M = T if rows is None else rows.shape[0]
-    device = W.device
-    _need(W, "W", torch.int8, w_shape, device)
-    _need(X, "X", X.dtype, (T, K if act is None else 2 * K), device)
-    _need(ws, "ws", torch.float32, w_shape[:-1], device)
     if (xs is None) == (name == "int8"):
         raise ValueError("xs comes with int8 X, and only with it")
-    if xs is not None:
-        _need(xs, "xs", torch.float32, (T,), device)
-    if offsets is not None:
-        _need(offsets, "offsets", torch.int32, (E + 1,), device)
-    elif E != 1:
+    if offsets is None and E != 1:
         raise ValueError("W of several experts comes with offsets")
-    if rows is not None:
-        _need(rows, "rows", torch.int32, (M,), device)
+    # the common case in few calls; what fails here is named below
+    on = W.get_device()
+    if not (W.dtype is i8 and W.is_contiguous() and ws.dtype is f32 and ws.shape == w_shape[:-1] and ws.is_contiguous()
+            and x_shape[1] == (K if act is None else 2 * K) and X.is_contiguous() and on == X.get_device() == ws.get_device()
+            and (xs is None or (xs.dtype is f32 and xs.shape == x_shape[:1] and xs.is_contiguous() and xs.get_device() == on))
+            and (offsets is None or (offsets.dtype is i32 and offsets.shape == (E + 1,) and offsets.is_contiguous()
+                                     and offsets.get_device() == on))
+            and (rows is None or (rows.dtype is i32 and rows.dim() == 1 and rows.is_contiguous() and rows.get_device() == on))):
+        device = W.device
+        _need(W, "W", i8, w_shape, device)
+        _need(X, "X", X.dtype, (T, K if act is None else 2 * K), device)
+        _need(ws, "ws", f32, w_shape[:-1], device)
+        if xs is not None:
+            _need(xs, "xs", f32, (T,), device)
+        if offsets is not None:
+            _need(offsets, "offsets", i32, (E + 1,), device)
+        if rows is not None:
+            _need(rows, "rows", i32, (M,), device)
     if plan is None:
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
     elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], I8_ACTS[act], _dtype_code(out_dtype)):
         raise ValueError("the plan is another problem's")
     if out is None:
-        out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=device)
-    else:
-        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), device)
+        import torch
+        out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=W.device)
+    elif not (out.dtype is _torch_out_dtype(out_dtype) and out.shape == (M, N) and out.is_contiguous()
+              and out.get_device() == on):
+        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), W.device)
     if workspace is None:
-        workspace = make_workspace(plan, device)
+        workspace = make_workspace(plan, W.device)
     if stream is None:
-        stream = _current_stream(device.index) if device.type == "cuda" else 0
+        stream = _current_stream(on) if on >= 0 else 0
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     # (the call of cake_gg_i8_gemm() above, without its conversions: a short product's

@@ -92,7 +92,10 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
 
 // One block per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
-// rest again (from L2).
+// rest again (from L2).  Bound by HBM (3001 x 5120 FP32: 13.5 us, 5.8 TB/s read and
+// written; 8192 x 6144 BF16: 35 us), gated rows by the exponential and the division
+// (32768 x 2048: 92 us, 35 instructions a value).  Two vectors a thread was best of
+// 1 (50 us for the second), 2, 3 (42), 4 (39) and 8 (50).
 constexpr int kHeld = 2;
 constexpr int64_t kFewBlocks = 304;   // two rows a multiprocessor
 

@@ -9,7 +9,10 @@
 // in flight per lane before the first is used.  Products are summed four at a
 // time in 32-bit integers (exact: K < 2^17 keeps |sum| below 2^31), so the
 // order of the sums is free and a row's K can be divided over S warps of a
-// block; the result is rounded once, at the end.
+// block; the result is rounded once, at the end.  One token through 4 of 32
+// experts 6144 -> 4096 takes 17.6 us with its token pass (5.7 TB/s over the call;
+// two channels a warp with four loads each 18.9, one channel 19.3, K over two
+// warps 21).
 //
 // Activations of one or two rows over few weights (up to 32 MB) are quantised by
 // every block for itself, into shared memory, while its first weights are on

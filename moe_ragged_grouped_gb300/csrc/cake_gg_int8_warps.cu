@@ -16,6 +16,10 @@
 // take k in any order that both operands share, the lane's 16 values are the
 // A and B fragments of four m16n8k16 products without any exchange.  The warps'
 // sums meet in shared memory and are added in warp order.
+//
+// Bound: small weights by the start of the kernel (16 x 1024 -> 2048: 4.4 us with
+// the token pass), larger ones by the loads that the registers hold in flight (16 x
+// 4096 -> 5120: 11.5 us, 1.9 TB/s), which is where the tensor-core path takes over.
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
