@@ -247,6 +247,14 @@ int slots_for(int nt)
     return n > kSlotsMost ? kSlotsMost : n;
 }
 
+// Widened tiles that may be ahead of the MMAs.  The converter groups take alternate
+// stages, so with an odd ring a group meets a stage's barrier every second round
+// only and must not come there before the round between is over, or the
+// barrier's parity would deceive it: it waits for the MMAs of the stage `slots`
+// before its last, which have to be of that round or later.  (An even ring gives
+// a group the same stages every round.)
+int slots_most(int stages) { return stages % 2 == 0 ? stages : stages - 2; }
+
 int stages_for(int pair, int nt, int splits, int E)
 {
     int s = kStagesMost;
@@ -321,8 +329,10 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     const int sp = env_int("CAKE_GG_I8_SPLITS", pl->splits);
     pl->splits = sp >= 1 && sp <= 8 && pl->pair == 1 ? sp : 1;
     pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
+    if (pl->stages == 3) pl->stages = 2;
     pl->slots = slots_for(pl->tile_rows);
-    if (pl->slots > pl->stages) pl->slots = pl->stages;
+    const int most = slots_most(pl->stages);
+    if (pl->slots > most) pl->slots = most;
 }
 
 // What the tensor-core kernel can run.
@@ -330,7 +340,7 @@ bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
 {
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= (pl.pair == 2 ? 192 : 128) &&
            pl.tile_rows % 32 == 0 && pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
-           pl.slots <= pl.stages && pl.slots <= slots_for(pl.tile_rows) && pl.splits >= 1 && pl.splits <= 8 &&
+           pl.slots <= slots_most(pl.stages) && pl.slots <= slots_for(pl.tile_rows) && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) &&
            i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }

@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         const int n_kb = kb1 - kb0;
         grid_dependency_wait();
         // A slot is free once the MMAs of the stage that last used it, `slots` before
-        // this one, are done: that stage's `empty` says so (slots <= stages).
+        // this one, are done: that stage's `empty` says so.  (slots <= stages, and <=
+        // stages - 2 in an odd ring: a group then meets a barrier every second round,
+        // and this wait at its last stage has to cover the round between.)
         Turn st, sl, last;
         if (group) st.next(p.stages), sl.next(p.slots);
         int it = group, kb = group;

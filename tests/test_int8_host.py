@@ -133,3 +133,26 @@ def test_helpers_refuse():
                             (TypeError, (x,), dict(out=x)), (ValueError, (x,), dict(scale=s[:2]))]:
         with pytest.raises(err):
             gg.quantize_rows(*args, **more)
+
+
+@pytest.mark.parametrize("E", [1, 3, 30, 400, 1024])
+def test_every_plan_keeps_the_converters_within_a_round(E, monkeypatch):
+    """Two converter groups take alternate stages.  In an odd ring each meets a stage's barrier every
+    second round, so widened tiles may run at most stages - 2 ahead of the MMAs."""
+    for splits in (None, "1", "2", "3", "5", "8"):
+        if splits:
+            monkeypatch.setenv("CAKE_GG_I8_SPLITS", splits)
+        for M in (9, 20, 40, 70, 100, 200, 500, 1500, 6000, 40000):
+            for N in (8, 136, 1000, 4096, 8192):
+                for K in (16, 512, 2048, 8192):
+                    plan = gg.cake_gg_i8_plan(E, M, M, N, K)
+                    if plan.path == 1:
+                        assert plan.stages >= 2 and plan.slots >= 2
+                        assert plan.slots <= (plan.stages if plan.stages % 2 == 0 else plan.stages - 2), plan.as_dict()
+
+
+def test_call_refuses_a_plan_whose_converters_could_run_a_round_ahead():
+    plan = gg.cake_gg_i8_plan(**{**GOOD, "M_max": 4096, "T": 4096})
+    assert plan.path == 1
+    plan.stages, plan.slots = 3, 3
+    assert _call(plan, rows=None) == gg.CAKE_GG_ERR_INVALID_ARG
