@@ -341,7 +341,7 @@ bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= (pl.pair == 2 ? 192 : 128) &&
            pl.tile_rows % 32 == 0 && pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
            pl.slots <= slots_most(pl.stages) && pl.slots <= slots_for(pl.tile_rows) && pl.splits >= 1 && pl.splits <= 8 &&
-           (pl.splits == 1 || pl.pair == 1) &&
+           (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 127) / 128 &&   // (a stage for every CTA)
            i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }
 

@@ -145,6 +145,8 @@ def test_every_plan_keeps_the_converters_within_a_round(E, monkeypatch):
         for M in (9, 20, 40, 70, 100, 200, 500, 1500, 6000, 40000):
             for N in (8, 136, 1000, 4096, 8192):
                 for K in (16, 512, 2048, 8192):
+                    if splits and int(splits) > (K + 127) // 128:
+                        continue
                     plan = gg.cake_gg_i8_plan(E, M, M, N, K)
                     if plan.path == 1:
                         assert plan.stages >= 2 and plan.slots >= 2
@@ -156,3 +158,12 @@ def test_call_refuses_a_plan_whose_converters_could_run_a_round_ahead():
     assert plan.path == 1
     plan.stages, plan.slots = 3, 3
     assert _call(plan, rows=None) == gg.CAKE_GG_ERR_INVALID_ARG
+
+
+def test_more_splits_than_stages_are_refused(monkeypatch):
+    monkeypatch.setenv("CAKE_GG_I8_PAIR", "1")
+    monkeypatch.setenv("CAKE_GG_I8_SPLITS", "3")
+    with pytest.raises(gg.CakeGGError) as err:                    # two stages of 128
+        gg.cake_gg_i8_plan(1, 4096, 4096, 128, 256)
+    assert err.value.code == gg.CAKE_GG_ERR_INVALID_ARG
+    assert gg.cake_gg_i8_plan(1, 4096, 4096, 128, 384).splits == 3
