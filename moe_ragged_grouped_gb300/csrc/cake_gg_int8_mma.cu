@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         Turn st;
         int issued = 0;
         bool ok = true;
-        grid_dependency_wait();                                  // the tokens
         if (p.b.rows == nullptr) {
+            grid_dependency_wait();                              // the tokens
             for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
                 const Tile t = w.tile(p.nt, off, pref);
                 const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                     const int32_t id = m < t.end ? p.b.rows[m] : 0;
                     mine[i] = id >= 0 && id < p.b.T ? id : 0;    // (reported where it is scaled)
                 }
+                grid_dependency_wait();                          // the tokens (the caller's row numbers were there)
                 __syncwarp();
                 for (; kb < n_kb; kb += 2) {
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
@@ -614,6 +615,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                 }
                 kb -= n_kb;
             }
+            grid_dependency_wait();
             if (!ok || aborted(c)) drain_stages(st, issued, 2, lane, p.stages, c);
         }
         __syncwarp();
@@ -630,21 +632,31 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
             const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
             const float ws = ws_split;
             const int m0 = rank * per;
-            for (int j = 0; j < per && m0 + j < t.rows; j += 4) {
-                float4 sum = *reinterpret_cast<const float4 *>(recv + size_t(row) * (per + 4) + j);
-                for (int v = 1; v < p.splits; ++v) {
-                    const float4 o = *reinterpret_cast<const float4 *>(recv + (size_t(v) * 128 + row) * (per + 4) + j);
-                    sum.x += o.x, sum.y += o.y, sum.z += o.z, sum.w += o.w;
-                }
-                const float4 x4 = *reinterpret_cast<const float4 *>(xs_tile + m0 + j);
-                const float v[4] = {sum.x * ws * x4.x, sum.y * ws * x4.y, sum.z * ws * x4.z, sum.w * ws * x4.w};
+            for (int j0 = 0; j0 < per && m0 + j0 < t.rows; j0 += 16) {
+                // up to 16 rows at a time: their loads do not wait for each other's sums
+                float4 sum[4];
+                for (int v = 0; v < p.splits; ++v)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (m0 + j + i < t.rows && n < p.b.N) {
-                        const int64_t at = (int64_t(t.m0) + m0 + j + i) * p.b.N + n;
-                        if (OUT_F32) static_cast<float *>(p.b.Y)[at] = v[i];
-                        else static_cast<uint16_t *>(p.b.Y)[at] = uint16_t(pack_bf16x2(v[i], 0.0f) & 0xffffu);
+                    for (int i = 0; i < 4; ++i)
+                        if (j0 + 4 * i < per) {
+                            const float4 o = *reinterpret_cast<const float4 *>(recv + (size_t(v) * 128 + row) * (per + 4) + j0 + 4 * i);
+                            if (v == 0) sum[i] = o;
+                            else sum[i].x += o.x, sum[i].y += o.y, sum[i].z += o.z, sum[i].w += o.w;
+                        }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int m = m0 + j0 + 4 * i + k;
+                        if (j0 + 4 * i < per && m < t.rows && n < p.b.N) {
+                            const float y = v[k] * ws * xs_tile[m];
+                            const int64_t at = (int64_t(t.m0) + m) * p.b.N + n;
+                            if (OUT_F32) static_cast<float *>(p.b.Y)[at] = y;
+                            else static_cast<uint16_t *>(p.b.Y)[at] = uint16_t(pack_bf16x2(y, 0.0f) & 0xffffu);
+                        }
                     }
+                }
             }
         }
     }
