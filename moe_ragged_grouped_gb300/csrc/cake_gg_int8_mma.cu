@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                 }
                 acc.next(2);
             }
-            if (!ok && any && lane == 0) {
+            if (!ok && any && elect_one()) {                     // (the lane that issued them)
                 umma_commit<PAIR>(smem_u32(&c->drain));
                 drain_wait(smem_u32(&c->drain), 0);
             }
