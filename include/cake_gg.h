@@ -69,7 +69,8 @@
  *   read by cake_gg_i8_plan(), recorded in its plan (no result bit follows them
  *   while a sum stays below 2^24):
  *     CAKE_GG_I8_PATH (cake_gg_i8_path_t), CAKE_GG_I8_PAIR (1 or 2),
- *     CAKE_GG_I8_ROWS_PER_TILE (32 .. 192), CAKE_GG_I8_SPLITS (1 .. 8);
+ *     CAKE_GG_I8_ROWS_PER_TILE (32 .. 192), CAKE_GG_I8_SPLITS (1 .. 8),
+ *     CAKE_GG_I8_FIRST_ROWS (0 .. M_max - 1);
  *   read by each compute call, changing no result:
  *     CAKE_GG_PDL=0 (no programmatic dependent launch), CAKE_GG_ROUTER_STAGGER
  *     (the router's per-unit k-order stagger, default 7, 0 = in order;
@@ -341,7 +342,9 @@ typedef struct cake_gg_i8_plan {
     int32_t stages;          /* shared-memory ring depth                            */
     int32_t splits;          /* CTAs of a cluster that share a tile's reduction     */
     int32_t debug_flags;     /* test-only fault injection; 0 in normal use          */
-    int32_t reserved;
+    int32_t first_rows;      /* without rows: a product of its own for this many
+                                rows, beside which the other tokens are prepared;
+                                0 = one product                                     */
     uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
     uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
 } cake_gg_i8_plan_t;
@@ -356,7 +359,7 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
 
 /* The product.  X, W, Y, workspace: device pointers, 16-byte aligned; xs, ws,
  * rows, offsets 4-byte aligned.  The workspace is plan->workspace_bytes,
- * zero-filled once after allocation.  Enqueues one or two kernels on `stream`;
+ * zero-filled once after allocation.  Enqueues one to four kernels on `stream`;
  * allocates nothing, never synchronises.  Host-detected errors return
  * non-zero and enqueue nothing; offsets that the device finds invalid
  * (CAKE_GG_ERR_BAD_OFFSETS) and a row index outside [0, T)

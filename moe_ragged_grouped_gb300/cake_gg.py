@@ -115,7 +115,7 @@ class CakeGGI8Plan(ctypes.Structure):
         ("stages", ctypes.c_int32),
         ("splits", ctypes.c_int32),
         ("debug_flags", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("first_rows", ctypes.c_int32),
         ("timeout_ns", ctypes.c_uint64),
         ("workspace_bytes", ctypes.c_uint64),
     ]

@@ -90,6 +90,11 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
     *reinterpret_cast<uint4 *>(out) = halves8(r);
 }
 
+// Both kernels of the pass may run `beside` a product of other rows.  They then
+// read what was there before the call and write rows that nobody else touches, so
+// they wait for that product only at their end, in one block: their completion
+// implies the product's, and with it everything before in the stream.
+
 // One block per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
 // rest again (from L2).  Bound by HBM (3001 x 5120 FP32: 13.5 us, 5.8 TB/s read and
@@ -101,10 +106,10 @@ constexpr int64_t kFewBlocks = 304;   // two rows a multiprocessor
 
 template <typename XT, bool ACT, typename QT>
 __global__ void __launch_bounds__(1024)
-    i8_quant_kernel(const XT *__restrict__ X, int32_t K, QT *__restrict__ Q, float *__restrict__ S)
+    i8_quant_kernel(const XT *__restrict__ X, int32_t K, QT *__restrict__ Q, float *__restrict__ S, bool beside)
 {
     __shared__ uint32_t warp_max[32];
-    grid_dependency_wait();
+    if (!beside) grid_dependency_wait();
     grid_launch_dependents();
     const int64_t t = blockIdx.x;
     const XT *row = X + t * (ACT ? 2 : 1) * int64_t(K);
@@ -142,12 +147,13 @@ __global__ void __launch_bounds__(1024)
         row8<XT, ACT>(row, K, k, v);
         store8(out + k, v, rs);
     }
+    if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
 // 8-bit tokens as FP16 integers, 16 values a thread.
-__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ X, __half *__restrict__ Q, int64_t n16)
+__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ X, __half *__restrict__ Q, int64_t n16, bool beside)
 {
-    grid_dependency_wait();
+    if (!beside) grid_dependency_wait();
     grid_launch_dependents();
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n16) return;
@@ -160,9 +166,10 @@ __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict
         for (int j = 0; j < 8; ++j) v[j] = float(int8_t(u[h * 2 + j / 4] >> (8 * (j % 4))));
         *reinterpret_cast<uint4 *>(Q + i * 16 + h * 8) = halves8(v);
     }
+    if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
-// A kernel of the token pass: a programmatic dependent of the stream's
+// A kernel of the token pass: unless it runs beside a product, a programmatic dependent of the stream's
 // previous kernel (it waits for it before it reads anything), and only then
 // lets the product start, whose early reads of weights and offsets are thus
 // ordered after everything before this call.
@@ -182,34 +189,37 @@ cudaLaunchConfig_t pass_config(int64_t blocks, int threads, cudaLaunchAttribute 
 }
 
 template <typename XT, typename QT>
-cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q, float *S, cudaStream_t stream)
+cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q, float *S, bool beside,
+                            cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
     // one vector a thread where rows are few and their latency counts, else kHeld
     const int held = T <= kFewBlocks ? 1 : kHeld;
     int threads = int(align_up((uint64_t(K) / 8 + held - 1) / held, 32));
     if (threads > 1024) threads = 1024;
+    if (beside && threads > 256) threads = 256;   // (what fits beside the product)
     const cudaLaunchConfig_t cfg = pass_config(T, threads, &attr, stream);
     const XT *x = static_cast<const XT *>(X);
-    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, true, QT>, x, K, Q, S)
-                                       : cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, false, QT>, x, K, Q, S);
+    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, true, QT>, x, K, Q, S, beside)
+                                       : cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, false, QT>, x, K, Q, S, beside);
 }
 
 template <typename QT>
-int launch_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, QT *Q, float *S, cudaStream_t stream)
+int launch_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, QT *Q, float *S, bool beside,
+                 cudaStream_t stream)
 {
-    const cudaError_t err = x_dtype == CAKE_GG_BF16 ? launch_quant_as<uint16_t>(X, act, T, K, Q, S, stream)
-                                                    : launch_quant_as<float>(X, act, T, K, Q, S, stream);
+    const cudaError_t err = x_dtype == CAKE_GG_BF16 ? launch_quant_as<uint16_t>(X, act, T, K, Q, S, beside, stream)
+                                                    : launch_quant_as<float>(X, act, T, K, Q, S, beside, stream);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
-int launch_expand(const void *X, int64_t T, int32_t K, __half *Q, cudaStream_t stream)
+int launch_expand(const void *X, int64_t T, int32_t K, __half *Q, bool beside, cudaStream_t stream)
 {
     const int64_t n16 = T * (K / 16), blocks = (n16 + 255) / 256;
     if (blocks > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = pass_config(blocks, 256, &attr, stream);
-    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, static_cast<const int8_t *>(X), Q, n16) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, i8_expand_kernel, static_cast<const int8_t *>(X), Q, n16, beside) == cudaSuccess
                ? CAKE_GG_OK
                : CAKE_GG_ERR_CUDA;
 }
@@ -290,6 +300,41 @@ int64_t row_tiles(const cake_gg_i8_plan_t &pl, int nt)
     return whole + busy / 2 > busy ? whole + busy / 2 : busy;
 }
 
+constexpr int kSms = 152;
+int64_t stage_ns(int pair, int nt) { return pair == 2 ? 250 + nt * 7 / 6 : 280 + nt * 11 / 10; }
+
+// Rows of a first product, beside which the token pass prepares the others: its
+// blocks live on the registers and threads that a product CTA leaves (a product
+// is bound by the tensor cores, the pass by HBM and its arithmetic).  The pass
+// runs there at some 0.4 of its own speed, so the first product should take 2.5
+// times as long as the rest of the pass: that share f of the rows, for one
+// expert cut where a wave of units ends.  Worth it where the pass hidden, of
+// which about half is won (the power limit takes the rest), is more than a
+// wave that the cut adds and the start of two more kernels.  Measured in turn:
+// 16384 x 4096 -> 4096 from 8-bit tokens 320 us undivided, 312, 307, 322 with f =
+// 0.12, 0.22, 0.28; gated 32768 x 2048 -> 6144 over 32 experts 533, 533, 520,
+// 511, 517 with f = 0, 0.12, 0.24, 0.37, 0.49.
+int choose_first(const cake_gg_i8_plan_t &pl)
+{
+    const int nt = pl.tile_rows;
+    const int64_t workers = kSms / pl.pair, n_ct = (pl.N + 128 * pl.pair - 1) / (128 * pl.pair);
+    const int64_t wave = (pl.K + 127) / 128 * stage_ns(pl.pair, nt), tiles = row_tiles(pl, nt);
+    auto waves = [&](int64_t t) { return (t * n_ct + workers - 1) / workers; };
+    // nanoseconds of the whole token pass: bytes at 5.8 TB/s, gated values 1.37 ps each
+    const double values = double(pl.M_max) * pl.K;
+    const double pass = pl.act != CAKE_GG_ACT_NONE ? values * 1.37e-3
+                                                   : values * (pl.x_dtype == CAKE_GG_INT8 ? 3 : pl.x_dtype == CAKE_GG_BF16 ? 4 : 6) / 5800.0;
+    const double product = double(waves(tiles) * wave), f = 2.5 * pass / (product + 2.5 * pass);
+    int64_t t = int64_t(f * double(tiles)), extra = wave / 2;
+    if (pl.E == 1) {
+        t = (int64_t(f * double(tiles * n_ct)) / workers) * workers / n_ct;
+        extra = (waves(t) + waves(tiles - t) - waves(tiles)) * wave;
+    }
+    const int64_t rows = pl.E == 1 ? t * nt : int64_t(f * double(pl.M_max));
+    if (t < 1 || rows >= pl.M_max || pass * (1 - f) / 2 < double(extra) + 8000) return 0;
+    return int(rows);
+}
+
 // Shape of the tensor-core path, from a model of its time in nanoseconds: waves
 // of units over the multiprocessors (152, or 76 pairs), the stages of a unit,
 // the storing of the last one, and the exchange between the CTAs that share a
@@ -304,15 +349,13 @@ int64_t row_tiles(const cake_gg_i8_plan_t &pl, int nt)
 // undivided).
 void choose_mma(cake_gg_i8_plan_t *pl)
 {
-    constexpr int kSms = 152;
     const int64_t n_kb = (pl->K + 127) / 128;
     int64_t best = -1;
     auto consider = [&](int pair, int nt, int splits) {
         const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
         if (splits > 1 && (units * splits > kSms || n_kb < 2 * splits)) return;
         const int64_t waves = (units * pair + kSms - 1) / kSms;
-        const int64_t stage = pair == 2 ? 250 + nt * 7 / 6 : 280 + nt * 11 / 10;
-        const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage + 16 * nt + (splits > 1 ? 1100 * splits : 0);
+        const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage_ns(pair, nt) + 16 * nt + (splits > 1 ? 1100 * splits : 0);
         if (best < 0 || ns < best) {
             best = ns;
             pl->pair = pair;
@@ -333,6 +376,8 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     pl->slots = slots_for(pl->tile_rows);
     const int most = slots_most(pl->stages);
     if (pl->slots > most) pl->slots = most;
+    const int first = env_int("CAKE_GG_I8_FIRST_ROWS", -1);
+    pl->first_rows = pl->splits > 1 ? 0 : first < 0 ? choose_first(*pl) : first < pl->M_max ? first : 0;
 }
 
 // What the tensor-core kernel can run.
@@ -341,6 +386,7 @@ bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= (pl.pair == 2 ? 192 : 128) &&
            pl.tile_rows % 32 == 0 && pl.stages >= 2 && pl.stages <= kStagesMost && pl.slots >= 2 &&
            pl.slots <= slots_most(pl.stages) && pl.slots <= slots_for(pl.tile_rows) && pl.splits >= 1 && pl.splits <= 8 &&
+           pl.first_rows >= 0 && (pl.first_rows == 0 || (pl.first_rows < pl.M_max && pl.splits == 1)) &&
            (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 127) / 128 &&   // (a stage for every CTA)
            i8_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kI8SmemLimit;
 }
@@ -390,7 +436,7 @@ int cake_gg_i8_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, 
     int sms;
     const int dev = device_sms(&sms);
     if (dev != CAKE_GG_OK) return dev;
-    return launch_quant(X, x_dtype, act, T, K, Xq, xs, static_cast<cudaStream_t>(stream));
+    return launch_quant(X, x_dtype, act, T, K, Xq, xs, false, static_cast<cudaStream_t>(stream));
 }
 
 int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *xs, const int32_t *rows,
@@ -445,16 +491,19 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
 
     // the token pass, then the product
     void *tokens = base + L.tokens;
-    if (!ready) {
-        float *scales = reinterpret_cast<float *>(base + L.scales);
-        rc = mma ? launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<__half *>(tokens), scales, s)
-                 : launch_quant(X, pl.x_dtype, pl.act, pl.T, pl.K, static_cast<int8_t *>(tokens), scales, s);
-        p.xs = scales;
-    } else {
-        rc = launch_expand(X, pl.T, pl.K, static_cast<__half *>(tokens), s);
-    }
-    if (rc != CAKE_GG_OK) return rc;
+    float *scales = reinterpret_cast<float *>(base + L.scales);
+    if (!ready) p.xs = scales;
+    auto pass = [&](int64_t t0, int64_t n, bool beside) {
+        __half *q = static_cast<__half *>(tokens) + t0 * pl.K;
+        if (ready) return launch_expand(static_cast<const int8_t *>(X) + t0 * pl.K, n, pl.K, q, beside, s);
+        const int64_t row = int64_t(pl.K) * (pl.act == CAKE_GG_ACT_NONE ? 1 : 2) * (pl.x_dtype == CAKE_GG_BF16 ? 2 : 4);
+        const uint8_t *x = static_cast<const uint8_t *>(X) + t0 * row;
+        return mma ? launch_quant(x, pl.x_dtype, pl.act, n, pl.K, q, scales + t0, beside, s)
+                   : launch_quant(x, pl.x_dtype, pl.act, n, pl.K, static_cast<int8_t *>(tokens), scales, false, s);
+    };
     p.early = 1;
+    const int64_t first = mma && !rows && pdl ? pl.first_rows : 0;
+    if ((rc = pass(0, first ? first : pl.T, false)) != CAKE_GG_OK) return rc;
     if (warps) return status(launch_i8_warps(p, static_cast<const int8_t *>(tokens), pl.tile_rows, pdl, s));
     if (!mma) return status(launch_i8_rows(p, tokens, CAKE_GG_INT8, CAKE_GG_ACT_NONE, pdl, s));
     I8MmaParams m{};
@@ -464,7 +513,16 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     m.slots = pl.slots;
     m.splits = pl.splits;
     m.debug_flags = pl.debug_flags;
-    return launch_i8_mma(m, static_cast<const uint16_t *>(tokens), pl.pair, pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms, pdl, s);
+    const uint16_t *q = static_cast<const uint16_t *>(tokens);
+    const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
+    if (first) {
+        m.b.m_hi = first;
+        if ((rc = launch_i8_mma(m, q, pl.pair, cap, pdl, s)) != CAKE_GG_OK) return rc;
+        if ((rc = pass(first, pl.T - first, true)) != CAKE_GG_OK) return rc;
+    }
+    m.b.m_lo = first;
+    m.b.m_hi = pl.M_max;
+    return launch_i8_mma(m, q, pl.pair, cap, pdl, s);
 }
 
 }  // extern "C"

@@ -29,7 +29,8 @@ struct I8Params {
     const float *xs;          // [T]
     void *Y;                  // [M, N]
     int32_t *status;          // sticky status word (workspace byte 0)
-    int64_t M, T;
+    int64_t M, T;             // rows of all experts (offsets' bound), tokens
+    int64_t m_lo, m_hi;       // rows of this launch (tensor-core path)
     int32_t E, N, K;
     int32_t out_f32;
     int32_t early;            // the grid before this one is this call's own token pass, so

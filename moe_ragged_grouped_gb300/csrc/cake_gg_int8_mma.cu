@@ -150,6 +150,8 @@ __device__ __forceinline__ void drain_stages(Turn st, int issued, int every, int
     }
 }
 
+__device__ __forceinline__ int32_t within(int32_t v, int32_t lo, int32_t hi) { return min(max(v, lo), hi); }
+
 // Row tiles of n rows: n / nt rounded up, by a multiplication (nt = 16 k, 2 <= k <=
 // 12; exact for n < 2^31).
 __device__ __forceinline__ int32_t row_tiles(int32_t n, const I8MmaParams &p)
@@ -252,13 +254,17 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         __syncwarp();
         // lane l sums the row tiles of its run of experts, then the runs are scanned
         const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+        const int32_t lo = int32_t(p.b.m_lo), hi = int32_t(p.b.m_hi);
         int32_t sum = 0;
         bool bad = lane == 0 && off[0] != 0;
         for (int e = e0; e < e1; ++e) {
-            const int32_t n = off[e + 1] - off[e];
-            bad |= n < 0 || int64_t(off[e + 1]) > p.b.M;
-            sum += row_tiles(n, p);
+            bad |= off[e + 1] < off[e] || int64_t(off[e + 1]) > p.b.M;
+            sum += row_tiles(within(off[e + 1], lo, hi) - within(off[e], lo, hi), p);
         }
+        __syncwarp();
+        if (lo > 0 || hi < p.b.M)                                // each expert's rows of this launch
+            for (int i = lane; i <= E; i += 32) off[i] = within(off[i], lo, hi);
+        __syncwarp();
         int32_t inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -746,7 +752,8 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
     if (rc != CAKE_GG_OK) return rc;
 
     // row tiles at most: a whole one per nt rows and a last one per expert with rows
-    const int64_t tiles = p.b.E == 1 ? (p.b.M + p.nt - 1) / p.nt : p.b.M / p.nt + (p.b.M < p.b.E ? p.b.M : p.b.E);
+    const int64_t m = p.b.m_hi - p.b.m_lo;
+    const int64_t tiles = p.b.E == 1 ? (m + p.nt - 1) / p.nt : m / p.nt + (m < p.b.E ? m : p.b.E);
     const int64_t bound = tiles * p.n_ct;
     int64_t grid;
     if (p.splits > 1) {

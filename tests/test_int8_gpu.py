@@ -386,3 +386,77 @@ def test_sums_past_24_bits(T, K):
     off = float(((got.double() - want).abs() / want.abs()).max())
     print(f"T {T} K {K}: {off:.3e}")
     assert off <= K / 16 * 2.0 ** -23 + 2.0 ** -21
+
+
+@pytest.mark.parametrize("first", [1, 63, 160, 333, 409])
+@pytest.mark.parametrize("x_dtype,act", [("int8", None), ("bf16", None), ("fp32", None), ("bf16", "silu_mul")])
+@pytest.mark.parametrize("sizes", [[410], [5, 0, 290, 1, 0, 33, 64, 15]], ids=["dense", "grouped"])
+def test_first_product(sizes, x_dtype, act, first, monkeypatch):
+    """The rows divided between two products give the undivided call's bits, also where the second
+    token pass of one call and the first of the next follow at once on the same workspace."""
+    import torch
+    E, N, K, M = len(sizes), 392, 1200, 410                     # (grouped: two rows past the last offset)
+    rng = np.random.default_rng(first)
+    W, ws = _ints((E, N, K), rng), _scales((E, N), rng)
+    monkeypatch.setenv("CAKE_GG_I8_PATH", "1")
+    plans = []
+    for rows in (0, first):
+        monkeypatch.setenv("CAKE_GG_I8_FIRST_ROWS", str(rows))
+        plans.append(gg.cake_gg_i8_plan(E, M, M, N, K, x_dtype, act, "bf16"))
+        assert plans[-1].first_rows == (rows if plans[-1].splits == 1 else 0)
+    xs = _scales(M, rng) if x_dtype == "int8" else None
+    inputs = []
+    for seed in range(4):
+        if x_dtype == "int8":
+            inputs.append(_ints((M, K), rng))
+        else:
+            dtype = torch.bfloat16 if x_dtype == "bf16" else torch.float32
+            inputs.append(_rows_of(M, 2 * K if act else K, dtype, seed))
+    got = []
+    for plan in plans:
+        work = gg.make_workspace(plan, "cuda")
+        outs = [torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in inputs]
+        for x, out in zip(inputs * 3, outs * 3):
+            gg.int8_gemm(x, W, ws, xs=xs, offsets=_offsets(sizes), act=act, out=out, plan=plan, workspace=work, check=False)
+        assert gg.cake_gg_check_status(work) == gg.CAKE_GG_OK
+        got.append(outs)
+    for x, one, two in zip(inputs, *got):
+        assert torch.equal(one, two)
+        q, s = (x, xs) if xs is not None else gg.quantize_rows(x, act=act)
+        used = sum(sizes)
+        _close(two[:used], _want(q, s, W, ws, sizes), "bf16")
+        assert (two[used:] == 7).all()
+
+
+@pytest.mark.parametrize("E", [1, 6])
+def test_first_product_by_its_own_rule(E):
+    """A call long enough to be divided, as planned, against the same call undivided; routed rows
+    leave it undivided, and a graph replays it."""
+    import torch
+    M, N, K = 12000, 2048, 8192
+    rng = np.random.default_rng(E)
+    W, ws = _ints((E, N, K), rng), _scales((E, N), rng)
+    x = _rows_of(M, 2 * K, torch.bfloat16, 2)
+    sizes = [M] if E == 1 else [0, 5000, 1, 1999, 0, 5000]
+    plan, whole = (gg.cake_gg_i8_plan(E, M, M, N, K, "bf16", "silu_mul", "bf16") for _ in range(2))
+    assert plan.first_rows > 0
+    whole.first_rows = 0
+    work = gg.make_workspace(plan, "cuda")
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    more = dict(offsets=_offsets(sizes), act="silu_mul", out=out, workspace=work)
+    call = lambda p: gg.int8_gemm(x, W, ws, plan=p, **more)
+    want = call(whole).clone()
+    for _ in range(5):
+        out.zero_()
+        assert torch.equal(call(plan), want)
+    rows = torch.arange(M, dtype=torch.int32, device="cuda")
+    out.zero_()
+    gg.int8_gemm(x, W, ws, rows=rows, plan=plan, **more)
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gg.int8_gemm(x, W, ws, plan=plan, check=False, **more)
+    out.zero_()
+    graph.replay()
+    graph.replay()
+    assert torch.equal(out, want)

@@ -167,3 +167,28 @@ def test_more_splits_than_stages_are_refused(monkeypatch):
         gg.cake_gg_i8_plan(1, 4096, 4096, 128, 256)
     assert err.value.code == gg.CAKE_GG_ERR_INVALID_ARG
     assert gg.cake_gg_i8_plan(1, 4096, 4096, 128, 384).splits == 3
+
+
+def test_a_first_product_where_the_token_pass_is_long(monkeypatch):
+    """Plans divide long calls only, by less than all their rows, and not over a split reduction."""
+    for M, N, K in ((1, 8, 16), (64, 4096, 6144), (3001, 1000, 5120)):
+        assert gg.cake_gg_i8_plan(1, M, M, N, K).first_rows == 0
+    for M in (16384, 20001, 1 << 20, 2 ** 31 - 1):
+        for E in (1, 32):
+            assert 0 < gg.cake_gg_i8_plan(E, M, M, 4096, 4096, "fp32").first_rows < M
+    for value, want in (("0", 0), ("77", 77), ("4096", 0)):
+        monkeypatch.setenv("CAKE_GG_I8_FIRST_ROWS", value)
+        assert gg.cake_gg_i8_plan(1, 4096, 4096, 4096, 4096).first_rows == want
+    monkeypatch.setenv("CAKE_GG_I8_PAIR", "1")
+    monkeypatch.setenv("CAKE_GG_I8_ROWS_PER_TILE", "64")
+    monkeypatch.setenv("CAKE_GG_I8_SPLITS", "2")
+    monkeypatch.setenv("CAKE_GG_I8_FIRST_ROWS", "77")
+    plan = gg.cake_gg_i8_plan(1, 4096, 4096, 4096, 4096)
+    assert plan.splits == 2 and plan.first_rows == 0
+
+
+@pytest.mark.parametrize("first", [-1, 4096, 2 ** 31 - 1])
+def test_call_refuses_a_first_product_of_no_or_all_rows(first):
+    plan = gg.cake_gg_i8_plan(**{**GOOD, "M_max": 4096, "T": 4096})
+    plan.first_rows = first
+    assert _call(plan, rows=None) == gg.CAKE_GG_ERR_INVALID_ARG
