@@ -95,7 +95,7 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
 // they wait for that product only at their end, in one block: their completion
 // implies the product's, and with it everything before in the stream.
 
-// One block per row.  The first kHeld vectors of 8 values that a thread owns
+// blockDim.x threads per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
 // rest again (from L2).  Bound by HBM (3001 x 5120 FP32: 13.5 us, 5.8 TB/s read and
 // written; 8192 x 6144 BF16: 35 us), gated rows by the exponential and the division
@@ -106,12 +106,13 @@ constexpr int64_t kFewBlocks = 304;   // two rows a multiprocessor
 
 template <typename XT, bool ACT, typename QT>
 __global__ void __launch_bounds__(1024)
-    i8_quant_kernel(const XT *__restrict__ X, int32_t K, QT *__restrict__ Q, float *__restrict__ S, bool beside)
+    i8_quant_kernel(const XT *__restrict__ X, int64_t T, int32_t K, QT *__restrict__ Q, float *__restrict__ S, bool beside)
 {
     __shared__ uint32_t warp_max[32];
     if (!beside) grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t t = blockIdx.x;
+    const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int n = t < T ? K : 0;                                 // values of this row
     const XT *row = X + t * (ACT ? 2 : 1) * int64_t(K);
     const int stride = int(blockDim.x) * 8;
     float held[kHeld][8];
@@ -119,30 +120,33 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int k = int(threadIdx.x) * 8 + j * stride;
-        if (k < K) {
+        if (k < n) {
             row8<XT, ACT>(row, K, k, held[j]);
             m = max_bits(held[j], m);
         }
     }
-    for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < K; k += stride) {
+    for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < n; k += stride) {
         float v[8];
         row8<XT, ACT>(row, K, k, v);
         m = max_bits(v, m);
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = threadIdx.x % 32 < blockDim.x / 32 ? warp_max[threadIdx.x % 32] : 0;
-    m = __reduce_max_sync(0xffffffffu, m);
+    const int warps = int(blockDim.x) / 32;
+    if (warps > 1) {
+        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.y * warps + threadIdx.x / 32] = m;
+        __syncthreads();
+        m = int(threadIdx.x % 32) < warps ? warp_max[threadIdx.y * warps + threadIdx.x % 32] : 0;
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
     const RowScale rs(m);
-    if (threadIdx.x == 0) S[t] = rs.scale;
+    if (threadIdx.x == 0 && n) S[t] = rs.scale;
     QT *out = Q + t * int64_t(K);
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
         const int k = int(threadIdx.x) * 8 + j * stride;
-        if (k < K) store8(out + k, held[j], rs);
+        if (k < n) store8(out + k, held[j], rs);
     }
-    for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < K; k += stride) {
+    for (int k = int(threadIdx.x) * 8 + kHeld * stride; k < n; k += stride) {
         float v[8];
         row8<XT, ACT>(row, K, k, v);
         store8(out + k, v, rs);
@@ -198,10 +202,15 @@ cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q,
     int threads = int(align_up((uint64_t(K) / 8 + held - 1) / held, 32));
     if (threads > 1024) threads = 1024;
     if (beside && threads > 256) threads = 256;   // (what fits beside the product)
-    const cudaLaunchConfig_t cfg = pass_config(T, threads, &attr, stream);
+    // short rows share a block of 256 threads: with a block of one or two warps each
+    // the launching of blocks is the bound (12000 x 272: 13.0 us, 5.2; 12000 x 768: 12.9,
+    // 9.0; 20000 x 1024: 21.4, 19.8, but gated 31.5, 33.6; gated 12000 x 512: 12.9, 10.0)
+    const int rows = T > kFewBlocks && threads <= (act == CAKE_GG_ACT_NONE ? 64 : 32) ? 256 / threads : 1;
+    cudaLaunchConfig_t cfg = pass_config((T + rows - 1) / rows, threads, &attr, stream);
+    cfg.blockDim.y = unsigned(rows);
     const XT *x = static_cast<const XT *>(X);
-    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, true, QT>, x, K, Q, S, beside)
-                                       : cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, false, QT>, x, K, Q, S, beside);
+    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, true, QT>, x, T, K, Q, S, beside)
+                                       : cudaLaunchKernelEx(&cfg, i8_quant_kernel<XT, false, QT>, x, T, K, Q, S, beside);
 }
 
 template <typename QT>
