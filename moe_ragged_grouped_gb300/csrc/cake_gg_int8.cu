@@ -310,6 +310,12 @@ int64_t row_tiles(const cake_gg_i8_plan_t &pl, int nt)
 }
 
 constexpr int kSms = 152;
+// Multiprocessors that clusters of `splits` CTAs can hold at once: a cluster lies
+// within one of the GPU's groups of them, whose sizes differ from part to part.
+// Here 152, 138, 144, 140, 138, 105, 120 for 2 .. 8; a call of one cluster more
+// takes a second wave (374 x 3328 -> 1000 as 48 clusters of three 20.6 us, 14
+// undivided).
+int cluster_sms(int splits) { return splits <= 2 ? kSms : splits <= 6 ? 132 : 104; }
 int64_t stage_ns(int pair, int nt) { return pair == 2 ? 250 + nt * 7 / 6 : 280 + nt * 11 / 10; }
 
 // Rows of a first product, beside which the token pass prepares the others: its
@@ -362,7 +368,7 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     int64_t best = -1;
     auto consider = [&](int pair, int nt, int splits) {
         const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
-        if (splits > 1 && (units * splits > kSms || n_kb < 2 * splits)) return;
+        if (splits > 1 && (units * splits > cluster_sms(splits) || n_kb < 2 * splits)) return;
         const int64_t waves = (units * pair + kSms - 1) / kSms;
         const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage_ns(pair, nt) + 16 * nt + (splits > 1 ? 1100 * splits : 0);
         if (best < 0 || ns < best) {
