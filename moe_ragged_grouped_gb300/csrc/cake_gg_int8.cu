@@ -282,10 +282,13 @@ int stages_for(int pair, int nt, int splits, int E)
 }
 
 // Which kernels: by the rows M and the weights that they meet.
-//  - Up to 4 rows, or up to 8 that meet mostly experts of their own over more than
-//    16 MB: integer dot products (4 x 4096 -> 4096: 8.7 us, 9.2 from warps'
-//    registers, 9.4 on the tensor cores; 8 rows in 32 experts 6144 -> 4096: 30, 52,
-//    43 us).
+//  - Rows that meet mostly experts of their own (at most two of an expert), up to
+//    8 or up to 512 MB of weights: integer dot products (16 rows in 32 experts 4096 ->
+//    1000: 12.3 us, 21.4 from warps' registers, 19.0 on the tensor cores; 64 rows
+//    in 64, 3056 -> 2048: 51, 75, 54; 128 rows in 128, 562 MB: 74, 126, 75, 764 MB: 96,
+//    145, 90).
+//  - One or two rows, and three or four of 2048 and longer: the same (4 x 4096 ->
+//    6144: 7.1, 10.6, 17.6; but 4 x 1024 -> 5120: 4.7, 4.0, 7.1).
 //  - Up to 16 rows over at most 16 MB, up to 32 over 4 MB: warps' registers, which
 //    start at once (16 x 2048 -> 4096: 6.8 us, 8.6 on the tensor cores; 24 x 1024 ->
 //    1024: 4.7, 7.2; but 16 x 8192 -> 4096: 20.5, 12.1).
@@ -293,7 +296,8 @@ int stages_for(int pair, int nt, int splits, int E)
 int choose_path(const cake_gg_i8_plan_t &pl)
 {
     const int64_t M = pl.M_max, weights = (M < pl.E ? M : pl.E) * int64_t(pl.N) * pl.K;
-    if (M <= 4 || (M <= 8 && weights > (16 << 20) && i8_run_rows(pl.E, M, pl.T) <= 2)) return CAKE_GG_I8_ROWS;
+    const bool spread = i8_run_rows(pl.E, M, pl.T) <= 2;
+    if ((spread && (M <= 8 || weights <= (512 << 20))) || (M <= 4 && pl.K >= 2048)) return CAKE_GG_I8_ROWS;
     if ((M <= 16 && weights <= (16 << 20)) || (M <= 32 && weights <= (4 << 20))) return CAKE_GG_I8_WARPS;
     return CAKE_GG_I8_MMA;
 }
@@ -501,7 +505,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     auto status = [](cudaError_t err) { return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA; };
     if (warps && ready)
         return status(launch_i8_warps(p, static_cast<const int8_t *>(X), pl.tile_rows, pdl, s));
-    if (pl.path == CAKE_GG_I8_ROWS && (ready || i8_rows_fused(p)))
+    if (pl.path == CAKE_GG_I8_ROWS && (ready || i8_rows_fused(p, pl.act)))
         return status(launch_i8_rows(p, X, pl.x_dtype, pl.act, pdl, s));
 
     // the token pass, then the product

@@ -67,7 +67,7 @@ int launch_i8_mma(const I8MmaParams &p, const uint16_t *q, int pair, int sms, bo
 // an expert's rows.  X: the quantised tokens [T, K] (x_dtype CAKE_GG_INT8), or
 // activations where i8_rows_fused() says that the blocks quantise their rows
 // themselves.
-bool i8_rows_fused(const I8Params &p);
+bool i8_rows_fused(const I8Params &p, int act);
 int i8_run_rows(int32_t E, int64_t M, int64_t T);   // rows of a run: 1, 2 or 4
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream);
 

@@ -14,11 +14,9 @@
 // two channels a warp with four loads each 18.9, one channel 19.3, K over two
 // warps 21).
 //
-// Activations of one or two rows over few weights (up to 32 MB) are quantised by
-// every block for itself, into shared memory, while its first weights are on
-// the way: called one by one, a launch less is worth more (4096 -> 4096, one
-// token: 8.6 against 10.9 us).  Over more weights the token pass comes first:
-// every block repeats the quantising (4 x 6144 -> 4096: 18.5 against 17.5 us).
+// Activations of one or two rows over few weights may be quantised by every
+// block for itself, into shared memory, while its first weights are on the way
+// (i8_rows_fused): called one by one, a launch less is worth more.
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_quant.cuh"
 #include "cake_gg_ptx.cuh"
@@ -32,6 +30,27 @@ constexpr int kC = 4;              // channels of a warp
 constexpr int kU = 2;              // vectors of each in flight per lane
 constexpr int kFusedBytes = 32768; // rows quantised in shared memory at most
 constexpr int64_t kFusedWeights = 32 << 20;
+constexpr int64_t kFusedValues = 1 << 22, kFusedGated = 1 << 19;
+
+// Blocks of a multiprocessor: the launch bounds below hold the registers to it.
+// (Two rows at 66 registers had three: 2 x 4096 -> 4096 6.0 us, 4.5 with four.)
+constexpr int blocks_of(int R) { return R == 4 ? 3 : 4; }
+
+// K is divided over S warps while all warps still fit the multiprocessors at
+// once and each has a vector of every lane (a wave and a bit: one token 4096 ->
+// 6144 5.5 us, 4.7 with half the warps).
+int k_warps(int R, int32_t E, int64_t M, int32_t N, int32_t K)
+{
+    const int64_t runs = E > 1 ? M : (M + R - 1) / R, warps = runs * (N / kC), most = 152ll * kWarps * blocks_of(R);
+    int S = 1;
+    while (S < kWarps && warps * S * 2 <= most && 512 * S < K) S *= 2;
+    return S;
+}
+int channel_blocks(int S, int32_t N)
+{
+    const int per_block = kWarps / S * kC;
+    return (N + per_block - 1) / per_block;
+}
 
 // 16 weight bytes, read once: not kept in L1.
 __device__ __forceinline__ uint4 ld_weights(const int8_t *p)
@@ -97,7 +116,7 @@ __device__ __forceinline__ void quantise_rows(const XT *const (&x)[R], int32_t K
 // blockIdx.x = row * blocks_n + channel block.  The block whose row starts a
 // run of R of its expert's rows computes the run; the others leave.
 template <int R, typename XT, bool ACT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, blocks_of(R))
     i8_rows_kernel(const I8Params p, const XT *__restrict__ X, int blocks_n, int S)
 {
     constexpr bool kFused = sizeof(XT) > 1;
@@ -222,12 +241,7 @@ __global__ void __launch_bounds__(kThreads)
 template <int R, typename XT, bool ACT>
 cudaError_t launch(const I8Params &p, const void *X, bool pdl, cudaStream_t stream)
 {
-    // K is divided over S warps until about 4096 warps share the weights (27 a
-    // multiprocessor), as long as each has a vector of every lane
-    int S = 1;
-    while (S < kWarps && p.M / R * (p.N / kC) * S < 4096 && 512 * S < p.K) S *= 2;
-    const int per_block = kWarps / S * kC;
-    const int blocks_n = (p.N + per_block - 1) / per_block;
+    const int S = k_warps(R, p.E, p.M, p.N, p.K), blocks_n = channel_blocks(S, p.N);
     const int64_t blocks = p.M * blocks_n;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -264,11 +278,21 @@ int i8_run_rows(int32_t E, int64_t M, int64_t T)
     return most <= 2 || (E > 1 && E >= M) ? 2 : 4;
 }
 
-bool i8_rows_fused(const I8Params &p)
+// Every block repeats the quantising of its rows, against one launch less: 2.1 us
+// of the host where calls follow one another.  On the GPU the repeats cost 0.5 us
+// a million values, gated ones 5 (two readings, each with an exponential and a
+// division), and the limits leave them at most the launch's price.  Measured,
+// graph replays, repeated and with a token pass (in brackets called one by one):
+// one token 4096 -> 4096 5.0 (6.6), 3.8 (8.4) us; 8192 -> 2048, at the limit, 6.2
+// (6.5), 4.0 (8.5); 8192 -> 4096 8.4 (8.7), 5.3 (8.5); gated 2048 -> 2048 4.1 (6.6),
+// 3.5 (8.6); gated 4096 -> 4096 8.8 (9.1), 4.2 (8.5).
+bool i8_rows_fused(const I8Params &p, int act)
 {
     const int64_t bytes = (p.M < p.E ? p.M : p.E) * p.N * p.K;
     const int run = i8_run_rows(p.E, p.M, p.T);
-    return bytes <= kFusedWeights && run <= 2 && int64_t(run) * p.K <= kFusedBytes;
+    if (run > 2 || bytes * run > kFusedWeights || int64_t(run) * p.K > kFusedBytes) return false;
+    const int64_t values = p.M * p.K * channel_blocks(k_warps(run, p.E, p.M, p.N, p.K), p.N);
+    return values <= (act == CAKE_GG_ACT_NONE ? kFusedValues : kFusedGated);
 }
 
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream)
