@@ -18,6 +18,7 @@
 
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_quant.cuh"
+#include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
 
 using namespace cakegg;
@@ -67,27 +68,13 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 // ---------------------------------------------------------------- token pass
 
-// Eight integers as the FP16 operands of the tensor cores.
-__device__ __forceinline__ uint4 halves8(const float (&v)[8])
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 __device__ __forceinline__ void store8(int8_t *out, const float (&v)[8], const RowScale &s)
 {
     *reinterpret_cast<uint2 *>(out) = bytes8(v, s);
 }
 __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const RowScale &s)
 {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = s.integer(v[i]);
-    *reinterpret_cast<uint4 *>(out) = halves8(r);
+    *reinterpret_cast<uint4 *>(out) = halves8(v, s);
 }
 
 // Both kernels of the pass may run `beside` a product of other rows.  They then
@@ -165,10 +152,10 @@ __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = float(int8_t(u[h * 2 + j / 4] >> (8 * (j % 4))));
-        *reinterpret_cast<uint4 *>(Q + i * 16 + h * 8) = halves8(v);
+        uint4 o;
+        widen4(u[2 * h], o.x, o.y);
+        widen4(u[2 * h + 1], o.z, o.w);
+        *reinterpret_cast<uint4 *>(Q + i * 16 + h * 8) = o;
     }
     if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
