@@ -84,15 +84,18 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
 
 // blockDim.x threads per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
-// rest again (from L2).  Bound by HBM (3001 x 5120 FP32: 13.5 us, 5.8 TB/s read and
-// written; 8192 x 6144 BF16: 35 us), gated rows by the exponential and the division
-// (32768 x 2048: 92 us, 35 instructions a value).  Two vectors a thread was best of
-// 1 (50 us for the second), 2, 3 (42), 4 (39) and 8 (50).
+// rest again (from L2).  Bound by HBM (3001 x 5120 FP32 to FP16: 13.5 us, 5.8 TB/s
+// read and written) and by how many rows are resident, so registers are held
+// down as far as that pays (to bytes, BF16 16384 x 4096: 55 us with 50 registers, 41
+// with 32; FP32 51, 49 with 48, 69 with 32, but to FP16 3001 x 5120 the 48 lose 1 us;
+// gated BF16 92, 85 with 48); gated rows by the exponential and the division (some
+// 30 instructions a value).  Two vectors a thread was best of 1, 2 and 4 (41 us; 58
+// and 48).
 constexpr int kHeld = 2;
 constexpr int64_t kFewBlocks = 304;   // two rows a multiprocessor
 
 template <typename XT, bool ACT, typename QT>
-__global__ void __launch_bounds__(1024)
+__global__ void __maxnreg__(ACT ? 48 : sizeof(XT) == 2 ? 32 : 64)
     i8_quant_kernel(const XT *__restrict__ X, int64_t T, int32_t K, QT *__restrict__ Q, float *__restrict__ S, bool beside)
 {
     __shared__ uint32_t warp_max[32];
@@ -188,6 +191,10 @@ cudaError_t launch_quant_as(const void *X, int act, int64_t T, int32_t K, QT *Q,
     const int held = T <= kFewBlocks ? 1 : kHeld;
     int threads = int(align_up((uint64_t(K) / 8 + held - 1) / held, 32));
     if (threads > 1024) threads = 1024;
+    // many long rows: few threads each, so that several rows are resident and one's
+    // loads run beside another's barrier (8192 x 16384 BF16: 92 us with 1024, 71 with
+    // 256; but 4096 x 9216 FP32 31.7 with 576, 34.2)
+    if (T > kFewBlocks && threads > 640) threads = 256;
     if (beside && threads > 256) threads = 256;   // (what fits beside the product)
     // short rows share a block of 256 threads: with a block of one or two warps each
     // the launching of blocks is the bound (12000 x 272: 13.0 us, 5.2; 12000 x 768: 12.9,
