@@ -281,18 +281,23 @@ int stages_for(int pair, int nt, int splits, int E)
 //    1000: 12.3 us, 21.4 from warps' registers, 19.0 on the tensor cores; 64 rows
 //    in 64, 3056 -> 2048: 51, 75, 54; 128 rows in 128, 562 MB: 74, 126, 75, 764 MB: 96,
 //    145, 90).
-//  - One or two rows, and three or four of 2048 and longer: the same (4 x 4096 ->
-//    6144: 7.1, 10.6, 17.6; but 4 x 1024 -> 5120: 4.7, 4.0, 7.1).
-//  - Up to 16 rows over at most 16 MB, up to 32 over 4 MB: warps' registers, which
-//    start at once (16 x 2048 -> 4096: 6.8 us, 8.6 on the tensor cores; 24 x 1024 ->
-//    1024: 4.7, 7.2; but 16 x 8192 -> 4096: 20.5, 12.1).
+//  - One or two rows, three or four of 2048 and longer, and up to 16 long ones
+//    of few channels: the same (4 x 4096 -> 6144: 7.1, 10.6, 17.6; but 4 x 1024 ->
+//    5120: 4.7, 4.0, 7.1; 6 x 8192 -> 256: 4.8, 11.3, 9.2; 12 x 4096 -> 256: 5.1, 7.7, 8.1).
+//  - Up to 16 rows up to 4608 long over at most 16 MB, up to 32 up to 3200 long of
+//    2048 channels: warps' registers, which start at once (16 x 2048 -> 4096: 6.6 us,
+//    8.7 on the tensor cores; 32 x 2816 -> 1024: 8.0, 8.2; 24 x 1024 -> 2048: 4.7, 7.3;
+//    but 16 x 8192 -> 1024: 15.8, 9.6; 32 x 1024 -> 4096: 9.5, 7.3).
 //  - Else the tensor cores.
 int choose_path(const cake_gg_i8_plan_t &pl)
 {
-    const int64_t M = pl.M_max, weights = (M < pl.E ? M : pl.E) * int64_t(pl.N) * pl.K;
+    const int64_t M = pl.M_max, channels = (M < pl.E ? M : pl.E) * int64_t(pl.N), weights = channels * pl.K;
     const bool spread = i8_run_rows(pl.E, M, pl.T) <= 2;
-    if ((spread && (M <= 8 || weights <= (512 << 20))) || (M <= 4 && pl.K >= 2048)) return CAKE_GG_I8_ROWS;
-    if ((M <= 16 && weights <= (16 << 20)) || (M <= 32 && weights <= (4 << 20))) return CAKE_GG_I8_WARPS;
+    if ((spread && (M <= 8 || weights <= (512 << 20))) || (M <= 4 && (pl.K >= 2048 || weights > (16 << 20))) ||
+        (pl.E == 1 && M <= 16 && pl.K > 2560 && M * pl.N <= 8192))
+        return CAKE_GG_I8_ROWS;
+    if ((M <= 16 && weights <= (16 << 20) && pl.K <= 4608) || (M <= 32 && channels <= 2048 && pl.K <= 3200))
+        return CAKE_GG_I8_WARPS;
     return CAKE_GG_I8_MMA;
 }
 
@@ -351,7 +356,8 @@ int choose_first(const cake_gg_i8_plan_t &pl)
 // Shape of the tensor-core path, from a model of its time in nanoseconds: waves
 // of units over the multiprocessors (152, or 76 pairs), the stages of a unit,
 // the storing of the last one, and the exchange between the CTAs that share a
-// tile.  The times of a stage were measured with all multiprocessors at work
+// tile (33 x 4608 -> 496 over 1, 2, 3, 4, 6, 8 CTAs, 32 rows a tile: 15.6, 12.0, 10.7, 9.7,
+// 9.2, 8.7 us; 247 x 4528 -> 304, 64 rows: 17.4, 14.9, 12.6, 11.4, 12.5, 11.9).  The times of a stage were measured with all multiprocessors at work
 // (12288 x 4096 -> 4096): pairs 323, 358, 368, 432, 473 ns for 64, 96, 128, 160,
 // 192 rows, single CTAs 314, 348, 382, 451 ns for 32, 64, 96, 128.  (Pairs of 256
 // rows hold one accumulator, whose storing nothing overlaps: 774 ns.)  What it
@@ -368,7 +374,7 @@ void choose_mma(cake_gg_i8_plan_t *pl)
         const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
         if (splits > 1 && (units * splits > cluster_sms(splits) || n_kb < 2 * splits)) return;
         const int64_t waves = (units * pair + kSms - 1) / kSms;
-        const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage_ns(pair, nt) + 16 * nt + (splits > 1 ? 1100 * splits : 0);
+        const int64_t ns = waves * ((n_kb + splits - 1) / splits) * stage_ns(pair, nt) + 16 * nt + (splits > 1 ? 300 + nt * (45 + 4 * splits) : 0);
         if (best < 0 || ns < best) {
             best = ns;
             pl->pair = pair;
