@@ -23,11 +23,13 @@
 // 1.99), decoding batches by the weights' bytes (64 tokens through 4 of 32 experts
 // 6144 -> 4096: 6.2 TB/s over the call).
 //
-// Roles of a CTA: warp 0 copies weights, warp 1 issues MMAs, warps 2-5 scale and
-// store, warps 6-13 convert (two groups on alternate stages), warp 14 copies
-// rows, or, where they are routed, warps 14-17 gather them, two on every other
-// stage (the first issue of a batch of copies takes a few hundred clocks: all
-// four on every stage were late).
+// Roles of a CTA: warp 0 copies weights, warp 1 issues MMAs, warps 2-9 scale and
+// store (two groups on alternate 32 rows of a tile; with one group short
+// reductions wait for it: 20000 x 512 -> 4096 104 us, 88 with two and a tile's scales
+// loaded during the one before, long ones 0.5 % less), warps 10-17 convert (two
+// groups on alternate stages), warp 18 copies rows, or, where they are routed,
+// warps 18-21 gather them, two on every other stage (the first issue of a batch
+// of copies takes a few hundred clocks: all four on every stage were late).
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
@@ -35,16 +37,17 @@
 namespace cakegg {
 namespace {
 
-constexpr int kThreads = 480, kThreadsRouted = 576;
-constexpr int kConvWarp0 = 6;
+constexpr int kThreads = 608, kThreadsRouted = 704;
+constexpr int kStoreWarp0 = 2, kStoreWarps = 8, kStoreThreads = kStoreWarps * 32;
+constexpr int kConvWarp0 = 10;
 constexpr int kKB = 128;                     // reduction length of a stage
 constexpr uint32_t kWBytes = 128 * kKB;      // 8-bit weight tile of a stage
 constexpr int kStagesMax = 12;
 constexpr int kSlotsMax = 8;
-constexpr int kRowsWarp0 = 14;
+constexpr int kRowsWarp0 = 18;
 constexpr int kGatherWarps = 4;
 constexpr int kRowsPerCta = 128;             // B rows of a CTA at most
-constexpr uint32_t kOutTile = 32 * 32 * 4;   // 32 rows x 32 channels of output, per storing warp
+constexpr uint32_t kOutTile = 2048;           // 32 BF16 or 16 FP32 rows x 32 channels of output, per storing warp
 constexpr uint32_t kSlotCols = kKB / 2;      // tensor memory columns of a widened weight tile
 constexpr uint64_t kDrainNs = 20000000ull;
 
@@ -220,7 +223,7 @@ struct Walk {
 };
 
 template <int PAIR, bool OUT_F32>
-__global__ void __launch_bounds__(kThreadsRouted, 1)
+__global__ void __maxnreg__(80)
     i8_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                   const I8MmaParams p)
 {
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
     float *recv = reinterpret_cast<float *>(after);              // split: [split][channel][columns + 4]
     after += p.splits > 1 ? split_bytes(p.nt, p.splits) : 0;
     uint8_t *out_tile = after;                                   // [warp][row][32 channels]
-    after += 4 * kOutTile;
+    after += kStoreWarps * kOutTile;
     Ctrl *c = reinterpret_cast<Ctrl *>(after);
     float *xs_tile = reinterpret_cast<float *>(c + 1);           // [2][nt]
     int32_t *row_ids = reinterpret_cast<int32_t *>(xs_tile + 2 * p.nt);   // [gathering warp][row]
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         for (int a = 0; a < p.slots; ++a) mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);   // the group's warps, of both CTAs
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c->tfull[b]), 1);
-            mbar_init(smem_u32(&c->tempty[b]), 4u * PAIR);       // storing warps, of both CTAs
+            mbar_init(smem_u32(&c->tempty[b]), uint32_t(kStoreWarps) * PAIR);       // storing warps, of both CTAs
         }
         mbar_init(smem_u32(&c->drain), 1);
         fence_barrier_init();
@@ -405,44 +408,60 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         // ======================= scales and stores =======================
         grid_dependency_wait();                                  // the token scales
         const int q = warp & 3;                                  // tensor memory lanes 32 q ..
+        const int side = (warp - kStoreWarp0) >> 2;              // which 32 rows of 64
         Turn acc, xb;
-        for (Walk w(unit0, step, p.n_ct); w.g < tiles; w.next()) {
-            const Tile t = w.tile(p.nt, off, pref);
-            float *xs = xs_tile + xb.at * p.nt;
-            for (int j = tid - 64; j < t.rows; j += 128) {
-                int64_t r = t.m0 + j;
+        // A tile's scales (a row and a channel of each thread) are loaded while the
+        // tile before it is stored.
+        static_assert(kStoreThreads >= 192, "a row a thread");
+        const int mine = tid - 32 * kStoreWarp0;
+        float x_next = 0.0f, ws_next = 0.0f;
+        auto scales = [&](const Tile &t) {
+            if (mine < t.rows) {
+                int64_t r = t.m0 + mine;
                 if (p.b.rows) r = p.b.rows[r];
                 const bool bad = r < 0 || r >= p.b.T;
                 if (bad) atomicCAS(p.b.status, 0, kI8StatusBadRows);
-                xs[j] = bad ? 0.0f : p.b.xs[r];
+                x_next = bad ? 0.0f : p.b.xs[r];
             }
             const int n = (t.ct * PAIR + half) * 128 + q * 32 + lane;
-            const bool ch_ok = n < p.b.N;
-            const float ws = ch_ok ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
+            ws_next = n < p.b.N ? p.b.ws[int64_t(t.e) * p.b.N + n] : 0.0f;
+        };
+        Walk w(unit0, step, p.n_ct);
+        Tile t = {}, t_next = {};
+        if (w.g < tiles) scales(t_next = w.tile(p.nt, off, pref));
+        while (w.g < tiles) {
+            t = t_next;
+            float *xs = xs_tile + xb.at * p.nt;
+            if (mine < t.rows) xs[mine] = x_next;
+            const float ws = ws_next;
+            const int n = (t.ct * PAIR + half) * 128 + q * 32 + lane;
             const int buf = acc.at;
             const bool ok = warp_wait(smem_u32(&c->tfull[buf]), acc.parity, c, p.b);
             // the scales are in (their buffer is rewritten two tiles on, after the
-            // barrier between), and the four warps go on or give up together
-            if (!named_bar_and(1, 128, ok)) break;
+            // barrier between), and the warps go on or give up together
+            if (!named_bar_and(1, kStoreThreads, ok)) break;
             tc_fence_after_sync();
+            w.next();
+            if (w.g < tiles) scales(t_next = w.tile(p.nt, off, pref));
             const uint32_t d = tmem + uint32_t(buf) * d_stride + (uint32_t(q * 32) << 16);
             const int per = split_columns(t.rows, p.splits);
-            uint8_t *tile = out_tile + q * kOutTile;
-            int owner = 0, col = 0;                              // split: where the next columns go
-            uint32_t to = p.splits > 1 ? map_to_cta(smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4)), 0u) : 0u;
+            uint8_t *tile = out_tile + (warp - kStoreWarp0) * kOutTile;
             ws_split = ws;
-            for (int c0 = 0; c0 < t.rows; c0 += 32) {
+            for (int c0 = 32 * side; c0 < t.rows; c0 += 64) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(d + uint32_t(c0), r);
                 tmem_ld_wait();
                 if (p.splits > 1) {
                     // four columns at a time to the CTA that sums them
+                    const uint32_t mine = smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4));
+                    int owner = c0 / per, col = c0 - owner * per;
+                    uint32_t to = map_to_cta(mine, uint32_t(owner));
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         if (c0 + j < t.rows) {
                             if (col == per) {
                                 col = 0;
-                                to = map_to_cta(smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4)), uint32_t(++owner));
+                                to = map_to_cta(mine, uint32_t(++owner));
                             }
                             st_cluster_v4(to + uint32_t(col) * 4u,
                                           make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
@@ -451,35 +470,39 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
                         }
                     continue;
                 }
-                // through shared memory, transposed: a lane writes its channel of 32
+                // through shared memory, transposed: a lane writes its channel of kRows
                 // rows, then stores 16 bytes of a row's channels at a time
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 x4 = *reinterpret_cast<const float4 *>(xs + c0 + j);
-                    const float v[4] = {__uint_as_float(r[j]) * ws * x4.x, __uint_as_float(r[j + 1]) * ws * x4.y,
-                                        __uint_as_float(r[j + 2]) * ws * x4.z, __uint_as_float(r[j + 3]) * ws * x4.w};
-                    if (OUT_F32) {
-                        float *dst = reinterpret_cast<float *>(tile) + j * 32 + lane;
-                        dst[0] = v[0], dst[32] = v[1], dst[64] = v[2], dst[96] = v[3];
-                    } else {
-                        const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
-                        uint16_t *dst = reinterpret_cast<uint16_t *>(tile) + j * 32 + lane;
-                        dst[0] = uint16_t(a & 0xffffu), dst[32] = uint16_t(a >> 16);
-                        dst[64] = uint16_t(b & 0xffffu), dst[96] = uint16_t(b >> 16);
-                    }
-                }
-                __syncwarp();
-                constexpr int kSize = OUT_F32 ? 4 : 2, kPieces = 2 * kSize, kPer = 16 / kSize;   // 16-byte pieces of a row
+                constexpr int kSize = OUT_F32 ? 4 : 2, kRows = int(kOutTile) / (32 * kSize);
+                constexpr int kPieces = 2 * kSize, kPer = 16 / kSize;   // 16-byte pieces of a row
                 const int piece = lane % kPieces, nv = n - lane + piece * kPer;
-                uint8_t *y = static_cast<uint8_t *>(p.b.Y) + ((int64_t(t.m0) + c0) * p.b.N + nv) * kSize;
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int row = lane / kPieces + i * (32 / kPieces);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * (32 * kSize) + piece * 16);
-                    if (c0 + row < t.rows && nv < p.b.N)
-                        *reinterpret_cast<uint4 *>(y + int64_t(row) * p.b.N * kSize) = v;
+                for (int h = 0; h < 32; h += kRows) {
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 4) {
+                        const float4 x4 = *reinterpret_cast<const float4 *>(xs + c0 + h + j);
+                        const float v[4] = {__uint_as_float(r[h + j]) * ws * x4.x, __uint_as_float(r[h + j + 1]) * ws * x4.y,
+                                            __uint_as_float(r[h + j + 2]) * ws * x4.z, __uint_as_float(r[h + j + 3]) * ws * x4.w};
+                        if (OUT_F32) {
+                            float *dst = reinterpret_cast<float *>(tile) + j * 32 + lane;
+                            dst[0] = v[0], dst[32] = v[1], dst[64] = v[2], dst[96] = v[3];
+                        } else {
+                            const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+                            uint16_t *dst = reinterpret_cast<uint16_t *>(tile) + j * 32 + lane;
+                            dst[0] = uint16_t(a & 0xffffu), dst[32] = uint16_t(a >> 16);
+                            dst[64] = uint16_t(b & 0xffffu), dst[96] = uint16_t(b >> 16);
+                        }
+                    }
+                    __syncwarp();
+                    uint8_t *y = static_cast<uint8_t *>(p.b.Y) + ((int64_t(t.m0) + c0 + h) * p.b.N + nv) * kSize;
+#pragma unroll
+                    for (int i = 0; i < kRows * kPieces / 32; ++i) {
+                        const int row = lane / kPieces + i * (32 / kPieces);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * (32 * kSize) + piece * 16);
+                        if (c0 + h + row < t.rows && nv < p.b.N)
+                            *reinterpret_cast<uint4 *>(y + int64_t(row) * p.b.N * kSize) = v;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             tc_fence_before_sync();
             __syncwarp();
@@ -503,7 +526,6 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         Turn st, sl, last;
         if (group) st.next(p.stages), sl.next(p.slots);
         int it = group, kb = group;
-        bool ok = true;
         Walk w(unit0, step, p.n_ct);
         auto widen = [&](const uint8_t *src, int h, uint32_t (&f)[32]) {
 #pragma unroll
@@ -632,13 +654,13 @@ __global__ void __launch_bounds__(kThreadsRouted, 1)
         __syncwarp();
         cluster_sync_all();
         Walk w(unit0, step, p.n_ct);
-        if (warp >= 2 && warp < kConvWarp0 && w.g < tiles && !aborted(c)) {
+        if (warp >= kStoreWarp0 && warp < kConvWarp0 && w.g < tiles && !aborted(c)) {
             const Tile t = w.tile(p.nt, off, pref);
             const int per = split_columns(t.rows, p.splits);
             const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
             const float ws = ws_split;
             const int m0 = rank * per;
-            for (int j0 = 0; j0 < per && m0 + j0 < t.rows; j0 += 16) {
+            for (int j0 = 16 * ((warp - kStoreWarp0) >> 2); j0 < per && m0 + j0 < t.rows; j0 += 32) {
                 // up to 16 rows at a time: their loads do not wait for each other's sums
                 float4 sum[4];
                 for (int v = 0; v < p.splits; ++v)
@@ -727,7 +749,7 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaPara
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
     return 1024 + size_t(stages) * (kWBytes + size_t(nt / pair) * 256) +
-           (splits > 1 ? split_bytes(nt, splits) : 0) + 4 * kOutTile + sizeof(Ctrl) + size_t(2 * nt) * 4 +
+           (splits > 1 ? split_bytes(nt, splits) : 0) + kStoreWarps * kOutTile + sizeof(Ctrl) + size_t(2 * nt) * 4 +
            size_t(kGatherWarps * kRowsPerCta / 2) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
