@@ -460,3 +460,55 @@ def test_first_product_by_its_own_rule(E):
     graph.replay()
     graph.replay()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,K", [(305, 16), (700, 272), (401, 512), (333, 528), (306, 1040), (310, 11008)])
+@pytest.mark.parametrize("act", [None, "silu_mul"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_quantize_many_rows(T, K, act, dtype):
+    """More rows than blocks of a row each start at once: several short rows in a block, the last block
+    with fewer, and long rows by fewer threads.  Each row is what the same row alone gives (bit for bit:
+    its values do not depend on the threads that share it)."""
+    import torch
+    x = _rows_of(T, 2 * K if act else K, torch.bfloat16 if dtype == "bf16" else torch.float32, T)
+    q, s = gg.quantize_rows(x, act=act)
+    for rows in (slice(0, 5), slice(T // 2, T // 2 + 3), slice(T - 3, T)):
+        one_q, one_s = gg.quantize_rows(x[rows].contiguous(), act=act)
+        assert torch.equal(q[rows], one_q) and torch.equal(s[rows], one_s)
+    wide = q.int().abs().max(dim=1).values
+    assert (wide == 127).all()                                   # the largest value of a row is 127
+
+
+@pytest.mark.parametrize("sizes", [[5, 0, 3, 0, 0, 4, 0, 0, 0, 0, 0, 0], [12] + [0] * 11, [0] * 15 + [16], [1, 2] * 8 + [0] * 8])
+@pytest.mark.parametrize("x_dtype", ["int8", "bf16"])
+def test_few_rows_of_many_experts_that_meet(sizes, x_dtype):
+    """Plans for rows that meet experts of their own, with rows that do not: longer runs than planned for."""
+    import torch
+    E, M, N, K = len(sizes), sum(sizes), 136, 2064
+    rng = np.random.default_rng(M)
+    W, ws = _ints((E, N, K), rng), _scales((E, N), rng)
+    assert gg.cake_gg_i8_plan(E, M, M, N, K, x_dtype, None, "bf16").path == 0
+    if x_dtype == "int8":
+        q, xs = _ints((M, K), rng), _scales(M, rng)
+        got = gg.int8_gemm(q, W, ws, xs=xs, offsets=_offsets(sizes))
+    else:
+        x = _rows_of(M, K, torch.bfloat16, 3)
+        q, xs = gg.quantize_rows(x)
+        got = gg.int8_gemm(x, W, ws, offsets=_offsets(sizes))
+    _close(got, _want(q, xs, W, ws, sizes), "bf16")
+
+
+@pytest.mark.parametrize("K", [16, 144, 400])
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+def test_short_reductions(K, out_dtype):
+    """One to four stages a tile and many tiles a CTA: a tile's scales are loaded during the one before."""
+    import torch
+    sizes = [700, 0, 1, 3000, 64, 33, 2000, 202]
+    E, M, N, T = len(sizes), sum(sizes), 904, 1500
+    rng = np.random.default_rng(K)
+    q, W, xs, ws = _ints((T, K), rng), _ints((E, N, K), rng), _scales(T, rng), _scales((E, N), rng)
+    rows = torch.from_numpy(rng.integers(0, T, size=M).astype(np.int32)).cuda()
+    want = _want(q, xs, W, ws, sizes, rows)
+    for cap in (0, 3):
+        got = gg.int8_gemm(q, W, ws, xs=xs, offsets=_offsets(sizes), rows=rows, out_dtype=out_dtype, max_sms=cap)
+        _close(got, want, out_dtype)
