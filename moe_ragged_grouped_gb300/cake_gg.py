@@ -455,6 +455,25 @@ def _i8_x_name(X):
     return name
 
 
+_raw_device = None
+
+
+def _current_device():
+    """The current CUDA device's index (asked only with a CUDA tensor in hand)."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_device()
+
+
+def _refuse_device(tensor):
+    """Raises: the kernels launch on the current CUDA device and take its addresses only."""
+    if tensor.get_device() < 0:
+        raise ValueError(f"the tensors are on {tensor.device}: CUDA tensors are needed")
+    raise ValueError(f"the tensors are on {tensor.device}, the current CUDA device is {_current_device()}")
+
+
 def _need(tensor, name, dtype, shape, device):
     """A dense tensor of this type and shape on `device`."""
     if tensor.dtype != dtype:
@@ -474,7 +493,8 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     The scale of a row is its largest magnitude / 127; integers are rounded to
     nearest, ties to even.  A row that holds a NaN or an infinity gets the scale
     NaN and zeros, one whose values are all below 2^-120 the scale 0 and zeros.
-    Quantising W.reshape(E * N, K) gives int8_gemm's weights.
+    Quantising W.reshape(E * N, K) gives int8_gemm's weights.  All tensors are on
+    the current CUDA device (others are refused).
     """
     import torch
     name = _i8_x_name(X)
@@ -484,12 +504,16 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
         raise ValueError("X is [T, K], or [T, 2 K] with an activation")
     T, K = int(X.shape[0]), int(X.shape[1]) // (1 if act is None else 2)
     _need(X, "X", X.dtype, tuple(X.shape), X.device)
+    if out is not None:
+        _need(out, "out", torch.int8, (T, K), X.device)
+    if scale is not None:
+        _need(scale, "scale", torch.float32, (T,), X.device)
+    if X.get_device() < 0 or X.get_device() != _current_device():
+        _refuse_device(X)
     if out is None:
         out = torch.empty((T, K), dtype=torch.int8, device=X.device)
     if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=X.device)
-    _need(out, "out", torch.int8, (T, K), X.device)
-    _need(scale, "scale", torch.float32, (T,), X.device)
     rc = cake_gg_i8_quant(X, name, act, T, K, out, scale, stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_i8_quant")
@@ -508,7 +532,8 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     X is the tokens: int8 [T, K] with their scales xs [T], or bf16 / fp32
     [T, K] quantised on the way ([T, 2 K] with act="silu_mul", see
     quantize_rows).  Rows >= offsets[E] of Y are left as allocated.  Output and
-    workspace are allocated through torch when not given.
+    workspace are allocated through torch when not given.  All tensors are on
+    the current CUDA device (others are refused).
     """
     names, i8, f32, i32 = _i8_types or _i8_torch()
     name = names.get(X.dtype) or _i8_x_name(X)
@@ -547,16 +572,20 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
     elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], I8_ACTS[act], _dtype_code(out_dtype)):
         raise ValueError("the plan is another problem's")
+    if out is not None and not (out.dtype is _torch_out_dtype(out_dtype) and out.shape == (M, N)
+                                and out.is_contiguous() and out.get_device() == on):
+        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), W.device)
+    if on < 0 or on != _current_device():
+        _refuse_device(W)
+    if workspace is not None and workspace.get_device() != on:
+        raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
     if out is None:
         import torch
         out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=W.device)
-    elif not (out.dtype is _torch_out_dtype(out_dtype) and out.shape == (M, N) and out.is_contiguous()
-              and out.get_device() == on):
-        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), W.device)
     if workspace is None:
         workspace = make_workspace(plan, W.device)
     if stream is None:
-        stream = _current_stream(on) if on >= 0 else 0
+        stream = _current_stream(on)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     # (the call of cake_gg_i8_gemm() above, without its conversions: a short product's
