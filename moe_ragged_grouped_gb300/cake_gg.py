@@ -365,6 +365,31 @@ def _torch_out_dtype(out_dtype):
     return torch.float32 if _dtype_code(out_dtype) == CAKE_GG_FP32 else torch.bfloat16
 
 
+def _for_stream(stream, device, make, result=False):
+    """make()'s tensor as memory of `stream` (None: the current one).
+
+    What a call on another stream than the current one writes has to come from
+    that stream's memory and be filled in its order: filled on the current
+    stream, a workspace could be cleared under the running product, and its
+    memory would go back to a pool that does not wait for the product.  The
+    caller reads a result on the current stream, so its memory waits for both.
+    """
+    if stream is None or device.type != "cuda":
+        return make()
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle == _current_stream(device.index):
+        return make()
+    import torch
+    current = torch.cuda.current_stream(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        tensor = make()
+    if result:
+        tensor.record_stream(current)
+    return tensor
+
+
 def make_workspace(plan, device):
     """A zero-filled workspace of plan.workspace_bytes (the library expects zeros before first use)."""
     import torch
@@ -374,7 +399,7 @@ def make_workspace(plan, device):
 
 def grouped_gemm(pass_, a, b, offsets, out_dtype="bf16", deterministic=True, max_sms=0, out=None,
                  plan=None, workspace=None, stream=None, check=True):
-    """Run one pass on torch CUDA tensors, allocating the output and workspace through torch.
+    """Run one pass on torch CUDA tensors, allocating the output and workspace through torch (for `stream`).
 
     fwd:   a = X [M, K], b = W [E, N, K] -> Y [M, N]
     dgrad: a = G [M, N], b = W [E, N, K] -> dX [M, K]
@@ -397,9 +422,10 @@ def grouped_gemm(pass_, a, b, offsets, out_dtype="bf16", deterministic=True, max
     if plan is None:
         plan = cake_gg_plan(p, E, M, N, K, out_dtype, deterministic, max_sms)
     if out is None:
-        out = torch.empty(shape, dtype=_torch_out_dtype(out_dtype), device=a.device)
+        out = _for_stream(stream, a.device, lambda: torch.empty(shape, dtype=_torch_out_dtype(out_dtype), device=a.device),
+                          result=True)
     if workspace is None:
-        workspace = make_workspace(plan, a.device)
+        workspace = _for_stream(stream, a.device, lambda: make_workspace(plan, a.device))
     fn = {CAKE_GG_FWD: cake_gg_fwd, CAKE_GG_DGRAD: cake_gg_dgrad, CAKE_GG_WGRAD: cake_gg_wgrad}[p]
     rc = fn(plan, a, b, out, offsets, out_dtype, deterministic, workspace, stream=stream)
     if rc != CAKE_GG_OK:
@@ -414,7 +440,7 @@ def grouped_gemm(pass_, a, b, offsets, out_dtype="bf16", deterministic=True, max
 def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=None, check=True):
     """FP32 router logits Y [T, R] = X [T, K] W [R, K]^T by BF16x3 emulation (float32 torch tensors).
 
-    Allocates the output and the workspace through torch when not given.
+    Allocates the output and the workspace through torch (for `stream`) when not given.
     """
     import torch
     T, K = int(X.shape[0]), int(X.shape[1])
@@ -422,9 +448,9 @@ def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=Non
     if plan is None:
         plan = cake_gg_router_plan(T, R, K, max_sms)
     if out is None:
-        out = torch.empty((T, R), dtype=torch.float32, device=X.device)
+        out = _for_stream(stream, X.device, lambda: torch.empty((T, R), dtype=torch.float32, device=X.device), result=True)
     if workspace is None:
-        workspace = torch.zeros(max(int(plan.workspace_bytes), 256), dtype=torch.uint8, device=X.device)
+        workspace = _for_stream(stream, X.device, lambda: make_workspace(plan, X.device))
     rc = cake_gg_router_fp32(plan, X, W, out, workspace, stream=stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_router_fp32")
@@ -494,7 +520,7 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     nearest, ties to even.  A row that holds a NaN or an infinity gets the scale
     NaN and zeros, one whose values are all below 2^-120 the scale 0 and zeros.
     Quantising W.reshape(E * N, K) gives int8_gemm's weights.  All tensors are on
-    the current CUDA device (others are refused).
+    the current CUDA device (others are refused); stream as in int8_gemm.
     """
     import torch
     name = _i8_x_name(X)
@@ -511,9 +537,9 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     if X.get_device() < 0 or X.get_device() != _current_device():
         _refuse_device(X)
     if out is None:
-        out = torch.empty((T, K), dtype=torch.int8, device=X.device)
+        out = _for_stream(stream, X.device, lambda: torch.empty((T, K), dtype=torch.int8, device=X.device), result=True)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=X.device)
+        scale = _for_stream(stream, X.device, lambda: torch.empty(T, dtype=torch.float32, device=X.device), result=True)
     rc = cake_gg_i8_quant(X, name, act, T, K, out, scale, stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_i8_quant")
@@ -532,8 +558,13 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     X is the tokens: int8 [T, K] with their scales xs [T], or bf16 / fp32
     [T, K] quantised on the way ([T, 2 K] with act="silu_mul", see
     quantize_rows).  Rows >= offsets[E] of Y are left as allocated.  Output and
-    workspace are allocated through torch when not given.  All tensors are on
-    the current CUDA device (others are refused).
+    workspace are allocated through torch when not given, as memory of `stream`.
+    All tensors are on the current CUDA device (others are refused).
+
+    stream (a torch stream or a cudaStream_t value; none: the current stream)
+    is where the kernels go.  On another stream than the current one the caller
+    orders them after what wrote the inputs, and whatever reads the output, or
+    writes or frees the inputs, after them.
     """
     names, i8, f32, i32 = _i8_types or _i8_torch()
     name = names.get(X.dtype) or _i8_x_name(X)
@@ -581,9 +612,10 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
     if out is None:
         import torch
-        out = torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=W.device)
+        out = _for_stream(stream, W.device, lambda: torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=W.device),
+                          result=True)
     if workspace is None:
-        workspace = make_workspace(plan, W.device)
+        workspace = _for_stream(stream, W.device, lambda: make_workspace(plan, W.device))
     if stream is None:
         stream = _current_stream(on)
     elif not isinstance(stream, int):
