@@ -13,11 +13,14 @@ The layer chains the library's calls as a server does: the FP32 router GEMM,
 the grouped 8-bit product over rows routed by index (tokens quantised once,
 gathered by expert), and the second grouped product, whose rows are gated and
 quantised on the way.  Weights are quantised per output channel when the layer
-is made.  Plans, workspaces and the products' outputs are kept per token count,
-device and stream and reused, as the workspace contract allows; y is a new
-tensor each call.
+is made.  Plans, workspaces and the products' outputs are kept per thread, token
+count, device and stream and reused, as the workspace contract allows; y is a
+new tensor each call.  Threads may call one layer at the same time, on one
+stream or several.
 """
 from __future__ import annotations
+
+import threading
 
 import torch
 
@@ -38,7 +41,7 @@ class Int8Experts:
         self.router = router.float().contiguous()
         self.up_q, self.up_s = self._quantise(gate_up)
         self.down_q, self.down_s = self._quantise(down)
-        self._kept = {}
+        self._mine = threading.local()   # a thread's calls may interleave with another's on one stream
 
     @staticmethod
     def _quantise(w):
@@ -49,7 +52,8 @@ class Int8Experts:
     def _for(self, T, device):
         """What a call of T tokens reuses: plans, workspaces, and the two products' outputs."""
         key = (T, str(device), torch.cuda.current_stream(device).cuda_stream)
-        kept = self._kept.get(key)
+        mine = self._mine.__dict__
+        kept = mine.get(key)
         if kept is None:
             M = T * self.top_k
             route = gg.cake_gg_router_plan(T, self.E, self.K)
@@ -60,7 +64,7 @@ class Int8Experts:
                 (up, gg.make_workspace(up, device), torch.empty((M, 2 * self.F), dtype=torch.bfloat16, device=device)),
                 (down, gg.make_workspace(down, device), torch.empty((M, self.K), dtype=torch.float32, device=device)),
             )
-            self._kept[key] = kept
+            mine[key] = kept
         return kept
 
     def route(self, x):

@@ -1,0 +1,92 @@
+"""What the quantised expert layer keeps between calls, and who may use it."""
+import threading
+
+import pytest
+
+from moe_ragged_grouped_gb300 import build as gg_build
+from moe_ragged_grouped_gb300 import cake_gg as gg
+
+
+class FakeStream:
+    cuda_stream = 0x1000
+
+
+@pytest.fixture
+def host_layer(monkeypatch):
+    """A layer on the CPU: its calls' buffers can be made there, its kernels cannot run."""
+    import torch
+    from moe_ragged_grouped_gb300 import experts
+    gg_build.build()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: FakeStream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(experts.gg, "quantize_rows",
+                        lambda w: (torch.zeros(w.shape, dtype=torch.int8), torch.zeros(w.shape[0])))
+    z = torch.zeros
+    return experts.Int8Experts(z(8, 64), z(8, 64, 64), z(8, 64, 32), 2)
+
+
+def _tensors(kept):
+    import torch
+    if isinstance(kept, torch.Tensor):
+        return [kept]
+    return [t for part in kept for t in _tensors(part)] if isinstance(kept, tuple) else []
+
+
+def test_threads_do_not_share_what_a_call_writes(host_layer):
+    """Two threads' calls interleave on one stream: the first product of one may come between
+    the two products of the other, and each call's token pass before the other's product."""
+    import torch
+    device, got = torch.device("cpu"), []
+    got.append(_tensors(host_layer._for(40, device)))
+    thread = threading.Thread(target=lambda: got.append(_tensors(host_layer._for(40, device))))
+    thread.start()
+    thread.join(60)
+    mine, other = ({t.untyped_storage().data_ptr() for t in got[i]} for i in range(2))
+    assert len(got[0]) == len(got[1]) >= 4 and not mine & other
+
+
+def _gpu_layer(E=8, K=256, F=144, top=3):
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    gg_build.build()
+    from moe_ragged_grouped_gb300.experts import Int8Experts
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    return Int8Experts(rand(E, K) / K ** 0.5, rand(E, 2 * F, K) / K ** 0.5, rand(E, K, F) / F ** 0.5, top), rand
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 333])
+def test_two_threads_on_one_stream(T, monkeypatch):
+    """Calls of two threads, made to alternate after every product, give what each gives alone."""
+    import torch
+    layer, rand = _gpu_layer()
+    xs = [rand(T, 256).to(torch.bfloat16) for _ in range(2)]
+    want = [layer(x).clone() for x in xs]
+    torch.cuda.synchronize()
+    product, turn, got, failed = gg.int8_gemm, threading.Barrier(2), [None, None], []
+
+    def after_both(*args, **more):
+        out = product(*args, **more)
+        turn.wait(60)
+        return out
+
+    monkeypatch.setattr(gg, "int8_gemm", after_both)
+
+    def call(i):
+        try:
+            got[i] = [layer(xs[i]).clone() for _ in range(3)]
+        except Exception as e:   # noqa: BLE001 (shown by the assertion)
+            failed.append(e)
+            turn.abort()
+
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not failed
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
