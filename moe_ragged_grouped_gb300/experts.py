@@ -13,18 +13,27 @@ The layer chains the library's calls as a server does: the FP32 router GEMM,
 the grouped 8-bit product over rows routed by index (tokens quantised once,
 gathered by expert), and the second grouped product, whose rows are gated and
 quantised on the way.  Weights are quantised per output channel when the layer
-is made.  Plans, workspaces and the products' outputs are kept per thread, token
-count, device and stream and reused, as the workspace contract allows; y is a
-new tensor each call.  Threads may call one layer at the same time, on one
-stream or several.
+is made.  Each thread keeps, for each device and stream, a workspace of the
+largest size that it needed there and the two products' outputs of its last
+call, which the next call of as many tokens writes again; y is a new tensor each
+call.  Threads may call one layer at the same time, on one stream or several.
+A call that is being captured in a CUDA graph has buffers of the graph's own.
 """
 from __future__ import annotations
 
+import functools
 import threading
 
 import torch
 
 from . import cake_gg as gg
+
+
+def _plans(E, K, F, top_k, T):
+    """Plans of a layer's call of T tokens: the router's, and the two products'."""
+    M = T * top_k
+    return (gg.cake_gg_router_plan(T, E, K), gg.cake_gg_i8_plan(E, M, T, 2 * F, K, "bf16", None, "bf16"),
+            gg.cake_gg_i8_plan(E, M, M, K, F, "bf16", "silu_mul", "fp32"))
 
 
 class Int8Experts:
@@ -41,6 +50,7 @@ class Int8Experts:
         self.router = router.float().contiguous()
         self.up_q, self.up_s = self._quantise(gate_up)
         self.down_q, self.down_s = self._quantise(down)
+        self._planned = functools.lru_cache(maxsize=256)(functools.partial(_plans, E, K, F, top_k))
         self._mine = threading.local()   # a thread's calls may interleave with another's on one stream
 
     @staticmethod
@@ -50,26 +60,36 @@ class Int8Experts:
         return q.view(E, N, K), s.view(E, N)
 
     def _for(self, T, device):
-        """What a call of T tokens reuses: plans, workspaces, and the two products' outputs."""
-        key = (T, str(device), torch.cuda.current_stream(device).cuda_stream)
-        mine = self._mine.__dict__
-        kept = mine.get(key)
-        if kept is None:
+        """A call's plans, each with its workspace, and the two products' outputs."""
+        route, up, down = self._planned(T)
+        if torch.cuda.is_current_stream_capturing():
+            mine = {}                      # (what is kept may be replaced while the graph still replays)
+        else:
+            mine = self._mine.__dict__.setdefault((str(device), torch.cuda.current_stream(device).cuda_stream), {})
+        if "route" not in mine:
+            mine["route"] = gg.make_workspace(route, device)         # (the same size for every T)
+        # the products share a workspace: each call's kernels wait for those of the one before
+        larger = up if up.workspace_bytes > down.workspace_bytes else down
+        work = mine.get("products")
+        if work is None or work.numel() < larger.workspace_bytes:
+            grown = gg.make_workspace(larger, device)
+            if work is not None:
+                grown[:256] = work[:256]   # the header: a status that no check has reported yet
+            mine["products"] = work = grown
+        if mine.get("T") != T:
+            mine.pop("out", None)
             M = T * self.top_k
-            route = gg.cake_gg_router_plan(T, self.E, self.K)
-            up = gg.cake_gg_i8_plan(self.E, M, T, 2 * self.F, self.K, "bf16", None, "bf16")
-            down = gg.cake_gg_i8_plan(self.E, M, M, self.K, self.F, "bf16", "silu_mul", "fp32")
-            kept = (
-                (route, gg.make_workspace(route, device)),
-                (up, gg.make_workspace(up, device), torch.empty((M, 2 * self.F), dtype=torch.bfloat16, device=device)),
-                (down, gg.make_workspace(down, device), torch.empty((M, self.K), dtype=torch.float32, device=device)),
-            )
-            mine[key] = kept
-        return kept
+            mine["out"] = (torch.empty((M, 2 * self.F), dtype=torch.bfloat16, device=device),
+                           torch.empty((M, self.K), dtype=torch.float32, device=device))
+            mine["T"] = T
+        h, out = mine["out"]
+        return (route, mine["route"]), (up, work, h), (down, work, out)
 
     def route(self, x):
         """Experts [T, top_k] and weights [T, top_k] of each token."""
-        plan, work = self._for(x.shape[0], x.device)[0]
+        return self._route(x, *self._for(x.shape[0], x.device)[0])
+
+    def _route(self, x, plan, work):
         logits = gg.router_gemm(x.float(), self.router, plan=plan, workspace=work, check=False)
         top, expert = torch.topk(logits, self.top_k, dim=1)
         return expert, torch.softmax(top, dim=1)
@@ -78,17 +98,17 @@ class Int8Experts:
         T = x.shape[0]
         if T == 0:
             return torch.empty_like(x)
-        _, (up, up_work, h), (down, down_work, out) = self._for(T, x.device)
-        expert, weight = self.route(x)
+        route, (up, work, h), (down, _, out) = self._for(T, x.device)
+        expert, weight = self._route(x, *route)
         # rows in expert order, the token of each, and where each token's rows went
         flat = expert.reshape(-1)
         order = torch.argsort(flat, stable=True)
         rows = torch.div(order, self.top_k, rounding_mode="floor").to(torch.int32)
         counts = (flat[:, None] == torch.arange(self.E, device=x.device)).sum(dim=0)
         offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
-        gg.int8_gemm(x, self.up_q, self.up_s, offsets=offsets, rows=rows, out=h, plan=up, workspace=up_work, check=check)
+        gg.int8_gemm(x, self.up_q, self.up_s, offsets=offsets, rows=rows, out=h, plan=up, workspace=work, check=check)
         gg.int8_gemm(h, self.down_q, self.down_s, offsets=offsets, act="silu_mul", out_dtype="fp32", out=out, plan=down,
-                     workspace=down_work, check=check)
+                     workspace=work, check=check)
         at = torch.empty_like(order)
         at[order] = torch.arange(order.numel(), device=x.device)
         return (out[at].view(T, self.top_k, self.K) * weight[:, :, None]).sum(dim=1).to(x.dtype)
