@@ -85,8 +85,19 @@ class Int8Experts:
         h, out = mine["out"]
         return (route, mine["route"]), (up, work, h), (down, work, out)
 
+    def _check(self, x):
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"x is {x.dtype}: torch.bfloat16 is needed")
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise ValueError(f"x has shape {tuple(x.shape)}: [T, {self.K}] is needed")
+        if x.device != self.router.device:
+            raise ValueError(f"x is on {x.device}, the layer on {self.router.device}")
+        if not x.is_contiguous():
+            raise ValueError("x is not contiguous")
+
     def route(self, x):
         """Experts [T, top_k] and weights [T, top_k] of each token."""
+        self._check(x)
         return self._route(x, *self._for(x.shape[0], x.device)[0])
 
     def _route(self, x, plan, work):
@@ -95,6 +106,7 @@ class Int8Experts:
         return expert, torch.softmax(top, dim=1)
 
     def __call__(self, x, check=False):
+        self._check(x)
         T = x.shape[0]
         if T == 0:
             return torch.empty_like(x)
