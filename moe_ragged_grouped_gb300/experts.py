@@ -32,7 +32,7 @@ from . import cake_gg as gg
 def _plans(E, K, F, top_k, T):
     """Plans of a layer's call of T tokens: the router's, and the two products'."""
     M = T * top_k
-    return (gg.cake_gg_router_plan(T, E, K), gg.cake_gg_i8_plan(E, M, T, 2 * F, K, "bf16", None, "bf16"),
+    return (gg.cake_gg_router_plan(T, (E + 7) // 8 * 8, K), gg.cake_gg_i8_plan(E, M, T, 2 * F, K, "bf16", None, "bf16"),
             gg.cake_gg_i8_plan(E, M, M, K, F, "bf16", "silu_mul", "fp32"))
 
 
@@ -47,7 +47,8 @@ class Int8Experts:
         if not 1 <= top_k <= E:
             raise ValueError("top_k is 1 .. E")
         self.E, self.K, self.F, self.top_k = E, K, F, top_k
-        self.router = router.float().contiguous()
+        # (the router product takes rows in eights: the rows added are cut off its logits)
+        self.router = torch.nn.functional.pad(router.float(), (0, 0, 0, -E % 8)).contiguous()
         self.up_q, self.up_s = self._quantise(gate_up)
         self.down_q, self.down_s = self._quantise(down)
         self._planned = functools.lru_cache(maxsize=256)(functools.partial(_plans, E, K, F, top_k))
@@ -102,7 +103,7 @@ class Int8Experts:
 
     def _route(self, x, plan, work):
         logits = gg.router_gemm(x.float(), self.router, plan=plan, workspace=work, check=False)
-        top, expert = torch.topk(logits, self.top_k, dim=1)
+        top, expert = torch.topk(logits[:, :self.E], self.top_k, dim=1)
         return expert, torch.softmax(top, dim=1)
 
     def __call__(self, x, check=False):

@@ -37,3 +37,30 @@ def test_tokens_are_named_in_what_refuses_them(host_layer, method):
         call(torch.zeros((64, 3), dtype=torch.bfloat16).T)
     with pytest.raises(ValueError, match="x is on"):
         call(torch.zeros((3, 64), dtype=torch.bfloat16, device="meta"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,top", [(4, 2), (13, 3), (1, 1)])
+def test_expert_counts_that_are_no_multiple_of_eight(E, top):
+    """The layer with E experts gives what one of 16 does whose other experts no token takes."""
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    gg_build.build()
+    from moe_ragged_grouped_gb300.experts import Int8Experts
+    K, F = 256, 144
+    g = torch.Generator(device="cuda").manual_seed(E)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    router, up, down = rand(E, K), rand(E, 2 * F, K), rand(E, K, F)
+    more = lambda w, value: torch.cat([w, w.new_full((16 - E, *w.shape[1:]), value)])  # noqa: E731
+    # (tokens whose first value is large, and a router that counts it against the others)
+    x = rand(50, K)
+    x[:, 0] = 100.0
+    router[:, 0] = 0.0
+    wide = more(router, 0.0)
+    wide[E:, 0] = -1000.0
+    x = x.to(torch.bfloat16)
+    y = Int8Experts(router, up, down, top)(x, check=True)
+    assert torch.equal(y, Int8Experts(wide, more(up, 1.0), more(down, 1.0), top)(x, check=True))
+    expert, weight = Int8Experts(router, up, down, top).route(x)
+    assert int(expert.max()) < E and expert.shape == weight.shape == (50, top)
