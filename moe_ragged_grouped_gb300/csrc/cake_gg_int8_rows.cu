@@ -269,11 +269,12 @@ cudaError_t launch_fused(const I8Params &p, const void *X, bool pdl, cudaStream_
 
 // Rows of an expert that a block takes: all that there can be where rows are
 // dense.  Where few rows meet many experts nearly every expert has one row (and
-// a token never meets an expert twice), and the kernels for fewer rows hold
-// more loads in flight; a second row of an expert is another block.
+// a token does not meet an expert twice, unless there are more rows than tokens
+// times experts), and the kernels for fewer rows hold more loads in flight; a
+// second row of an expert is another block.
 int i8_run_rows(int32_t E, int64_t M, int64_t T)
 {
-    const int64_t most = E > 1 && T < M ? T : M;
+    const int64_t most = T < M && M <= E * T ? T : M;
     if (most <= 1 || (E > 1 && E >= 4 * M)) return 1;
     return most <= 2 || (E > 1 && E >= M) ? 2 : 4;
 }

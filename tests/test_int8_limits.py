@@ -1,0 +1,57 @@
+"""Sizes at the ends of what the 8-bit products take: plans, refusals, and index ranges."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from moe_ragged_grouped_gb300 import build as gg_build
+from moe_ragged_grouped_gb300 import cake_gg as gg
+
+ROWS, MMA, WARPS = 0, 1, 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    gg_build.build()
+    return gg.load_library()
+
+
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return torch
+
+
+@pytest.mark.parametrize("E,T,M,N,K", [(4, 2, 10000, 512, 1024), (8, 2, 1 << 24, 4096, 256), (4, 1, 64, 2048, 8192),
+                                       (64, 2, 129, 2048, 4096), (2, 1, 3000, 1000, 512)])
+def test_a_few_tokens_that_many_rows_name_are_many_rows(E, T, M, N, K):
+    """More rows than experts times tokens: a token meets an expert more than once, and the few-row
+    path would read an expert's weights again for every two rows."""
+    assert gg.cake_gg_i8_plan(E, M, T, N, K).path == MMA
+
+
+def test_a_token_through_experts_of_its_own_keeps_the_few_row_path():
+    for E, T, M in ((32, 1, 4), (8, 1, 8), (32, 2, 8), (64, 2, 16), (32, 16, 16)):
+        assert gg.cake_gg_i8_plan(E, M, T, 4096, 2048).path == ROWS
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_dtype", ["int8", "bf16"])
+def test_few_tokens_named_by_many_rows(x_dtype):
+    torch = _gpu()
+    E, T, M, N, K = 4, 2, 10000, 136, 272
+    g = torch.Generator(device="cuda").manual_seed(0)
+    W = torch.randint(-128, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand((E, N), generator=g, device="cuda") + 0.5
+    sizes = [5000, 0, 4999, 1]
+    off = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32, device="cuda")
+    rows = torch.randint(0, T, (M,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((T, K), generator=g, device="cuda").to(torch.bfloat16)
+    q, xs = gg.quantize_rows(x)
+    got = gg.int8_gemm(q, W, ws, xs=xs, offsets=off, rows=rows) if x_dtype == "int8" else gg.int8_gemm(x, W, ws, offsets=off, rows=rows)
+    e_of = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(sizes, device="cuda"))
+    sums = torch.einsum("tk,enk->ten", q.double(), W.double())          # every token through every expert
+    t = rows.long()
+    want = sums[t, e_of].float() * ws[e_of] * xs[t, None]
+    assert torch.equal(got, want.to(torch.bfloat16))
