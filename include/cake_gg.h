@@ -69,7 +69,8 @@
  *   read by cake_gg_i8_plan(), recorded in its plan (no result bit follows them
  *   while a sum stays below 2^24):
  *     CAKE_GG_I8_PATH (cake_gg_i8_path_t), CAKE_GG_I8_PAIR (1 or 2),
- *     CAKE_GG_I8_ROWS_PER_TILE (32 .. 192), CAKE_GG_I8_SPLITS (1 .. 8),
+ *     CAKE_GG_I8_ROWS_PER_TILE (32 .. 192 in steps of 32; 16 or 32 for
+ *     CAKE_GG_I8_WARPS), CAKE_GG_I8_SPLITS (1 .. 8),
  *     CAKE_GG_I8_FIRST_ROWS (0 .. M_max - 1);
  *   read by each compute call, changing no result:
  *     CAKE_GG_PDL=0 (no programmatic dependent launch), CAKE_GG_ROUTER_STAGGER

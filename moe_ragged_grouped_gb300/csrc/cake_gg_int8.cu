@@ -399,6 +399,9 @@ void choose_mma(cake_gg_i8_plan_t *pl)
     pl->first_rows = pl->splits > 1 ? 0 : first < 0 ? choose_first(*pl) : first < pl->M_max ? first : 0;
 }
 
+bool path_ok(int path) { return path == CAKE_GG_I8_ROWS || path == CAKE_GG_I8_MMA || path == CAKE_GG_I8_WARPS; }
+bool warps_rows_ok(int rows) { return rows == 16 || rows == 32; }
+
 // What the tensor-core kernel can run.
 bool mma_plan_ok(const cake_gg_i8_plan_t &pl)
 {
@@ -432,13 +435,17 @@ int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T
     plan->act = act;
     plan->out_dtype = out_dtype;
     plan->max_sms = max_sms;
-    const int path = env_int("CAKE_GG_I8_PATH", choose_path(*plan));
-    plan->path = path;
-    if (path == CAKE_GG_I8_MMA) {
+    // (overrides that name no path, or no run of the path's, change nothing)
+    const int path = env_int("CAKE_GG_I8_PATH", -1);
+    plan->path = path_ok(path) ? path : choose_path(*plan);
+    if (plan->path == CAKE_GG_I8_MMA) {
         choose_mma(plan);
         if (!mma_plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
     }
-    if (path == CAKE_GG_I8_WARPS) plan->tile_rows = env_int("CAKE_GG_I8_ROWS_PER_TILE", M_max <= 16 ? 16 : 32);
+    if (plan->path == CAKE_GG_I8_WARPS) {
+        const int rows = env_int("CAKE_GG_I8_ROWS_PER_TILE", 0);
+        plan->tile_rows = warps_rows_ok(rows) ? rows : M_max <= 16 ? 16 : 32;
+    }
     plan->timeout_ns = kTimeoutNs;
     plan->workspace_bytes = layout(*plan).total;
     return CAKE_GG_OK;
@@ -467,9 +474,8 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     int rc = check_problem(pl.E, pl.M_max, pl.T, pl.N, pl.K, pl.x_dtype, pl.act, pl.out_dtype);
     if (rc != CAKE_GG_OK) return rc;
     const bool warps = pl.path == CAKE_GG_I8_WARPS;
-    if (pl.max_sms < 0 || (pl.path != CAKE_GG_I8_ROWS && !warps && pl.path != CAKE_GG_I8_MMA) ||
-        (pl.path == CAKE_GG_I8_MMA && !mma_plan_ok(pl)) ||
-        (warps && (pl.tile_rows != 16 && pl.tile_rows != 32)))
+    if (pl.max_sms < 0 || !path_ok(pl.path) || (pl.path == CAKE_GG_I8_MMA && !mma_plan_ok(pl)) ||
+        (warps && !warps_rows_ok(pl.tile_rows)))
         return CAKE_GG_ERR_INVALID_ARG;
     const bool ready = pl.x_dtype == CAKE_GG_INT8;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))

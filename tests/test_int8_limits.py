@@ -55,3 +55,20 @@ def test_few_tokens_named_by_many_rows(x_dtype):
     t = rows.long()
     want = sums[t, e_of].float() * ws[e_of] * xs[t, None]
     assert torch.equal(got, want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("value", ["-1", "3", "7", "1000000"])
+def test_a_path_that_is_none_is_no_override(value, monkeypatch):
+    want = gg.cake_gg_i8_plan(1, 12, 12, 256, 1024).as_dict()
+    monkeypatch.setenv("CAKE_GG_I8_PATH", value)
+    assert gg.cake_gg_i8_plan(1, 12, 12, 256, 1024).as_dict() == want
+
+
+@pytest.mark.parametrize("rows", ["0", "8", "48", "64", "192"])
+@pytest.mark.parametrize("M", [12, 30])
+def test_rows_that_a_path_cannot_take_are_no_override(M, rows, monkeypatch):
+    """A documented value of another path's range: the call would refuse the plan it was written into."""
+    want = gg.cake_gg_i8_plan(1, M, M, 256, 1024)
+    assert want.path == WARPS and want.tile_rows in (16, 32)
+    monkeypatch.setenv("CAKE_GG_I8_ROWS_PER_TILE", rows)
+    assert gg.cake_gg_i8_plan(1, M, M, 256, 1024).as_dict() == want.as_dict()
