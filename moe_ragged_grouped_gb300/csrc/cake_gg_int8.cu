@@ -216,12 +216,13 @@ int launch_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, QT *
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
+int64_t expand_blocks(int64_t T, int32_t K) { return (T * (K / 16) + 255) / 256; }
+
 int launch_expand(const void *X, int64_t T, int32_t K, __half *Q, bool beside, cudaStream_t stream)
 {
-    const int64_t n16 = T * (K / 16), blocks = (n16 + 255) / 256;
-    if (blocks > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    const int64_t n16 = T * (K / 16);
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pass_config(blocks, 256, &attr, stream);
+    const cudaLaunchConfig_t cfg = pass_config(expand_blocks(T, K), 256, &attr, stream);
     return cudaLaunchKernelEx(&cfg, i8_expand_kernel, static_cast<const int8_t *>(X), Q, n16, beside) == cudaSuccess
                ? CAKE_GG_OK
                : CAKE_GG_ERR_CUDA;
@@ -509,6 +510,10 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
     const bool mma = pl.path == CAKE_GG_I8_MMA, pdl = pdl_enabled();
     auto status = [](cudaError_t err) { return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA; };
+    // what cannot be launched is refused before anything is enqueued
+    if ((warps ? i8_warps_blocks(p) : pl.path == CAKE_GG_I8_ROWS ? i8_rows_blocks(p) : ready ? expand_blocks(pl.T, pl.K) : 0) >
+        INT32_MAX)
+        return CAKE_GG_ERR_OVERFLOW;
     if (warps && ready)
         return status(launch_i8_warps(p, static_cast<const int8_t *>(X), pl.tile_rows, pdl, s));
     if (pl.path == CAKE_GG_I8_ROWS && (ready || i8_rows_fused(p, pl.act)))
@@ -528,26 +533,31 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     };
     p.early = 1;
     const int64_t first = mma && !rows && pdl ? pl.first_rows : 0;
+    I8MmaLaunch products[2];
+    if (mma) {
+        I8MmaParams m{};
+        m.b = p;
+        m.nt = pl.tile_rows;
+        m.stages = pl.stages;
+        m.slots = pl.slots;
+        m.splits = pl.splits;
+        m.debug_flags = pl.debug_flags;
+        const uint16_t *q = static_cast<const uint16_t *>(tokens);
+        const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
+        m.b.m_hi = first;
+        if (first && (rc = prepare_i8_mma(&products[0], m, q, pl.pair, cap)) != CAKE_GG_OK) return rc;
+        m.b.m_lo = first;
+        m.b.m_hi = pl.M_max;
+        if ((rc = prepare_i8_mma(&products[1], m, q, pl.pair, cap)) != CAKE_GG_OK) return rc;
+    }
     if ((rc = pass(0, first ? first : pl.T, false)) != CAKE_GG_OK) return rc;
     if (warps) return status(launch_i8_warps(p, static_cast<const int8_t *>(tokens), pl.tile_rows, pdl, s));
     if (!mma) return status(launch_i8_rows(p, tokens, CAKE_GG_INT8, CAKE_GG_ACT_NONE, pdl, s));
-    I8MmaParams m{};
-    m.b = p;
-    m.nt = pl.tile_rows;
-    m.stages = pl.stages;
-    m.slots = pl.slots;
-    m.splits = pl.splits;
-    m.debug_flags = pl.debug_flags;
-    const uint16_t *q = static_cast<const uint16_t *>(tokens);
-    const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
     if (first) {
-        m.b.m_hi = first;
-        if ((rc = launch_i8_mma(m, q, pl.pair, cap, pdl, s)) != CAKE_GG_OK) return rc;
+        if ((rc = launch_i8_mma(products[0], pdl, s)) != CAKE_GG_OK) return rc;
         if ((rc = pass(first, pl.T - first, true)) != CAKE_GG_OK) return rc;
     }
-    m.b.m_lo = first;
-    m.b.m_hi = pl.M_max;
-    return launch_i8_mma(m, q, pl.pair, cap, pdl, s);
+    return launch_i8_mma(products[1], pdl, s);
 }
 
 }  // extern "C"

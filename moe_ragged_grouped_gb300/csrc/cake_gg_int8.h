@@ -60,8 +60,16 @@ constexpr size_t kI8SmemLimit = 232448;   // opt-in dynamic shared memory per CT
 // Dynamic shared memory of a CTA.
 size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E);
 
-// Tensor-core path: q [T, K] as FP16 integers.  Returns a cake_gg_status_t.
-int launch_i8_mma(const I8MmaParams &p, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream);
+// Tensor-core path: q [T, K] as FP16 integers.  Everything that can be refused
+// is refused by the preparation, which enqueues nothing.  Both return a
+// cake_gg_status_t.
+struct I8MmaLaunch {
+    CUtensorMap mw, mx;
+    I8MmaParams p;
+    int32_t pair, grid;
+};
+int prepare_i8_mma(I8MmaLaunch *l, const I8MmaParams &p, const uint16_t *q, int pair, int sms);
+int launch_i8_mma(const I8MmaLaunch &l, bool pdl, cudaStream_t stream);
 
 // Few-row path: 32-bit integer dot products, weights streamed once per run of
 // an expert's rows.  X: the quantised tokens [T, K] (x_dtype CAKE_GG_INT8), or
@@ -69,10 +77,12 @@ int launch_i8_mma(const I8MmaParams &p, const uint16_t *q, int pair, int sms, bo
 // themselves.
 bool i8_rows_fused(const I8Params &p, int act);
 int i8_run_rows(int32_t E, int64_t M, int64_t T);   // rows of a run: 1, 2 or 4
+int64_t i8_rows_blocks(const I8Params &p);          // blocks of the launch, at most INT32_MAX of which there can be
 cudaError_t launch_i8_rows(const I8Params &p, const void *X, int x_dtype, int act, bool pdl, cudaStream_t stream);
 
 // A few dozen rows: warp-level products from registers, runs of 16 or 32 of an
 // expert's rows; q [T, K].
+int64_t i8_warps_blocks(const I8Params &p);
 cudaError_t launch_i8_warps(const I8Params &p, const int8_t *q, int rows, bool pdl, cudaStream_t stream);
 
 }  // namespace cakegg

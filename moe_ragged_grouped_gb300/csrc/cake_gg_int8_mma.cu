@@ -706,21 +706,27 @@ __global__ void __maxnreg__(80)
     }
 }
 
+// The opt-in limit of shared memory, raised once per device.
 template <int PAIR, bool OUT_F32>
-cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaParams &p, int grid, bool pdl,
-                   cudaStream_t stream)
+cudaError_t raise_limit()
 {
-    auto kern = i8_mma_kernel<PAIR, OUT_F32>;
-    static bool raised[64] = {};   // the opt-in limit is raised once per device
+    static bool raised[64] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!raised[dev]) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kI8SmemLimit));
+        err = cudaFuncSetAttribute(i8_mma_kernel<PAIR, OUT_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kI8SmemLimit));
         if (err != cudaSuccess) return err;
         raised[dev] = true;
     }
+    return cudaSuccess;
+}
+
+template <int PAIR, bool OUT_F32>
+cudaError_t launch(const I8MmaLaunch &l, bool pdl, cudaStream_t stream)
+{
+    const I8MmaParams &p = l.p;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     int na = 0;
@@ -735,13 +741,13 @@ cudaError_t launch(const CUtensorMap &mw, const CUtensorMap &mx, const I8MmaPara
         attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }
-    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.gridDim = dim3(unsigned(l.grid), 1, 1);
     cfg.blockDim = dim3(p.b.rows ? kThreadsRouted : kThreads, 1, 1);
     cfg.dynamicSmemBytes = i8_mma_smem(PAIR, p.nt, p.stages, p.splits, p.b.E);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = unsigned(na);
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
+    return cudaLaunchKernelEx(&cfg, i8_mma_kernel<PAIR, OUT_F32>, l.mw, l.mx, p);
 }
 
 }  // namespace
@@ -753,24 +759,24 @@ size_t i8_mma_smem(int pair, int nt, int stages, int splits, int E)
            size_t(kGatherWarps * kRowsPerCta / 2) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
-int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, bool pdl, cudaStream_t stream)
+int prepare_i8_mma(I8MmaLaunch *l, const I8MmaParams &p0, const uint16_t *q, int pair, int sms)
 {
-    I8MmaParams p = p0;
+    I8MmaParams &p = l->p;
+    p = p0;
     p.n_ct = (p.b.N + 128 * pair - 1) / (128 * pair);
     p.n_kb = (p.b.K + kKB - 1) / kKB;
     p.div_nt = uint32_t((uint64_t(1) << 32) / uint32_t(p.nt / 16) + ((uint64_t(1) << 32) % uint32_t(p.nt / 16) != 0));
     p.box = p.nt / pair % 32 == 0 ? 32 : 16;
-    CUtensorMap mw, mx;
     const uint64_t dw[3] = {uint64_t(p.b.K), uint64_t(p.b.N), uint64_t(p.b.E)};
     const uint64_t sw[2] = {uint64_t(p.b.K), uint64_t(p.b.N) * uint64_t(p.b.K)};
     const uint32_t bw[3] = {uint32_t(kKB), 128, 1};
-    int rc = encode_tiled(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.b.W, dw, sw, bw);
+    int rc = encode_tiled(&l->mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.b.W, dw, sw, bw);
     if (rc != CAKE_GG_OK) return rc;
 
     const uint64_t dx[2] = {uint64_t(p.b.K), uint64_t(p.b.T)};
     const uint64_t sx[1] = {uint64_t(p.b.K) * 2};
     const uint32_t bx[2] = {64, p.b.rows ? 1u : uint32_t(p.box)};   // (gathered four rows at a time)
-    rc = encode_tiled(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, dx, sx, bx);
+    rc = encode_tiled(&l->mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, dx, sx, bx);
     if (rc != CAKE_GG_OK) return rc;
 
     // row tiles at most: a whole one per nt rows and a last one per expert with rows
@@ -785,13 +791,18 @@ int launch_i8_mma(const I8MmaParams &p0, const uint16_t *q, int pair, int sms, b
         grid = sms / pair < bound ? sms / pair : bound;
         grid = (grid < 1 ? 1 : grid) * pair;
     }
+    l->pair = pair;
+    l->grid = int32_t(grid);
+    const cudaError_t err = pair == 2 ? (p.b.out_f32 ? raise_limit<2, true>() : raise_limit<2, false>())
+                                      : (p.b.out_f32 ? raise_limit<1, true>() : raise_limit<1, false>());
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+int launch_i8_mma(const I8MmaLaunch &l, bool pdl, cudaStream_t stream)
+{
     cudaError_t err;
-    if (pair == 2)
-        err = p.b.out_f32 ? launch<2, true>(mw, mx, p, int(grid), pdl, stream)
-                          : launch<2, false>(mw, mx, p, int(grid), pdl, stream);
-    else
-        err = p.b.out_f32 ? launch<1, true>(mw, mx, p, int(grid), pdl, stream)
-                          : launch<1, false>(mw, mx, p, int(grid), pdl, stream);
+    if (l.pair == 2) err = l.p.b.out_f32 ? launch<2, true>(l, pdl, stream) : launch<2, false>(l, pdl, stream);
+    else err = l.p.b.out_f32 ? launch<1, true>(l, pdl, stream) : launch<1, false>(l, pdl, stream);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 

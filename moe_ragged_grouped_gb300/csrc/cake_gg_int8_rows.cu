@@ -242,11 +242,9 @@ template <int R, typename XT, bool ACT>
 cudaError_t launch(const I8Params &p, const void *X, bool pdl, cudaStream_t stream)
 {
     const int S = k_warps(R, p.E, p.M, p.N, p.K), blocks_n = channel_blocks(S, p.N);
-    const int64_t blocks = p.M * blocks_n;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.gridDim = dim3(unsigned(i8_rows_blocks(p)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = sizeof(XT) > 1 ? size_t(R) * size_t(p.K) : 0;
     cfg.stream = stream;
@@ -277,6 +275,11 @@ int i8_run_rows(int32_t E, int64_t M, int64_t T)
     const int64_t most = T < M && M <= E * T ? T : M;
     if (most <= 1 || (E > 1 && E >= 4 * M)) return 1;
     return most <= 2 || (E > 1 && E >= M) ? 2 : 4;
+}
+
+int64_t i8_rows_blocks(const I8Params &p)
+{
+    return p.M * channel_blocks(k_warps(i8_run_rows(p.E, p.M, p.T), p.E, p.M, p.N, p.K), p.N);
 }
 
 // Every block repeats the quantising of its rows, against one launch less: 2.1 us

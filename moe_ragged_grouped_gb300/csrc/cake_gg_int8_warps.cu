@@ -186,18 +186,18 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+int channel_blocks(int32_t N) { return (N + kChannels - 1) / kChannels; }
+
 template <int NT>
 cudaError_t launch(const I8Params &p, const int8_t *q, bool pdl, cudaStream_t stream)
 {
     auto kern = i8_warps_kernel<NT>;
     constexpr size_t smem = size_t(kWarps) * 8 * NT * kPad * sizeof(float);
     static_assert(smem <= 48 * 1024, "no opt-in needed");
-    const int blocks_n = (p.N + kChannels - 1) / kChannels;
-    const int64_t blocks = p.M * blocks_n;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const int blocks_n = channel_blocks(p.N);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(unsigned(blocks), 1, 1);
+    cfg.gridDim = dim3(unsigned(i8_warps_blocks(p)), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -211,6 +211,8 @@ cudaError_t launch(const I8Params &p, const int8_t *q, bool pdl, cudaStream_t st
 }
 
 }  // namespace
+
+int64_t i8_warps_blocks(const I8Params &p) { return p.M * channel_blocks(p.N); }
 
 cudaError_t launch_i8_warps(const I8Params &p, const int8_t *q, int rows, bool pdl, cudaStream_t stream)
 {

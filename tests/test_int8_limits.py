@@ -72,3 +72,29 @@ def test_rows_that_a_path_cannot_take_are_no_override(M, rows, monkeypatch):
     assert want.path == WARPS and want.tile_rows in (16, 32)
     monkeypatch.setenv("CAKE_GG_I8_ROWS_PER_TILE", rows)
     assert gg.cake_gg_i8_plan(1, M, M, 256, 1024).as_dict() == want.as_dict()
+
+
+def _raw_plan(E, M, T, N, K, x_dtype, path, monkeypatch):
+    monkeypatch.setenv("CAKE_GG_I8_PATH", str(path))
+    plan = gg.cake_gg_i8_plan(E, M, T, N, K, x_dtype)
+    assert plan.path == path
+    return plan
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path,M,N,K", [(ROWS, 1 << 24, 4096, 256), (WARPS, 1 << 24, 4096, 256), (MMA, 64, 1 << 24, 131056)],
+                         ids=["rows", "warps", "mma"])
+def test_a_refused_call_enqueues_nothing(path, M, N, K, monkeypatch):
+    """Grids and strides past the hardware's limits, with activations: no token pass before the refusal.
+    (Y, W and the row numbers are made up: no kernel that reads them can be launched.)"""
+    torch = _gpu()
+    T = 64
+    plan = _raw_plan(1, M, T, N, K, "bf16", path, monkeypatch)
+    x = torch.ones((T, K), dtype=torch.bfloat16, device="cuda")
+    work = torch.full((int(plan.workspace_bytes),), 0x5A, dtype=torch.uint8, device="cuda")
+    address = 1 << 20
+    rc = gg.cake_gg_i8_gemm(plan, x, None, address if M != T else None, address, address, address, None, work,
+                            stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc != gg.CAKE_GG_OK
+    assert bool((work == 0x5A).all())
