@@ -327,7 +327,7 @@ typedef struct cake_gg_i8_plan {
     int32_t E;               /* experts, 1 .. 1024                                  */
     int64_t M_max;           /* rows of Y (0 .. 2^31 - 1)                           */
     int64_t T;               /* rows of X (= M_max without rows)                    */
-    int32_t N;               /* output channels, a multiple of 8                    */
+    int32_t N;               /* output channels, a multiple of 8, at most 2^31 - 512 */
     int32_t K;               /* reduction length, a multiple of 16, below 2^17      */
     int32_t x_dtype;         /* cake_gg_dtype_t: CAKE_GG_INT8, _BF16 or _FP32       */
     int32_t act;             /* cake_gg_act_t (CAKE_GG_ACT_NONE for int8 X)         */
@@ -353,8 +353,8 @@ typedef struct cake_gg_i8_plan {
 /* Fill *plan.  Pure host arithmetic.  CAKE_GG_ERR_INVALID_ARG for sizes out of
  * range, T < 1 with rows to compute, an activation with int8 X;
  * CAKE_GG_ERR_UNSUPPORTED for other types; CAKE_GG_ERR_ALIGNMENT unless N is a
- * multiple of 8 and K of 16; CAKE_GG_ERR_OVERFLOW for K >= 2^17 or a size
- * product past 64 bits. */
+ * multiple of 8 and K of 16; CAKE_GG_ERR_OVERFLOW for K >= 2^17, N > 2^31 - 512
+ * or a size product past 64 bits. */
 int cake_gg_i8_plan(cake_gg_i8_plan_t *plan, int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K,
                     int x_dtype, int act, int out_dtype, int32_t max_sms);
 

@@ -30,6 +30,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kStagesMost = 12, kSlotsMost = 8;
 constexpr int32_t kMaxExperts = 1024;
 constexpr int32_t kMaxK = (1 << 17) - 16;      // |sum of K products| <= 2^14 K stays below 2^31
+constexpr int32_t kMaxN = INT32_MAX - 511;     // channels of whole tiles (256) and storing warps stay below 2^31
 
 uint64_t align_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
@@ -239,7 +240,7 @@ int check_problem(int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K, int
     if (act != CAKE_GG_ACT_NONE && act != CAKE_GG_ACT_SILU_MUL) return CAKE_GG_ERR_INVALID_ARG;
     if (act != CAKE_GG_ACT_NONE && x_dtype == CAKE_GG_INT8) return CAKE_GG_ERR_INVALID_ARG;
     if (N % 8 != 0 || K % 16 != 0) return CAKE_GG_ERR_ALIGNMENT;
-    if (K > kMaxK) return CAKE_GG_ERR_OVERFLOW;
+    if (K > kMaxK || N > kMaxN) return CAKE_GG_ERR_OVERFLOW;
     uint64_t t;
     if (!mul_ok(uint64_t(T), uint64_t(K) * 8u, &t) || !mul_ok(uint64_t(E) * uint64_t(N), uint64_t(K), &t) ||
         !mul_ok(uint64_t(M_max), uint64_t(N) * 4u, &t))

@@ -98,3 +98,17 @@ def test_a_refused_call_enqueues_nothing(path, M, N, K, monkeypatch):
     torch.cuda.synchronize()
     assert rc != gg.CAKE_GG_OK
     assert bool((work == 0x5A).all())
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 8, 2 ** 31 - 504])
+@pytest.mark.parametrize("M", [1, 40, 4096])
+def test_channels_whose_tiles_pass_32_bits_are_refused(N, M):
+    """N rounded up to whole tiles has to fit the kernels' 32-bit channel numbers."""
+    with pytest.raises(gg.CakeGGError) as err:
+        gg.cake_gg_i8_plan(1, M, M, N, 16)
+    assert err.value.code == gg.CAKE_GG_ERR_OVERFLOW
+    plan = gg.cake_gg_i8_plan(1, M, M, 2 ** 31 - 512, 16)
+    plan.N = N
+    address = 1 << 20
+    assert gg.cake_gg_i8_gemm(plan, address, None, None, address, address, address, None, address,
+                              workspace_bytes=plan.workspace_bytes, stream=0) == gg.CAKE_GG_ERR_OVERFLOW
