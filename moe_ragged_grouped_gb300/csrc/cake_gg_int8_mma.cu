@@ -185,7 +185,7 @@ __host__ __device__ constexpr size_t split_bytes(int nt, int splits)
 
 struct Tile {
     int e, ct;                // expert, channel tile
-    int32_t m0, rows, end;    // first row, rows in the tile, end of the expert's rows
+    int32_t m0, rows;         // first row, rows in the tile
 };
 
 // The units of a CTA (pair), a fixed stride over (row tile, channel tile) with
@@ -216,8 +216,7 @@ struct Walk {
         t.ct = ct;
         t.e = e;
         t.m0 = off[e] + (g - pref[e]) * nt;
-        t.end = off[e + 1];
-        t.rows = min(nt, t.end - t.m0);
+        t.rows = min(nt, off[e + 1] - t.m0);
         return t;
     }
 };
@@ -585,7 +584,7 @@ __global__ void __maxnreg__(80)
                 const Tile t = w.tile(p.nt, off, pref);
                 const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
                 const int n_box = (n_half + p.box - 1) / p.box;
-                const int32_t mb = t.m0 + half * n_half;
+                const uint32_t mb = uint32_t(t.m0 + half * n_half);         // (a box past 2^31 is past the tokens)
                 const uint32_t bytes = 256u * uint32_t(n_box * p.box);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
@@ -594,8 +593,8 @@ __global__ void __maxnreg__(80)
                         const uint32_t bar = smem_u32(&c->full[st.at]), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
                         mbar_arrive_expect_tx(bar, bytes);
                         for (int b = 0; b < n_box; ++b) {
-                            tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, mb + b * p.box);
-                            tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, mb + b * p.box);
+                            tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, int32_t(mb + uint32_t(b * p.box)));
+                            tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, int32_t(mb + uint32_t(b * p.box)));
                         }
                     }
                     __syncwarp();
@@ -616,8 +615,9 @@ __global__ void __maxnreg__(80)
                 const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
                 __syncwarp();
                 for (int i = lane; i < n_half / 2; i += 32) {
-                    const int32_t m = t.m0 + half * n_half + (i >> 2) * 8 + side * 4 + (i & 3);
-                    const int32_t id = m < t.end ? p.b.rows[m] : 0;
+                    // (counted from the tile's first row: past its last one the sum may pass 2^31)
+                    const int32_t m = half * n_half + (i >> 2) * 8 + side * 4 + (i & 3);
+                    const int32_t id = m < t.rows ? p.b.rows[t.m0 + m] : 0;
                     mine[i] = id >= 0 && id < p.b.T ? id : 0;    // (reported where it is scaled)
                 }
                 grid_dependency_wait();                          // the tokens (the caller's row numbers were there)

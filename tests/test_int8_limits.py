@@ -112,3 +112,26 @@ def test_channels_whose_tiles_pass_32_bits_are_refused(N, M):
     address = 1 << 20
     assert gg.cake_gg_i8_gemm(plan, address, None, None, address, address, address, None, address,
                               workspace_bytes=plan.workspace_bytes, stream=0) == gg.CAKE_GG_ERR_OVERFLOW
+
+
+@pytest.mark.gpu
+def test_routed_rows_up_to_2_31():
+    """The last expert's one row is the last row there can be: its tile ends past 2^31, and what it
+    reads of the row numbers must not.  (M * N passes 2^31 sixteen times.)"""
+    torch = _gpu()
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    M, T, N, K = 2 ** 31 - 1, 1000, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randint(-128, 128, (T, K), generator=g, device="cuda", dtype=torch.int8)
+    W = torch.randint(-128, 128, (2, N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs, ws = torch.rand(T, generator=g, device="cuda") + 0.5, torch.rand((2, N), generator=g, device="cuda") + 0.5
+    rows = torch.arange(M, dtype=torch.int32, device="cuda").remainder_(T)
+    off = torch.tensor([0, M - 1, M], dtype=torch.int32, device="cuda")
+    assert gg.cake_gg_i8_plan(2, M, T, N, K, "int8").path == MMA
+    y = gg.int8_gemm(q, W, ws, xs=xs, offsets=off, rows=rows)
+    each = ((q.double() @ W.double().transpose(1, 2)).float() * ws[:, None] * xs[:, None]).to(torch.bfloat16)
+    for at in range(0, M, 1 << 27):
+        end = min(at + (1 << 27), M - 1)
+        assert torch.equal(y[at:end], each[0][rows[at:end].long()])
+    assert torch.equal(y[M - 1], each[1][int(rows[M - 1])])
