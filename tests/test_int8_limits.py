@@ -135,3 +135,48 @@ def test_routed_rows_up_to_2_31():
         end = min(at + (1 << 27), M - 1)
         assert torch.equal(y[at:end], each[0][rows[at:end].long()])
     assert torch.equal(y[M - 1], each[1][int(rows[M - 1])])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path", [ROWS, MMA, WARPS])
+def test_weights_past_2_31(path, monkeypatch):
+    """More than 2^31 weights: the last expert's, and its last channels, are read where they lie."""
+    torch = _gpu()
+    E, N, K, M = 33, 8200, 8192, 9
+    assert E * N * K > 2 ** 31
+    monkeypatch.setenv("CAKE_GG_I8_PATH", str(path))
+    W = torch.empty((E, N, K), dtype=torch.int8, device="cuda")
+    for e in range(E):
+        W[e] = torch.randint(-128, 128, (N, K), device="cuda", dtype=torch.int8)
+    ws = torch.rand((E, N), device="cuda") + 0.5
+    q, xs = torch.randint(-128, 128, (M, K), device="cuda", dtype=torch.int8), torch.rand(M, device="cuda") + 0.5
+    sizes = [2] + [0] * (E - 3) + [3, 4]
+    off = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32, device="cuda")
+    assert gg.cake_gg_i8_plan(E, M, M, N, K, "int8").path == path
+    got = gg.int8_gemm(q, W, ws, xs=xs, offsets=off)
+    want = torch.cat([(q[a:b].double() @ W[e].double().T).float() * ws[e] for a, b, e in ((0, 2, 0), (2, 5, E - 2), (5, 9, E - 1))])
+    assert torch.equal(got, (want * xs[:, None]).to(torch.bfloat16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_dtype", ["int8", "bf16"])
+def test_outputs_past_2_31(x_dtype):
+    """More than 2^31 outputs and tokens' values, not routed; activations are divided between two products."""
+    torch = _gpu()
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    M, N, K = 525000, 4096, 4112
+    assert M * N > 2 ** 31 and M * K > 2 ** 31
+    W, ws = torch.randint(-128, 128, (N, K), device="cuda", dtype=torch.int8), torch.rand(N, device="cuda") + 0.5
+    if x_dtype == "int8":
+        q = torch.empty((M, K), dtype=torch.int8, device="cuda").random_(-128, 128)
+        xs = torch.rand(M, device="cuda") + 0.5
+        y = gg.int8_gemm(q, W, ws, xs=xs)
+    else:
+        x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda").normal_()
+        y = gg.int8_gemm(x, W, ws)
+        q, xs = gg.quantize_rows(x)
+    for at in (0, 130000, 262143, 400001, M - 500):
+        rows = slice(at, at + 500)
+        want = (q[rows].double() @ W.double().T).float() * ws * xs[rows, None]
+        assert torch.equal(y[rows], want.to(torch.bfloat16))
