@@ -299,10 +299,14 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
  * a byte allowed.  Rows at or past offsets[E] of Y are never written, and an
  * expert without rows reads no weights.  Sums are exact 32-bit integers (few
  * rows) or FP32 sums of exact products (tensor cores: exact too while their
- * magnitude stays below 2^24; bytes of 90 .. 127 without a sign, the worst there
- * is, measured 2e-7 off at K = 4096, 4e-6 at 32768, 5e-5 at 131056); two FP32
- * multiplications follow, by ws and then xs, and one rounding for BF16 output.
- * The same call gives the same bits on every run and under every max_sms.
+ * magnitude stays below 2^24; past it each of the K / 16 steps is cut off at the
+ * running sum's last place, at most 2^-23 of it.  Bytes of 90 .. 127 without a
+ * sign, the worst there is, measured 4.3e-6 off at K = 4096, 1.5e-4 at 32768 and
+ * 7.6e-4 at 131056 where one CTA or pair sums all of K; over three CTAs 1.3e-7,
+ * 2.1e-5, 1.8e-4; over eight, and in the path of a few dozen rows, 2e-7, 3.8e-6,
+ * 5.2e-5); two FP32 multiplications follow, by ws and then xs, and one rounding
+ * for BF16 output.  The same call gives the same bits on every run and under
+ * every max_sms.
  *
  * X is q itself (x_dtype CAKE_GG_INT8, xs given), or BF16 / FP32 activations
  * (xs null) that the call quantises row by row first:
