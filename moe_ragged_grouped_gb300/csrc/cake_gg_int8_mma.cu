@@ -64,16 +64,19 @@ struct __align__(16) Ctrl {
 __device__ __forceinline__ bool aborted(Ctrl *c) { return *reinterpret_cast<volatile int32_t *>(&c->abort_flag) != 0; }
 
 // Bounded wait on one mbarrier phase by every lane of a warp; warp-uniform
-// verdict (false: it ran out, or another role gave up).
+// verdict (false: it ran out, or another role gave up).  PEERS: a barrier on
+// which the other CTA of a pair arrives too.
+template <bool PEERS = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctrl *c, const I8Params &p)
 {
-    bool ok = mbar_try_wait(bar, parity);
+    auto poll = [&] { return PEERS ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    bool ok = poll();
     // (the global timer is slow to read: a wait that is soon over never asks it)
-    for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    for (int i = 0; i < 256 && !ok; ++i) ok = poll();
     if (!ok) {
         const uint64_t t0 = global_timer_ns();
         while (true) {
-            for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+            for (int i = 0; i < 256 && !ok; ++i) ok = poll();
             if (ok || aborted(c)) break;
             if (global_timer_ns() - t0 > p.timeout_ns) {
                 *reinterpret_cast<volatile int32_t *>(&c->abort_flag) = 1;
@@ -93,6 +96,14 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
         if (global_timer_ns() - t0 > kDrainNs) return;
 }
 
+// After an abort, copies whose barrier is another CTA's: they land in a time that
+// drain_wait would give up after.
+__device__ __forceinline__ void drain_blind()
+{
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kDrainNs) {}
+}
+
 // One lane of a converged warp.  (The MMA's descriptors then stay in uniform
 // registers: under a test of the lane number each of the eight issues of a
 // stage took 70 clocks, a stage 960; elected, 281.)
@@ -103,15 +114,30 @@ __device__ __forceinline__ bool elect_one()
     return e != 0;
 }
 
-// Four rows of a tensor (its box one row high) to consecutive 128-byte rows.
+// Four rows of a tensor (its box one row high) to consecutive 128-byte rows (of a
+// CTA of a pair: counted on the mbarrier of either of the two, by cluster address).
+template <int PAIR>
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t r0,
                                             int32_t r1, int32_t r2, int32_t r3)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
+    if constexpr (PAIR == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+            : "memory");
+}
+template <int PAIR>
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t row)
+{
+    if constexpr (PAIR == 2) tma_load_2d_pair(dst, map, bar, x, row);
+    else tma_load_2d(dst, map, bar, x, row);
 }
 
 // FP32 accumulators, FP16 operands (A and B format fields 0), both K-major.
@@ -289,7 +315,7 @@ __global__ void __maxnreg__(80)
         tmem_relinquish<PAIR>();
     } else if (tid == 64) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(smem_u32(&c->full[s]), p.b.rows ? 3 : 2);  // the weights' arming and the rows'
+            mbar_init(smem_u32(&c->full[s]), !leader ? 1 : p.b.rows ? 3 : 2);   // the weights' arming and the rows'
             mbar_init(smem_u32(&c->empty[s]), 1);
         }
         for (int a = 0; a < p.slots; ++a) mbar_init(smem_u32(&c->conv[a]), 4u * PAIR);   // the group's warps, of both CTAs
@@ -364,15 +390,16 @@ __global__ void __maxnreg__(80)
                 const uint32_t n = uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign);
                 const uint32_t idesc = idesc_f16(128u * PAIR, n);
                 const int buf = acc.at;
-                if (!warp_wait(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p.b)) {
+                if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p.b)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
                 const uint32_t d = tmem + uint32_t(buf) * d_stride;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    // the converters of both CTAs saw their stage's copies land
-                    ok = warp_wait(smem_u32(&c->conv[sl.at]), sl.parity, c, p.b);
+                    // the converters of both CTAs saw their weights land, and this
+                    // CTA's the rows of both
+                    ok = warp_wait<PAIR == 2>(smem_u32(&c->conv[sl.at]), sl.parity, c, p.b);
                     if (!ok) break;
                     if (elect_one()) {
                         tc_fence_after_sync();
@@ -507,7 +534,7 @@ __global__ void __maxnreg__(80)
             __syncwarp();
             if (lane == 0) {
                 if (leader) mbar_arrive(smem_u32(&c->tempty[buf]));
-                else mbar_arrive_remote(map_to_cta(smem_u32(&c->tempty[buf]), 0));
+                else mbar_arrive_relaxed_cluster(map_to_cta(smem_u32(&c->tempty[buf]), 0));
             }
             acc.next(2);
             xb.next(2);
@@ -561,10 +588,13 @@ __global__ void __maxnreg__(80)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                // (default semantics: what the MMA reads is complete and fenced; a
-                // release at cluster scope cost a tenth of the whole product)
+                // What the other CTA's MMAs read of this one: tensor memory, complete
+                // and ordered by the fence above and the one after their wait, for which
+                // an arrival at cluster scope is enough (as a release there it takes 557 us
+                // for 319, 16384 x 4096 -> 4096); and rows, whose copies count on that
+                // CTA's own barrier.
                 if (leader) mbar_arrive(smem_u32(&c->conv[sl.at]));
-                else mbar_arrive_remote(map_to_cta(smem_u32(&c->conv[sl.at]), 0));
+                else mbar_arrive_relaxed_cluster(map_to_cta(smem_u32(&c->conv[sl.at]), 0));
             }
             st.next(p.stages), st.next(p.stages);
             sl.next(p.slots), sl.next(p.slots);
@@ -574,7 +604,12 @@ __global__ void __maxnreg__(80)
         __syncwarp();
     } else {
         // ======================= rows =======================
+        // The MMAs of a pair read the rows of both CTAs, so both count on the even
+        // one's barrier, which it arms for both; the odd one's holds its weights only.
+        // (A stage's copies follow its `empty`, so the even one's barrier is in the
+        // same round; the bytes may come before the arming.)
         const int v = warp - kRowsWarp0, n_kb = kb1 - kb0;
+        auto full_bar = [&](int s) { return PAIR == 2 ? map_to_cta(smem_u32(&c->full[s]), 0) : smem_u32(&c->full[s]); };
         Turn st;
         int issued = 0;
         bool ok = true;
@@ -590,11 +625,11 @@ __global__ void __maxnreg__(80)
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
                     if (!ok) break;
                     if (elect_one()) {
-                        const uint32_t bar = smem_u32(&c->full[st.at]), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
-                        mbar_arrive_expect_tx(bar, bytes);
+                        const uint32_t bar = full_bar(st.at), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * bytes);
                         for (int b = 0; b < n_box; ++b) {
-                            tma_load_2d(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, int32_t(mb + uint32_t(b * p.box)));
-                            tma_load_2d(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, int32_t(mb + uint32_t(b * p.box)));
+                            tma_rows<PAIR>(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * kKB, int32_t(mb + uint32_t(b * p.box)));
+                            tma_rows<PAIR>(dst + (x_rows + uint32_t(b * p.box)) * 128u, &mapX, bar, kb * kKB + 64, int32_t(mb + uint32_t(b * p.box)));
                         }
                     }
                     __syncwarp();
@@ -602,7 +637,10 @@ __global__ void __maxnreg__(80)
                     if (issued < p.stages) ++issued;
                 }
             }
-            if (!ok || aborted(c)) drain_stages(st, issued, 1, lane, p.stages, c);
+            if (!ok || aborted(c)) {
+                if (leader) drain_stages(st, issued, 1, lane, p.stages, c);
+                else drain_blind();
+            }
         } else {
             // warps 0, 1 and 2, 3 gather alternate stages, each every other four rows
             const int group = v >> 1, side = v & 1;
@@ -626,15 +664,15 @@ __global__ void __maxnreg__(80)
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p.b);
                     if (!ok) break;
                     if (elect_one()) {
-                        const uint32_t bar = smem_u32(&c->full[st.at]);
+                        const uint32_t bar = full_bar(st.at);
                         const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(side) * 512u;
                         const int32_t k = (kb0 + kb) * kKB;
-                        mbar_arrive_expect_tx(bar, uint32_t(n_half) * 128u);
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * uint32_t(n_half) * 128u);
 #pragma unroll 4
                         for (int i = 0; i < n_half / 2; i += 4) {
                             const int4 id = lds_i4(ids + uint32_t(i) * 4u);
-                            tma_gather4(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
-                            tma_gather4(dst + x_rows * 128u + uint32_t(i) * 256u, &mapX, bar, k + 64, id.x, id.y, id.z, id.w);
+                            tma_gather4<PAIR>(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
+                            tma_gather4<PAIR>(dst + x_rows * 128u + uint32_t(i) * 256u, &mapX, bar, k + 64, id.x, id.y, id.z, id.w);
                         }
                     }
                     __syncwarp();
@@ -644,7 +682,10 @@ __global__ void __maxnreg__(80)
                 kb -= n_kb;
             }
             grid_dependency_wait();
-            if (!ok || aborted(c)) drain_stages(st, issued, 2, lane, p.stages, c);
+            if (!ok || aborted(c)) {
+                if (leader) drain_stages(st, issued, 2, lane, p.stages, c);
+                else drain_blind();
+            }
         }
         __syncwarp();
     }
