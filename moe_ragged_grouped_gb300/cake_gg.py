@@ -186,17 +186,17 @@ def _ptr(x):
     return x.data_ptr()
 
 
-_raw_stream = None
-
-
 def _current_stream(index):
-    """The current stream's handle on a device (a few times cheaper than through a Stream object, where torch allows)."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _raw_stream(index)
+    """The current stream's handle on a device (a few times cheaper than through a Stream object, where torch allows).
+
+    Gives its name to torch's own function on the first call, as _current_device() does: a short
+    product's time is the host's.
+    """
+    global _current_stream
+    import torch
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current_stream(index)
 
 
 def _stream(stream, *tensors):
@@ -390,6 +390,17 @@ def _for_stream(stream, device, make, result=False):
     return tensor
 
 
+def _result(shape, dtype, device, stream):
+    """An output of a call on `stream`."""
+    import torch
+    return _for_stream(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device), result=True)
+
+
+def _scratch(plan, device, stream):
+    """A workspace for one call on `stream`."""
+    return _for_stream(stream, device, lambda: make_workspace(plan, device))
+
+
 def make_workspace(plan, device):
     """A zero-filled workspace of plan.workspace_bytes (the library expects zeros before first use)."""
     import torch
@@ -406,7 +417,6 @@ def grouped_gemm(pass_, a, b, offsets, out_dtype="bf16", deterministic=True, max
     wgrad: a = G [M, N], b = X [M, K], E from offsets -> dW [E, N, K]
     Rows >= offsets[E] of Y / dX are left as allocated (uninitialised).
     """
-    import torch
     p = _pass_code(pass_)
     E = int(offsets.numel()) - 1
     M = int(a.shape[0])
@@ -422,10 +432,9 @@ def grouped_gemm(pass_, a, b, offsets, out_dtype="bf16", deterministic=True, max
     if plan is None:
         plan = cake_gg_plan(p, E, M, N, K, out_dtype, deterministic, max_sms)
     if out is None:
-        out = _for_stream(stream, a.device, lambda: torch.empty(shape, dtype=_torch_out_dtype(out_dtype), device=a.device),
-                          result=True)
+        out = _result(shape, _torch_out_dtype(out_dtype), a.device, stream)
     if workspace is None:
-        workspace = _for_stream(stream, a.device, lambda: make_workspace(plan, a.device))
+        workspace = _scratch(plan, a.device, stream)
     fn = {CAKE_GG_FWD: cake_gg_fwd, CAKE_GG_DGRAD: cake_gg_dgrad, CAKE_GG_WGRAD: cake_gg_wgrad}[p]
     rc = fn(plan, a, b, out, offsets, out_dtype, deterministic, workspace, stream=stream)
     if rc != CAKE_GG_OK:
@@ -448,9 +457,9 @@ def router_gemm(X, W, max_sms=0, out=None, plan=None, workspace=None, stream=Non
     if plan is None:
         plan = cake_gg_router_plan(T, R, K, max_sms)
     if out is None:
-        out = _for_stream(stream, X.device, lambda: torch.empty((T, R), dtype=torch.float32, device=X.device), result=True)
+        out = _result((T, R), torch.float32, X.device, stream)
     if workspace is None:
-        workspace = _for_stream(stream, X.device, lambda: make_workspace(plan, X.device))
+        workspace = _scratch(plan, X.device, stream)
     rc = cake_gg_router_fp32(plan, X, W, out, workspace, stream=stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_router_fp32")
@@ -465,12 +474,12 @@ _i8_types = None
 
 
 def _i8_torch():
-    """Names of the X types, and torch's int8, float32 and int32."""
+    """Names of the X types, torch's int8, float32 and int32, and its output types by whether they are FP32."""
     global _i8_types
     if _i8_types is None:
         import torch
         _i8_types = ({torch.bfloat16: "bf16", torch.float32: "fp32", torch.int8: "int8"},
-                     torch.int8, torch.float32, torch.int32)
+                     torch.int8, torch.float32, torch.int32, (torch.bfloat16, torch.float32))
     return _i8_types
 
 
@@ -481,16 +490,12 @@ def _i8_x_name(X):
     return name
 
 
-_raw_device = None
-
-
 def _current_device():
     """The current CUDA device's index (asked only with a CUDA tensor in hand)."""
-    global _raw_device
-    if _raw_device is None:
-        import torch
-        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    return _raw_device()
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
 
 
 def _refuse_device(tensor):
@@ -537,9 +542,9 @@ def quantize_rows(X, act=None, out=None, scale=None, stream=None):
     if X.get_device() < 0 or X.get_device() != _current_device():
         _refuse_device(X)
     if out is None:
-        out = _for_stream(stream, X.device, lambda: torch.empty((T, K), dtype=torch.int8, device=X.device), result=True)
+        out = _result((T, K), torch.int8, X.device, stream)
     if scale is None:
-        scale = _for_stream(stream, X.device, lambda: torch.empty(T, dtype=torch.float32, device=X.device), result=True)
+        scale = _result((T,), torch.float32, X.device, stream)
     rc = cake_gg_i8_quant(X, name, act, T, K, out, scale, stream)
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_i8_quant")
@@ -566,7 +571,7 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
     orders them after what wrote the inputs, and whatever reads the output, or
     writes or frees the inputs, after them.
     """
-    names, i8, f32, i32 = _i8_types or _i8_torch()
+    names, i8, f32, i32, out_types = _i8_types or _i8_torch()
     name = names.get(X.dtype) or _i8_x_name(X)
     if act not in I8_ACTS:
         raise ValueError(f"act is None or 'silu_mul', got {act!r}")
@@ -599,23 +604,23 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
             _need(offsets, "offsets", i32, (E + 1,), device)
         if rows is not None:
             _need(rows, "rows", i32, (M,), device)
+    out_code = _dtype_code(out_dtype)
+    out_type = out_types[out_code == CAKE_GG_FP32]
     if plan is None:
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
-    elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], I8_ACTS[act], _dtype_code(out_dtype)):
+    elif getattr(plan, "problem", None) != (E, M, T, N, K, I8_X_DTYPES[name], I8_ACTS[act], out_code):
         raise ValueError("the plan is another problem's")
-    if out is not None and not (out.dtype is _torch_out_dtype(out_dtype) and out.shape == (M, N)
-                                and out.is_contiguous() and out.get_device() == on):
-        _need(out, "out", _torch_out_dtype(out_dtype), (M, N), W.device)
+    if out is not None and not (out.dtype is out_type and out.shape == (M, N) and out.is_contiguous()
+                                and out.get_device() == on):
+        _need(out, "out", out_type, (M, N), W.device)
     if on < 0 or on != _current_device():
         _refuse_device(W)
     if workspace is not None and workspace.get_device() != on:
         raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
     if out is None:
-        import torch
-        out = _for_stream(stream, W.device, lambda: torch.empty((M, N), dtype=_torch_out_dtype(out_dtype), device=W.device),
-                          result=True)
+        out = _result((M, N), out_type, W.device, stream)
     if workspace is None:
-        workspace = _for_stream(stream, W.device, lambda: make_workspace(plan, W.device))
+        workspace = _scratch(plan, W.device, stream)
     if stream is None:
         stream = _current_stream(on)
     elif not isinstance(stream, int):
