@@ -309,7 +309,8 @@ int cake_gg_router_fp32(const cake_gg_router_plan_t *rp, const float *X, const f
  * every max_sms.
  *
  * X is q itself (x_dtype CAKE_GG_INT8, xs given), or BF16 / FP32 activations
- * (xs null) that the call quantises row by row first:
+ * (xs null) that the call quantises row by row first (all T of them, whichever
+ * `rows` names):
  *
  *   h = x, or with CAKE_GG_ACT_SILU_MUL  h = g / (1 + exp(-g)) * u  of rows
  *       x[t] = [g | u] of 2 K values (what stands between the two products

@@ -5,9 +5,11 @@
 //   a[t] = max_k |h[t, k]|     s[t] = a / 127     q[t, k] = rint(h[t, k] * (127 / a))
 //   Y[m, n] = (sum_k q[r(m), k] W[e(m), n, k]) * ws[e(m), n] * s[r(m)]
 //
-// A call is one launch when X is already 8-bit and its rows are few, else two:
-// the token pass below writes 8-bit rows and their scales to the workspace,
-// and the product reads them.
+// A call is one launch when its rows are few and X is 8-bit, or activations that
+// the product's blocks quantise themselves.  Else it is two: the token pass below
+// writes the integers of the tokens (for the tensor cores as FP16) and their
+// scales to the workspace, and the product reads them.  A long call without
+// routed rows may be two of each (choose_first).
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -85,8 +87,10 @@ __device__ __forceinline__ void store8(__half *out, const float (&v)[8], const R
 
 // blockDim.x threads per row.  The first kHeld vectors of 8 values that a thread owns
 // stay in registers between the maximum and the rounding; longer rows read the
-// rest again (from L2).  Bound by HBM (3001 x 5120 FP32 to FP16: 13.5 us, 5.8 TB/s
-// read and written) and by how many rows are resident, so registers are held
+// rest again (from L2).  FP32 is bound by HBM (to bytes 16384 x 4096: 52 us, 6.5 TB/s
+// read and written; to FP16 3001 x 5120: 16.5 us, 5.6), BF16 by its instructions and
+// the latency of its loads (16384 x 4096: 41 us, 4.9 TB/s, 0.69 of the issue slots) and
+// by how many rows are resident, so registers are held
 // down as far as that pays (to bytes, BF16 16384 x 4096: 55 us with 50 registers, 41
 // with 32; FP32 51, 49 with 48, 69 with 32, but to FP16 3001 x 5120 the 48 lose 1 us;
 // gated BF16 92, 85 with 48); gated rows by the exponential and the division (some
@@ -318,7 +322,7 @@ constexpr int kSms = 152;
 // Multiprocessors that clusters of `splits` CTAs can hold at once: a cluster lies
 // within one of the GPU's groups of them, whose sizes differ from part to part.
 // Here 152, 138, 144, 140, 138, 105, 120 for 2 .. 8; a call of one cluster more
-// takes a second wave (374 x 3328 -> 1000 as 48 clusters of three 20.6 us, 14
+// takes a second wave (374 x 3328 -> 1000 as 48 clusters of three 21.3 us, 15
 // undivided).
 int cluster_sms(int splits) { return splits <= 2 ? kSms : splits <= 6 ? 132 : 104; }
 int64_t stage_ns(int pair, int nt) { return pair == 2 ? 250 + nt * 7 / 6 : 280 + nt * 11 / 10; }
@@ -330,10 +334,17 @@ int64_t stage_ns(int pair, int nt) { return pair == 2 ? 250 + nt * 7 / 6 : 280 +
 // times as long as the rest of the pass: that share f of the rows, for one
 // expert cut where a wave of units ends.  Worth it where the pass hidden, of
 // which about half is won (the power limit takes the rest), is more than a
-// wave that the cut adds and the start of two more kernels.  Measured in turn:
-// 16384 x 4096 -> 4096 from 8-bit tokens 320 us undivided, 312, 307, 322 with f =
-// 0.12, 0.22, 0.28; gated 32768 x 2048 -> 6144 over 32 experts 533, 533, 520,
-// 511, 517 with f = 0, 0.12, 0.24, 0.37, 0.49.
+// wave that the cut adds and the start of two more kernels.  Measured in turn, one
+// call after another, so under the power limit: 16384 x 4096 -> 4096 from 8-bit
+// tokens 333 us undivided, 317, 316, 329 with f = 0.12, 0.22, 0.28 (by itself, a few
+// calls at a time, 315 and 297 with 0.22); gated 32768 x 2048 -> 6144 over 32
+// experts 564, 567, 557, 551, 543 with f = 0, 0.12, 0.24, 0.37, 0.49.  8-bit tokens
+// gain 4 to 9 % (32768 x 4096 -> 2048: 359 to 329; 16384 x 8192 -> 1024: 228 to 208),
+// gated ones 2.5 % (16384 x 4096 -> 4096: 379 to 370).  BF16 that is not gated gains up
+// to 2 % over long reductions (16384 x 8192 -> 8192: 1308 to 1280) and loses as much over
+// short ones (16384 x 5120 -> 1000: 162 to 165), and FP32 loses 1 to 3 % (16384 x 4096 ->
+// 4096: 334 to 341; 5 % into 1000 channels): there the pass takes from HBM and L2 what
+// the product needs.
 int choose_first(const cake_gg_i8_plan_t &pl)
 {
     const int nt = pl.tile_rows;
@@ -358,16 +369,16 @@ int choose_first(const cake_gg_i8_plan_t &pl)
 // Shape of the tensor-core path, from a model of its time in nanoseconds: waves
 // of units over the multiprocessors (152, or 76 pairs), the stages of a unit,
 // the storing of the last one, and the exchange between the CTAs that share a
-// tile (33 x 4608 -> 496 over 1, 2, 3, 4, 6, 8 CTAs, 32 rows a tile: 15.6, 12.0, 10.7, 9.7,
-// 9.2, 8.7 us; 247 x 4528 -> 304, 64 rows: 17.4, 14.9, 12.6, 11.4, 12.5, 11.9).  The times of a stage were measured with all multiprocessors at work
-// (12288 x 4096 -> 4096): pairs 323, 358, 368, 432, 473 ns for 64, 96, 128, 160,
-// 192 rows, single CTAs 314, 348, 382, 451 ns for 32, 64, 96, 128.  (Pairs of 256
-// rows hold one accumulator, whose storing nothing overlaps: 774 ns.)  What it
-// decides, measured with the neighbours: 3001 x 5120 -> 1000 takes 160 rows (38.6
-// us; 39.8 with 192, 48.5 with 128), 701 tokens through 2 of 8 experts 4096 ->
-// 2048 take 96 (31.5; 32.7 with 128, 35.4 with 192), 200 x 4096 -> 4096 take 64
-// (16.6; 20.5 with 192), 33 x 4096 -> 5120 divide the reduction by 3 (11.3; 14.6
-// undivided).
+// tile (33 x 4608 -> 496 over 1, 2, 3, 4, 6, 8 CTAs, 32 rows a tile: 16.3, 12.9, 11.4, 10.5,
+// 10.2, 9.7 us; 247 x 4528 -> 304, 64 rows: 17.9, 15.1, 12.8, 12.0, 12.9, 12.6).  The
+// times of a stage, with all multiprocessors at work (12288 x 4096 -> 4096), are for
+// pairs 325, 362, 362, 419, 454 ns for 64, 96, 128, 160, 192 rows, for single CTAs
+// 327, 348, 383, 435 ns for 32, 64, 96, 128; the lines that stand for them above are
+// within 5 % of that but for pairs of 128 rows (10 % above).  What the model decides,
+// measured with the neighbours: 3001 x 5120 -> 1000 takes 160 rows (40.4 us; 40.8 with
+// 192, 50.6 with 128), 701 tokens through 2 of 8 experts 4096 -> 2048 take 96 (32.4;
+// 34.1 with 128, 35.8 with 192), 200 x 4096 -> 4096 take 64 (17.7; 21.7 with pairs of
+// 192), 33 x 4096 -> 5120 divide the reduction by 3 (12.2; 16.0 undivided).
 void choose_mma(cake_gg_i8_plan_t *pl)
 {
     const int64_t n_kb = (pl->K + 127) / 128;

@@ -18,10 +18,11 @@
 // B's width follows the rows the tile really has, so a ragged end costs its own
 // size only.
 //
-// Bound: long inputs by the tensor cores (16384 x 4096 -> 4096: 265 us, 2.07
-// PFLOP/s at full clocks; 32768 tokens through 2 of 8 experts 4096 -> 4096 1.10 ms,
-// 1.99), decoding batches by the weights' bytes (64 tokens through 4 of 32 experts
-// 6144 -> 4096: 6.2 TB/s over the call).
+// Bound: long inputs by the tensor cores and the power limit (12288 x 4096 -> 4096 a
+// few calls at a time 204 us, 2.02 PFLOP/s; one after another 16384 x 4096 -> 4096 290
+// us, 1.89, and 32768 tokens through 2 of 8 experts 4096 -> 4096 1.24 ms, 1.77),
+// decoding batches by the weights' bytes (64 tokens through 4 of 32 experts 6144 ->
+// 4096: 6.2 TB/s over the call).
 //
 // Roles of a CTA: warp 0 copies weights, warp 1 issues MMAs, warps 2-9 scale and
 // store (two groups on alternate 32 rows of a tile; with one group short
