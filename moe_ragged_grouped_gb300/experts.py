@@ -51,8 +51,18 @@ class Int8Experts:
         self.router = torch.nn.functional.pad(router.float(), (0, 0, 0, -E % 8)).contiguous()
         self.up_q, self.up_s = self._quantise(gate_up)
         self.down_q, self.down_s = self._quantise(down)
-        self._planned = functools.lru_cache(maxsize=256)(functools.partial(_plans, E, K, F, top_k))
+        self._keep_nothing()
+
+    def _keep_nothing(self):
+        self._planned = functools.lru_cache(maxsize=256)(functools.partial(_plans, self.E, self.K, self.F, self.top_k))
         self._mine = threading.local()   # a thread's calls may interleave with another's on one stream
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_planned", "_mine")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._keep_nothing()
 
     @staticmethod
     def _quantise(w):

@@ -78,6 +78,21 @@ def test_a_layer_is_freed_with_its_last_name(host_layer):
         gc.enable()
 
 
+def test_a_layer_can_be_copied_and_pickled(host_layer):
+    """Its weights go along, what it keeps between calls does not."""
+    import copy
+    import pickle
+
+    import torch
+    device = torch.device("cpu")
+    mine = {t.untyped_storage().data_ptr() for t in _tensors(host_layer._for(5, device))}
+    for other in (copy.deepcopy(host_layer), pickle.loads(pickle.dumps(host_layer))):
+        assert torch.equal(other.up_q, host_layer.up_q) and other.top_k == host_layer.top_k
+        assert other.up_q.data_ptr() != host_layer.up_q.data_ptr()
+        theirs = {t.untyped_storage().data_ptr() for t in _tensors(other._for(5, device))}
+        assert theirs and not theirs & mine
+
+
 def _gpu_layer(E=8, K=256, F=144, top=3):
     import torch
     if not torch.cuda.is_available():
