@@ -604,7 +604,7 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
             _need(offsets, "offsets", i32, (E + 1,), device)
         if rows is not None:
             _need(rows, "rows", i32, (M,), device)
-    out_code = _dtype_code(out_dtype)
+    out_code = DTYPES[out_dtype] if out_dtype.__class__ is str else int(out_dtype)
     out_type = out_types[out_code == CAKE_GG_FP32]
     if plan is None:
         plan = cake_gg_i8_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
@@ -615,12 +615,12 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         _need(out, "out", out_type, (M, N), W.device)
     if on < 0 or on != _current_device():
         _refuse_device(W)
-    if workspace is not None and workspace.get_device() != on:
-        raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
     if out is None:
         out = _result((M, N), out_type, W.device, stream)
     if workspace is None:
         workspace = _scratch(plan, W.device, stream)
+    elif workspace.get_device() != on:
+        raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
     if stream is None:
         stream = _current_stream(on)
     elif not isinstance(stream, int):
