@@ -21,6 +21,7 @@
 // the token pass), larger ones by the loads that the registers hold in flight (16 x
 // 4096 -> 5120: 11.5 us, 1.9 TB/s), which is where the tensor-core path takes over.
 #include "cake_gg_int8.h"
+#include "cake_gg_int8_index.h"
 #include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
 
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads)
     const int n_rows = int(found[2] - m < R ? found[2] - m : R);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int at = (lane & 3) * 16;
+    const int at = i8_warps_place(lane);
     const int steps = (p.K + 63) / 64;
     const int8_t *w[4];
 #pragma unroll
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     uint4 wv[4];
     auto load_w = [&](int s) {
-        const bool in = s < steps && s * 64 + at < p.K;
+        const bool in = i8_warps_in(s, lane, p.K);
 #pragma unroll
         for (int i = 0; i < 4; ++i) wv[i] = in ? ld_weights(w[i] + s * 64) : make_uint4(0, 0, 0, 0);
     };
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
     for (int s = warp; s < steps; s += kWarps) {
-        const int k = s * 64 + at < p.K ? s * 64 : 0;            // past the end: weights are zero
+        const int k = i8_warps_token(s, lane, p.K) - at;
         uint4 xv[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j)

@@ -180,3 +180,21 @@ def test_outputs_past_2_31(x_dtype):
         rows = slice(at, at + 500)
         want = (q[rows].double() @ W.double().T).float() * ws * xs[rows, None]
         assert torch.equal(y[rows], want.to(torch.bfloat16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("path", [ROWS, MMA, WARPS])
+@pytest.mark.parametrize("K", [16, 32, 48, 64, 80, 112])
+@pytest.mark.parametrize("x_dtype", ["int8", "bf16"])
+def test_rows_shorter_than_a_step(path, K, x_dtype, monkeypatch):
+    torch = _gpu()
+    monkeypatch.setenv("CAKE_GG_I8_PATH", str(path))
+    g = torch.Generator(device="cuda").manual_seed(K)
+    for M, N in ((1, 8), (5, 40), (16, 72), (31, 264)):
+        W = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        ws = torch.rand(N, generator=g, device="cuda") + 0.5
+        x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+        q, xs = gg.quantize_rows(x)
+        got = gg.int8_gemm(q, W, ws, xs=xs) if x_dtype == "int8" else gg.int8_gemm(x, W, ws)
+        want = (q.double() @ W.double().T).float() * ws * xs[:, None]
+        assert torch.equal(got, want.to(torch.bfloat16))
