@@ -111,12 +111,13 @@ typedef enum {
     CAKE_GG_ERR_BAD_OFFSETS = 7,  /* device-detected: offsets not 0-based, decreasing or > M_max */
     CAKE_GG_ERR_TIMEOUT = 8,      /* device-detected: a bounded wait inside the kernel expired */
     CAKE_GG_ERR_SCRATCH_LIMIT = 9,/* the problem needs more scratch than cake_gg_wgrad_noalloc's fixed maximum */
-    CAKE_GG_ERR_BAD_ROWS = 10     /* device-detected: a row index of the 8-bit products outside [0, T) */
+    CAKE_GG_ERR_BAD_ROWS = 10     /* device-detected: a row index of the 8- or 4-bit products outside [0, T) */
 } cake_gg_status_t;
 
 typedef enum { CAKE_GG_FWD = 0, CAKE_GG_DGRAD = 1, CAKE_GG_WGRAD = 2 } cake_gg_pass_t;
-/* CAKE_GG_INT8: the 8-bit products' tokens only (cake_gg_i8_plan's x_dtype). */
-typedef enum { CAKE_GG_BF16 = 0, CAKE_GG_FP32 = 1, CAKE_GG_INT8 = 2 } cake_gg_dtype_t;
+/* CAKE_GG_INT8: the 8-bit products' tokens only (cake_gg_i8_plan's x_dtype);
+ * CAKE_GG_MX4: the 4-bit products' (cake_gg_mx4_plan's). */
+typedef enum { CAKE_GG_BF16 = 0, CAKE_GG_FP32 = 1, CAKE_GG_INT8 = 2, CAKE_GG_MX4 = 3 } cake_gg_dtype_t;
 
 /* Plan: a caller-owned plain struct filled by cake_gg_plan(); nothing to free.
  * The first block holds the problem as given; the second holds the choices
@@ -379,6 +380,92 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
  * CAKE_GG_ACT_SILU_MUL) into Xq [T, K] and xs [T], as above.  One kernel. */
 int cake_gg_i8_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, int8_t *Xq, float *xs,
                      void *stream);
+
+/* ---- 4-bit floating-point products with a scale per block -----------------
+ *
+ * A linear layer in serving whose weights and tokens are 4-bit floating point
+ * with a shared power of two for each block of 32 values along the reduction
+ * (the OCP Microscaling Formats specification's MXFP4): dense (E = 1), or
+ * grouped by expert with ragged sizes and rows routed from tokens by index.
+ *
+ *   Y[m, n] = sum_k x[r(m), k] w[e(m), n, k]
+ *
+ * with e(m) and r(m) as in the 8-bit products.  A value is an E2M1 code (0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 the sign) times 2^(s - 127), s the byte of its
+ * block.  Codes are packed two to a byte along the reduction, the even one in
+ * the low half: W [E, N, K / 2], X [T, K / 2].  Scales lie as the tensor cores
+ * take them, in tiles of 128 rows x 4 blocks of 512 bytes: the byte of row r and
+ * block b is
+ *
+ *   S[r / 128][b / 4][r % 32][r % 128 / 32][b % 4],
+ *
+ * for X one matrix [ceil(T / 128), ceil(K / 128), 32, 4, 4], for W one per
+ * expert, [E, ceil(N / 128), ceil(K / 128), 32, 4, 4].  s = 255 is a NaN, of the
+ * whole block.  The bytes of blocks past K in a row's last tile must not be 255
+ * (cake_gg_mx4_quant writes zeros); those of rows past the last may be
+ * anything.  Products are exact, their sums FP32; the same call gives the same
+ * bits on every run and under every max_sms.  Rows at or past offsets[E] of Y
+ * are never written, and an expert without rows reads no weights.
+ *
+ * X is the codes (x_dtype CAKE_GG_MX4, xs given), or BF16 / FP32 activations
+ * (xs null) that the call quantises first (all T rows, whichever `rows`
+ * names), block by block:
+ *
+ *   h = x, or with CAKE_GG_ACT_SILU_MUL  h = g / (1 + exp(-g)) * u  of rows
+ *       x[t] = [g | u] of 2 K values
+ *   e = max(floor(log2(max |h|)) - 2, -127),  s = e + 127,
+ *   code of h / 2^e: the nearest, ties to the even code, 6 at most.
+ *
+ * This is the rounding of h itself: where FP32 arithmetic cannot tell on which
+ * side of a border a gated value lies, 64 bits decide.  A block of zeros has s = 0; one
+ * that holds a NaN or an infinity s = 255 and codes 0, so the products of its
+ * row are NaN. */
+typedef struct cake_gg_mx4_plan {
+    int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
+    int32_t E;               /* experts, 1 .. 1024                                  */
+    int64_t M_max;           /* rows of Y (0 .. 2^31 - 1)                           */
+    int64_t T;               /* rows of X (= M_max without rows)                    */
+    int32_t N;               /* output channels, a multiple of 8, at most 2^31 - 512 */
+    int32_t K;               /* reduction length, a multiple of 32, below 2^17      */
+    int32_t x_dtype;         /* cake_gg_dtype_t: CAKE_GG_MX4, _BF16 or _FP32        */
+    int32_t act;             /* cake_gg_act_t (CAKE_GG_ACT_NONE for 4-bit X)        */
+    int32_t out_dtype;       /* CAKE_GG_BF16 or CAKE_GG_FP32                        */
+    int32_t max_sms;         /* cap on persistent CTAs (without splits);
+                                0 = every SM of the device                          */
+    /* chosen by cake_gg_mx4_plan() */
+    int32_t pair;            /* 2: two CTAs compute 256 channels as one MMA, else 1 */
+    int32_t tile_rows;       /* rows of a tile at most                              */
+    int32_t stages;          /* shared-memory ring depth                            */
+    int32_t splits;          /* CTAs of a cluster that share a tile's reduction     */
+    int32_t debug_flags;     /* test-only fault injection; 0 in normal use          */
+    int32_t reserved;
+    uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
+    uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
+} cake_gg_mx4_plan_t;
+
+/* Fill *plan.  Pure host arithmetic.  CAKE_GG_ERR_INVALID_ARG for sizes out of
+ * range, T < 1 with rows to compute, an activation with 4-bit X;
+ * CAKE_GG_ERR_UNSUPPORTED for other types; CAKE_GG_ERR_ALIGNMENT unless N is a
+ * multiple of 8 and K of 32; CAKE_GG_ERR_OVERFLOW for K >= 2^17, N > 2^31 - 512,
+ * 2^31 scale tiles of weights or a size product past 64 bits. */
+int cake_gg_mx4_plan(cake_gg_mx4_plan_t *plan, int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K,
+                     int x_dtype, int act, int out_dtype, int32_t max_sms);
+
+/* The product.  X, xs, W, ws, Y, workspace: device pointers, 16-byte aligned;
+ * rows, offsets 4-byte aligned.  The workspace is plan->workspace_bytes,
+ * zero-filled once after allocation.  Enqueues one or two kernels on `stream`;
+ * allocates nothing, never synchronises.  Errors as cake_gg_i8_gemm's. */
+int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_t *xs, const int32_t *rows,
+                     const uint8_t *W, const uint8_t *ws, void *Y, const int32_t *offsets, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Quantise E matrices X [E, R, K] (BF16 or FP32; [E, R, 2 K] with
+ * CAKE_GG_ACT_SILU_MUL) into codes Xq [E, R, K / 2] and scales xs, E times
+ * ceil(R / 128) * ceil(K / 128) tiles, as above: tokens with E = 1, weights
+ * with their experts.  The scales of rows past R in a matrix's last tile are left
+ * as they were.  One kernel. */
+int cake_gg_mx4_quant(const void *X, int x_dtype, int act, int32_t E, int64_t R, int32_t K, uint8_t *Xq,
+                      uint8_t *xs, void *stream);
 
 /* Synchronise `stream`, return the status word of `workspace` (CAKE_GG_OK,
  * or the first _BAD_OFFSETS / _TIMEOUT / _BAD_ROWS recorded by a call since the last

@@ -31,19 +31,21 @@ CAKE_GG_ERR_BAD_ROWS = 10
 CAKE_GG_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 CAKE_GG_FWD, CAKE_GG_DGRAD, CAKE_GG_WGRAD = 0, 1, 2
-CAKE_GG_BF16, CAKE_GG_FP32, CAKE_GG_INT8 = 0, 1, 2
+CAKE_GG_BF16, CAKE_GG_FP32, CAKE_GG_INT8, CAKE_GG_MX4 = 0, 1, 2, 3
 CAKE_GG_ACT_NONE, CAKE_GG_ACT_SILU_MUL = 0, 1
 CAKE_GG_DEBUG_DROP_FIRST_LOAD = 1
 
 PASSES = {"fwd": CAKE_GG_FWD, "dgrad": CAKE_GG_DGRAD, "wgrad": CAKE_GG_WGRAD}
 DTYPES = {"bf16": CAKE_GG_BF16, "fp32": CAKE_GG_FP32}
 I8_X_DTYPES = {**DTYPES, "int8": CAKE_GG_INT8}
+MX4_X_DTYPES = {**DTYPES, "mx4": CAKE_GG_MX4}
 I8_ACTS = {None: CAKE_GG_ACT_NONE, "silu_mul": CAKE_GG_ACT_SILU_MUL}
 
 EXPORTED = ["cake_gg_plan", "cake_gg_fwd", "cake_gg_dgrad", "cake_gg_wgrad",
             "cake_gg_check_status", "cake_gg_strerror", "cake_gg_tile_walk", "cake_gg_corun_spinner",
             "cake_gg_router_plan", "cake_gg_router_fp32",
-            "cake_gg_i8_plan", "cake_gg_i8_gemm", "cake_gg_i8_quant"]
+            "cake_gg_i8_plan", "cake_gg_i8_gemm", "cake_gg_i8_quant",
+            "cake_gg_mx4_plan", "cake_gg_mx4_gemm", "cake_gg_mx4_quant"]
 
 
 class CakeGGPlan(ctypes.Structure):
@@ -124,6 +126,33 @@ class CakeGGI8Plan(ctypes.Structure):
         return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
 
 
+class CakeGGMx4Plan(ctypes.Structure):
+    """Mirror of cake_gg_mx4_plan_t (same field order, same C layout)."""
+    _fields_ = [
+        ("abi_version", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("M_max", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("max_sms", ctypes.c_int32),
+        ("pair", ctypes.c_int32),
+        ("tile_rows", ctypes.c_int32),
+        ("stages", ctypes.c_int32),
+        ("splits", ctypes.c_int32),
+        ("debug_flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("timeout_ns", ctypes.c_uint64),
+        ("workspace_bytes", ctypes.c_uint64),
+    ]
+
+    def as_dict(self):
+        return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
+
+
 class CakeGGError(RuntimeError):
     def __init__(self, code, where):
         super().__init__(f"{where}: {cake_gg_strerror(code)} (status {code})")
@@ -174,6 +203,13 @@ def load_library(path: str = LIB_PATH):
     lib.cake_gg_i8_gemm.restype = ctypes.c_int
     lib.cake_gg_i8_quant.argtypes = [vp, ctypes.c_int, ctypes.c_int, i64, i32, vp, vp, vp]
     lib.cake_gg_i8_quant.restype = ctypes.c_int
+    mx4plan_p = ctypes.POINTER(CakeGGMx4Plan)
+    lib.cake_gg_mx4_plan.argtypes = [mx4plan_p, i32, i64, i64, i32, i32, ctypes.c_int, ctypes.c_int, ctypes.c_int, i32]
+    lib.cake_gg_mx4_plan.restype = ctypes.c_int
+    lib.cake_gg_mx4_gemm.argtypes = [mx4plan_p, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.cake_gg_mx4_gemm.restype = ctypes.c_int
+    lib.cake_gg_mx4_quant.argtypes = [vp, ctypes.c_int, ctypes.c_int, i32, i64, i32, vp, vp, vp]
+    lib.cake_gg_mx4_quant.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -355,6 +391,36 @@ def cake_gg_i8_quant(X, x_dtype, act, T, K, Xq, xs, stream=None) -> int:
     """cake_gg_i8_quant(): rows of X to 8-bit rows and scales; returns the status code."""
     return load_library().cake_gg_i8_quant(_ptr(X), _i8_x_code(x_dtype), _act_code(act), int(T), int(K), _ptr(Xq),
                                            _ptr(xs), _stream(stream, X))
+
+
+def _mx4_x_code(d):
+    return MX4_X_DTYPES[d] if isinstance(d, str) else int(d)
+
+
+def cake_gg_mx4_plan(E, M_max, T, N, K, x_dtype="bf16", act=None, out_dtype="bf16", max_sms=0) -> CakeGGMx4Plan:
+    """cake_gg_mx4_plan(): plan of a 4-bit product of M_max rows from T tokens; raises on error."""
+    plan = CakeGGMx4Plan()
+    # the problem as mx4_gemm compares it (a changed field is the library's to refuse)
+    plan.problem = (int(E), int(M_max), int(T), int(N), int(K), _mx4_x_code(x_dtype), _act_code(act),
+                    _dtype_code(out_dtype))
+    rc = load_library().cake_gg_mx4_plan(ctypes.byref(plan), int(E), int(M_max), int(T), int(N), int(K),
+                                         _mx4_x_code(x_dtype), _act_code(act), _dtype_code(out_dtype), int(max_sms))
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_mx4_plan")
+    return plan
+
+
+def cake_gg_mx4_gemm(plan, X, xs, rows, W, ws, Y, offsets, workspace, workspace_bytes=None, stream=None) -> int:
+    """cake_gg_mx4_gemm(): the 4-bit product; returns the status code."""
+    nb = int(workspace.numel() * workspace.element_size()) if workspace_bytes is None else int(workspace_bytes)
+    return load_library().cake_gg_mx4_gemm(ctypes.byref(plan), _ptr(X), _ptr(xs), _ptr(rows), _ptr(W), _ptr(ws), _ptr(Y),
+                                           _ptr(offsets), _ptr(workspace), nb, _stream(stream, W))
+
+
+def cake_gg_mx4_quant(X, x_dtype, act, E, R, K, Xq, xs, stream=None) -> int:
+    """cake_gg_mx4_quant(): E matrices of R rows to 4-bit codes and block scales; returns the status code."""
+    return load_library().cake_gg_mx4_quant(_ptr(X), _mx4_x_code(x_dtype), _act_code(act), int(E), int(R), int(K),
+                                            _ptr(Xq), _ptr(xs), _stream(stream, X))
 
 
 # ---------------------------------------------------------------- tensor-level helpers
@@ -637,4 +703,165 @@ def int8_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="b
         st = cake_gg_check_status(workspace, stream)
         if st != CAKE_GG_OK:
             raise CakeGGError(st, "cake_gg_i8_gemm (device status)")
+    return out
+
+
+def _mx4_tiles(R, K):
+    """Shape of the scale tiles of a matrix of R rows of K values."""
+    return (-(-R // 128), -(-K // 128), 32, 4, 4)
+
+
+def quantize_mx4(X, act=None, out=None, scale=None, stream=None):
+    """X [T, K] or [E, R, K] (bf16 or fp32) as 4-bit codes [.., K / 2] and block scales (both uint8).
+
+    A block of 32 values along K shares a power of two; the codes are E2M1,
+    two to a byte, the even one low, and the scales E8M0 in tiles of 128 rows x 4 blocks:
+    [ceil(T / 128), ceil(K / 128), 32, 4, 4], or [E, ceil(R / 128), ..] with a
+    tile grid for each of E matrices, which are mx4_gemm's tokens and weights
+    (mx4_values() says what they stand for).  ``act="silu_mul"`` takes rows
+    [g | u] of 2 K values and quantises silu(g) * u.  A block that holds a NaN or
+    an infinity becomes NaN.  K is a multiple of 32.  In a `scale` that is given,
+    rows past the last of a tile stay as they were.  All tensors are on the
+    current CUDA device (others are refused); stream as in int8_gemm.
+    """
+    import torch
+    name = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(X.dtype)
+    if name is None:
+        raise TypeError(f"X is {X.dtype}: bfloat16 or float32 are taken")
+    if act not in I8_ACTS:
+        raise ValueError(f"act is None or 'silu_mul', got {act!r}")
+    if X.dim() not in (2, 3) or (act is not None and X.shape[-1] % 2 != 0):
+        raise ValueError("X is [T, K] or [E, R, K], or twice as wide with an activation")
+    E = int(X.shape[0]) if X.dim() == 3 else 1
+    R, K = int(X.shape[-2]), int(X.shape[-1]) // (1 if act is None else 2)
+    lead = (E,) if X.dim() == 3 else ()
+    _need(X, "X", X.dtype, tuple(X.shape), X.device)
+    if out is not None:
+        _need(out, "out", torch.uint8, lead + (R, K // 2), X.device)
+    if scale is not None:
+        _need(scale, "scale", torch.uint8, lead + _mx4_tiles(R, K), X.device)
+    if X.get_device() < 0 or X.get_device() != _current_device():
+        _refuse_device(X)
+    if out is None:
+        out = _result(lead + (R, K // 2), torch.uint8, X.device, stream)
+    if scale is None:
+        scale = _for_stream(stream, X.device, lambda: torch.zeros(lead + _mx4_tiles(R, K), dtype=torch.uint8, device=X.device),
+                            result=True)
+    rc = cake_gg_mx4_quant(X, name, act, E, R, K, out, scale, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_mx4_quant")
+    return out, scale
+
+
+def mx4_values(q, scale):
+    """The FP32 numbers [.., K] that 4-bit codes [.., K / 2] and their scale tiles stand for (torch operations, any device)."""
+    import torch
+    R, K = int(q.shape[-2]), 2 * int(q.shape[-1])
+    sizes = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=q.device)
+    codes = torch.stack([q & 15, q >> 4], dim=-1).reshape(*q.shape[:-1], K).long()
+    v = torch.where(codes < 8, sizes[codes & 7], -sizes[codes & 7])
+    s = scale.transpose(-4, -2)                         # [.., tile, r % 128 / 32, r % 32, K / 128, block]
+    s = s.reshape(*scale.shape[:-5], scale.shape[-5] * 128, -1)[..., :R, :K // 32].to(torch.int32)
+    # the power of two by its bits: 2^-127 is below the normal range
+    power = torch.where(s == 0, torch.full_like(s, 1 << 22), s << 23).view(torch.float32)
+    power = torch.where(s == 255, torch.full_like(power, float("nan")), power)
+    return v * power.repeat_interleave(32, dim=-1)
+
+
+_mx4_types = None
+
+
+def _mx4_torch():
+    """Names of the X types, torch's uint8 and int32, and its output types by whether they are FP32."""
+    global _mx4_types
+    if _mx4_types is None:
+        import torch
+        _mx4_types = ({torch.bfloat16: "bf16", torch.float32: "fp32", torch.uint8: "mx4"}, torch.uint8, torch.int32,
+                      (torch.bfloat16, torch.float32))
+    return _mx4_types
+
+
+def mx4_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="bf16", max_sms=0, out=None,
+             plan=None, workspace=None, stream=None, check=True):
+    """Product of 4-bit rows and weights with a power of two for each block of 32 values.
+
+        Y[m, n] = sum_k x[r, k] w[e, n, k]
+
+    W [E, N, K / 2] uint8 and its scale tiles ws (dense: [N, K / 2]) are
+    quantize_mx4's; expert e owns the rows [offsets[e], offsets[e+1]) of Y
+    (int32 [E + 1]; none for dense); r = rows[m] (int32 [M], the token that row m
+    was routed from) or m itself.  X is the tokens: uint8 [T, K / 2] with their
+    scale tiles xs, or bf16 / fp32 [T, K] quantised on the way ([T, 2 K] with
+    act="silu_mul", see quantize_mx4).  Rows >= offsets[E] of Y are left as
+    allocated.  Output, workspace, devices, `stream` and `check` as in int8_gemm.
+    """
+    names, u8, i32, out_types = _mx4_types or _mx4_torch()
+    name = names.get(X.dtype)
+    if name is None:
+        raise TypeError(f"X is {X.dtype}: uint8, bfloat16 or float32 are taken")
+    if act not in I8_ACTS:
+        raise ValueError(f"act is None or 'silu_mul', got {act!r}")
+    x_shape, w_shape = X.shape, W.shape
+    if len(w_shape) not in (2, 3) or len(x_shape) != 2:
+        raise ValueError("X is [T, K] and W [N, K / 2] or [E, N, K / 2]")
+    E = w_shape[0] if len(w_shape) == 3 else 1
+    N, K = w_shape[-2], 2 * w_shape[-1]
+    T = x_shape[0]
+    M = T if rows is None else rows.shape[0]
+    if (xs is None) == (name == "mx4"):
+        raise ValueError("xs comes with 4-bit X, and only with it")
+    if offsets is None and E != 1:
+        raise ValueError("W of several experts comes with offsets")
+    width = K // 2 if name == "mx4" else K if act is None else 2 * K
+    tiles = w_shape[:-2] + _mx4_tiles(N, K)
+    # the common case in few calls; what fails here is named below
+    on = W.get_device()
+    if not (W.dtype is u8 and W.is_contiguous() and ws.dtype is u8 and ws.shape == tiles and ws.is_contiguous()
+            and x_shape[1] == width and X.is_contiguous() and on == X.get_device() == ws.get_device()
+            and (xs is None or (xs.dtype is u8 and xs.shape == _mx4_tiles(T, K) and xs.is_contiguous() and xs.get_device() == on))
+            and (offsets is None or (offsets.dtype is i32 and offsets.shape == (E + 1,) and offsets.is_contiguous()
+                                     and offsets.get_device() == on))
+            and (rows is None or (rows.dtype is i32 and rows.dim() == 1 and rows.is_contiguous() and rows.get_device() == on))):
+        device = W.device
+        _need(W, "W", u8, w_shape, device)
+        _need(X, "X", X.dtype, (T, width), device)
+        _need(ws, "ws", u8, tiles, device)
+        if xs is not None:
+            _need(xs, "xs", u8, _mx4_tiles(T, K), device)
+        if offsets is not None:
+            _need(offsets, "offsets", i32, (E + 1,), device)
+        if rows is not None:
+            _need(rows, "rows", i32, (M,), device)
+    out_code = DTYPES[out_dtype] if out_dtype.__class__ is str else int(out_dtype)
+    out_type = out_types[out_code == CAKE_GG_FP32]
+    if plan is None:
+        plan = cake_gg_mx4_plan(E, M, T, N, K, name, act, out_dtype, max_sms)
+    elif getattr(plan, "problem", None) != (E, M, T, N, K, MX4_X_DTYPES[name], I8_ACTS[act], out_code):
+        raise ValueError("the plan is another problem's")
+    if out is not None and not (out.dtype is out_type and out.shape == (M, N) and out.is_contiguous()
+                                and out.get_device() == on):
+        _need(out, "out", out_type, (M, N), W.device)
+    if on < 0 or on != _current_device():
+        _refuse_device(W)
+    if out is None:
+        out = _result((M, N), out_type, W.device, stream)
+    if workspace is None:
+        workspace = _scratch(plan, W.device, stream)
+    elif workspace.get_device() != on:
+        raise ValueError(f"workspace is on {workspace.device}, not on {W.device}")
+    if stream is None:
+        stream = _current_stream(on)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    # (the call of cake_gg_mx4_gemm() above, without its conversions)
+    rc = (_lib or load_library()).cake_gg_mx4_gemm(
+        ctypes.byref(plan), X.data_ptr(), None if xs is None else xs.data_ptr(),
+        None if rows is None else rows.data_ptr(), W.data_ptr(), ws.data_ptr(), out.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_mx4_gemm")
+    if check:
+        st = cake_gg_check_status(workspace, stream)
+        if st != CAKE_GG_OK:
+            raise CakeGGError(st, "cake_gg_mx4_gemm (device status)")
     return out

@@ -704,7 +704,7 @@ int device_sms(int *sms)
 }
 
 int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
-                 const uint64_t *strides, const uint32_t *box)
+                 const uint64_t *strides, const uint32_t *box, bool swizzled)
 {
     const int rc = get_encoder();
     if (rc != CAKE_GG_OK) return rc;
@@ -717,7 +717,7 @@ int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void 
         if (i > 0) gstride[i - 1] = strides[i - 1];
     }
     const CUresult r = g_encode(m, type, cuuint32_t(rank), const_cast<void *>(base), gdim, gstride, bx, estride,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }

@@ -15,9 +15,9 @@ namespace cakegg {
 // (cake_gg_capi.cu) checks that the current device is sm_103 and gives its SM count
 int device_sms(int *sms);
 // (cake_gg_capi.cu) tensor map of a dense tensor, dims[0] contiguous, byte strides of
-// dims 1 .. given, 128-byte swizzled boxes, zero fill outside the tensor
+// dims 1 .. given, zero fill outside the tensor, 128-byte swizzled boxes unless told
 int encode_tiled(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
-                 const uint64_t *strides, const uint32_t *box);
+                 const uint64_t *strides, const uint32_t *box, bool swizzled = true);
 
 // One call of the products, as every kernel sees it.
 //   Y[m, n] = (sum_k q[r(m), k] W[e(m), n, k]) * ws[e(m), n] * xs[r(m)]

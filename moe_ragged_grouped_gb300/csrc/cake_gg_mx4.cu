@@ -1,0 +1,387 @@
+// cake_gg_mx4.cu -- C entry points of the 4-bit products, and the kernel that
+// quantises rows.
+//
+//   h = x, or silu(g) * u of x = [g | u];  a block is 32 values of a row
+//   e = max(floor(log2(max |h|)) - 2, -127),  scale 2^e,  code = E2M1 nearest to h / 2^e
+//   Y[m, n] = sum_k x[r(m), k] w[e(m), n, k]
+//
+// A call is one launch when X comes quantised; else the token pass below writes
+// the tokens' codes and scales to the workspace and the product reads them.
+#include <cmath>
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "cake_gg_int8_quant.cuh"
+#include "cake_gg_mx4.h"
+#include "cake_gg_ptx.cuh"
+
+using namespace cakegg;
+
+namespace {
+
+constexpr uint64_t kHeader = 256;              // status word at byte 0
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int32_t kMaxExperts = 1024;
+constexpr int32_t kMaxK = (1 << 17) - 32;
+constexpr int32_t kMaxN = INT32_MAX - 511;     // channels of whole tiles (256) and storing warps stay below 2^31
+constexpr int kSms = 152;
+constexpr int kStagesLeast = 4;                // a warp that serves every fourth stage meets no barrier two rounds late
+
+uint64_t align_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
+
+bool mul_ok(uint64_t a, uint64_t b, uint64_t *out)
+{
+    if (a != 0 && b > UINT64_MAX / a) return false;
+    *out = a * b;
+    return true;
+}
+
+bool pdl_enabled()
+{
+    const char *v = std::getenv("CAKE_GG_PDL");
+    return !(v && std::atoi(v) == 0);
+}
+
+int env_int(const char *name, int dflt)
+{
+    const char *v = std::getenv(name);
+    return v && *v ? std::atoi(v) : dflt;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+uint64_t scale_bytes(uint64_t rows, int32_t K) { return (rows + 127) / 128 * uint64_t((K + 127) / 128) * kMx4Tile; }
+
+// Workspace: header | the tokens' scales | their codes (activations only).
+struct Layout {
+    uint64_t scales, tokens, total;
+};
+Layout layout(const cake_gg_mx4_plan_t &pl)
+{
+    Layout L;
+    const uint64_t T = pl.x_dtype == CAKE_GG_MX4 ? 0 : uint64_t(pl.T);
+    L.scales = kHeader;
+    L.tokens = L.scales + scale_bytes(T, pl.K);
+    L.total = L.tokens + align_up(T * uint64_t(pl.K) / 2, 256);
+    return L;
+}
+
+// ---------------------------------------------------------------- token pass
+
+// Four pairs of values as E2M1 codes, to nearest, ties to even, held at 6; the
+// first of a pair in the low half of its byte.
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv), "f"(v[4] * inv), "f"(v[5] * inv),
+          "f"(v[6] * inv), "f"(v[7] * inv));
+    return r;
+}
+
+// The scale's byte (exponent + 127; 255: a NaN) of a block's largest magnitude,
+// by its bits, and the reciprocal of the scale.  (Powers of two: exact.)
+__device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits)
+{
+    const int e = int(max_bits >> 23);
+    return e == 255 ? 255u : uint32_t(max(e - 2, 0));
+}
+__device__ __forceinline__ float scale_inverse(uint32_t byte)
+{
+    return byte == 255 ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t m)    // over the four lanes of a block
+{
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Where FP32 cannot tell on which side of a border between two codes, or between
+// two scales, a gated value lies, 64 bits do.  FP32 is off by less than
+// kGateError of the value: two units in the last place of the exponential, one
+// half each of the sum, the quotient and the product.  A negative g far out,
+// whose exponential leaves FP32's range, counts as unsure where the block is as
+// small as that.
+constexpr float kGateError = 0x1p-20f, kDeep = -80.0f;
+__device__ __noinline__ uint32_t codes8_in_64_bits(const float (&g)[8], const float (&u)[8], uint32_t *byte)
+{
+    double h[8], m = 0.0;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        h[i] = double(g[i]) / (1.0 + exp(-double(g[i]))) * double(u[i]);
+        nan |= !isfinite(float(h[i]));
+        m = fmax(m, fabs(h[i]));
+    }
+    m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    nan = (__ballot_sync(0xffffffffu, nan) >> (threadIdx.x & 28) & 0xfu) != 0;
+    const int e = m > 0.0 ? ilogb(m) + 125 : 0;
+    *byte = nan ? 255u : uint32_t(max(e, 0));
+    uint32_t w = 0;
+    if (!nan) {
+        const double inv = scalbn(1.0, 127 - int(*byte));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double a = fabs(h[i]) * inv;
+            const uint32_t c = uint32_t(a > 0.25) + uint32_t(a >= 0.75) + uint32_t(a > 1.25) + uint32_t(a >= 1.75) +
+                               uint32_t(a > 2.5) + uint32_t(a >= 3.5) + uint32_t(a > 5.0);
+            w |= (c | (signbit(h[i]) ? 8u : 0u)) << (4 * i);
+        }
+    }
+    return w;
+}
+
+// E matrices of R rows.  A lane has 8 values of a row at a time, four lanes a block,
+// a warp 256 values; it serves kRun such runs of one row, eight rows a block.
+constexpr int kRun = 4;
+
+template <typename XT, bool ACT>
+__global__ void __launch_bounds__(256)
+    mx4_quant_kernel(const XT *__restrict__ X, int64_t rows, int64_t R, int32_t K, uint8_t *__restrict__ Q, uint8_t *__restrict__ S)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (t >= rows) return;
+    const int32_t kt = (K + 127) / 128;
+    // (the scales of each matrix begin a tile of their own)
+    const int64_t e = rows == R ? 0 : t / R;
+    uint8_t *s = S + e * ((R + 127) / 128 * kt * kMx4Tile) + mx4_scale_at(t - e * R, 0, kt);
+    const XT *row = X + t * (ACT ? 2 : 1) * int64_t(K);
+    uint8_t *q = Q + t * (int64_t(K) / 2);
+    const int k0 = int(blockIdx.y) * (256 * kRun) + lane * 8;
+    float v[kRun][8], u[ACT ? kRun : 1][8];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        const int k = k0 + i * 256;
+        if (k < K) {
+            load8(row + k, v[i]);
+            if (ACT) load8(row + K + k, u[ACT ? i : 0]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = u[ACT ? i : 0][j] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        const int k = k0 + i * 256;
+        if (k - lane * 8 >= K) break;
+        uint32_t byte, w;
+        if constexpr (!ACT) {
+            byte = scale_byte(block_max(max_bits(v[i], 0)));
+            w = byte == 255 ? 0 : codes8(v[i], scale_inverse(byte));
+        } else {
+            float h[8], least = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[j] = v[i][j] / (1.0f + expf(-v[i][j])) * u[i][j];
+                least = fminf(least, v[i][j]);
+            }
+            const uint32_t m = block_max(max_bits(h, 0));
+            byte = scale_byte(m);
+            const float inv = scale_inverse(byte);
+            w = codes8(h, inv * (1.0f + kGateError));
+            const float a = __uint_as_float(m);
+            bool unsure = w != codes8(h, inv * (1.0f - kGateError)) ||
+                          scale_byte(__float_as_uint(a * (1.0f + kGateError))) != scale_byte(__float_as_uint(a * (1.0f - kGateError))) ||
+                          (least < kDeep && a < 0x1p-80f);
+            unsure = unsure && byte != 255;
+            if (__any_sync(0xffffffffu, unsure)) w = codes8_in_64_bits(v[i], u[i], &byte);
+            if (byte == 255) w = 0;
+        }
+        if (k < K) *reinterpret_cast<uint32_t *>(q + k / 2) = w;
+        uint32_t word = byte << (8 * ((lane >> 2) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if ((lane & 15) == 0 && k < K) *reinterpret_cast<uint32_t *>(s + int64_t(k / 128) * kMx4Tile) = word;
+    }
+}
+
+// The token pass: a programmatic dependent of the stream's previous kernel (it
+// waits for it before it reads anything), and only then lets the product start,
+// whose early reads of weights and offsets are thus ordered after everything
+// before this call.
+template <typename XT>
+cudaError_t launch_quant_as(const void *X, int act, int64_t E, int64_t R, int32_t K, uint8_t *Q, uint8_t *S, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((E * R + 7) / 8), unsigned((K + 256 * kRun - 1) / (256 * kRun)), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    if (pdl_enabled()) {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    const XT *x = static_cast<const XT *>(X);
+    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, true>, x, E * R, R, K, Q, S)
+                                       : cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, false>, x, E * R, R, K, Q, S);
+}
+
+int launch_quant(const void *X, int x_dtype, int act, int64_t E, int64_t R, int32_t K, uint8_t *Q, uint8_t *S, cudaStream_t stream)
+{
+    const cudaError_t err = x_dtype == CAKE_GG_BF16 ? launch_quant_as<uint16_t>(X, act, E, R, K, Q, S, stream)
+                                                    : launch_quant_as<float>(X, act, E, R, K, Q, S, stream);
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+// The problem's own checks, shared by the plan and the call.
+int check_problem(int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K, int x_dtype, int act, int out_dtype)
+{
+    if (E < 1 || E > kMaxExperts || M_max < 0 || M_max > INT32_MAX || T < 0 || T > INT32_MAX || N < 1 || K < 1 ||
+        (M_max > 0 && T < 1))
+        return CAKE_GG_ERR_INVALID_ARG;
+    if (x_dtype != CAKE_GG_BF16 && x_dtype != CAKE_GG_FP32 && x_dtype != CAKE_GG_MX4) return CAKE_GG_ERR_UNSUPPORTED;
+    if (out_dtype != CAKE_GG_BF16 && out_dtype != CAKE_GG_FP32) return CAKE_GG_ERR_UNSUPPORTED;
+    if (act != CAKE_GG_ACT_NONE && act != CAKE_GG_ACT_SILU_MUL) return CAKE_GG_ERR_INVALID_ARG;
+    if (act != CAKE_GG_ACT_NONE && x_dtype == CAKE_GG_MX4) return CAKE_GG_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 32 != 0) return CAKE_GG_ERR_ALIGNMENT;
+    if (K > kMaxK || N > kMaxN) return CAKE_GG_ERR_OVERFLOW;
+    // (addresses of 64 bits, and scale tiles that a copy numbers in 31)
+    uint64_t t;
+    if (!mul_ok(uint64_t(E) * uint64_t(N), uint64_t(K), &t) || !mul_ok(uint64_t(M_max), uint64_t(N) * 4u, &t) ||
+        uint64_t(E) * uint64_t((N + 127) / 128) > uint64_t(INT32_MAX) / uint64_t((K + 127) / 128))
+        return CAKE_GG_ERR_OVERFLOW;
+    return CAKE_GG_OK;
+}
+
+int stages_for(int pair, int nt, int splits, int E)
+{
+    int s = kMx4StagesMost;
+    while (s > 0 && mx4_mma_smem(pair, nt, s, splits, E) > kMx4SmemLimit) --s;
+    return s;
+}
+
+void choose(cake_gg_mx4_plan_t *pl)
+{
+    pl->pair = 1;
+    pl->tile_rows = 128;
+    pl->splits = 1;
+    pl->pair = env_int("CAKE_GG_MX4_PAIR", pl->pair) == 2 ? 2 : 1;
+    const int nt = env_int("CAKE_GG_MX4_ROWS_PER_TILE", pl->tile_rows);
+    if (nt >= 32 && nt <= 224 && nt % 32 == 0) pl->tile_rows = nt;
+    const int sp = env_int("CAKE_GG_MX4_SPLITS", pl->splits);
+    pl->splits = sp >= 1 && sp <= 8 && pl->pair == 1 ? sp : 1;
+    pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
+}
+
+// What the kernel can run.
+bool plan_ok(const cake_gg_mx4_plan_t &pl)
+{
+    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= 224 && pl.tile_rows % 32 == 0 &&
+           pl.stages >= kStagesLeast && pl.stages <= kMx4StagesMost && pl.splits >= 1 && pl.splits <= 8 &&
+           (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 255) / 256 &&   // (a stage for every CTA)
+           mx4_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kMx4SmemLimit;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cake_gg_mx4_plan(cake_gg_mx4_plan_t *plan, int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K, int x_dtype, int act,
+                     int out_dtype, int32_t max_sms)
+{
+    if (!plan) return CAKE_GG_ERR_INVALID_ARG;
+    std::memset(plan, 0, sizeof(*plan));
+    if (max_sms < 0) return CAKE_GG_ERR_INVALID_ARG;
+    const int rc = check_problem(E, M_max, T, N, K, x_dtype, act, out_dtype);
+    if (rc != CAKE_GG_OK) return rc;
+    plan->abi_version = CAKE_GG_ABI_VERSION;
+    plan->E = E;
+    plan->M_max = M_max;
+    plan->T = T;
+    plan->N = N;
+    plan->K = K;
+    plan->x_dtype = x_dtype;
+    plan->act = act;
+    plan->out_dtype = out_dtype;
+    plan->max_sms = max_sms;
+    choose(plan);
+    if (!plan_ok(*plan)) return CAKE_GG_ERR_INVALID_ARG;   // (an override that does not fit)
+    plan->timeout_ns = kTimeoutNs;
+    plan->workspace_bytes = layout(*plan).total;
+    return CAKE_GG_OK;
+}
+
+int cake_gg_mx4_quant(const void *X, int x_dtype, int act, int32_t E, int64_t R, int32_t K, uint8_t *Xq, uint8_t *xs, void *stream)
+{
+    if (x_dtype != CAKE_GG_BF16 && x_dtype != CAKE_GG_FP32) return CAKE_GG_ERR_UNSUPPORTED;
+    if (E < 1 || E > kMaxExperts) return CAKE_GG_ERR_INVALID_ARG;
+    const int rc = check_problem(1, 0, R, 8, K, x_dtype, act, CAKE_GG_BF16);
+    if (rc != CAKE_GG_OK) return rc;
+    if (R == 0) return CAKE_GG_OK;
+    if ((int64_t(E) * R + 7) / 8 > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    if (!X || !Xq || !xs) return CAKE_GG_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(Xq, 16) || !aligned(xs, 16)) return CAKE_GG_ERR_ALIGNMENT;
+    int sms;
+    const int dev = device_sms(&sms);
+    if (dev != CAKE_GG_OK) return dev;
+    return launch_quant(X, x_dtype, act, E, R, K, Xq, xs, static_cast<cudaStream_t>(stream));
+}
+
+int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_t *xs, const int32_t *rows, const uint8_t *W,
+                     const uint8_t *ws, void *Y, const int32_t *offsets, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!plan || plan->abi_version != CAKE_GG_ABI_VERSION) return CAKE_GG_ERR_INVALID_ARG;
+    const cake_gg_mx4_plan_t &pl = *plan;
+    int rc = check_problem(pl.E, pl.M_max, pl.T, pl.N, pl.K, pl.x_dtype, pl.act, pl.out_dtype);
+    if (rc != CAKE_GG_OK) return rc;
+    if (pl.max_sms < 0 || !plan_ok(pl)) return CAKE_GG_ERR_INVALID_ARG;
+    const bool ready = pl.x_dtype == CAKE_GG_MX4;   // tokens come quantised
+    if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))
+        return CAKE_GG_ERR_INVALID_ARG;
+    if ((!offsets && pl.E != 1) || (!rows && pl.T != pl.M_max)) return CAKE_GG_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(workspace, 16) || !aligned(xs, 16) ||
+        !aligned(ws, 16) || !aligned(rows, 4) || !aligned(offsets, 4))
+        return CAKE_GG_ERR_ALIGNMENT;
+    const Layout L = layout(pl);
+    if (workspace_bytes < L.total || pl.workspace_bytes != L.total) return CAKE_GG_ERR_WORKSPACE;
+    int sms;
+    if ((rc = device_sms(&sms)) != CAKE_GG_OK) return rc;
+    if (pl.M_max == 0) return CAKE_GG_OK;
+
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Mx4Params p{};
+    p.offsets = offsets;
+    p.rows = rows;
+    p.xs = ready ? xs : base + L.scales;
+    p.Y = Y;
+    p.status = reinterpret_cast<int32_t *>(base);
+    p.M = pl.M_max;
+    p.T = pl.T;
+    p.E = pl.E;
+    p.N = pl.N;
+    p.K = pl.K;
+    p.out_f32 = pl.out_dtype == CAKE_GG_FP32;
+    p.early = !ready;
+    p.nt = pl.tile_rows;
+    p.stages = pl.stages;
+    p.splits = pl.splits;
+    p.debug_flags = pl.debug_flags;
+    p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
+    const uint8_t *x = ready ? static_cast<const uint8_t *>(X) : base + L.tokens;
+    const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
+    // what cannot be launched is refused before anything is enqueued
+    Mx4Launch product;
+    if ((rc = prepare_mx4_mma(&product, p, W, ws, x, pl.pair, cap)) != CAKE_GG_OK) return rc;
+    if (!ready && (rc = launch_quant(X, pl.x_dtype, pl.act, 1, pl.T, pl.K, base + L.tokens, base + L.scales, s)) != CAKE_GG_OK)
+        return rc;
+    return launch_mx4_mma(product, pdl_enabled(), s);
+}
+
+}  // extern "C"

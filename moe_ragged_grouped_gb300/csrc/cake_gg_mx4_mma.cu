@@ -1,0 +1,686 @@
+// cake_gg_mx4_mma.cu -- the 4-bit products on the tensor cores.
+//
+//   Y[m, n] = sum_k x[r(m), k] w[e(m), n, k]
+//
+// Both operands are E2M1 with a power of two for each block of 32 along k, which
+// tcgen05.mma.kind::mxf4 multiplies as they lie in memory: two values a byte in
+// shared memory, the scales in tensor memory, sums in FP32.
+//
+// A tile is 128 channels (256 for a pair of CTAs) x up to nt rows of one
+// expert, computed transposed: D[channel, row] += W x^T, so the width of B
+// follows the rows that the tile really has and a ragged end or a decoding
+// batch costs its own size only.  A stage is 256 values of the reduction: 128
+// bytes of every channel and row, two scale tiles of 128 channels x 4 blocks, and
+// the same of the rows.  The scales of the channels lie in memory as the tensor
+// cores take them and come by TMA; those of the rows, which begin anywhere in a
+// scale tile, or are routed, are put together by warps.  Both go from shared to
+// tensor memory by tcgen05.cp, which the MMAs of the stage follow in the pipe.
+//
+// Roles of a CTA: warp 0 copies weights and their scales, warp 1 issues copies to
+// tensor memory and MMAs, warps 2-9 store (two groups on alternate 32 rows of a
+// tile), warps 10-13 put the rows' scales together, every fourth stage each, warp
+// 14 copies rows, or, where they are routed, warps 14-17 gather them, two on every
+// other stage.
+#include "cake_gg_mx4.h"
+#include "cake_gg_ptx.cuh"
+#include "cake_gg_roles.cuh"
+
+namespace cakegg {
+namespace {
+
+constexpr int kThreads = 480, kThreadsRouted = 576;
+constexpr int kStoreWarp0 = 2, kStoreWarps = 8, kStoreThreads = kStoreWarps * 32;
+constexpr int kScaleWarp0 = 10, kScaleWarps = 4;
+constexpr int kRowsWarp0 = 14, kGatherWarps = 4;
+constexpr int kKB = 256;                      // reduction length of a stage
+constexpr uint32_t kWBytes = 128 * kKB / 2;   // weight tile of a stage
+constexpr uint32_t kOutTile = 2048;           // 32 BF16 or 16 FP32 rows x 32 channels of output, per storing warp
+constexpr int kRowsMost = 224;                // two accumulators of 224 columns leave 64 for scales
+constexpr int kGatherRows = 112;              // rows that a gathering warp serves at most: half a tile's
+
+// Scale tiles of a word (128 values) of the reduction, for the rows of a tile.
+__host__ __device__ constexpr int row_atoms(int nt) { return nt > 128 ? 2 : 1; }
+// Shared memory of a stage: weights, rows, the channels' scales, the rows'.
+__host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt)
+{
+    return kWBytes + uint32_t(nt / pair) * 128u + 2u * kMx4Tile * uint32_t(1 + row_atoms(nt));
+}
+
+struct __align__(16) Ctrl {
+    uint64_t full[kMx4StagesMost], empty[kMx4StagesMost];   // stage: copies landed / MMAs done
+    uint64_t tfull[2], tempty[2];                           // accumulator: complete / stored
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t total;                                          // row tiles of all experts
+};
+
+// E2M1 operands (format 1), both K-major, E8M0 scales (bit 23), FP32 accumulators;
+// the two bytes of a scale word that an MMA of 64 values takes begin at `id`.
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t id)
+{
+    return (id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | (id << 29);
+}
+
+// Descriptor of a scale tile for tcgen05.cp: no swizzle, 32 rows of 16 bytes, eight
+// to a core matrix of 128.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+{
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+
+// A scale tile to four columns of tensor memory, lane r % 32 of every quarter,
+// column r / 32 (of both CTAs of a pair, each from its own shared memory).
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc)
+{
+    if constexpr (CG == 2) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over 64 values, each block of 32 scaled.
+template <int CG>
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sa,
+                                          uint32_t sb, uint32_t accumulate)
+{
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+}
+
+template <int PAIR, bool OUT_F32>
+__global__ void __maxnreg__(96)
+    mx4_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
+                   const __grid_constant__ CUtensorMap mapX, const Mx4Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    const uint32_t x_bytes = uint32_t(p.nt / PAIR) * 128u;       // B of this CTA in a stage
+    const uint32_t stage_bytes = stage_bytes_of(PAIR, p.nt);
+    const uint32_t sa_at = kWBytes + x_bytes, sb_at = sa_at + 2u * kMx4Tile;   // the scales in a stage
+    const int atoms = row_atoms(p.nt);
+    uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
+    float *recv = reinterpret_cast<float *>(after);              // split: [split][channel][columns + 4]
+    after += p.splits > 1 ? split_bytes(p.nt, p.splits) : 0;
+    uint8_t *out_tile = after;                                   // [warp][row][32 channels]
+    after += kStoreWarps * kOutTile;
+    Ctrl *c = reinterpret_cast<Ctrl *>(after);
+    int32_t *row_ids = reinterpret_cast<int32_t *>(c + 1);       // [gathering warp][row]
+    int32_t *off = row_ids + kGatherWarps * kGatherRows;
+    int32_t *pref = off + p.E + 1;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = p.E;
+    const int rank = PAIR == 2 || p.splits > 1 ? int(cluster_ctarank()) : 0;
+    const int half = PAIR == 2 ? rank : 0;
+    const bool leader = half == 0;
+
+    // ---- set-up: TMEM, barriers, offsets and the prefix of their row tiles ----
+    if (!p.early) grid_dependency_wait();
+    grid_launch_dependents();
+    if (warp == 0) {
+        for (int i = lane; i <= E; i += 32) off[i] = p.offsets ? p.offsets[i] : (i ? int32_t(p.M) : 0);
+        __syncwarp();
+        // lane l sums the row tiles of its run of experts, then the runs are scanned
+        const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+        int32_t sum = 0;
+        bool bad = lane == 0 && off[0] != 0;
+        for (int e = e0; e < e1; ++e) {
+            bad |= off[e + 1] < off[e] || int64_t(off[e + 1]) > p.M;
+            sum += row_tiles(off[e + 1] - off[e], p);
+        }
+        int32_t inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        int32_t at = inc - sum;
+        for (int e = e0; e < e1; ++e) {
+            pref[e] = at;
+            at += row_tiles(off[e + 1] - off[e], p);
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 31) {
+            pref[E] = inc;
+            c->total = bad ? 0 : inc;
+            if (bad) atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_OFFSETS);
+        }
+    } else if (warp == 1) {
+        tmem_alloc<PAIR>(smem_u32(&c->tmem_base), 512u);
+        tmem_relinquish<PAIR>();
+    } else if (tid == 64) {
+        for (int s = 0; s < p.stages; ++s) {
+            // the weights' arming, the rows' and the rows' scales, of both CTAs
+            mbar_init(smem_u32(&c->full[s]), uint32_t(p.rows ? 3 : 2) + PAIR);
+            mbar_init(smem_u32(&c->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c->tfull[b]), 1);
+            mbar_init(smem_u32(&c->tempty[b]), uint32_t(kStoreWarps) * PAIR);       // storing warps, of both CTAs
+        }
+        mbar_init(smem_u32(&c->drain), 1);
+        fence_barrier_init();
+    } else if (tid == 96) {
+        c->abort_flag = 0;
+        tma_prefetch_desc(&mapW);
+        tma_prefetch_desc(&mapS);
+        tma_prefetch_desc(&mapX);
+    }
+    if (PAIR == 2 || p.splits > 1) cluster_sync_all();           // peers' barriers are ready
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = c->tmem_base;
+    const uint32_t d_stride = uint32_t(p.nt);                    // two accumulators, then two stages' scales
+    const uint32_t scales0 = tmem + 2u * d_stride, scales_step = 8u + 8u * uint32_t(atoms);
+
+    // A split cluster takes one unit, each of its CTAs a part of the reduction.
+    const uint32_t unit0 = blockIdx.x / uint32_t(PAIR * p.splits);
+    const uint32_t step = p.splits > 1 ? uint32_t(p.n_ct) : gridDim.x / PAIR;
+    const int32_t tiles = p.splits > 1 ? min(c->total, int32_t(unit0 / uint32_t(p.n_ct)) + 1) : c->total;
+    const int kb0 = p.splits > 1 ? p.n_kb * rank / p.splits : 0;
+    const int kb1 = p.splits > 1 ? p.n_kb * (rank + 1) / p.splits : p.n_kb;
+    constexpr int kNAlign = 16 * PAIR;
+    const uint16_t pair_mask = 3;
+    // The MMAs of a pair read the operands and scales of both CTAs, so everything
+    // counts on the even one's barrier, which it arms for both.  (A stage's copies
+    // follow its `empty`, so that barrier is in the same round; the bytes may come
+    // before the arming.)
+    auto full_bar = [&](int s) { return PAIR == 2 ? map_to_cta(smem_u32(&c->full[s]), 0) : smem_u32(&c->full[s]); };
+
+    if (warp == 0) {
+        // ======================= weight copies =======================
+        // The first ring of them does not wait for the token pass.  (Every role waits
+        // for the pass before its first wait with a limit, so that the limit does
+        // not count the pass.)
+        Turn st;
+        int issued = 0;       // stages filled, up to the ring's depth
+        bool ok = true, passed = false;
+        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
+            const int ct = t.ct * PAIR + half;
+            // (a pair's last channel tile may have no channels of the odd CTA: the copies
+            // of weights bring zeros, and the scales of the last tile that there is)
+            const int32_t scale0 = (t.e * p.n_nt + min(ct, p.n_nt - 1)) * p.n_kt;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (issued == p.stages && !passed) {
+                    grid_dependency_wait();
+                    passed = true;
+                }
+                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = full_bar(st.at), dst = ring + uint32_t(st.at) * stage_bytes;
+                    const bool both = 2 * kb + 1 < p.n_kt;       // (a last stage may have one scale tile)
+                    if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * (kWBytes + (both ? 2u : 1u) * kMx4Tile));
+                    if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0)) {
+                        if (PAIR == 2) tma_load_3d_pair(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
+                        else tma_load_3d(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
+                    }
+                    tma_rows<PAIR>(dst + sa_at, &mapS, bar, 0, scale0 + 2 * kb);
+                    if (both) tma_rows<PAIR>(dst + sa_at + kMx4Tile, &mapS, bar, 0, scale0 + 2 * kb + 1);
+                }
+                __syncwarp();
+                st.next(p.stages);
+                if (issued < p.stages) ++issued;
+            }
+        }
+        grid_dependency_wait();
+        if (!ok || aborted(c)) {
+            if (leader) drain_stages(st, issued, 1, lane, p.stages, c);
+            else drain_blind();
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ======================= MMAs (the even CTA of a pair) =======================
+        grid_dependency_wait();
+        Turn st, acc, old;
+        bool ok = true, any = false;
+        if (leader) {
+            uint32_t count = 0;                                  // stages so far
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
+                const uint32_t n = uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign);
+                const uint32_t id0 = idesc_mxf4(128u * PAIR, n, 0), id2 = idesc_mxf4(128u * PAIR, n, 2);
+                const int buf = acc.at;
+                if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + uint32_t(buf) * d_stride;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = warp_wait<PAIR == 2>(smem_u32(&c->full[st.at]), st.parity, c, p);
+                    // the columns of scales were the stage's before last: its MMAs are done
+                    if (ok && count >= 2) {
+                        ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
+                        old.next(p.stages);
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        tc_fence_after_sync();
+                        const uint32_t at = ring + uint32_t(st.at) * stage_bytes;
+                        const uint64_t a = smem_desc_sw128(at, 16, 1024), b = smem_desc_sw128(at + kWBytes, 16, 1024);
+                        const uint32_t sa = scales0 + (count & 1u) * scales_step, sb = sa + 8u;
+                        const uint64_t da = scale_desc(at + sa_at);
+                        const uint64_t db = scale_desc(at + sb_at);
+                        const int steps = min(4, (p.K - kb * kKB + 63) / 64);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (2 * h < steps) {
+                                copy_scales<PAIR>(sa + uint32_t(h) * 4u, da + uint64_t(h * (kMx4Tile >> 4)));
+                                const uint32_t to = sb + uint32_t(h * atoms) * 4u;
+                                const uint64_t from = db + uint64_t(h * atoms * (kMx4Tile >> 4));
+                                copy_scales<PAIR>(to, from);
+                                if (atoms == 2) copy_scales<PAIR>(to + 4u, from + uint64_t(kMx4Tile >> 4));
+                                umma_mxf4<PAIR>(d, a + uint64_t(h * 4), b + uint64_t(h * 4), id0, sa + uint32_t(h) * 4u, to,
+                                                kb > kb0 || h > 0 ? 1u : 0u);
+                                if (2 * h + 1 < steps)
+                                    umma_mxf4<PAIR>(d, a + uint64_t(h * 4 + 2), b + uint64_t(h * 4 + 2), id2, sa + uint32_t(h) * 4u, to, 1u);
+                            }
+                        }
+                        if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->empty[st.at]), pair_mask);
+                        else umma_commit<1>(smem_u32(&c->empty[st.at]));
+                        if (kb + 1 == kb1) {
+                            if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
+                            else umma_commit<1>(smem_u32(&c->tfull[buf]));
+                        }
+                    }
+                    any = true;
+                    ++count;
+                    __syncwarp();
+                    st.next(p.stages);
+                }
+                acc.next(2);
+            }
+            if (!ok && any && elect_one()) {                     // (the lane that issued them)
+                umma_commit<PAIR>(smem_u32(&c->drain));
+                drain_wait(smem_u32(&c->drain), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < kScaleWarp0) {
+        // ======================= stores =======================
+        grid_dependency_wait();                                  // (Y may still be read by the grid before the pass)
+        const int q = warp & 3;                                  // tensor memory lanes 32 q ..
+        const int side = (warp - kStoreWarp0) >> 2;              // which 32 rows of 64
+        Turn acc;
+        for (Walk w(unit0, step, p.n_ct); w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
+            const int n = (t.ct * PAIR + half) * 128 + q * 32 + lane;
+            const int buf = acc.at;
+            if (!warp_wait(smem_u32(&c->tfull[buf]), acc.parity, c, p)) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + uint32_t(buf) * d_stride + (uint32_t(q * 32) << 16);
+            const int per = split_columns(t.rows, p.splits);
+            uint8_t *tile = out_tile + (warp - kStoreWarp0) * kOutTile;
+            for (int c0 = 32 * side; c0 < t.rows; c0 += 64) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(d + uint32_t(c0), r);
+                tmem_ld_wait();
+                if (p.splits > 1) {
+                    // four columns at a time to the CTA that sums them
+                    const uint32_t mine = smem_u32(recv + (size_t(rank) * 128 + q * 32 + lane) * (per + 4));
+                    int owner = c0 / per, col = c0 - owner * per;
+                    uint32_t to = map_to_cta(mine, uint32_t(owner));
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        if (c0 + j < t.rows) {
+                            if (col == per) {
+                                col = 0;
+                                to = map_to_cta(mine, uint32_t(++owner));
+                            }
+                            st_cluster_v4(to + uint32_t(col) * 4u,
+                                          make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
+                                                      __uint_as_float(r[j + 3])));
+                            col += 4;
+                        }
+                    continue;
+                }
+                // through shared memory, transposed: a lane writes its channel of kRows
+                // rows, then stores 16 bytes of a row's channels at a time
+                constexpr int kSize = OUT_F32 ? 4 : 2, kRows = int(kOutTile) / (32 * kSize);
+                constexpr int kPieces = 2 * kSize, kPer = 16 / kSize;   // 16-byte pieces of a row
+                const int piece = lane % kPieces, nv = n - lane + piece * kPer;
+#pragma unroll
+                for (int h = 0; h < 32; h += kRows) {
+#pragma unroll
+                    for (int j = 0; j < kRows; j += 4) {
+                        if (OUT_F32) {
+                            uint32_t *dst = reinterpret_cast<uint32_t *>(tile) + j * 32 + lane;
+                            dst[0] = r[h + j], dst[32] = r[h + j + 1], dst[64] = r[h + j + 2], dst[96] = r[h + j + 3];
+                        } else {
+                            const uint32_t a = pack_bf16x2(__uint_as_float(r[h + j]), __uint_as_float(r[h + j + 1]));
+                            const uint32_t b = pack_bf16x2(__uint_as_float(r[h + j + 2]), __uint_as_float(r[h + j + 3]));
+                            uint16_t *dst = reinterpret_cast<uint16_t *>(tile) + j * 32 + lane;
+                            dst[0] = uint16_t(a & 0xffffu), dst[32] = uint16_t(a >> 16);
+                            dst[64] = uint16_t(b & 0xffffu), dst[96] = uint16_t(b >> 16);
+                        }
+                    }
+                    __syncwarp();
+                    uint8_t *y = static_cast<uint8_t *>(p.Y) + ((int64_t(t.m0) + c0 + h) * p.N + nv) * kSize;
+#pragma unroll
+                    for (int i = 0; i < kRows * kPieces / 32; ++i) {
+                        const int row = lane / kPieces + i * (32 / kPieces);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(tile + row * (32 * kSize) + piece * 16);
+                        if (c0 + h + row < t.rows && nv < p.N)
+                            *reinterpret_cast<uint4 *>(y + int64_t(row) * p.N * kSize) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(smem_u32(&c->tempty[buf]));
+                else mbar_arrive_relaxed_cluster(map_to_cta(smem_u32(&c->tempty[buf]), 0));
+            }
+            acc.next(2);
+        }
+    } else if (warp < kRowsWarp0) {
+        // ======================= the rows' scales =======================
+        // Lane l has the rows l, l + 32, .. of the tile: a word of theirs is 16 bytes of
+        // a scale tile's lane.  In a pair both CTAs hold the scales of all rows.
+        grid_dependency_wait();                                  // the tokens
+        const int v = warp - kScaleWarp0, n_kb = kb1 - kb0;
+        Turn st;
+        for (int i = 0; i < v; ++i) st.next(p.stages);
+        int kb = v;
+        bool ok = true;
+        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+            const Tile t = w.tile(p.nt, off, pref);
+            const uint8_t *src[kRowsMost / 32 + 1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t m = i * 32 + lane;
+                src[i] = nullptr;
+                if (m < t.rows && kb < n_kb) {
+                    int64_t r = int64_t(t.m0) + m;
+                    if (p.rows) r = p.rows[r];
+                    if (r >= 0 && r < p.T) src[i] = p.xs + mx4_scale_at(r, 0, p.n_kt);
+                    else atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_ROWS);
+                }
+            }
+            for (; kb < n_kb; kb += kScaleWarps) {
+                uint32_t s[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int kt = 2 * (kb0 + kb) + h;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
+                }
+                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
+                if (!ok) break;
+                const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + sb_at + uint32_t(lane) * 16u;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sts_v4(dst + uint32_t(h * atoms) * kMx4Tile, s[h][0], s[h][1], s[h][2], s[h][3]);
+                    if (atoms == 2) sts_v4(dst + uint32_t(h * 2 + 1) * kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(smem_u32(&c->full[st.at]));
+                    else mbar_arrive_cluster(full_bar(st.at));
+                }
+                for (int i = 0; i < kScaleWarps; ++i) st.next(p.stages);
+            }
+            kb -= n_kb;
+        }
+        __syncwarp();
+    } else {
+        // ======================= rows =======================
+        const int v = warp - kRowsWarp0, n_kb = kb1 - kb0;
+        Turn st;
+        int issued = 0;
+        bool ok = true;
+        if (p.rows == nullptr) {
+            grid_dependency_wait();                              // the tokens
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
+                const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;   // rows of B in this CTA
+                const int n_box = (n_half + p.box - 1) / p.box;
+                const uint32_t mb = uint32_t(t.m0 + half * n_half);         // (a box past 2^31 is past the tokens)
+                const uint32_t bytes = 128u * uint32_t(n_box * p.box);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t bar = full_bar(st.at), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * bytes);
+                        for (int b = 0; b < n_box; ++b)
+                            tma_rows<PAIR>(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * (kKB / 2), int32_t(mb + uint32_t(b * p.box)));
+                    }
+                    __syncwarp();
+                    st.next(p.stages);
+                    if (issued < p.stages) ++issued;
+                }
+            }
+            if (!ok || aborted(c)) {
+                if (leader) drain_stages(st, issued, 1, lane, p.stages, c);
+                else drain_blind();
+            }
+        } else {
+            // warps 0, 1 and 2, 3 gather alternate stages, each every other four rows
+            const int group = v >> 1, side = v & 1;
+            int32_t *mine = row_ids + v * kGatherRows;           // tokens of this warp's rows
+            const uint32_t ids = smem_u32(mine);
+            if (group) st.next(p.stages);
+            int kb = group;
+            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                const Tile t = w.tile(p.nt, off, pref);
+                const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
+                __syncwarp();
+                for (int i = lane; i < n_half / 2; i += 32) {
+                    // (counted from the tile's first row: past its last one the sum may pass 2^31)
+                    const int32_t m = half * n_half + (i >> 2) * 8 + side * 4 + (i & 3);
+                    const int32_t id = m < t.rows ? p.rows[t.m0 + m] : 0;
+                    mine[i] = id >= 0 && id < p.T ? id : 0;      // (reported where its scales are read)
+                }
+                grid_dependency_wait();                          // the tokens (the caller's row numbers were there)
+                __syncwarp();
+                for (; kb < n_kb; kb += 2) {
+                    ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t bar = full_bar(st.at);
+                        const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(side) * 512u;
+                        const int32_t k = (kb0 + kb) * (kKB / 2);
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * uint32_t(n_half) * 64u);
+#pragma unroll 4
+                        for (int i = 0; i < n_half / 2; i += 4) {
+                            const int4 id = lds_i4(ids + uint32_t(i) * 4u);
+                            tma_gather4<PAIR>(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
+                        }
+                    }
+                    __syncwarp();
+                    st.next(p.stages), st.next(p.stages);
+                    if (issued < p.stages) ++issued;
+                }
+                kb -= n_kb;
+            }
+            grid_dependency_wait();
+            if (!ok || aborted(c)) {
+                if (leader) drain_stages(st, issued, 2, lane, p.stages, c);
+                else drain_blind();
+            }
+        }
+        __syncwarp();
+    }
+
+    if (PAIR == 1 && p.splits > 1) {
+        // every part of this CTA's columns has arrived: sum them in split order
+        __syncwarp();
+        cluster_sync_all();
+        Walk w(unit0, step, p.n_ct);
+        if (warp >= kStoreWarp0 && warp < kScaleWarp0 && w.g < tiles && !aborted(c)) {
+            const Tile t = w.tile(p.nt, off, pref);
+            const int per = split_columns(t.rows, p.splits);
+            const int row = (warp & 3) * 32 + lane, n = t.ct * 128 + row;
+            const int m0 = rank * per;
+            for (int j0 = 16 * ((warp - kStoreWarp0) >> 2); j0 < per && m0 + j0 < t.rows; j0 += 32) {
+                // up to 16 rows at a time: their loads do not wait for each other's sums
+                float4 sum[4];
+                for (int v = 0; v < p.splits; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j0 + 4 * i < per) {
+                            const float4 o = *reinterpret_cast<const float4 *>(recv + (size_t(v) * 128 + row) * (per + 4) + j0 + 4 * i);
+                            if (v == 0) sum[i] = o;
+                            else sum[i].x += o.x, sum[i].y += o.y, sum[i].z += o.z, sum[i].w += o.w;
+                        }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int m = m0 + j0 + 4 * i + k;
+                        if (j0 + 4 * i < per && m < t.rows && n < p.N) {
+                            const int64_t at = (int64_t(t.m0) + m) * p.N + n;
+                            if (OUT_F32) static_cast<float *>(p.Y)[at] = y[k];
+                            else static_cast<uint16_t *>(p.Y)[at] = uint16_t(pack_bf16x2(y[k], 0.0f) & 0xffffu);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1 && PAIR == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<1>(tmem, 512u);
+    }
+    if (PAIR == 2) {
+        // no CTA leaves while its peer may still use its memory or barriers
+        cluster_sync_all();
+        if (warp == 1) {
+            tc_fence_after_sync();
+            tmem_dealloc<2>(tmem, 512u);
+        }
+    }
+}
+
+// The opt-in limit of shared memory, raised once per device.
+template <int PAIR, bool OUT_F32>
+cudaError_t raise_limit()
+{
+    static bool raised[64] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!raised[dev]) {
+        err = cudaFuncSetAttribute(mx4_mma_kernel<PAIR, OUT_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMx4SmemLimit));
+        if (err != cudaSuccess) return err;
+        raised[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+template <int PAIR, bool OUT_F32>
+cudaError_t launch(const Mx4Launch &l, bool pdl, cudaStream_t stream)
+{
+    const Mx4Params &p = l.p;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    const int cluster = PAIR * p.splits;
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = unsigned(cluster);
+        attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = 1;
+    }
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.gridDim = dim3(unsigned(l.grid), 1, 1);
+    cfg.blockDim = dim3(p.rows ? kThreadsRouted : kThreads, 1, 1);
+    cfg.dynamicSmemBytes = mx4_mma_smem(PAIR, p.nt, p.stages, p.splits, p.E);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = unsigned(na);
+    return cudaLaunchKernelEx(&cfg, mx4_mma_kernel<PAIR, OUT_F32>, l.mw, l.ms, l.mx, p);
+}
+
+}  // namespace
+
+size_t mx4_mma_smem(int pair, int nt, int stages, int splits, int E)
+{
+    return 1024 + size_t(stages) * stage_bytes_of(pair, nt) + (splits > 1 ? split_bytes(nt, splits) : 0) +
+           kStoreWarps * kOutTile + sizeof(Ctrl) + size_t(kGatherWarps * kGatherRows) * 4 + size_t(2 * (E + 1)) * 4;
+}
+
+int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p0, const uint8_t *W, const uint8_t *ws, const uint8_t *x, int pair, int sms)
+{
+    Mx4Params &p = l->p;
+    p = p0;
+    p.n_ct = (p.N + 128 * pair - 1) / (128 * pair);
+    p.n_nt = (p.N + 127) / 128;
+    p.n_kb = (p.K + kKB - 1) / kKB;
+    p.n_kt = (p.K + 127) / 128;
+    p.div_nt = uint32_t((uint64_t(1) << 32) / uint32_t(p.nt / 16) + ((uint64_t(1) << 32) % uint32_t(p.nt / 16) != 0));
+    p.box = p.nt / pair % 32 == 0 ? 32 : 16;
+    const uint64_t row = uint64_t(p.K) / 2;
+    const uint64_t dw[3] = {row, uint64_t(p.N), uint64_t(p.E)};
+    const uint64_t sw[2] = {row, uint64_t(p.N) * row};
+    const uint32_t bw[3] = {uint32_t(kKB) / 2, 128, 1};
+    int rc = encode_tiled(&l->mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, W, dw, sw, bw);
+    if (rc != CAKE_GG_OK) return rc;
+    const uint64_t ds[2] = {uint64_t(kMx4Tile) / 4, uint64_t(p.E) * uint64_t(p.n_nt) * uint64_t(p.n_kt)};
+    const uint64_t ss[1] = {uint64_t(kMx4Tile)};
+    const uint32_t bs[2] = {uint32_t(kMx4Tile) / 4, 1};
+    if (ds[1] > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    rc = encode_tiled(&l->ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, ws, ds, ss, bs, false);
+    if (rc != CAKE_GG_OK) return rc;
+    const uint64_t dx[2] = {row, uint64_t(p.T)};
+    const uint64_t sx[1] = {row};
+    const uint32_t bx[2] = {uint32_t(kKB) / 2, p.rows ? 1u : uint32_t(p.box)};   // (gathered four rows at a time)
+    rc = encode_tiled(&l->mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x, dx, sx, bx);
+    if (rc != CAKE_GG_OK) return rc;
+
+    // row tiles at most: a whole one per nt rows and a last one per expert with rows
+    const int64_t tiles = p.E == 1 ? (p.M + p.nt - 1) / p.nt : p.M / p.nt + (p.M < p.E ? p.M : p.E);
+    const int64_t bound = tiles * p.n_ct;
+    int64_t grid;
+    if (p.splits > 1) {
+        grid = bound * p.splits;                       // one cluster per unit
+        if (grid > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+    } else {
+        grid = sms / pair < bound ? sms / pair : bound;
+        grid = (grid < 1 ? 1 : grid) * pair;
+    }
+    l->pair = pair;
+    l->grid = int32_t(grid);
+    const cudaError_t err = pair == 2 ? (p.out_f32 ? raise_limit<2, true>() : raise_limit<2, false>())
+                                      : (p.out_f32 ? raise_limit<1, true>() : raise_limit<1, false>());
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+int launch_mx4_mma(const Mx4Launch &l, bool pdl, cudaStream_t stream)
+{
+    cudaError_t err;
+    if (l.pair == 2) err = l.p.out_f32 ? launch<2, true>(l, pdl, stream) : launch<2, false>(l, pdl, stream);
+    else err = l.p.out_f32 ? launch<1, true>(l, pdl, stream) : launch<1, false>(l, pdl, stream);
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+}  // namespace cakegg
