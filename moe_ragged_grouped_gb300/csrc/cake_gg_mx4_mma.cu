@@ -21,6 +21,8 @@
 // tile), warps 10-13 put the rows' scales together, every fourth stage each, warp
 // 14 copies rows, or, where they are routed, warps 14-17 gather them, two on every
 // other stage.
+#include <type_traits>
+
 #include "cake_gg_mx4.h"
 #include "cake_gg_ptx.cuh"
 #include "cake_gg_roles.cuh"
@@ -40,6 +42,8 @@ constexpr int kGatherRows = 112;              // rows that a gathering warp serv
 
 // Scale tiles of a word (128 values) of the reduction, for the rows of a tile.
 __host__ __device__ constexpr int row_atoms(int nt) { return nt > 128 ? 2 : 1; }
+// Stages whose scales tensor memory holds beside the two accumulators.
+__host__ __device__ constexpr int scale_slots(int nt) { return (512 - 2 * nt) / (8 + 8 * row_atoms(nt)); }
 // Shared memory of a stage: weights, rows, the channels' scales, the rows'.
 __host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt)
 {
@@ -56,11 +60,13 @@ struct __align__(16) Ctrl {
 };
 
 // E2M1 operands (format 1), both K-major, E8M0 scales (bit 23), FP32 accumulators;
-// the two bytes of a scale word that an MMA of 64 values takes begin at `id`.
-__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t id)
+// an MMA of 64 values takes two bytes of a scale word, from byte 0 or (kSecondHalf) 2.
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N)
 {
-    return (id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | (id << 29);
+    return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24);
 }
+
+constexpr uint32_t kSecondHalf = (2u << 4) | (2u << 29);
 
 // Descriptor of a scale tile for tcgen05.cp: no swizzle, 32 rows of 16 bytes, eight
 // to a core matrix of 128.
@@ -99,6 +105,27 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
             : "memory");
 }
 
+// A stage's copies of scales and its MMAs, of a word of 128 values at a time.
+// WHOLE: all four MMAs; else `steps` of them, at the end of the reduction.
+template <int PAIR, int ATOMS, bool WHOLE>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t at, uint32_t sa_at, uint32_t sa, uint32_t idesc, bool more, int steps)
+{
+    constexpr uint64_t kStep = kMx4Tile >> 4;
+    const uint64_t a = smem_desc_sw128(at, 16, 1024), b = smem_desc_sw128(at + kWBytes, 16, 1024);
+    const uint64_t from = scale_desc(at + sa_at);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (!WHOLE && 2 * h >= steps) break;
+        const uint32_t ca = sa + uint32_t(h) * 4u, cb = sa + 8u + uint32_t(h * ATOMS) * 4u;
+        copy_scales<PAIR>(ca, from + uint64_t(h) * kStep);
+#pragma unroll
+        for (int i = 0; i < ATOMS; ++i) copy_scales<PAIR>(cb + uint32_t(i) * 4u, from + uint64_t(2 + h * ATOMS + i) * kStep);
+        umma_mxf4<PAIR>(d, a + uint64_t(h * 4), b + uint64_t(h * 4), idesc, ca, cb, h > 0 || more ? 1u : 0u);
+        if (WHOLE || 2 * h + 1 < steps)
+            umma_mxf4<PAIR>(d, a + uint64_t(h * 4 + 2), b + uint64_t(h * 4 + 2), idesc | kSecondHalf, ca, cb, 1u);
+    }
+}
+
 template <int PAIR, bool OUT_F32>
 __global__ void __maxnreg__(96)
     mx4_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
@@ -121,7 +148,7 @@ __global__ void __maxnreg__(96)
     int32_t *off = row_ids + kGatherWarps * kGatherRows;
     int32_t *pref = off + p.E + 1;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // (uniform to the compiler)
     const int E = p.E;
     const int rank = PAIR == 2 || p.splits > 1 ? int(cluster_ctarank()) : 0;
     const int half = PAIR == 2 ? rank : 0;
@@ -183,14 +210,16 @@ __global__ void __maxnreg__(96)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = c->tmem_base;
-    const uint32_t d_stride = uint32_t(p.nt);                    // two accumulators, then two stages' scales
+    const uint32_t tmem = __shfl_sync(0xffffffffu, c->tmem_base, 0);
+    const uint32_t d_stride = uint32_t(p.nt);                    // two accumulators, then some stages' scales
     const uint32_t scales0 = tmem + 2u * d_stride, scales_step = 8u + 8u * uint32_t(atoms);
+    const int slots = min(scale_slots(p.nt), p.stages);
 
     // A split cluster takes one unit, each of its CTAs a part of the reduction.
     const uint32_t unit0 = blockIdx.x / uint32_t(PAIR * p.splits);
     const uint32_t step = p.splits > 1 ? uint32_t(p.n_ct) : gridDim.x / PAIR;
-    const int32_t tiles = p.splits > 1 ? min(c->total, int32_t(unit0 / uint32_t(p.n_ct)) + 1) : c->total;
+    const int32_t total = __shfl_sync(0xffffffffu, c->total, 0);
+    const int32_t tiles = p.splits > 1 ? min(total, int32_t(unit0 / uint32_t(p.n_ct)) + 1) : total;
     const int kb0 = p.splits > 1 ? p.n_kb * rank / p.splits : 0;
     const int kb1 = p.splits > 1 ? p.n_kb * (rank + 1) / p.splits : p.n_kb;
     constexpr int kNAlign = 16 * PAIR;
@@ -247,65 +276,57 @@ __global__ void __maxnreg__(96)
     } else if (warp == 1) {
         // ======================= MMAs (the even CTA of a pair) =======================
         grid_dependency_wait();
-        Turn st, acc, old;
         bool ok = true, any = false;
         if (leader) {
-            uint32_t count = 0;                                  // stages so far
-            for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
-                const Tile t = w.tile(p.nt, off, pref);
-                const uint32_t n = uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign);
-                const uint32_t id0 = idesc_mxf4(128u * PAIR, n, 0), id2 = idesc_mxf4(128u * PAIR, n, 2);
-                const int buf = acc.at;
-                if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem + uint32_t(buf) * d_stride;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    ok = warp_wait<PAIR == 2>(smem_u32(&c->full[st.at]), st.parity, c, p);
-                    // the columns of scales were the stage's before last: its MMAs are done
-                    if (ok && count >= 2) {
-                        ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
-                        old.next(p.stages);
+            // (with the number of scale tiles a constant each issue is a few instructions)
+            auto run = [&](auto n_atoms) {
+                constexpr int ATOMS = decltype(n_atoms)::value;
+                Turn st, acc, old, sl;
+                int count = 0;                                   // stages so far, up to the slots
+                for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                    const Tile t = w.tile(p.nt, off, pref);
+                    const uint32_t n = __shfl_sync(0xffffffffu, uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign), 0);
+                    const uint32_t idesc = idesc_mxf4(128u * PAIR, n);
+                    const int buf = acc.at;
+                    if (!warp_wait<PAIR == 2>(smem_u32(&c->tempty[buf]), acc.parity ^ 1u, c, p)) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
-                    if (elect_one()) {
-                        tc_fence_after_sync();
-                        const uint32_t at = ring + uint32_t(st.at) * stage_bytes;
-                        const uint64_t a = smem_desc_sw128(at, 16, 1024), b = smem_desc_sw128(at + kWBytes, 16, 1024);
-                        const uint32_t sa = scales0 + (count & 1u) * scales_step, sb = sa + 8u;
-                        const uint64_t da = scale_desc(at + sa_at);
-                        const uint64_t db = scale_desc(at + sb_at);
-                        const int steps = min(4, (p.K - kb * kKB + 63) / 64);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (2 * h < steps) {
-                                copy_scales<PAIR>(sa + uint32_t(h) * 4u, da + uint64_t(h * (kMx4Tile >> 4)));
-                                const uint32_t to = sb + uint32_t(h * atoms) * 4u;
-                                const uint64_t from = db + uint64_t(h * atoms * (kMx4Tile >> 4));
-                                copy_scales<PAIR>(to, from);
-                                if (atoms == 2) copy_scales<PAIR>(to + 4u, from + uint64_t(kMx4Tile >> 4));
-                                umma_mxf4<PAIR>(d, a + uint64_t(h * 4), b + uint64_t(h * 4), id0, sa + uint32_t(h) * 4u, to,
-                                                kb > kb0 || h > 0 ? 1u : 0u);
-                                if (2 * h + 1 < steps)
-                                    umma_mxf4<PAIR>(d, a + uint64_t(h * 4 + 2), b + uint64_t(h * 4 + 2), id2, sa + uint32_t(h) * 4u, to, 1u);
+                    const uint32_t d = tmem + uint32_t(buf) * d_stride;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        ok = warp_wait<PAIR == 2>(smem_u32(&c->full[st.at]), st.parity, c, p);
+                        // the stage that had these columns of scales is done (with a slot for
+                        // every stage the copies' landing says so)
+                        if (slots < p.stages) {
+                            if (ok && count == slots) {
+                                ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
+                                old.next(p.stages);
+                            } else ++count;
+                        }
+                        if (!ok) break;
+                        if (elect_one()) {
+                            tc_fence_after_sync();
+                            const uint32_t at = ring + uint32_t(st.at) * stage_bytes, sa = scales0 + uint32_t(sl.at) * scales_step;
+                            const int steps = (p.K - kb * kKB + 63) / 64;
+                            if (steps >= 4) issue_stage<PAIR, ATOMS, true>(d, at, sa_at, sa, idesc, kb > kb0, 4);
+                            else issue_stage<PAIR, ATOMS, false>(d, at, sa_at, sa, idesc, kb > kb0, steps);
+                            if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->empty[st.at]), pair_mask);
+                            else umma_commit<1>(smem_u32(&c->empty[st.at]));
+                            if (kb + 1 == kb1) {
+                                if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
+                                else umma_commit<1>(smem_u32(&c->tfull[buf]));
                             }
                         }
-                        if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->empty[st.at]), pair_mask);
-                        else umma_commit<1>(smem_u32(&c->empty[st.at]));
-                        if (kb + 1 == kb1) {
-                            if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->tfull[buf]), pair_mask);
-                            else umma_commit<1>(smem_u32(&c->tfull[buf]));
-                        }
+                        any = true;
+                        __syncwarp();
+                        st.next(p.stages);
+                        sl.next(slots);
                     }
-                    any = true;
-                    ++count;
-                    __syncwarp();
-                    st.next(p.stages);
+                    acc.next(2);
                 }
-                acc.next(2);
-            }
+            };
+            if (atoms == 2) run(std::integral_constant<int, 2>());
+            else run(std::integral_constant<int, 1>());
             if (!ok && any && elect_one()) {                     // (the lane that issued them)
                 umma_commit<PAIR>(smem_u32(&c->drain));
                 drain_wait(smem_u32(&c->drain), 0);
@@ -398,48 +419,65 @@ __global__ void __maxnreg__(96)
         const int v = warp - kScaleWarp0, n_kb = kb1 - kb0;
         Turn st;
         for (int i = 0; i < v; ++i) st.next(p.stages);
+        Walk w(unit0, step, p.n_ct);
+        const uint8_t *src[8];
         int kb = v;
-        bool ok = true;
-        for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
-            const Tile t = w.tile(p.nt, off, pref);
-            const uint8_t *src[kRowsMost / 32 + 1];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int32_t m = i * 32 + lane;
-                src[i] = nullptr;
-                if (m < t.rows && kb < n_kb) {
-                    int64_t r = int64_t(t.m0) + m;
-                    if (p.rows) r = p.rows[r];
-                    if (r >= 0 && r < p.T) src[i] = p.xs + mx4_scale_at(r, 0, p.n_kt);
-                    else atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_ROWS);
-                }
+        bool fresh = true;
+        // the warp's next stage: on to a unit that has one, whose rows are looked up
+        auto find = [&] {
+            while (kb >= n_kb) {
+                kb -= n_kb;
+                w.next();
+                fresh = true;
             }
-            for (; kb < n_kb; kb += kScaleWarps) {
-                uint32_t s[2][8];
+            if (w.g >= tiles) return false;
+            if (fresh) {
+                const Tile t = w.tile(p.nt, off, pref);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kt = 2 * (kb0 + kb) + h;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t m = i * 32 + lane;
+                    src[i] = nullptr;
+                    if (m < t.rows) {
+                        int64_t r = int64_t(t.m0) + m;
+                        if (p.rows) r = p.rows[r];
+                        if (r >= 0 && r < p.T) src[i] = p.xs + mx4_scale_at(r, 0, p.n_kt);
+                        else atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_ROWS);
+                    }
                 }
-                ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
-                if (!ok) break;
-                const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + sb_at + uint32_t(lane) * 16u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sts_v4(dst + uint32_t(h * atoms) * kMx4Tile, s[h][0], s[h][1], s[h][2], s[h][3]);
-                    if (atoms == 2) sts_v4(dst + uint32_t(h * 2 + 1) * kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader) mbar_arrive(smem_u32(&c->full[st.at]));
-                    else mbar_arrive_cluster(full_bar(st.at));
-                }
-                for (int i = 0; i < kScaleWarps; ++i) st.next(p.stages);
+                fresh = false;
             }
-            kb -= n_kb;
+            return true;
+        };
+        uint32_t s[2][8];
+        auto load = [&] {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kt = 2 * (kb0 + kb) + h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
+            }
+        };
+        bool more = find();
+        if (more) load();
+        while (more) {
+            if (!warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p)) break;
+            const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + sb_at + uint32_t(lane) * 16u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sts_v4(dst + uint32_t(h * atoms) * kMx4Tile, s[h][0], s[h][1], s[h][2], s[h][3]);
+                if (atoms == 2) sts_v4(dst + uint32_t(h * 2 + 1) * kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(smem_u32(&c->full[st.at]));
+                else mbar_arrive_cluster(full_bar(st.at));
+            }
+            for (int i = 0; i < kScaleWarps; ++i) st.next(p.stages);
+            kb += kScaleWarps;
+            // (loaded while the stage is waited for)
+            if ((more = find())) load();
         }
         __syncwarp();
     } else {
