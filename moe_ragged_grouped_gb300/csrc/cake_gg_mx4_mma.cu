@@ -30,12 +30,15 @@
 namespace cakegg {
 namespace {
 
-constexpr int kThreads = 480, kThreadsRouted = 576;
+constexpr int kThreads = 512, kThreadsRouted = 608;
 constexpr int kStoreWarp0 = 2, kStoreWarps = 8, kStoreThreads = kStoreWarps * 32;
 constexpr int kScaleWarp0 = 10, kScaleWarps = 4;
-constexpr int kRowsWarp0 = 14, kGatherWarps = 4;
+constexpr int kCopyWarp = 14;
+constexpr int kRowsWarp0 = 15, kGatherWarps = 4;
 constexpr int kKB = 256;                      // reduction length of a stage
 constexpr uint32_t kWBytes = 128 * kKB / 2;   // weight tile of a stage
+constexpr int kChunk = 2;                     // stages whose scales come together
+constexpr int kWords = 2 * kChunk;            // words (128 values) of the reduction in them
 constexpr uint32_t kOutTile = 2048;           // 32 BF16 or 16 FP32 rows x 32 channels of output, per storing warp
 constexpr int kRowsMost = 224;                // two accumulators of 224 columns leave 64 for scales
 constexpr int kGatherRows = 112;              // rows that a gathering warp serves at most: half a tile's
@@ -44,16 +47,15 @@ constexpr int kGatherRows = 112;              // rows that a gathering warp serv
 __host__ __device__ constexpr int row_atoms(int nt) { return nt > 128 ? 2 : 1; }
 // Stages whose scales tensor memory holds beside the two accumulators.
 __host__ __device__ constexpr int scale_slots(int nt) { return (512 - 2 * nt) / (8 + 8 * row_atoms(nt)); }
-// Shared memory of a stage: weights, rows, the channels' scales, the rows'.
-__host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt)
-{
-    return kWBytes + uint32_t(nt / pair) * 128u + 2u * kMx4Tile * uint32_t(1 + row_atoms(nt));
-}
+// Shared memory of a stage: weights, rows; of a chunk: the channels' scales, the rows'.
+__host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt) { return kWBytes + uint32_t(nt / pair) * 128u; }
+__host__ __device__ constexpr uint32_t chunk_bytes_of(int nt) { return uint32_t(kWords * kMx4Tile) * uint32_t(1 + row_atoms(nt)); }
 
 struct __align__(16) Ctrl {
-    uint64_t full[kMx4StagesMost], empty[kMx4StagesMost];   // stage: copies landed / MMAs done
+    uint64_t full[kMx4StagesMost], empty[kMx4StagesMost];   // stage: copies landed, scales in tensor memory / MMAs done
+    uint64_t scales[kScaleWarps], sfree[kScaleWarps];       // chunk: scales in shared memory / copied from there
     uint64_t tfull[2], tempty[2];                           // accumulator: complete / stored
-    uint64_t drain;
+    uint64_t drain, drain_copies;
     uint32_t tmem_base;
     int32_t abort_flag;
     int32_t total;                                          // row tiles of all experts
@@ -105,24 +107,32 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
             : "memory");
 }
 
-// A stage's copies of scales and its MMAs, of a word of 128 values at a time.
-// WHOLE: all four MMAs; else `steps` of them, at the end of the reduction.
+// A stage's copies of scales to tensor memory, and its MMAs.  WHOLE: all four
+// MMAs; else `steps` of them, at the end of the reduction.  (ATOMS: scale tiles of
+// the rows in a word.)
 template <int PAIR, int ATOMS, bool WHOLE>
-__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t at, uint32_t sa_at, uint32_t sa, uint32_t idesc, bool more, int steps)
+__device__ __forceinline__ void issue_copies(uint32_t from_a, uint32_t from_b, uint32_t to, int steps)
 {
     constexpr uint64_t kStep = kMx4Tile >> 4;
-    const uint64_t a = smem_desc_sw128(at, 16, 1024), b = smem_desc_sw128(at + kWBytes, 16, 1024);
-    const uint64_t from = scale_desc(at + sa_at);
+    const uint64_t a = scale_desc(from_a), b = scale_desc(from_b);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (!WHOLE && 2 * h >= steps) break;
-        const uint32_t ca = sa + uint32_t(h) * 4u, cb = sa + 8u + uint32_t(h * ATOMS) * 4u;
-        copy_scales<PAIR>(ca, from + uint64_t(h) * kStep);
+        copy_scales<PAIR>(to + uint32_t(h) * 4u, a + uint64_t(h) * kStep);
 #pragma unroll
-        for (int i = 0; i < ATOMS; ++i) copy_scales<PAIR>(cb + uint32_t(i) * 4u, from + uint64_t(2 + h * ATOMS + i) * kStep);
-        umma_mxf4<PAIR>(d, a + uint64_t(h * 4), b + uint64_t(h * 4), idesc, ca, cb, h > 0 || more ? 1u : 0u);
-        if (WHOLE || 2 * h + 1 < steps)
-            umma_mxf4<PAIR>(d, a + uint64_t(h * 4 + 2), b + uint64_t(h * 4 + 2), idesc | kSecondHalf, ca, cb, 1u);
+        for (int i = 0; i < ATOMS; ++i)
+            copy_scales<PAIR>(to + 8u + uint32_t(h * ATOMS + i) * 4u, b + uint64_t(h * ATOMS + i) * kStep);
+    }
+}
+template <int PAIR, int ATOMS, bool WHOLE>
+__device__ __forceinline__ void issue_mmas(uint32_t d, uint32_t at, uint32_t sa, uint32_t idesc, bool more, int steps)
+{
+    const uint64_t a = smem_desc_sw128(at, 16, 1024), b = smem_desc_sw128(at + kWBytes, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (!WHOLE && k >= steps) break;
+        umma_mxf4<PAIR>(d, a + uint64_t(k * 2), b + uint64_t(k * 2), k & 1 ? idesc | kSecondHalf : idesc, sa + uint32_t(k >> 1) * 4u,
+                        sa + 8u + uint32_t((k >> 1) * ATOMS) * 4u, k > 0 || more ? 1u : 0u);
     }
 }
 
@@ -134,11 +144,12 @@ __global__ void __maxnreg__(96)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-    const uint32_t x_bytes = uint32_t(p.nt / PAIR) * 128u;       // B of this CTA in a stage
     const uint32_t stage_bytes = stage_bytes_of(PAIR, p.nt);
-    const uint32_t sa_at = kWBytes + x_bytes, sb_at = sa_at + 2u * kMx4Tile;   // the scales in a stage
     const int atoms = row_atoms(p.nt);
     uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
+    const uint32_t chunks = ring + uint32_t(p.stages) * stage_bytes, chunk_bytes = chunk_bytes_of(p.nt);
+    constexpr uint32_t kRowScales = kWords * kMx4Tile;           // the rows' in a chunk
+    after += kScaleWarps * chunk_bytes;
     float *recv = reinterpret_cast<float *>(after);              // split: [split][channel][columns + 4]
     after += p.splits > 1 ? split_bytes(p.nt, p.splits) : 0;
     uint8_t *out_tile = after;                                   // [warp][row][32 channels]
@@ -190,15 +201,19 @@ __global__ void __maxnreg__(96)
         tmem_relinquish<PAIR>();
     } else if (tid == 64) {
         for (int s = 0; s < p.stages; ++s) {
-            // the weights' arming, the rows' and the rows' scales, of both CTAs
-            mbar_init(smem_u32(&c->full[s]), uint32_t(p.rows ? 3 : 2) + PAIR);
+            mbar_init(smem_u32(&c->full[s]), p.rows ? 4 : 3);    // the weights' arming, the rows', the copies of scales
             mbar_init(smem_u32(&c->empty[s]), 1);
+        }
+        for (int v = 0; v < kScaleWarps; ++v) {
+            mbar_init(smem_u32(&c->scales[v]), PAIR);            // the warp that put them together, of both CTAs
+            mbar_init(smem_u32(&c->sfree[v]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c->tfull[b]), 1);
             mbar_init(smem_u32(&c->tempty[b]), uint32_t(kStoreWarps) * PAIR);       // storing warps, of both CTAs
         }
         mbar_init(smem_u32(&c->drain), 1);
+        mbar_init(smem_u32(&c->drain_copies), 1);
         fence_barrier_init();
     } else if (tid == 96) {
         c->abort_flag = 0;
@@ -240,10 +255,7 @@ __global__ void __maxnreg__(96)
         bool ok = true, passed = false;
         for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
             const Tile t = w.tile(p.nt, off, pref);
-            const int ct = t.ct * PAIR + half;
-            // (a pair's last channel tile may have no channels of the odd CTA: the copies
-            // of weights bring zeros, and the scales of the last tile that there is)
-            const int32_t scale0 = (t.e * p.n_nt + min(ct, p.n_nt - 1)) * p.n_kt;
+            const int ct = t.ct * PAIR + half;                   // (of a pair's last tile perhaps past the channels: zeros)
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (issued == p.stages && !passed) {
                     grid_dependency_wait();
@@ -253,14 +265,11 @@ __global__ void __maxnreg__(96)
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t bar = full_bar(st.at), dst = ring + uint32_t(st.at) * stage_bytes;
-                    const bool both = 2 * kb + 1 < p.n_kt;       // (a last stage may have one scale tile)
-                    if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * (kWBytes + (both ? 2u : 1u) * kMx4Tile));
+                    if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * kWBytes);
                     if (!((p.debug_flags & CAKE_GG_DEBUG_DROP_FIRST_LOAD) && blockIdx.x == 0 && issued == 0)) {
                         if (PAIR == 2) tma_load_3d_pair(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
                         else tma_load_3d(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
                     }
-                    tma_rows<PAIR>(dst + sa_at, &mapS, bar, 0, scale0 + 2 * kb);
-                    if (both) tma_rows<PAIR>(dst + sa_at + kMx4Tile, &mapS, bar, 0, scale0 + 2 * kb + 1);
                 }
                 __syncwarp();
                 st.next(p.stages);
@@ -281,8 +290,7 @@ __global__ void __maxnreg__(96)
             // (with the number of scale tiles a constant each issue is a few instructions)
             auto run = [&](auto n_atoms) {
                 constexpr int ATOMS = decltype(n_atoms)::value;
-                Turn st, acc, old, sl;
-                int count = 0;                                   // stages so far, up to the slots
+                Turn st, acc, sl;
                 for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
                     const Tile t = w.tile(p.nt, off, pref);
                     const uint32_t n = __shfl_sync(0xffffffffu, uint32_t((t.rows + kNAlign - 1) / kNAlign * kNAlign), 0);
@@ -294,22 +302,14 @@ __global__ void __maxnreg__(96)
                     }
                     const uint32_t d = tmem + uint32_t(buf) * d_stride;
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        ok = warp_wait<PAIR == 2>(smem_u32(&c->full[st.at]), st.parity, c, p);
-                        // the stage that had these columns of scales is done (with a slot for
-                        // every stage the copies' landing says so)
-                        if (slots < p.stages) {
-                            if (ok && count == slots) {
-                                ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
-                                old.next(p.stages);
-                            } else ++count;
-                        }
+                        ok = warp_wait(smem_u32(&c->full[st.at]), st.parity, c, p);
                         if (!ok) break;
                         if (elect_one()) {
                             tc_fence_after_sync();
                             const uint32_t at = ring + uint32_t(st.at) * stage_bytes, sa = scales0 + uint32_t(sl.at) * scales_step;
                             const int steps = (p.K - kb * kKB + 63) / 64;
-                            if (steps >= 4) issue_stage<PAIR, ATOMS, true>(d, at, sa_at, sa, idesc, kb > kb0, 4);
-                            else issue_stage<PAIR, ATOMS, false>(d, at, sa_at, sa, idesc, kb > kb0, steps);
+                            if (steps >= 4) issue_mmas<PAIR, ATOMS, true>(d, at, sa, idesc, kb > kb0, 4);
+                            else issue_mmas<PAIR, ATOMS, false>(d, at, sa, idesc, kb > kb0, steps);
                             if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->empty[st.at]), pair_mask);
                             else umma_commit<1>(smem_u32(&c->empty[st.at]));
                             if (kb + 1 == kb1) {
@@ -411,28 +411,33 @@ __global__ void __maxnreg__(96)
             }
             acc.next(2);
         }
-    } else if (warp < kRowsWarp0) {
+    } else if (warp < kCopyWarp) {
         // ======================= the rows' scales =======================
-        // Lane l has the rows l, l + 32, .. of the tile: a word of theirs is 16 bytes of
-        // a scale tile's lane.  In a pair both CTAs hold the scales of all rows.
+        // A chunk of stages at a time, each warp with a buffer of its own: the
+        // channels' by TMA, the rows' put together, lane l those of the rows l, l + 32, ..
+        // of the tile (a word of theirs is 16 bytes of a scale tile's lane).  In a pair
+        // both CTAs hold the scales of all rows.  (A chunk is ordered for the other CTA
+        // once, by a release at cluster scope, which takes a microsecond: a release for
+        // each stage held 16384 x 4096 -> 4096 at 117 us.)
         grid_dependency_wait();                                  // the tokens
         const int v = warp - kScaleWarp0, n_kb = kb1 - kb0;
-        Turn st;
-        for (int i = 0; i < v; ++i) st.next(p.stages);
+        const uint32_t dst = chunks + uint32_t(v) * chunk_bytes, bar_free = smem_u32(&c->sfree[v]);
+        const uint32_t bar = PAIR == 2 ? map_to_cta(smem_u32(&c->scales[v]), 0) : smem_u32(&c->scales[v]);
         Walk w(unit0, step, p.n_ct);
         const uint8_t *src[8];
-        int kb = v;
+        int kb = v * kChunk;
         bool fresh = true;
-        // the warp's next stage: on to a unit that has one, whose rows are looked up
+        Tile t = {};
+        // the warp's next chunk: on to a unit that has one, whose rows are looked up
         auto find = [&] {
             while (kb >= n_kb) {
-                kb -= n_kb;
+                kb -= (n_kb + kChunk - 1) / kChunk * kChunk;     // (a unit's last chunk may be short)
                 w.next();
                 fresh = true;
             }
             if (w.g >= tiles) return false;
             if (fresh) {
-                const Tile t = w.tile(p.nt, off, pref);
+                t = w.tile(p.nt, off, pref);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int32_t m = i * 32 + lane;
@@ -448,36 +453,101 @@ __global__ void __maxnreg__(96)
             }
             return true;
         };
-        uint32_t s[2][8];
+        uint32_t s[kWords][8];
         auto load = [&] {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kWords; ++h) {
                 const int kt = 2 * (kb0 + kb) + h;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
             }
         };
-        bool more = find();
+        uint32_t round = 0;
+        bool more = find(), ok = true;
         if (more) load();
         while (more) {
-            if (!warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p)) break;
-            const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + sb_at + uint32_t(lane) * 16u;
+            ok = warp_wait(bar_free, round ^ 1u, c, p);
+            if (!ok) break;
+            // (a pair's last channel tile may be past the channels: any scales do; a copy may
+            // go on into the next tile's, which nobody uses)
+            if (elect_one())
+                tma_rows<PAIR>(dst, &mapS, bar, 0, (t.e * p.n_nt + min(t.ct * PAIR + half, p.n_nt - 1)) * p.n_kt + 2 * (kb0 + kb));
+            __syncwarp();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sts_v4(dst + uint32_t(h * atoms) * kMx4Tile, s[h][0], s[h][1], s[h][2], s[h][3]);
-                if (atoms == 2) sts_v4(dst + uint32_t(h * 2 + 1) * kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
+            for (int h = 0; h < kWords; ++h) {
+                const uint32_t to = dst + kRowScales + uint32_t(h * atoms) * kMx4Tile + uint32_t(lane) * 16u;
+                sts_v4(to, s[h][0], s[h][1], s[h][2], s[h][3]);
+                if (atoms == 2) sts_v4(to + kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (leader) mbar_arrive(smem_u32(&c->full[st.at]));
-                else mbar_arrive_cluster(full_bar(st.at));
+                if (leader) mbar_arrive_expect_tx(bar, PAIR * kRowScales);
+                else mbar_arrive_cluster(bar);
             }
-            for (int i = 0; i < kScaleWarps; ++i) st.next(p.stages);
-            kb += kScaleWarps;
-            // (loaded while the stage is waited for)
+            round ^= 1u;
+            kb += kScaleWarps * kChunk;
+            // (loaded while the buffer is waited for)
             if ((more = find())) load();
+        }
+        if (!ok || aborted(c)) {
+            if (!leader) drain_blind();
+            else if (lane == 0) drain_wait(smem_u32(&c->scales[v]), round ^ 1u);
+        }
+        __syncwarp();
+    } else if (warp == kCopyWarp) {
+        // ======================= scales to tensor memory (the even CTA of a pair) =======================
+        grid_dependency_wait();
+        bool ok = true, any = false;
+        if (leader) {
+            auto run = [&](auto n_atoms) {
+                constexpr int ATOMS = decltype(n_atoms)::value;
+                Turn st, sl, old, ch;
+                int count = 0;                                   // stages so far, up to the slots
+                for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
+                    for (int kb = kb0; kb < kb1; kb += kChunk) {
+                        ok = warp_wait<PAIR == 2>(smem_u32(&c->scales[ch.at]), ch.parity, c, p);
+                        const uint32_t from = chunks + uint32_t(ch.at) * chunk_bytes;
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            if (!ok || kb + i >= kb1) break;
+                            // the stage that had these columns is done (and with it all of this
+                            // stage's barrier that came before)
+                            if (count == slots) {
+                                ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
+                                old.next(p.stages);
+                            } else ++count;
+                            if (!ok) break;
+                            if (elect_one()) {
+                                tc_fence_after_sync();
+                                const int steps = (p.K - (kb + i) * kKB + 63) / 64;
+                                const uint32_t to = scales0 + uint32_t(sl.at) * scales_step;
+                                const uint32_t fa = from + uint32_t(2 * i) * kMx4Tile, fb = from + kRowScales + uint32_t(2 * i * ATOMS) * kMx4Tile;
+                                if (steps >= 4) issue_copies<PAIR, ATOMS, true>(fa, fb, to, 4);
+                                else issue_copies<PAIR, ATOMS, false>(fa, fb, to, steps);
+                                umma_commit<PAIR>(smem_u32(&c->full[st.at]));
+                                if (i + 1 == kChunk || kb + i + 1 == kb1) {
+                                    if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->sfree[ch.at]), pair_mask);
+                                    else umma_commit<1>(smem_u32(&c->sfree[ch.at]));
+                                }
+                            }
+                            any = true;
+                            __syncwarp();
+                            st.next(p.stages);
+                            sl.next(slots);
+                        }
+                        if (!ok) break;
+                        ch.next(kScaleWarps);
+                    }
+                }
+            };
+            if (atoms == 2) run(std::integral_constant<int, 2>());
+            else run(std::integral_constant<int, 1>());
+            if ((!ok || aborted(c)) && any && elect_one()) {     // (the lane that issued them)
+                umma_commit<PAIR>(smem_u32(&c->drain_copies));
+                drain_wait(smem_u32(&c->drain_copies), 0);
+            }
         }
         __syncwarp();
     } else {
@@ -663,7 +733,7 @@ cudaError_t launch(const Mx4Launch &l, bool pdl, cudaStream_t stream)
 
 size_t mx4_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
-    return 1024 + size_t(stages) * stage_bytes_of(pair, nt) + (splits > 1 ? split_bytes(nt, splits) : 0) +
+    return 1024 + size_t(stages) * stage_bytes_of(pair, nt) + size_t(kScaleWarps) * chunk_bytes_of(nt) + (splits > 1 ? split_bytes(nt, splits) : 0) +
            kStoreWarps * kOutTile + sizeof(Ctrl) + size_t(kGatherWarps * kGatherRows) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
@@ -685,7 +755,7 @@ int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p0, const uint8_t *W, const u
     if (rc != CAKE_GG_OK) return rc;
     const uint64_t ds[2] = {uint64_t(kMx4Tile) / 4, uint64_t(p.E) * uint64_t(p.n_nt) * uint64_t(p.n_kt)};
     const uint64_t ss[1] = {uint64_t(kMx4Tile)};
-    const uint32_t bs[2] = {uint32_t(kMx4Tile) / 4, 1};
+    const uint32_t bs[2] = {uint32_t(kMx4Tile) / 4, uint32_t(kWords)};
     if (ds[1] > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
     rc = encode_tiled(&l->ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, ws, ds, ss, bs, false);
     if (rc != CAKE_GG_OK) return rc;
