@@ -28,7 +28,7 @@ constexpr int32_t kMaxExperts = 1024;
 constexpr int32_t kMaxK = (1 << 17) - 32;
 constexpr int32_t kMaxN = INT32_MAX - 511;     // channels of whole tiles (256) and storing warps stay below 2^31
 constexpr int kSms = 152;
-constexpr int kStagesLeast = 4;                // a warp that serves every fourth stage meets no barrier two rounds late
+constexpr int kStagesLeast = 3;
 
 uint64_t align_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
@@ -55,9 +55,10 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 uint64_t scale_bytes(uint64_t rows, int32_t K) { return (rows + 127) / 128 * uint64_t((K + 127) / 128) * kMx4Tile; }
 
-// Workspace: header | the tokens' scales | their codes (activations only).
+// Workspace: header | the tokens' scales | their codes (activations only) | the
+// rows' scales as a pair takes them | their codes, where they are routed.
 struct Layout {
-    uint64_t scales, tokens, total;
+    uint64_t scales, tokens, arranged, rows, total;
 };
 Layout layout(const cake_gg_mx4_plan_t &pl)
 {
@@ -65,7 +66,15 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
     const uint64_t T = pl.x_dtype == CAKE_GG_MX4 ? 0 : uint64_t(pl.T);
     L.scales = kHeader;
     L.tokens = L.scales + scale_bytes(T, pl.K);
-    L.total = L.tokens + align_up(T * uint64_t(pl.K) / 2, 256);
+    L.arranged = L.tokens + align_up(T * uint64_t(pl.K) / 2, 256);
+    L.rows = L.arranged;
+    L.total = L.arranged;
+    if (pl.pair == 2) {
+        L.rows += uint64_t(mx4_slots(pl.M_max, pl.E, pl.tile_rows)) * uint64_t((pl.K + 127) / 128 * mx4_row_atoms(pl.tile_rows)) * kMx4Tile;
+        // (whether a call routes is known with the call: T other than M_max says that it
+        // does, and it may all the same)
+        L.total = L.rows + align_up(uint64_t(pl.M_max) * uint64_t(pl.K) / 2, 256);
+    }
     return L;
 }
 
@@ -239,6 +248,92 @@ int launch_quant(const void *X, int x_dtype, int act, int64_t E, int64_t R, int3
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- scales of a pair's rows
+
+// The scales of a slot's rows, put together from those of their tokens, and where
+// rows are routed their codes.  A pair's even CTA issues for both, so what the odd
+// one reads has to be ordered for the even one: copies by TMA are, by their barrier;
+// stores of the odd CTA's warps are by a release at cluster scope, which takes some
+// microseconds while outputs are stored (16384 x 4096 -> 4096: 117 us with one for each
+// stage, 103 for every other, 87 so).  And gathered by TMA a row of 128 bytes takes
+// some 8 clocks, for every channel tile again (32768 tokens through 2 of 8 experts
+// 4096 -> 4096: 445 us).  A block serves 128 rows: one scale tile of every word, a thread
+// four rows, 32 apart; then a warp a row's codes.
+__global__ void __launch_bounds__(256)
+    mx4_arrange_kernel(const int32_t *__restrict__ offsets, const int32_t *__restrict__ rows, const uint8_t *__restrict__ xs,
+                       const uint8_t *__restrict__ x, uint8_t *__restrict__ out, uint8_t *__restrict__ out_x, int32_t *status, int64_t M,
+                       int64_t T, int32_t E, int32_t K, int32_t nt, int32_t atoms)
+{
+    const int32_t n_kt = (K + 127) / 128;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int32_t slot = int32_t(blockIdx.x) / atoms, atom = int32_t(blockIdx.x) % atoms;
+    // the last expert whose slots begin at or before this one; what the product would
+    // refuse is left alone
+    int32_t e = 0, first = 0, end = int32_t(M);
+    if (offsets) {
+        int32_t hi = E;
+        while (hi - e > 1) {
+            const int32_t mid = (e + hi) / 2;
+            if (mx4_slot(offsets[mid], mid, 0, nt) <= slot) e = mid;
+            else hi = mid;
+        }
+        first = offsets[e], end = offsets[e + 1];
+    }
+    if (first < 0 || end < first || end > M) return;
+    const int64_t m0 = first + (int64_t(slot) - mx4_slot(first, e, 0, nt)) * nt + atom * 128;
+    const int64_t m1 = min(int64_t(end), m0 - atom * 128 + nt);
+    if (m0 < first || m0 >= m1) return;
+    const int lane = threadIdx.x & 31;
+    const uint8_t *src[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int64_t r = m0 + i * 32 + lane;
+        src[i] = nullptr;
+        if (r < m1) {
+            if (rows) r = rows[r];
+            if (r >= 0 && r < T) src[i] = xs + mx4_scale_at(r, 0, n_kt);
+            else atomicCAS(status, 0, CAKE_GG_ERR_BAD_ROWS);
+        }
+    }
+    uint8_t *dst = out + (int64_t(slot) * n_kt * atoms + atom) * kMx4Tile + lane * 16;
+    for (int kt = threadIdx.x >> 5; kt < n_kt; kt += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = src[i] ? *reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile) : 0u;
+        *reinterpret_cast<uint4 *>(dst + int64_t(kt) * atoms * kMx4Tile) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (!rows) return;
+    const int32_t pieces = K / 32;                               // 16 bytes each
+    const int64_t end_row = min(m1, m0 + 128);
+    for (int64_t m = m0 + (threadIdx.x >> 5); m < end_row; m += 8) {
+        const int64_t r = rows[m];
+        if (r < 0 || r >= T) continue;
+        const uint4 *from = reinterpret_cast<const uint4 *>(x + r * int64_t(K / 2));
+        uint4 *to = reinterpret_cast<uint4 *>(out_x + m * int64_t(K / 2));
+#pragma unroll 4
+        for (int i = lane; i < pieces; i += 32) to[i] = from[i];
+    }
+}
+
+cudaError_t launch_arrange(const Mx4Params &p, const int32_t *rows, int64_t T, const uint8_t *xs, const uint8_t *x, uint8_t *out,
+                           uint8_t *out_x, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = {};
+    const int32_t atoms = mx4_row_atoms(p.nt);
+    cfg.gridDim = dim3(unsigned(mx4_slots(p.M, p.E, p.nt) * atoms), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    if (pdl_enabled()) {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, mx4_arrange_kernel, p.offsets, rows, xs, x, out, out_x, p.status, p.M, T, p.E, p.K, p.nt, atoms);
+}
+
 // The problem's own checks, shared by the plan and the call.
 int check_problem(int32_t E, int64_t M_max, int64_t T, int32_t N, int32_t K, int x_dtype, int act, int out_dtype)
 {
@@ -273,7 +368,7 @@ void choose(cake_gg_mx4_plan_t *pl)
     pl->splits = 1;
     pl->pair = env_int("CAKE_GG_MX4_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_MX4_ROWS_PER_TILE", pl->tile_rows);
-    if (nt >= 32 && nt <= 224 && nt % 32 == 0) pl->tile_rows = nt;
+    if (nt >= 32 && nt <= kMx4RowsMost && nt % 32 == 0) pl->tile_rows = nt;
     const int sp = env_int("CAKE_GG_MX4_SPLITS", pl->splits);
     pl->splits = sp >= 1 && sp <= 8 && pl->pair == 1 ? sp : 1;
     pl->stages = stages_for(pl->pair, pl->tile_rows, pl->splits, pl->E);
@@ -282,9 +377,10 @@ void choose(cake_gg_mx4_plan_t *pl)
 // What the kernel can run.
 bool plan_ok(const cake_gg_mx4_plan_t &pl)
 {
-    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= 224 && pl.tile_rows % 32 == 0 &&
+    return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= kMx4RowsMost && pl.tile_rows % 32 == 0 &&
            pl.stages >= kStagesLeast && pl.stages <= kMx4StagesMost && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 255) / 256 &&   // (a stage for every CTA)
+           (pl.pair == 1 || mx4_slots(pl.M_max, pl.E, pl.tile_rows) * ((pl.K + 127) / 128) <= INT32_MAX / 4) &&
            mx4_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kMx4SmemLimit;
 }
 
@@ -358,29 +454,33 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Mx4Params p{};
     p.offsets = offsets;
-    p.rows = rows;
-    p.xs = ready ? xs : base + L.scales;
+    // (a pair's rows are laid out before: for it row m is token m)
+    const bool pair = pl.pair == 2;
+    const uint8_t *scales = ready ? xs : base + L.scales, *x = ready ? static_cast<const uint8_t *>(X) : base + L.tokens;
+    const uint8_t *x_rows = pair && rows ? base + L.rows : x;
+    p.rows = pair ? nullptr : rows;
+    p.xs = pair ? base + L.arranged : scales;
     p.Y = Y;
     p.status = reinterpret_cast<int32_t *>(base);
     p.M = pl.M_max;
-    p.T = pl.T;
+    p.T = pair ? pl.M_max : pl.T;
     p.E = pl.E;
     p.N = pl.N;
     p.K = pl.K;
     p.out_f32 = pl.out_dtype == CAKE_GG_FP32;
-    p.early = !ready;
+    p.early = !ready || pair;
     p.nt = pl.tile_rows;
     p.stages = pl.stages;
     p.splits = pl.splits;
     p.debug_flags = pl.debug_flags;
     p.timeout_ns = pl.timeout_ns ? pl.timeout_ns : kTimeoutNs;
-    const uint8_t *x = ready ? static_cast<const uint8_t *>(X) : base + L.tokens;
     const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
     // what cannot be launched is refused before anything is enqueued
     Mx4Launch product;
-    if ((rc = prepare_mx4_mma(&product, p, W, ws, x, pl.pair, cap)) != CAKE_GG_OK) return rc;
+    if ((rc = prepare_mx4_mma(&product, p, W, ws, x_rows, pl.pair, cap)) != CAKE_GG_OK) return rc;
     if (!ready && (rc = launch_quant(X, pl.x_dtype, pl.act, 1, pl.T, pl.K, base + L.tokens, base + L.scales, s)) != CAKE_GG_OK)
         return rc;
+    if (pair && launch_arrange(p, rows, pl.T, scales, x, base + L.arranged, base + L.rows, s) != cudaSuccess) return CAKE_GG_ERR_CUDA;
     return launch_mx4_mma(product, pdl_enabled(), s);
 }
 

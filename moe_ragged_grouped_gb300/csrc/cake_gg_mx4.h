@@ -28,12 +28,27 @@ __host__ __device__ __forceinline__ int64_t mx4_scale_at(int64_t r, int32_t b, i
 }
 constexpr int32_t kMx4Tile = 512;
 
+// Rows of a tile at most: two accumulators of 192 columns leave room in tensor
+// memory for the scales of five stages (beside two of 224 there are two, and each
+// stage waits for the one before last: 16384 x 4096 -> 4096 106 us, 87).
+constexpr int kMx4RowsMost = 192;
+
+// Scale tiles of a word (128 values) of the reduction for a tile of nt rows.
+__host__ __device__ constexpr int mx4_row_atoms(int nt) { return nt > 128 ? 2 : 1; }
+
+// A pair of CTAs takes the scales of its rows as a row tile has them: for each
+// slot and each word of the reduction the scale tiles of nt rows.  The slot of
+// an expert's tile j needs the expert's offset only: nothing is summed, and since
+// floor((a + n) / nt) + 1 >= floor(a / nt) + ceil(n / nt), no two tiles share one.
+__host__ __device__ __forceinline__ int32_t mx4_slot(int32_t offset, int32_t e, int32_t j, int32_t nt) { return offset / nt + e + j; }
+__host__ __device__ __forceinline__ int64_t mx4_slots(int64_t M, int32_t E, int32_t nt) { return M / nt + E; }
+
 // One call of the products.
 //   Y[m, n] = sum_k x[r(m), k] w[e(m), n, k]
 struct Mx4Params {
     const int32_t *offsets;   // [E + 1], or null: one expert owning rows [0, M)
-    const int32_t *rows;      // [M] token of each row, or null: the row itself
-    const uint8_t *xs;        // token scales, in tiles
+    const int32_t *rows;      // [M] token of each row, or null: the row itself (for a pair: laid out so)
+    const uint8_t *xs;        // token scales, in tiles (for a pair: of its rows, by slot)
     void *Y;                  // [M, N]
     int32_t *status;          // sticky status word (workspace byte 0)
     int64_t M, T;             // rows of all experts (offsets' bound), tokens
@@ -61,7 +76,7 @@ size_t mx4_mma_smem(int pair, int nt, int stages, int splits, int E);
 // Everything that can be refused is refused by the preparation, which enqueues
 // nothing.  Both return a cake_gg_status_t.
 struct Mx4Launch {
-    CUtensorMap mw, ms, mx;
+    CUtensorMap mw, ms, mx, mr;
     Mx4Params p;
     int32_t pair, grid;
 };

@@ -37,23 +37,26 @@ constexpr int kCopyWarp = 14;
 constexpr int kRowsWarp0 = 15, kGatherWarps = 4;
 constexpr int kKB = 256;                      // reduction length of a stage
 constexpr uint32_t kWBytes = 128 * kKB / 2;   // weight tile of a stage
+constexpr int kRowWords = kMx4RowsMost / 32;  // words of scales that a lane puts together
 constexpr int kChunk = 2;                     // stages whose scales come together
 constexpr int kWords = 2 * kChunk;            // words (128 values) of the reduction in them
 constexpr uint32_t kOutTile = 2048;           // 32 BF16 or 16 FP32 rows x 32 channels of output, per storing warp
-constexpr int kRowsMost = 224;                // two accumulators of 224 columns leave 64 for scales
-constexpr int kGatherRows = 112;              // rows that a gathering warp serves at most: half a tile's
+constexpr int kGatherRows = kMx4RowsMost / 2;  // rows that a gathering warp serves at most: half a tile's
 
-// Scale tiles of a word (128 values) of the reduction, for the rows of a tile.
-__host__ __device__ constexpr int row_atoms(int nt) { return nt > 128 ? 2 : 1; }
 // Stages whose scales tensor memory holds beside the two accumulators.
-__host__ __device__ constexpr int scale_slots(int nt) { return (512 - 2 * nt) / (8 + 8 * row_atoms(nt)); }
-// Shared memory of a stage: weights, rows; of a chunk: the channels' scales, the rows'.
-__host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt) { return kWBytes + uint32_t(nt / pair) * 128u; }
-__host__ __device__ constexpr uint32_t chunk_bytes_of(int nt) { return uint32_t(kWords * kMx4Tile) * uint32_t(1 + row_atoms(nt)); }
+__host__ __device__ constexpr int scale_slots(int nt) { return (512 - 2 * nt) / (8 + 8 * mx4_row_atoms(nt)); }
+// Shared memory of scales, the channels' and the rows', of some words; of a stage:
+// weights, rows, and for a pair the scales; of a chunk (not for a pair).
+__host__ __device__ constexpr uint32_t scale_bytes_of(int words, int nt) { return uint32_t(words * kMx4Tile) * uint32_t(1 + mx4_row_atoms(nt)); }
+__host__ __device__ constexpr uint32_t stage_bytes_of(int pair, int nt)
+{
+    return kWBytes + uint32_t(nt / pair) * 128u + (pair == 2 ? scale_bytes_of(2, nt) : 0u);
+}
+__host__ __device__ constexpr uint32_t chunk_bytes_of(int nt) { return scale_bytes_of(kWords, nt); }
 
 struct __align__(16) Ctrl {
     uint64_t full[kMx4StagesMost], empty[kMx4StagesMost];   // stage: copies landed, scales in tensor memory / MMAs done
-    uint64_t scales[kScaleWarps], sfree[kScaleWarps];       // chunk: scales in shared memory / copied from there
+    uint64_t scales[kMx4StagesMost], sfree[kScaleWarps];    // chunk (pair: stage): scales in shared memory / copied from there
     uint64_t tfull[2], tempty[2];                           // accumulator: complete / stored
     uint64_t drain, drain_copies;
     uint32_t tmem_base;
@@ -139,17 +142,19 @@ __device__ __forceinline__ void issue_mmas(uint32_t d, uint32_t at, uint32_t sa,
 template <int PAIR, bool OUT_F32>
 __global__ void __maxnreg__(96)
     mx4_mma_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapS,
-                   const __grid_constant__ CUtensorMap mapX, const Mx4Params p)
+                   const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapR,
+                   const Mx4Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
     const uint32_t stage_bytes = stage_bytes_of(PAIR, p.nt);
-    const int atoms = row_atoms(p.nt);
+    const int atoms = mx4_row_atoms(p.nt);
     uint8_t *after = ring_ptr + size_t(p.stages) * stage_bytes;
     const uint32_t chunks = ring + uint32_t(p.stages) * stage_bytes, chunk_bytes = chunk_bytes_of(p.nt);
     constexpr uint32_t kRowScales = kWords * kMx4Tile;           // the rows' in a chunk
-    after += kScaleWarps * chunk_bytes;
+    if (PAIR == 1) after += kScaleWarps * chunk_bytes;
+    const uint32_t scales_at = stage_bytes - scale_bytes_of(2, p.nt);   // (pair) in a stage
     float *recv = reinterpret_cast<float *>(after);              // split: [split][channel][columns + 4]
     after += p.splits > 1 ? split_bytes(p.nt, p.splits) : 0;
     uint8_t *out_tile = after;                                   // [warp][row][32 channels]
@@ -201,13 +206,11 @@ __global__ void __maxnreg__(96)
         tmem_relinquish<PAIR>();
     } else if (tid == 64) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(smem_u32(&c->full[s]), p.rows ? 4 : 3);    // the weights' arming, the rows', the copies of scales
+            mbar_init(smem_u32(&c->full[s]), PAIR == 1 && p.rows ? 4 : 3);    // the weights' arming, the rows', the copies of scales
             mbar_init(smem_u32(&c->empty[s]), 1);
+            mbar_init(smem_u32(&c->scales[s]), 1);               // the warp that puts them together; its arming
         }
-        for (int v = 0; v < kScaleWarps; ++v) {
-            mbar_init(smem_u32(&c->scales[v]), PAIR);            // the warp that put them together, of both CTAs
-            mbar_init(smem_u32(&c->sfree[v]), 1);
-        }
+        for (int v = 0; v < kScaleWarps; ++v) mbar_init(smem_u32(&c->sfree[v]), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c->tfull[b]), 1);
             mbar_init(smem_u32(&c->tempty[b]), uint32_t(kStoreWarps) * PAIR);       // storing warps, of both CTAs
@@ -220,6 +223,7 @@ __global__ void __maxnreg__(96)
         tma_prefetch_desc(&mapW);
         tma_prefetch_desc(&mapS);
         tma_prefetch_desc(&mapX);
+        if (PAIR == 2) tma_prefetch_desc(&mapR);
     }
     if (PAIR == 2 || p.splits > 1) cluster_sync_all();           // peers' barriers are ready
     tc_fence_before_sync();
@@ -255,7 +259,10 @@ __global__ void __maxnreg__(96)
         bool ok = true, passed = false;
         for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
             const Tile t = w.tile(p.nt, off, pref);
-            const int ct = t.ct * PAIR + half;                   // (of a pair's last tile perhaps past the channels: zeros)
+            // (the odd CTA's channels of a pair's last tile may be past the last: their
+            // weights come as zeros, for which any scales do)
+            const int ct = t.ct * PAIR + half;
+            const int32_t scale_w = (t.e * p.n_nt + min(ct, p.n_nt - 1)) * p.n_kt;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (issued == p.stages && !passed) {
                     grid_dependency_wait();
@@ -270,6 +277,12 @@ __global__ void __maxnreg__(96)
                         if (PAIR == 2) tma_load_3d_pair(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
                         else tma_load_3d(dst, &mapW, bar, kb * (kKB / 2), ct * 128, t.e);
                     }
+                    if (PAIR == 2) {
+                        // (the second words of an odd last stage are another row's: nobody uses them)
+                        const uint32_t bar_s = map_to_cta(smem_u32(&c->scales[st.at]), 0);
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->scales[st.at]), 2u * scale_bytes_of(2, p.nt));
+                        tma_load_2d_pair(dst + scales_at, &mapS, bar_s, 0, scale_w + 2 * kb);
+                    }
                 }
                 __syncwarp();
                 st.next(p.stages);
@@ -278,8 +291,10 @@ __global__ void __maxnreg__(96)
         }
         grid_dependency_wait();
         if (!ok || aborted(c)) {
-            if (leader) drain_stages(st, issued, 1, lane, p.stages, c);
-            else drain_blind();
+            if (leader) {
+                drain_stages(st, issued, 1, lane, p.stages, c);
+                drain_blind();                                   // (the scales)
+            } else drain_blind();
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -413,87 +428,79 @@ __global__ void __maxnreg__(96)
         }
     } else if (warp < kCopyWarp) {
         // ======================= the rows' scales =======================
-        // A chunk of stages at a time, each warp with a buffer of its own: the
-        // channels' by TMA, the rows' put together, lane l those of the rows l, l + 32, ..
-        // of the tile (a word of theirs is 16 bytes of a scale tile's lane).  In a pair
-        // both CTAs hold the scales of all rows.  (A chunk is ordered for the other CTA
-        // once, by a release at cluster scope, which takes a microsecond: a release for
-        // each stage held 16384 x 4096 -> 4096 at 117 us.)
+        // (A pair's are laid out before, see mx4_arrange_kernel.)  A chunk of stages at a
+        // time, each warp with a buffer of its own: the channels' by TMA, the rows' put
+        // together, lane l those of the rows l, l + 32, .. of the tile (a word of theirs is
+        // 16 bytes of a scale tile's lane).
         grid_dependency_wait();                                  // the tokens
-        const int v = warp - kScaleWarp0, n_kb = kb1 - kb0;
-        const uint32_t dst = chunks + uint32_t(v) * chunk_bytes, bar_free = smem_u32(&c->sfree[v]);
-        const uint32_t bar = PAIR == 2 ? map_to_cta(smem_u32(&c->scales[v]), 0) : smem_u32(&c->scales[v]);
-        Walk w(unit0, step, p.n_ct);
-        const uint8_t *src[8];
-        int kb = v * kChunk;
-        bool fresh = true;
-        Tile t = {};
-        // the warp's next chunk: on to a unit that has one, whose rows are looked up
-        auto find = [&] {
-            while (kb >= n_kb) {
-                kb -= (n_kb + kChunk - 1) / kChunk * kChunk;     // (a unit's last chunk may be short)
-                w.next();
-                fresh = true;
-            }
-            if (w.g >= tiles) return false;
-            if (fresh) {
-                t = w.tile(p.nt, off, pref);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t m = i * 32 + lane;
-                    src[i] = nullptr;
-                    if (m < t.rows) {
-                        int64_t r = int64_t(t.m0) + m;
-                        if (p.rows) r = p.rows[r];
-                        if (r >= 0 && r < p.T) src[i] = p.xs + mx4_scale_at(r, 0, p.n_kt);
-                        else atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_ROWS);
-                    }
+        if constexpr (PAIR == 1) {
+            const int v = warp - kScaleWarp0, n_kb = kb1 - kb0;
+            const uint32_t dst = chunks + uint32_t(v) * chunk_bytes, bar_free = smem_u32(&c->sfree[v]);
+            const uint32_t bar = smem_u32(&c->scales[v]);
+            Walk w(unit0, step, p.n_ct);
+            const uint8_t *src[kRowWords];
+            int kb = v * kChunk;
+            bool fresh = true;
+            Tile t = {};
+            // the warp's next chunk: on to a unit that has one, whose rows are looked up
+            auto find = [&] {
+                while (kb >= n_kb) {
+                    kb -= (n_kb + kChunk - 1) / kChunk * kChunk;     // (a unit's last chunk may be short)
+                    w.next();
+                    fresh = true;
                 }
-                fresh = false;
-            }
-            return true;
-        };
-        uint32_t s[kWords][8];
-        auto load = [&] {
+                if (w.g >= tiles) return false;
+                if (fresh) {
+                    t = w.tile(p.nt, off, pref);
 #pragma unroll
-            for (int h = 0; h < kWords; ++h) {
-                const int kt = 2 * (kb0 + kb) + h;
+                    for (int i = 0; i < kRowWords; ++i) {
+                        const int32_t m = i * 32 + lane;
+                        src[i] = nullptr;
+                        if (m < t.rows) {
+                            int64_t r = int64_t(t.m0) + m;
+                            if (p.rows) r = p.rows[r];
+                            if (r >= 0 && r < p.T) src[i] = p.xs + mx4_scale_at(r, 0, p.n_kt);
+                            else atomicCAS(p.status, 0, CAKE_GG_ERR_BAD_ROWS);
+                        }
+                    }
+                    fresh = false;
+                }
+                return true;
+            };
+            uint32_t s[kWords][8] = {};
+            auto load = [&] {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
-            }
-        };
-        uint32_t round = 0;
-        bool more = find(), ok = true;
-        if (more) load();
-        while (more) {
-            ok = warp_wait(bar_free, round ^ 1u, c, p);
-            if (!ok) break;
-            // (a pair's last channel tile may be past the channels: any scales do; a copy may
-            // go on into the next tile's, which nobody uses)
-            if (elect_one())
-                tma_rows<PAIR>(dst, &mapS, bar, 0, (t.e * p.n_nt + min(t.ct * PAIR + half, p.n_nt - 1)) * p.n_kt + 2 * (kb0 + kb));
-            __syncwarp();
+                for (int h = 0; h < kWords; ++h) {
+                    const int kt = 2 * (kb0 + kb) + h;
 #pragma unroll
-            for (int h = 0; h < kWords; ++h) {
-                const uint32_t to = dst + kRowScales + uint32_t(h * atoms) * kMx4Tile + uint32_t(lane) * 16u;
-                sts_v4(to, s[h][0], s[h][1], s[h][2], s[h][3]);
-                if (atoms == 2) sts_v4(to + kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
+                    for (int i = 0; i < kRowWords; ++i)
+                        s[h][i] = src[i] && kt < p.n_kt ? __ldg(reinterpret_cast<const uint32_t *>(src[i] + int64_t(kt) * kMx4Tile)) : 0u;
+                }
+            };
+            uint32_t round = 0;
+            bool more = find(), ok = true;
+            if (more) load();
+            while (more) {
+                ok = warp_wait(bar_free, round ^ 1u, c, p);
+                if (!ok) break;
+                // (a copy may go on into the next row's words, which nobody uses)
+                if (elect_one()) tma_load_2d(dst, &mapS, bar, 0, (t.e * p.n_nt + t.ct) * p.n_kt + 2 * (kb0 + kb));
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < kWords; ++h) {
+                    const uint32_t to = dst + kRowScales + uint32_t(h * atoms) * kMx4Tile + uint32_t(lane) * 16u;
+                    sts_v4(to, s[h][0], s[h][1], s[h][2], s[h][3]);
+                    if (atoms == 2) sts_v4(to + kMx4Tile, s[h][4], s[h][5], s[h][6], s[h][7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(bar, kRowScales);
+                round ^= 1u;
+                kb += kScaleWarps * kChunk;
+                // (loaded while the buffer is waited for)
+                if ((more = find())) load();
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (leader) mbar_arrive_expect_tx(bar, PAIR * kRowScales);
-                else mbar_arrive_cluster(bar);
-            }
-            round ^= 1u;
-            kb += kScaleWarps * kChunk;
-            // (loaded while the buffer is waited for)
-            if ((more = find())) load();
-        }
-        if (!ok || aborted(c)) {
-            if (!leader) drain_blind();
-            else if (lane == 0) drain_wait(smem_u32(&c->scales[v]), round ^ 1u);
+            if ((!ok || aborted(c)) && lane == 0) drain_wait(bar, round ^ 1u);
         }
         __syncwarp();
     } else if (warp == kCopyWarp) {
@@ -505,42 +512,36 @@ __global__ void __maxnreg__(96)
                 constexpr int ATOMS = decltype(n_atoms)::value;
                 Turn st, sl, old, ch;
                 int count = 0;                                   // stages so far, up to the slots
-                for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
-                    for (int kb = kb0; kb < kb1; kb += kChunk) {
-                        ok = warp_wait<PAIR == 2>(smem_u32(&c->scales[ch.at]), ch.parity, c, p);
-                        const uint32_t from = chunks + uint32_t(ch.at) * chunk_bytes;
-#pragma unroll
-                        for (int i = 0; i < kChunk; ++i) {
-                            if (!ok || kb + i >= kb1) break;
-                            // the stage that had these columns is done (and with it all of this
-                            // stage's barrier that came before)
-                            if (count == slots) {
-                                ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
-                                old.next(p.stages);
-                            } else ++count;
-                            if (!ok) break;
-                            if (elect_one()) {
-                                tc_fence_after_sync();
-                                const int steps = (p.K - (kb + i) * kKB + 63) / 64;
-                                const uint32_t to = scales0 + uint32_t(sl.at) * scales_step;
-                                const uint32_t fa = from + uint32_t(2 * i) * kMx4Tile, fb = from + kRowScales + uint32_t(2 * i * ATOMS) * kMx4Tile;
-                                if (steps >= 4) issue_copies<PAIR, ATOMS, true>(fa, fb, to, 4);
-                                else issue_copies<PAIR, ATOMS, false>(fa, fb, to, steps);
-                                umma_commit<PAIR>(smem_u32(&c->full[st.at]));
-                                if (i + 1 == kChunk || kb + i + 1 == kb1) {
-                                    if (PAIR == 2) umma_commit_mc<2>(smem_u32(&c->sfree[ch.at]), pair_mask);
-                                    else umma_commit<1>(smem_u32(&c->sfree[ch.at]));
-                                }
-                            }
-                            any = true;
-                            __syncwarp();
-                            st.next(p.stages);
-                            sl.next(slots);
-                        }
+                for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next())
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        const int i = PAIR == 2 ? 0 : (kb - kb0) % kChunk;
+                        if (i == 0) ok = warp_wait(smem_u32(&c->scales[PAIR == 2 ? st.at : ch.at]), PAIR == 2 ? st.parity : ch.parity, c, p);
+                        // the stage that had these columns is done (and with it all of this
+                        // stage's barrier that came before)
+                        if (ok && count == slots) {
+                            ok = warp_wait(smem_u32(&c->empty[old.at]), old.parity, c, p);
+                            old.next(p.stages);
+                        } else ++count;
                         if (!ok) break;
-                        ch.next(kScaleWarps);
+                        const bool last = PAIR == 1 && (i + 1 == kChunk || kb + 1 == kb1);   // of a chunk
+                        if (elect_one()) {
+                            tc_fence_after_sync();
+                            const int steps = (p.K - kb * kKB + 63) / 64;
+                            const uint32_t to = scales0 + uint32_t(sl.at) * scales_step;
+                            const uint32_t from = PAIR == 2 ? ring + uint32_t(st.at) * stage_bytes + scales_at : chunks + uint32_t(ch.at) * chunk_bytes;
+                            const uint32_t fa = from + uint32_t(2 * i) * kMx4Tile;
+                            const uint32_t fb = from + (PAIR == 2 ? 2u * kMx4Tile : kRowScales) + uint32_t(2 * i * ATOMS) * kMx4Tile;
+                            if (steps >= 4) issue_copies<PAIR, ATOMS, true>(fa, fb, to, 4);
+                            else issue_copies<PAIR, ATOMS, false>(fa, fb, to, steps);
+                            umma_commit<PAIR>(smem_u32(&c->full[st.at]));
+                            if (last) umma_commit<1>(smem_u32(&c->sfree[ch.at]));
+                        }
+                        any = true;
+                        __syncwarp();
+                        st.next(p.stages);
+                        sl.next(slots);
+                        if (last) ch.next(kScaleWarps);
                     }
-                }
             };
             if (atoms == 2) run(std::integral_constant<int, 2>());
             else run(std::integral_constant<int, 1>());
@@ -556,7 +557,13 @@ __global__ void __maxnreg__(96)
         Turn st;
         int issued = 0;
         bool ok = true;
-        if (p.rows == nullptr) {
+        // a pair's scales of a tile's rows, as they were laid out
+        auto scales_of = [&](const Tile &t) { return mx4_slot(off[t.e], t.e, (t.m0 - off[t.e]) / p.nt, p.nt) * int64_t(p.n_kt * atoms); };
+        auto load_scales = [&](int s, int64_t at, int kb) {
+            tma_load_2d_pair(ring + uint32_t(s) * stage_bytes + scales_at + 2u * kMx4Tile, &mapR, map_to_cta(smem_u32(&c->scales[s]), 0), 0,
+                             int32_t(at) + 2 * kb * atoms);
+        };
+        if (PAIR == 2 || p.rows == nullptr) {                    // (a pair's rows are laid out before)
             grid_dependency_wait();                              // the tokens
             for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
                 const Tile t = w.tile(p.nt, off, pref);
@@ -564,12 +571,14 @@ __global__ void __maxnreg__(96)
                 const int n_box = (n_half + p.box - 1) / p.box;
                 const uint32_t mb = uint32_t(t.m0 + half * n_half);         // (a box past 2^31 is past the tokens)
                 const uint32_t bytes = 128u * uint32_t(n_box * p.box);
+                const int64_t scales = scales_of(t);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
                     if (!ok) break;
                     if (elect_one()) {
                         const uint32_t bar = full_bar(st.at), dst = ring + uint32_t(st.at) * stage_bytes + kWBytes;
                         if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * bytes);
+                        if (PAIR == 2) load_scales(st.at, scales, kb);
                         for (int b = 0; b < n_box; ++b)
                             tma_rows<PAIR>(dst + uint32_t(b * p.box) * 128u, &mapX, bar, kb * (kKB / 2), int32_t(mb + uint32_t(b * p.box)));
                     }
@@ -591,11 +600,11 @@ __global__ void __maxnreg__(96)
             int kb = group;
             for (Walk w(unit0, step, p.n_ct); ok && w.g < tiles; w.next()) {
                 const Tile t = w.tile(p.nt, off, pref);
-                const int n_half = (t.rows + kNAlign - 1) / kNAlign * 16;
+                const int n = (t.rows + 15) / 16 * 16;
                 __syncwarp();
-                for (int i = lane; i < n_half / 2; i += 32) {
+                for (int i = lane; i < n / 2; i += 32) {
                     // (counted from the tile's first row: past its last one the sum may pass 2^31)
-                    const int32_t m = half * n_half + (i >> 2) * 8 + side * 4 + (i & 3);
+                    const int32_t m = (i >> 2) * 8 + side * 4 + (i & 3);
                     const int32_t id = m < t.rows ? p.rows[t.m0 + m] : 0;
                     mine[i] = id >= 0 && id < p.T ? id : 0;      // (reported where its scales are read)
                 }
@@ -605,14 +614,14 @@ __global__ void __maxnreg__(96)
                     ok = warp_wait(smem_u32(&c->empty[st.at]), st.parity ^ 1u, c, p);
                     if (!ok) break;
                     if (elect_one()) {
-                        const uint32_t bar = full_bar(st.at);
+                        const uint32_t bar = smem_u32(&c->full[st.at]);
                         const uint32_t dst = ring + uint32_t(st.at) * stage_bytes + kWBytes + uint32_t(side) * 512u;
                         const int32_t k = (kb0 + kb) * (kKB / 2);
-                        if (leader) mbar_arrive_expect_tx(smem_u32(&c->full[st.at]), PAIR * uint32_t(n_half) * 64u);
+                        mbar_arrive_expect_tx(bar, uint32_t(n) * 64u);
 #pragma unroll 4
-                        for (int i = 0; i < n_half / 2; i += 4) {
+                        for (int i = 0; i < n / 2; i += 4) {
                             const int4 id = lds_i4(ids + uint32_t(i) * 4u);
-                            tma_gather4<PAIR>(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
+                            tma_gather4<1>(dst + uint32_t(i) * 256u, &mapX, bar, k, id.x, id.y, id.z, id.w);
                         }
                     }
                     __syncwarp();
@@ -622,10 +631,7 @@ __global__ void __maxnreg__(96)
                 kb -= n_kb;
             }
             grid_dependency_wait();
-            if (!ok || aborted(c)) {
-                if (leader) drain_stages(st, issued, 2, lane, p.stages, c);
-                else drain_blind();
-            }
+            if (!ok || aborted(c)) drain_stages(st, issued, 2, lane, p.stages, c);
         }
         __syncwarp();
     }
@@ -721,19 +727,19 @@ cudaError_t launch(const Mx4Launch &l, bool pdl, cudaStream_t stream)
         attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }
     cfg.gridDim = dim3(unsigned(l.grid), 1, 1);
-    cfg.blockDim = dim3(p.rows ? kThreadsRouted : kThreads, 1, 1);
+    cfg.blockDim = dim3(PAIR == 1 && p.rows ? kThreadsRouted : kThreads, 1, 1);
     cfg.dynamicSmemBytes = mx4_mma_smem(PAIR, p.nt, p.stages, p.splits, p.E);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = unsigned(na);
-    return cudaLaunchKernelEx(&cfg, mx4_mma_kernel<PAIR, OUT_F32>, l.mw, l.ms, l.mx, p);
+    return cudaLaunchKernelEx(&cfg, mx4_mma_kernel<PAIR, OUT_F32>, l.mw, l.ms, l.mx, l.mr, p);
 }
 
 }  // namespace
 
 size_t mx4_mma_smem(int pair, int nt, int stages, int splits, int E)
 {
-    return 1024 + size_t(stages) * stage_bytes_of(pair, nt) + size_t(kScaleWarps) * chunk_bytes_of(nt) + (splits > 1 ? split_bytes(nt, splits) : 0) +
+    return 1024 + size_t(stages) * stage_bytes_of(pair, nt) + (pair == 2 ? 0 : size_t(kScaleWarps) * chunk_bytes_of(nt)) + (splits > 1 ? split_bytes(nt, splits) : 0) +
            kStoreWarps * kOutTile + sizeof(Ctrl) + size_t(kGatherWarps * kGatherRows) * 4 + size_t(2 * (E + 1)) * 4;
 }
 
@@ -755,7 +761,7 @@ int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p0, const uint8_t *W, const u
     if (rc != CAKE_GG_OK) return rc;
     const uint64_t ds[2] = {uint64_t(kMx4Tile) / 4, uint64_t(p.E) * uint64_t(p.n_nt) * uint64_t(p.n_kt)};
     const uint64_t ss[1] = {uint64_t(kMx4Tile)};
-    const uint32_t bs[2] = {uint32_t(kMx4Tile) / 4, uint32_t(kWords)};
+    const uint32_t bs[2] = {uint32_t(kMx4Tile) / 4, pair == 2 ? 2u : uint32_t(kWords)};
     if (ds[1] > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
     rc = encode_tiled(&l->ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, ws, ds, ss, bs, false);
     if (rc != CAKE_GG_OK) return rc;
@@ -764,6 +770,15 @@ int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p0, const uint8_t *W, const u
     const uint32_t bx[2] = {uint32_t(kKB) / 2, p.rows ? 1u : uint32_t(p.box)};   // (gathered four rows at a time)
     rc = encode_tiled(&l->mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x, dx, sx, bx);
     if (rc != CAKE_GG_OK) return rc;
+
+    if (pair == 2) {
+        const int atoms = mx4_row_atoms(p.nt);
+        const uint64_t dr[2] = {uint64_t(kMx4Tile) / 4, uint64_t(mx4_slots(p.M, p.E, p.nt)) * uint64_t(p.n_kt * atoms)};
+        const uint32_t br[2] = {uint32_t(kMx4Tile) / 4, 2u * uint32_t(atoms)};
+        if (dr[1] > INT32_MAX) return CAKE_GG_ERR_OVERFLOW;
+        rc = encode_tiled(&l->mr, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, p.xs, dr, ss, br, false);
+        if (rc != CAKE_GG_OK) return rc;
+    } else l->mr = l->ms;
 
     // row tiles at most: a whole one per nt rows and a last one per expert with rows
     const int64_t tiles = p.E == 1 ? (p.M + p.nt - 1) / p.nt : p.M / p.nt + (p.M < p.E ? p.M : p.E);
