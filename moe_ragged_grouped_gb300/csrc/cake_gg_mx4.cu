@@ -361,11 +361,56 @@ int stages_for(int pair, int nt, int splits, int E)
     return s;
 }
 
+// Row tiles of nt rows that the call will have: exact for one expert; where E
+// share the rows, whole tiles and half a tile more for each expert that can have
+// rows, at least one each (the sizes are the device's).
+int64_t row_tiles(const cake_gg_mx4_plan_t &pl, int nt)
+{
+    const int64_t whole = (pl.M_max + nt - 1) / nt;
+    if (pl.E == 1) return whole;
+    const int64_t busy = pl.M_max < pl.E ? pl.M_max : pl.E;
+    return whole + busy / 2 > busy ? whole + busy / 2 : busy;
+}
+
+// Multiprocessors that clusters of `splits` CTAs can hold at once: a cluster lies
+// within one of the GPU's groups of them, whose sizes differ from part to part.
+int cluster_sms(int splits) { return splits <= 2 ? kSms : splits <= 6 ? 132 : 104; }
+
+// The shape, from a model of its time in nanoseconds: waves of units over the
+// multiprocessors (152, or 76 pairs), the stages of a unit, or the reading of the
+// weights where that is longer; the storing of the last unit, the laying out of a
+// pair's rows, and the exchange between the CTAs that share a tile.  The times of a stage, with all multiprocessors at work (16384 x
+// 4096 -> 4096), are for single CTAs 260, 272, 307, 337 ns for 96, 128, 160, 192 rows,
+// for pairs 245, 238, 275, 276; the lines below are within 7 % of that.  What the model
+// decides, measured with the neighbours: 33 x 8192 -> 512 divides the reduction by 8
+// (8.2 us; 8.0 by 6, 10.9 undivided), 701 tokens through 2 of 8 experts 4096 -> 2048 take
+// tiles of 96 rows (16.4; 18.9 with 128, 18.5 with 64), 300 through 4 of 32 6144 -> 4096
+// take 64 (70.9; 78 with 32), 1024 x 4096 -> 4096 single CTAs of 128 (14.6; 15.3 with pairs of
+// 160), 3001 x 5120 -> 1000 of 160 (12.7; 12.5 with pairs of 192, 16.9 with 128).
 void choose(cake_gg_mx4_plan_t *pl)
 {
-    pl->pair = 1;
-    pl->tile_rows = 128;
-    pl->splits = 1;
+    const int64_t n_kb = (pl->K + 255) / 256;
+    // the weights of the experts that can have rows, at what HBM gives
+    const int64_t weights = (pl->M_max < pl->E ? pl->M_max : pl->E) * pl->N * pl->K / 2 / 6000;
+    int64_t best = -1;
+    auto consider = [&](int pair, int nt, int splits) {
+        const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
+        if (splits > 1 && (units * splits > cluster_sms(splits) || n_kb < 2 * splits)) return;
+        const int64_t waves = (units * pair + kSms - 1) / kSms;
+        int64_t ns = waves * ((n_kb + splits - 1) / splits) * (200 + nt * (pair == 2 ? 4 : 7) / 10);
+        ns = (ns > weights ? ns : weights) + 12 * nt;
+        if (splits > 1) ns += 300 + nt * (45 + 4 * splits);
+        if (pair == 2) ns += 1800 + (pl->T != pl->M_max ? pl->M_max * pl->K / 12000 : 0);   // (routed: rows copied)
+        if (best < 0 || ns < best) {
+            best = ns;
+            pl->pair = pair;
+            pl->tile_rows = nt;
+            pl->splits = splits;
+        }
+    };
+    for (int nt = kMx4RowsMost; nt >= 64; nt -= 32) consider(2, nt, 1);
+    for (int nt = kMx4RowsMost; nt >= 32; nt -= 32)
+        for (int sp = 1; sp <= (nt <= 64 ? 8 : 1); ++sp) consider(1, nt, sp);
     pl->pair = env_int("CAKE_GG_MX4_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_MX4_ROWS_PER_TILE", pl->tile_rows);
     if (nt >= 32 && nt <= kMx4RowsMost && nt % 32 == 0) pl->tile_rows = nt;
