@@ -115,41 +115,119 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m)    // over the four la
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
-// Where FP32 cannot tell on which side of a border between two codes, or between
-// two scales, a gated value lies, 64 bits do.  FP32 is off by less than
-// kGateError of the value: two units in the last place of the exponential, one
-// half each of the sum, the quotient and the product.  A negative g far out,
-// whose exponential leaves FP32's range, counts as unsure where the block is as
-// small as that.
-constexpr float kGateError = 0x1p-20f, kDeep = -80.0f;
-__device__ __noinline__ uint32_t codes8_in_64_bits(const float (&g)[8], const float (&u)[8], uint32_t *byte)
+// silu(g) * u, three ways.  By approximate instructions: the product g log2(e)
+// rounds to 2^-24 of it, which the exponential multiplies by at most 40 ln 2 / log2(e);
+// the exponential is off by 2^-22, the reciprocal by 2^-23, four roundings by 2^-24
+// each: together below 2^-18 for g > -40.  (Two values share a reciprocal: 1 / a = b /
+// (a b).)  In FP32: two units in the last place of the exponential, a half each of the
+// sum, the quotient and the product: below 2^-20.  And in 64 bits.
+constexpr float kFastError = 0x1p-18f, kSlowError = 0x1p-20f, kFastFrom = -40.0f, kSlowFrom = -80.0f;
+
+__device__ __forceinline__ void gate_fast(const float (&g)[8], const float (&u)[8], float (&h)[8])
 {
-    double h[8], m = 0.0;
-    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        h[i] = double(g[i]) / (1.0 + exp(-double(g[i]))) * double(u[i]);
-        nan |= !isfinite(float(h[i]));
-        m = fmax(m, fabs(h[i]));
+    for (int j = 0; j < 8; j += 2) {
+        float a, b, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g[j] * -1.44269504f));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(g[j + 1] * -1.44269504f));
+        a += 1.0f, b += 1.0f;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+        h[j] = g[j] * u[j] * (r * b);
+        h[j + 1] = g[j + 1] * u[j + 1] * (r * a);
     }
-    m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    nan = (__ballot_sync(0xffffffffu, nan) >> (threadIdx.x & 28) & 0xfu) != 0;
-    const int e = m > 0.0 ? ilogb(m) + 125 : 0;
-    *byte = nan ? 255u : uint32_t(max(e, 0));
-    uint32_t w = 0;
-    if (!nan) {
-        const double inv = scalbn(1.0, 127 - int(*byte));
+}
+__device__ __forceinline__ double gate_exact(float g, float u) { return double(g) / (1.0 + exp(-double(g))) * double(u); }
+
+// The code of a magnitude in units of its scale.
+__device__ __forceinline__ uint32_t code_of(double a)
+{
+    return uint32_t(a > 0.25) + uint32_t(a >= 0.75) + uint32_t(a > 1.25) + uint32_t(a >= 1.75) + uint32_t(a > 2.5) +
+           uint32_t(a >= 3.5) + uint32_t(a > 5.0);
+}
+
+// Codes of h, known to a relative `error`, under the scale of the block: those that
+// the error decides are marked in `unsure`, a bit in each's place (all of them: the
+// scale is).
+__device__ __forceinline__ uint32_t codes8_known(const float (&h)[8], float error, uint32_t *byte, uint32_t *unsure)
+{
+    const uint32_t m = block_max(max_bits(h, 0));
+    const float a = __uint_as_float(m);
+    *byte = scale_byte(m);
+    const float inv = scale_inverse(*byte);
+    const uint32_t w = codes8(h, inv * (1.0f + error)), d = w ^ codes8(h, inv * (1.0f - error));
+    *unsure = (d | d >> 1 | d >> 2) & 0x11111111u;
+    if (scale_byte(__float_as_uint(a * (1.0f + error))) != scale_byte(__float_as_uint(a * (1.0f - error)))) *unsure = ~0u;
+    if (*byte == 255) *unsure = 0;
+    return w;
+}
+
+// What the approximate instructions leave open (one block of some thousand): FP32,
+// and where that cannot tell either on which side of a border between two codes,
+// or between two scales, a value lies, 64 bits; and where a negative g's exponential
+// leaves FP32's range.
+__device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (&u)[8], uint32_t *byte)
+{
+    float h[8], least = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double a = fabs(h[i]) * inv;
-            const uint32_t c = uint32_t(a > 0.25) + uint32_t(a >= 0.75) + uint32_t(a > 1.25) + uint32_t(a >= 1.75) +
-                               uint32_t(a > 2.5) + uint32_t(a >= 3.5) + uint32_t(a > 5.0);
-            w |= (c | (signbit(h[i]) ? 8u : 0u)) << (4 * i);
+    for (int j = 0; j < 8; ++j) {
+        h[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
+        least = fminf(least, g[j]);
+    }
+    uint32_t unsure, w = codes8_known(h, kSlowError, byte, &unsure);
+    const bool whole = unsure == ~0u || (*byte != 255 && least < kSlowFrom);
+    if (__any_sync(0xffffffffu, whole)) {
+        double m = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmax(m, fabs(gate_exact(g[j], u[j])));
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (*byte != 255) {
+            const int e = m > 0.0 ? ilogb(m) + 125 : 0;
+            *byte = uint32_t(max(e, 0));
+            unsure = ~0u;
         }
+    }
+    // (of a block that is unsure as a whole every value)
+    if (unsure == ~0u) unsure = 0x11111111u;
+    while (unsure) {
+        const int at = __ffs(int(unsure)) - 1;
+        unsure &= unsure - 1;
+        float gj = g[0], uj = u[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (at == 4 * j) gj = g[j], uj = u[j];
+        const double v = gate_exact(gj, uj);
+        const uint32_t c = code_of(fabs(v) * scalbn(1.0, 127 - int(*byte))) | (signbit(v) ? 8u : 0u);
+        w = (w & ~(15u << at)) | c << at;
     }
     return w;
 }
+
+// Eight values of a row as they are in memory.
+template <typename XT> struct Raw;
+template <> struct Raw<uint16_t> {
+    uint4 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
 
 // E matrices of R rows.  A lane has 8 values of a row at a time, four lanes a block,
 // a warp 256 values; it serves kRun such runs of one row, eight rows a block.
@@ -171,45 +249,47 @@ __global__ void __launch_bounds__(256)
     const XT *row = X + t * (ACT ? 2 : 1) * int64_t(K);
     uint8_t *q = Q + t * (int64_t(K) / 2);
     const int k0 = int(blockIdx.y) * (256 * kRun) + lane * 8;
-    float v[kRun][8], u[ACT ? kRun : 1][8];
+    Raw<XT> raw[kRun], raw_u[ACT ? kRun : 1];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
         const int k = k0 + i * 256;
         if (k < K) {
-            load8(row + k, v[i]);
-            if (ACT) load8(row + K + k, u[ACT ? i : 0]);
+            raw[i].load(row + k);
+            if (ACT) raw_u[ACT ? i : 0].load(row + K + k);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = u[ACT ? i : 0][j] = 0.0f;
+            raw[i].zero();
+            if (ACT) raw_u[ACT ? i : 0].zero();
         }
     }
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
         const int k = k0 + i * 256;
         if (k - lane * 8 >= K) break;
+        float v[8];
+        raw[i].values(v);
         uint32_t byte, w;
         if constexpr (!ACT) {
-            byte = scale_byte(block_max(max_bits(v[i], 0)));
-            w = byte == 255 ? 0 : codes8(v[i], scale_inverse(byte));
+            byte = scale_byte(block_max(max_bits(v, 0)));
+            w = codes8(v, scale_inverse(byte));
         } else {
-            float h[8], least = 0.0f;
+            float u[8], h[8], least = v[0];
+            raw_u[i].values(u);
+            gate_fast(v, u, h);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                h[j] = v[i][j] / (1.0f + expf(-v[i][j])) * u[i][j];
-                least = fminf(least, v[i][j]);
+            for (int j = 1; j < 8; ++j) least = fminf(least, v[j]);
+            uint32_t unsure;
+            w = codes8_known(h, kFastError, &byte, &unsure);
+            bool open = unsure != 0 || !(least > kFastFrom);
+            if (byte < 32 || byte == 255) {
+                // g u leaves FP32's range before h does; but zeros are zeros
+                bool zero = true;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) zero = zero && (v[j] == 0.0f || u[j] == 0.0f);
+                open = open || !zero;
             }
-            const uint32_t m = block_max(max_bits(h, 0));
-            byte = scale_byte(m);
-            const float inv = scale_inverse(byte);
-            w = codes8(h, inv * (1.0f + kGateError));
-            const float a = __uint_as_float(m);
-            bool unsure = w != codes8(h, inv * (1.0f - kGateError)) ||
-                          scale_byte(__float_as_uint(a * (1.0f + kGateError))) != scale_byte(__float_as_uint(a * (1.0f - kGateError))) ||
-                          (least < kDeep && a < 0x1p-80f);
-            unsure = unsure && byte != 255;
-            if (__any_sync(0xffffffffu, unsure)) w = codes8_in_64_bits(v[i], u[i], &byte);
-            if (byte == 255) w = 0;
+            if (__any_sync(0xffffffffu, open)) w = codes8_gated(v, u, &byte);
         }
+        if (byte == 255) w = 0;
         if (k < K) *reinterpret_cast<uint32_t *>(q + k / 2) = w;
         uint32_t word = byte << (8 * ((lane >> 2) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
