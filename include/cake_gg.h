@@ -467,6 +467,103 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
 int cake_gg_mx4_quant(const void *X, int x_dtype, int act, int32_t E, int64_t R, int32_t K, uint8_t *Xq,
                       uint8_t *xs, void *stream);
 
+/* ---- routing to experts ---------------------------------------------------
+ *
+ * From router logits l [T, E] (BF16 or FP32, rows `row_stride` values apart) to
+ * each token's top_k experts and weights, and to the rows in expert order that
+ * the grouped products take.
+ *
+ *   s = softmax(l) or sigmoid(l) of a token's logits
+ *
+ * The experts are the top_k largest by s + bias [E], or without a bias by l
+ * (which orders as s), the largest first, ties to the lowest index, a NaN below
+ * all others.  Where `groups` > 1, groups of E / groups neighbouring experts
+ * compete first, by their largest key or by the sum of their two largest (s +
+ * bias, or s), and only experts of the top_groups best are chosen; ties to the
+ * lowest group.  The choice is that of 64-bit scores: where FP32 cannot tell,
+ * they are computed.  Weights are s of the chosen (without the bias), divided by
+ * their sum with `renormalize` (0 where none is above zero), times `scale`.
+ *
+ *   expert [T, top_k], weight [T, top_k]
+ *   offsets [E + 1]: expert e's rows are [offsets[e], offsets[e + 1])
+ *   rows [T top_k]: the token of each row; an expert's rows are in the order
+ *   of their tokens
+ *   position [T, top_k]: the row of each token's j-th expert
+ *
+ * The same call gives the same bits on every run. */
+typedef enum { CAKE_GG_SCORE_SOFTMAX = 0, CAKE_GG_SCORE_SIGMOID = 1 } cake_gg_score_t;
+typedef enum { CAKE_GG_GROUP_MAX = 0, CAKE_GG_GROUP_TOP2 = 1 } cake_gg_group_score_t;
+
+typedef struct cake_gg_route_options {
+    int32_t score;           /* cake_gg_score_t                                     */
+    int32_t groups;          /* 1 .. 32, divides E; 1 = no groups                   */
+    int32_t top_groups;      /* 1 .. groups                                         */
+    int32_t group_score;     /* cake_gg_group_score_t                               */
+    int32_t renormalize;     /* divide the chosen scores by their sum               */
+    float scale;             /* of the weights                                      */
+} cake_gg_route_options_t;
+
+typedef struct cake_gg_route_plan {
+    int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
+    int32_t E;               /* experts, 1 .. 1024                                  */
+    int64_t T;               /* tokens, 0 .. 2^24                                   */
+    int32_t top_k;           /* experts of a token, 1 .. min(E, 32)                 */
+    /* chosen by cake_gg_route_plan() */
+    int32_t cluster;         /* 1: one cluster of blocks, in one launch             */
+    int32_t blocks, block_tokens;
+    uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
+} cake_gg_route_plan_t;
+
+/* Fill *plan.  Pure host arithmetic.  CAKE_GG_ERR_INVALID_ARG for sizes out of
+ * range, CAKE_GG_ERR_OVERFLOW for T > 2^24 or T top_k >= 2^31. */
+int cake_gg_route_plan(cake_gg_route_plan_t *plan, int64_t T, int32_t E, int32_t top_k);
+
+/* Route.  Device pointers, aligned to their elements (bias null: none); the
+ * workspace 16-byte aligned, plan->workspace_bytes, zero-filled once after
+ * allocation.  Enqueues one or two kernels on `stream`; allocates nothing, never
+ * synchronises.  CAKE_GG_ERR_INVALID_ARG also for groups that do not divide E, a
+ * row_stride below E, more experts than the top_groups have, and two largest of
+ * groups of one. */
+int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_t *options, const void *logits,
+                  int logits_dtype, int64_t row_stride, const float *bias, int32_t *expert, float *weight,
+                  int32_t *offsets, int32_t *rows, int32_t *position, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* The logits' gradient d_logits [T, E] (of the logits' type, every value written)
+ * from that of the weights, d_weight [T, top_k], for the experts that
+ * cake_gg_route chose: the choice itself, and the bias that takes part in nothing
+ * else, have none.  With g = d_weight * scale, s the scores, r = s / sum of the
+ * chosen:
+ *   softmax, renormalised  dl_j = r_j (g_j - sum g r)
+ *   softmax                dl_e = s_e ([e chosen] g_e - sum g s), every e
+ *   sigmoid, renormalised  dl_j = r_j (1 - s_j) (g_j - sum g r)
+ *   sigmoid                dl_j = s_j (1 - s_j) g_j
+ * An expert outside [0, E) is nobody.  One kernel. */
+int cake_gg_route_grad(int64_t T, int32_t E, int32_t top_k, int score, int renormalize, float scale,
+                       const void *logits, int logits_dtype, int64_t row_stride, const int32_t *expert,
+                       const float *d_weight, void *d_logits, void *stream);
+
+/* ---- rows back to their tokens --------------------------------------------
+ *
+ *   out[t] = sum_j weight[t, j] rows[position[t, j]]     (weight null: 1)
+ *
+ * rows [M, K], out [T, K], each BF16 or FP32; position [T, top_k], as
+ * cake_gg_route gives it; weight FP32.  Sums are FP32 over j in order, rounded
+ * once.  A position outside [0, M) is no row and adds nothing.  K is a multiple of
+ * 8, up to 2^20, top_k up to 32; rows and out 16-byte aligned.  One kernel. */
+int cake_gg_combine_rows(int64_t T, int64_t M, int32_t top_k, int32_t K, const void *rows, int rows_dtype,
+                         const int32_t *position, const float *weight, void *out, int out_dtype, void *stream);
+
+/* Its gradients, from d_out [T, K]:
+ *   d_rows[position[t, j]] = weight[t, j] d_out[t]       (of the rows' type)
+ *   d_weight[t, j] = <d_out[t], rows[position[t, j]]>    (null: not wanted, and rows may be null)
+ * Without weights d_rows is what takes tokens to their rows.  Each row is named
+ * at most once by position (a row named twice gets one of the two); rows that it
+ * does not name are left as they were.  One kernel. */
+int cake_gg_combine_grad(int64_t T, int64_t M, int32_t top_k, int32_t K, const void *d_out, int out_dtype,
+                         const void *rows, int rows_dtype, const int32_t *position, const float *weight,
+                         void *d_rows, float *d_weight, void *stream);
+
 /* Synchronise `stream`, return the status word of `workspace` (CAKE_GG_OK,
  * or the first _BAD_OFFSETS / _TIMEOUT / _BAD_ROWS recorded by a call since the last
  * check) and reset it to CAKE_GG_OK; CAKE_GG_ERR_CUDA if a CUDA call failed. */

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 import numpy as np
 
@@ -34,18 +35,23 @@ CAKE_GG_FWD, CAKE_GG_DGRAD, CAKE_GG_WGRAD = 0, 1, 2
 CAKE_GG_BF16, CAKE_GG_FP32, CAKE_GG_INT8, CAKE_GG_MX4 = 0, 1, 2, 3
 CAKE_GG_ACT_NONE, CAKE_GG_ACT_SILU_MUL = 0, 1
 CAKE_GG_DEBUG_DROP_FIRST_LOAD = 1
+CAKE_GG_SCORE_SOFTMAX, CAKE_GG_SCORE_SIGMOID = 0, 1
+CAKE_GG_GROUP_MAX, CAKE_GG_GROUP_TOP2 = 0, 1
 
 PASSES = {"fwd": CAKE_GG_FWD, "dgrad": CAKE_GG_DGRAD, "wgrad": CAKE_GG_WGRAD}
 DTYPES = {"bf16": CAKE_GG_BF16, "fp32": CAKE_GG_FP32}
 I8_X_DTYPES = {**DTYPES, "int8": CAKE_GG_INT8}
 MX4_X_DTYPES = {**DTYPES, "mx4": CAKE_GG_MX4}
+SCORES = {"softmax": CAKE_GG_SCORE_SOFTMAX, "sigmoid": CAKE_GG_SCORE_SIGMOID}
+GROUP_SCORES = {"max": CAKE_GG_GROUP_MAX, "top2": CAKE_GG_GROUP_TOP2}
 I8_ACTS = {None: CAKE_GG_ACT_NONE, "silu_mul": CAKE_GG_ACT_SILU_MUL}
 
 EXPORTED = ["cake_gg_plan", "cake_gg_fwd", "cake_gg_dgrad", "cake_gg_wgrad",
             "cake_gg_check_status", "cake_gg_strerror", "cake_gg_tile_walk", "cake_gg_corun_spinner",
             "cake_gg_router_plan", "cake_gg_router_fp32",
             "cake_gg_i8_plan", "cake_gg_i8_gemm", "cake_gg_i8_quant",
-            "cake_gg_mx4_plan", "cake_gg_mx4_gemm", "cake_gg_mx4_quant"]
+            "cake_gg_mx4_plan", "cake_gg_mx4_gemm", "cake_gg_mx4_quant",
+            "cake_gg_route_plan", "cake_gg_route", "cake_gg_route_grad", "cake_gg_combine_rows", "cake_gg_combine_grad"]
 
 
 class CakeGGPlan(ctypes.Structure):
@@ -153,6 +159,35 @@ class CakeGGMx4Plan(ctypes.Structure):
         return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
 
 
+class CakeGGRouteOptions(ctypes.Structure):
+    """Mirror of cake_gg_route_options_t (same field order, same C layout)."""
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class CakeGGRoutePlan(ctypes.Structure):
+    """Mirror of cake_gg_route_plan_t (same field order, same C layout)."""
+    _fields_ = [
+        ("abi_version", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("T", ctypes.c_int64),
+        ("top_k", ctypes.c_int32),
+        ("cluster", ctypes.c_int32),
+        ("blocks", ctypes.c_int32),
+        ("block_tokens", ctypes.c_int32),
+        ("workspace_bytes", ctypes.c_uint64),
+    ]
+
+    def as_dict(self):
+        return {f[0]: getattr(self, f[0]) for f in self._fields_}
+
+
 class CakeGGError(RuntimeError):
     def __init__(self, code, where):
         super().__init__(f"{where}: {cake_gg_strerror(code)} (status {code})")
@@ -210,6 +245,18 @@ def load_library(path: str = LIB_PATH):
     lib.cake_gg_mx4_gemm.restype = ctypes.c_int
     lib.cake_gg_mx4_quant.argtypes = [vp, ctypes.c_int, ctypes.c_int, i32, i64, i32, vp, vp, vp]
     lib.cake_gg_mx4_quant.restype = ctypes.c_int
+    route_p, options_p = ctypes.POINTER(CakeGGRoutePlan), ctypes.POINTER(CakeGGRouteOptions)
+    lib.cake_gg_route_plan.argtypes = [route_p, i64, i32, i32]
+    lib.cake_gg_route_plan.restype = ctypes.c_int
+    lib.cake_gg_route.argtypes = [route_p, options_p, vp, ctypes.c_int, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.cake_gg_route.restype = ctypes.c_int
+    lib.cake_gg_route_grad.argtypes = [i64, i32, i32, ctypes.c_int, ctypes.c_int, ctypes.c_float, vp, ctypes.c_int, i64, vp,
+                                       vp, vp, vp]
+    lib.cake_gg_route_grad.restype = ctypes.c_int
+    lib.cake_gg_combine_rows.argtypes = [i64, i64, i32, i32, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, vp]
+    lib.cake_gg_combine_rows.restype = ctypes.c_int
+    lib.cake_gg_combine_grad.argtypes = [i64, i64, i32, i32, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp, vp]
+    lib.cake_gg_combine_grad.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -421,6 +468,47 @@ def cake_gg_mx4_quant(X, x_dtype, act, E, R, K, Xq, xs, stream=None) -> int:
     """cake_gg_mx4_quant(): E matrices of R rows to 4-bit codes and block scales; returns the status code."""
     return load_library().cake_gg_mx4_quant(_ptr(X), _mx4_x_code(x_dtype), _act_code(act), int(E), int(R), int(K),
                                             _ptr(Xq), _ptr(xs), _stream(stream, X))
+
+
+def cake_gg_route_plan(T, E, top_k) -> CakeGGRoutePlan:
+    """cake_gg_route_plan(): plan of routing T tokens to top_k of E experts each; raises on error."""
+    plan = CakeGGRoutePlan()
+    rc = load_library().cake_gg_route_plan(ctypes.byref(plan), int(T), int(E), int(top_k))
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_route_plan")
+    return plan
+
+
+def cake_gg_route(plan, options, logits, logits_dtype, row_stride, bias, expert, weight, offsets, rows, position, workspace,
+                  workspace_bytes=None, stream=None) -> int:
+    """cake_gg_route(): experts, weights and rows of tokens by their router logits; returns the status code."""
+    nb = int(workspace.numel() * workspace.element_size()) if workspace_bytes is None else int(workspace_bytes)
+    return load_library().cake_gg_route(ctypes.byref(plan), ctypes.byref(options), _ptr(logits), _dtype_code(logits_dtype),
+                                        int(row_stride), _ptr(bias), _ptr(expert), _ptr(weight), _ptr(offsets), _ptr(rows),
+                                        _ptr(position), _ptr(workspace), nb, _stream(stream, logits))
+
+
+def cake_gg_route_grad(T, E, top_k, score, renormalize, scale, logits, logits_dtype, row_stride, expert, d_weight, d_logits,
+                       stream=None) -> int:
+    """cake_gg_route_grad(): the logits' gradient from the weights'; returns the status code."""
+    return load_library().cake_gg_route_grad(int(T), int(E), int(top_k), SCORES.get(score, score), int(bool(renormalize)),
+                                             float(scale), _ptr(logits), _dtype_code(logits_dtype), int(row_stride),
+                                             _ptr(expert), _ptr(d_weight), _ptr(d_logits), _stream(stream, logits))
+
+
+def cake_gg_combine_rows(T, M, top_k, K, rows, rows_dtype, position, weight, out, out_dtype, stream=None) -> int:
+    """cake_gg_combine_rows(): tokens as weighted sums of their rows; returns the status code."""
+    return load_library().cake_gg_combine_rows(int(T), int(M), int(top_k), int(K), _ptr(rows), _dtype_code(rows_dtype),
+                                               _ptr(position), _ptr(weight), _ptr(out), _dtype_code(out_dtype),
+                                               _stream(stream, rows))
+
+
+def cake_gg_combine_grad(T, M, top_k, K, d_out, out_dtype, rows, rows_dtype, position, weight, d_rows, d_weight,
+                         stream=None) -> int:
+    """cake_gg_combine_grad(): the gradients of rows and weights; returns the status code."""
+    return load_library().cake_gg_combine_grad(int(T), int(M), int(top_k), int(K), _ptr(d_out), _dtype_code(out_dtype),
+                                               _ptr(rows), _dtype_code(rows_dtype), _ptr(position), _ptr(weight), _ptr(d_rows),
+                                               _ptr(d_weight), _stream(stream, d_out))
 
 
 # ---------------------------------------------------------------- tensor-level helpers
@@ -864,4 +952,224 @@ def mx4_gemm(X, W, ws, xs=None, offsets=None, rows=None, act=None, out_dtype="bf
         st = cake_gg_check_status(workspace, stream)
         if st != CAKE_GG_OK:
             raise CakeGGError(st, "cake_gg_mx4_gemm (device status)")
+    return out
+
+
+class Routing(typing.NamedTuple):
+    """Where T tokens go, each to top_k of E experts (what route() gives)."""
+    expert: typing.Any      # int32 [T, top_k]: experts, the best first
+    weight: typing.Any      # float32 [T, top_k]
+    offsets: typing.Any     # int32 [E + 1]: expert e's rows are [offsets[e], offsets[e + 1])
+    rows: typing.Any        # int32 [T * top_k]: the token of each row
+    position: typing.Any    # int32 [T, top_k]: the row of each token's j-th expert
+
+
+def empty_routing(T, E, top_k, device) -> Routing:
+    """An uninitialised Routing, for route()'s `out`."""
+    import torch
+    def i32(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    return Routing(i32(T, top_k), torch.empty((T, top_k), dtype=torch.float32, device=device), i32(E + 1), i32(T * top_k),
+                   i32(T, top_k))
+
+
+def _real_name(tensor, name):
+    """ "bf16" or "fp32"."""
+    import torch
+    kind = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(tensor.dtype)
+    if kind is None:
+        raise TypeError(f"{name} is {tensor.dtype}: bfloat16 or float32 are taken")
+    return kind
+
+
+def _logits(logits):
+    """The type of router logits [T, E] whose rows are dense (they may lie apart)."""
+    kind = _real_name(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits are [T, E]")
+    if (logits.shape[1] > 1 and logits.stride(1) != 1) or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+        raise ValueError("the rows of logits are not dense")
+    return kind
+
+
+def _row_stride(logits):
+    return int(logits.stride(0)) if logits.shape[0] > 1 else int(logits.shape[1])
+
+
+def _here(tensor):
+    if tensor.get_device() < 0 or tensor.get_device() != _current_device():
+        _refuse_device(tensor)
+
+
+def _score_code(score):
+    if score not in SCORES:
+        raise ValueError(f"score is 'softmax' or 'sigmoid', got {score!r}")
+    return SCORES[score]
+
+
+def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True,
+          scale=1.0, plan=None, workspace=None, out=None, stream=None) -> Routing:
+    """Routes T tokens by their router logits [T, E] (bf16 or fp32; rows may lie apart, as in a slice of columns).
+
+    Scores are the softmax of a token's logits or their sigmoid; its experts are
+    the top_k largest by score + bias (float32 [E]; none: by the logits), ties to
+    the lowest index, a NaN last; with groups > 1 only from the `top_groups` (none:
+    all) of the E / groups neighbouring experts that have the largest group_score: "max", the
+    largest of the group, or "top2", the sum of its two largest.  The choice is
+    that of 64-bit scores.  Weights are the chosen experts' scores, without the
+    bias, divided by their sum with `renormalize`, times `scale`.  Rows are numbered
+    by expert, then by token: offsets and rows are what int8_gemm, mx4_gemm and
+    grouped_gemm take, position leads back (combine_rows).  In a loop, make the plan
+    (cake_gg_route_plan), the workspace and the outputs (empty_routing) once.  All
+    tensors are on the current CUDA device; stream as in int8_gemm.
+    """
+    import torch
+    kind = _logits(logits)
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    if group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score is 'max' or 'top2', got {group_score!r}")
+    options = CakeGGRouteOptions(_score_code(score), int(groups), int(groups if top_groups is None else top_groups),
+                                 GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
+    if plan is None:
+        plan = cake_gg_route_plan(T, E, top_k)
+    elif (plan.T, plan.E, plan.top_k) != (T, E, top_k):
+        raise ValueError("the plan is another problem's")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), logits.device)
+    if out is not None:
+        for tensor, name, dtype, shape in zip(out, Routing._fields, (torch.int32, torch.float32) + 3 * (torch.int32,),
+                                              ((T, top_k), (T, top_k), (E + 1,), (T * top_k,), (T, top_k))):
+            _need(tensor, name, dtype, shape, logits.device)
+    _here(logits)
+    if out is None:
+        i32, f32 = torch.int32, torch.float32
+        out = Routing(*(_result(shape, dtype, logits.device, stream) for shape, dtype in
+                        (((T, top_k), i32), ((T, top_k), f32), ((E + 1,), i32), ((T * top_k,), i32), ((T, top_k), i32))))
+    if workspace is None:
+        workspace = _scratch(plan, logits.device, stream)
+    elif workspace.device != logits.device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {logits.device}")
+    rc = cake_gg_route(plan, options, logits, kind, _row_stride(logits), bias, *out, workspace, stream=stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_route")
+    return out
+
+
+def route_grad(logits, expert, d_weight, score="softmax", renormalize=True, scale=1.0, out=None, stream=None):
+    """The gradient [T, E] of route()'s logits, in their type, from that of its weights (float32 [T, top_k]).
+
+    expert, score, renormalize and scale are route()'s.  The choice of experts and
+    the bias have no gradient.  All tensors are on the current CUDA device.
+    """
+    import torch
+    kind = _logits(logits)
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    _score_code(score)
+    if expert.dim() != 2:
+        raise ValueError("expert is [T, top_k]")
+    top_k = int(expert.shape[1])
+    _need(expert, "expert", torch.int32, (T, top_k), logits.device)
+    _need(d_weight, "d_weight", torch.float32, (T, top_k), logits.device)
+    if out is not None:
+        _need(out, "out", logits.dtype, (T, E), logits.device)
+    _here(logits)
+    if out is None:
+        out = _result((T, E), logits.dtype, logits.device, stream)
+    rc = cake_gg_route_grad(T, E, top_k, score, renormalize, scale, logits, kind, _row_stride(logits), expert, d_weight, out,
+                            stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_route_grad")
+    return out
+
+
+def _need_position(position, weight, device):
+    """T and top_k of int32 [T, top_k] positions and their float32 weights."""
+    import torch
+    if position.dim() != 2:
+        raise ValueError("position is [T, top_k]")
+    shape = tuple(position.shape)
+    _need(position, "position", torch.int32, shape, device)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, shape, device)
+    return shape
+
+
+def combine_rows(rows, position, weight=None, out_dtype="bf16", out=None, stream=None):
+    """Tokens [T, K] as sums of their rows: out[t] = sum_j weight[t, j] * rows[position[t, j]].
+
+    rows [M, K] are bf16 or fp32, position int32 [T, top_k] (a Routing's; outside
+    [0, M): no row), weight float32 [T, top_k] (none: ones).  FP32 sums over j in
+    order, rounded once.  All tensors are on the current CUDA device; stream as in
+    int8_gemm.
+    """
+    kind = _real_name(rows, "rows")
+    if rows.dim() != 2:
+        raise ValueError("rows are [M, K]")
+    M, K = int(rows.shape[0]), int(rows.shape[1])
+    _need(rows, "rows", rows.dtype, (M, K), rows.device)
+    T, top_k = _need_position(position, weight, rows.device)
+    out_type = _torch_out_dtype(out_dtype)
+    if out is not None:
+        _need(out, "out", out_type, (T, K), rows.device)
+    _here(rows)
+    if out is None:
+        out = _result((T, K), out_type, rows.device, stream)
+    rc = cake_gg_combine_rows(T, M, top_k, K, rows, kind, position, weight, out, out_dtype, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_combine_rows")
+    return out
+
+
+def combine_grad(d_out, rows, position, weight, out=None, stream=None):
+    """Gradients of combine_rows: (d_rows [M, K] in the rows' type, d_weight float32 [T, top_k]), from d_out [T, K].
+
+    position names each of the M = T * top_k rows once, as a Routing's does (rows
+    of another number are refused; rows that it does not name keep what `out`, or
+    fresh memory, holds).
+    """
+    import torch
+    kind, out_kind = _real_name(rows, "rows"), _real_name(d_out, "d_out")
+    if rows.dim() != 2 or d_out.dim() != 2:
+        raise ValueError("rows are [M, K], d_out is [T, K]")
+    if weight is None:
+        raise ValueError("without weights the rows' gradient is gather_rows(d_out, position)")
+    M, K = int(rows.shape[0]), int(rows.shape[1])
+    _need(rows, "rows", rows.dtype, (M, K), rows.device)
+    T, top_k = _need_position(position, weight, rows.device)
+    _need(d_out, "d_out", d_out.dtype, (T, K), rows.device)
+    if M != T * top_k:
+        raise ValueError(f"{M} rows for {T} x {top_k} positions")
+    if out is not None:
+        _need(out, "out", rows.dtype, (M, K), rows.device)
+    _here(rows)
+    if out is None:
+        out = _result((M, K), rows.dtype, rows.device, stream)
+    d_weight = _result((T, top_k), torch.float32, rows.device, stream)
+    rc = cake_gg_combine_grad(T, M, top_k, K, d_out, out_kind, rows, kind, position, weight, out, d_weight, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_combine_grad")
+    return out, d_weight
+
+
+def gather_rows(X, position, out=None, stream=None):
+    """Tokens X [T, K] (bf16 or fp32) as rows in expert order [T * top_k, K]: out[position[t, j]] = X[t].
+
+    position names each row once, as a Routing's does.
+    """
+    kind = _real_name(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X is [T, K]")
+    _need(X, "X", X.dtype, tuple(X.shape), X.device)
+    T, top_k = _need_position(position, None, X.device)
+    if X.shape[0] != T:
+        raise ValueError(f"{X.shape[0]} tokens for {T} positions")
+    M, K = T * top_k, int(X.shape[1])
+    if out is not None:
+        _need(out, "out", X.dtype, (M, K), X.device)
+    _here(X)
+    if out is None:
+        out = _result((M, K), X.dtype, X.device, stream)
+    rc = cake_gg_combine_grad(T, M, top_k, K, X, kind, None, kind, position, None, out, None, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_combine_grad")
     return out

@@ -1,0 +1,247 @@
+// cake_gg_combine.cu -- the rows' way back to their tokens, and its gradients.
+//
+//   y[t] = sum_j w[t, j] r[position[t, j]]           (or without weights)
+//   dr[position[t, j]] = w[t, j] dy[t]               (without: tokens to their rows)
+//   dw[t, j] = <dy[t], r[position[t, j]]>
+//
+// Sums are FP32, over j in order, each product rounded with its addition; nothing
+// is added by atomics.  A position outside [0, M) is no row: it adds nothing and
+// gets nothing.
+#include <cstdint>
+#include <cstdlib>
+
+#include <cuda_runtime.h>
+
+#include "../../include/cake_gg.h"
+#include "cake_gg_ptx.cuh"
+
+namespace cakegg {
+int device_sms(int *sms);   // (cake_gg_capi.cu)
+}
+using namespace cakegg;
+
+namespace {
+
+constexpr int32_t kMaxTop = 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+// Eight values of a row in memory, as FP32.
+__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8])
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8])
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+struct CombineParams {
+    const void *rows;         // r [M, K]
+    const int32_t *position;  // [T, top_k]
+    const float *weight;      // [T, top_k] or null
+    void *out;                // y [T, K]
+    const void *d_out;        // dy [T, K]
+    void *d_rows;             // [M, K]
+    float *d_weight;          // [T, top_k] or null
+    int64_t M;
+    int32_t top_k, K;
+};
+
+// A block has a token (blockIdx.x) and 8 values a thread of a part of its row.
+template <typename RT, typename OT>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const CombineParams p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const int32_t k = int32_t(blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    if (k >= p.K) return;
+    const int32_t *position = p.position + t * p.top_k;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int j = 0; j < p.top_k; ++j) {
+        const int64_t m = position[j];
+        const float w = p.weight ? p.weight[t * p.top_k + j] : 1.0f;
+        if (m < 0 || m >= p.M) continue;
+        float v[8];
+        load8(static_cast<const RT *>(p.rows) + m * p.K + k, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+    }
+    store8(static_cast<OT *>(p.out) + t * p.K + k, sum);
+}
+
+// A block has a token; dy stays in registers for its rows where one pass of the
+// block covers it.
+template <typename RT, typename OT>
+__global__ void __launch_bounds__(256)
+    combine_grad_kernel(const CombineParams p)
+{
+    __shared__ float part[kMaxTop][8];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const int32_t *position = p.position + t * p.top_k;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = int(blockDim.x) * 8;
+    const OT *dy = static_cast<const OT *>(p.d_out) + t * p.K;
+    float g[8] = {};
+    if (int(threadIdx.x) * 8 < p.K) load8(dy + threadIdx.x * 8, g);
+    for (int j = 0; j < p.top_k; ++j) {
+        const int64_t m = position[j];
+        const bool row = m >= 0 && m < p.M;
+        const float w = p.weight ? p.weight[t * p.top_k + j] : 1.0f;
+        float dot = 0.0f;
+        if (row)
+            for (int k = int(threadIdx.x) * 8; k < p.K; k += step) {
+                float d[8];
+                if (k >= step) load8(dy + k, g);
+                if (p.d_weight) {
+                    float v[8];
+                    load8(static_cast<const RT *>(p.rows) + m * p.K + k, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = w * g[i];
+                store8(static_cast<RT *>(p.d_rows) + m * p.K + k, d);
+            }
+        if (p.K > step && int(threadIdx.x) * 8 < p.K) load8(dy + threadIdx.x * 8, g);
+        if (p.d_weight) {
+#pragma unroll
+            for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(kFull, dot, s);
+            if (lane == 0) part[j][warp] = dot;
+        }
+    }
+    if (!p.d_weight) return;
+    __syncthreads();
+    if (int(threadIdx.x) < p.top_k) {
+        float sum = 0.0f;
+        for (int w = 0; w < int(blockDim.x) / 32; ++w) sum += part[threadIdx.x][w];
+        p.d_weight[t * p.top_k + threadIdx.x] = sum;
+    }
+}
+
+bool pdl_enabled()
+{
+    const char *v = std::getenv("CAKE_GG_PDL");
+    return !(v && std::atoi(v) == 0);
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, int threads, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    if (pdl_enabled()) {
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    cfg.gridDim = dim3(unsigned(T), unsigned(parts), 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+int check(int64_t T, int64_t M, int32_t top_k, int32_t K, int rows_dtype, int out_dtype)
+{
+    if (T < 0 || T > INT32_MAX || M < 0 || M > INT32_MAX || top_k < 1 || top_k > kMaxTop || K < 1) return CAKE_GG_ERR_INVALID_ARG;
+    if ((rows_dtype != CAKE_GG_BF16 && rows_dtype != CAKE_GG_FP32) || (out_dtype != CAKE_GG_BF16 && out_dtype != CAKE_GG_FP32))
+        return CAKE_GG_ERR_UNSUPPORTED;
+    if (K % 8 != 0) return CAKE_GG_ERR_ALIGNMENT;
+    if (K > 1 << 20) return CAKE_GG_ERR_OVERFLOW;
+    return CAKE_GG_OK;
+}
+
+// Threads of a block for rows of K values, 8 a thread: whole warps, up to 256.
+int threads_for(int32_t K)
+{
+    const int n = (K / 8 + 31) / 32 * 32;
+    return n > 256 ? 256 : n;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cake_gg_combine_rows(int64_t T, int64_t M, int32_t top_k, int32_t K, const void *rows, int rows_dtype, const int32_t *position,
+                         const float *weight, void *out, int out_dtype, void *stream)
+{
+    int rc = check(T, M, top_k, K, rows_dtype, out_dtype);
+    if (rc != CAKE_GG_OK) return rc;
+    if (T == 0) return CAKE_GG_OK;
+    if ((M > 0 && !rows) || !position || !out) return CAKE_GG_ERR_INVALID_ARG;
+    if (!aligned(rows, 16) || !aligned(out, 16) || !aligned(position, 4) || !aligned(weight, 4)) return CAKE_GG_ERR_ALIGNMENT;
+    int sms;
+    if ((rc = device_sms(&sms)) != CAKE_GG_OK) return rc;
+    CombineParams p{};
+    p.rows = rows;
+    p.position = position;
+    p.weight = weight;
+    p.out = out;
+    p.M = M;
+    p.top_k = top_k;
+    p.K = K;
+    const int threads = threads_for(K), parts = (K / 8 + threads - 1) / threads;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (rows_dtype == CAKE_GG_BF16)
+        err = out_dtype == CAKE_GG_BF16 ? launch(combine_kernel<uint16_t, uint16_t>, p, T, parts, threads, s)
+                                        : launch(combine_kernel<uint16_t, float>, p, T, parts, threads, s);
+    else
+        err = out_dtype == CAKE_GG_BF16 ? launch(combine_kernel<float, uint16_t>, p, T, parts, threads, s)
+                                        : launch(combine_kernel<float, float>, p, T, parts, threads, s);
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+int cake_gg_combine_grad(int64_t T, int64_t M, int32_t top_k, int32_t K, const void *d_out, int out_dtype, const void *rows,
+                         int rows_dtype, const int32_t *position, const float *weight, void *d_rows, float *d_weight, void *stream)
+{
+    int rc = check(T, M, top_k, K, rows_dtype, out_dtype);
+    if (rc != CAKE_GG_OK) return rc;
+    if (T == 0) return CAKE_GG_OK;
+    if (!d_out || !position || (M > 0 && !d_rows) || (d_weight && M > 0 && !rows)) return CAKE_GG_ERR_INVALID_ARG;
+    if (!aligned(d_out, 16) || !aligned(rows, 16) || !aligned(d_rows, 16) || !aligned(position, 4) || !aligned(weight, 4) || !aligned(d_weight, 4))
+        return CAKE_GG_ERR_ALIGNMENT;
+    int sms;
+    if ((rc = device_sms(&sms)) != CAKE_GG_OK) return rc;
+    CombineParams p{};
+    p.d_out = d_out;
+    p.rows = rows;
+    p.position = position;
+    p.weight = weight;
+    p.d_rows = d_rows;
+    p.d_weight = d_weight;
+    p.M = M;
+    p.top_k = top_k;
+    p.K = K;
+    const int threads = threads_for(K);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (rows_dtype == CAKE_GG_BF16)
+        err = out_dtype == CAKE_GG_BF16 ? launch(combine_grad_kernel<uint16_t, uint16_t>, p, T, 1, threads, s)
+                                        : launch(combine_grad_kernel<uint16_t, float>, p, T, 1, threads, s);
+    else
+        err = out_dtype == CAKE_GG_BF16 ? launch(combine_grad_kernel<float, uint16_t>, p, T, 1, threads, s)
+                                        : launch(combine_grad_kernel<float, float>, p, T, 1, threads, s);
+    return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
+}
+
+}  // extern "C"
