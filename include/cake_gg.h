@@ -538,7 +538,7 @@ int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_
  *   softmax                dl_e = s_e ([e chosen] g_e - sum g s), every e
  *   sigmoid, renormalised  dl_j = r_j (1 - s_j) (g_j - sum g r)
  *   sigmoid                dl_j = s_j (1 - s_j) g_j
- * An expert outside [0, E) is nobody.  One kernel. */
+ * An expert outside [0, E) is nobody; those of a token differ.  One kernel. */
 int cake_gg_route_grad(int64_t T, int32_t E, int32_t top_k, int score, int renormalize, float scale,
                        const void *logits, int logits_dtype, int64_t row_stride, const int32_t *expert,
                        const float *d_weight, void *d_logits, void *stream);

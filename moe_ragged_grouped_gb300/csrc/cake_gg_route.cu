@@ -19,8 +19,7 @@
 // who chose it, so a token's place among them is a population count, in the
 // order of the tokens and the same on every run.  Up to kClusterTokens one cluster of
 // blocks does it all, counts read from one another's shared memory; more tokens
-// take a kernel that counts (its last block sums over the blocks) and one that
-// numbers.
+// take a kernel that counts and one that numbers.
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -43,9 +42,9 @@ constexpr int32_t kMaxExperts = 1024, kMaxTop = 32, kMaxGroups = 32;
 constexpr int64_t kMaxTokens = 1 << 24;
 constexpr int64_t kClusterTokens = 1024;       // what one cluster serves
 constexpr int kClusterBlocks = 8;
-constexpr int kBlockTokens = 1024;             // tokens of a block at most
+constexpr int kChunk = 1024;                   // tokens that a block numbers at a time, at most
 constexpr int kSms = 152;
-constexpr uint64_t kHeader = 256;              // the ticket at byte 4 (byte 0: the status word)
+constexpr uint64_t kHeader = 256;              // (as in the products' workspaces; its status word stays 0)
 constexpr unsigned kFull = 0xffffffffu;
 
 struct RouteParams {
@@ -53,10 +52,10 @@ struct RouteParams {
     const float *bias;
     int32_t *expert, *offsets, *rows, *position;
     float *weight;
-    uint32_t *ticket;
     int32_t *counts;          // [block][E]
     int64_t T, stride;
-    int32_t E, top_k, bf16, score, groups, top_groups, pair, renormalize, block_tokens;
+    int32_t E, top_k, bf16, score, groups, top_groups, pair, renormalize, block_tokens, chunk;
+    uint32_t div_top;         // 2^32 / top_k, rounded up
     uint32_t div_group;       // 2^20 / (E / groups), rounded up: e / (E / groups) for e < 1024
     float scale;
 };
@@ -271,10 +270,9 @@ __device__ __noinline__ int32_t choose_in_64_bits(const RouteParams &p, int64_t 
 // itself.
 constexpr float kSigmoidError = 0x1p-21f, kSoftmaxError = 0x1p-19f;
 
-// The experts of token t: lane j < top_k gets the j-th, and of it the logit, or
-// where the softmax is not renormalised the score.
+// The experts of token t by whole FP32 keys: lane j < top_k gets the j-th.
 template <int VPL>
-__device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int lane, float *of_it)
+__device__ __noinline__ int32_t choose_by_keys(const RouteParams &p, int64_t t, int lane)
 {
     float l[VPL];
     uint32_t key[VPL];
@@ -285,7 +283,7 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
     const bool by_score = p.bias || (p.pair && p.groups > 1);
     const float error = softmax ? kSoftmaxError : kSigmoidError;
     bool open = false;
-    if (by_score || (softmax && !p.renormalize)) {
+    if (by_score) {
         float s[VPL];
         scores(p, l, s, lane, &most, &sum);
 #pragma unroll
@@ -294,7 +292,7 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
             if (p.bias && e < p.E) s[i] += p.bias[e];
             key[i] = e < p.E ? order(s[i]) : 0;
         }
-        if (by_score && p.groups > 1) keep_groups(p, key, s, lane, error, &open);
+        if (p.groups > 1) keep_groups(p, key, s, lane, error, &open);
     }
     if (!p.bias) {
         const bool grouped = by_score;                           // (what is out has the key 0)
@@ -337,12 +335,256 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
             open = open || __any_sync(kFull, other);
         }
     }
-    if (open) mine = choose_in_64_bits<VPL>(p, t, lane);
-    *of_it = 0.0f;
-    if (lane < p.top_k) {
-        const float ml = load_logit(p, t, mine);
-        *of_it = softmax && !p.renormalize ? expf(ml - most) / sum : ml;
+    return open ? choose_in_64_bits<VPL>(p, t, lane) : mine;
+}
+
+// A lane's keys in descending order (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (p * 2) == (i + j + q) / (p * 2)) {
+                        const uint32_t a = max(k[i + j], k[i + j + q]), b = min(k[i + j], k[i + j + q]);
+                        k[i + j] = a, k[i + j + q] = b;
+                    }
+}
+
+// Packed keys of up to N experts: the upper bits of a key, which order as values
+// do, and below them the expert, counted down, so that one maximum gives both and
+// equals go to the lowest.  Experts beyond E are 0.
+template <int N>
+struct Packed {
+    static constexpr uint32_t kMask = uint32_t(N) - 1;           // (N a power of two)
+    // (a NaN without a sign above infinity, one with below: the caller looks at the largest)
+    static __device__ __forceinline__ uint32_t of(float v, int32_t e)
+    {
+        const uint32_t b = __float_as_uint(v + 0.0f);           // (-0 as 0)
+        return ((b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) & ~kMask) | (kMask - uint32_t(e));
     }
+    static __device__ __forceinline__ int32_t expert(uint32_t key) { return int32_t(kMask - (key & kMask)); }
+    // the largest value that a key may stand for
+    static __device__ __forceinline__ float most(uint32_t key) { return value_of(key | kMask); }
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504f;
+// How far scores by approximate instructions may be off, of the value: the argument
+// of the exponential rounds twice to 2^-24 of itself, which is 88 log2(e) at most
+// before it vanishes and counts e^-x x <= 0.37 times of the largest value, the
+// rest is 2^-21.
+constexpr float kFastError = 0x1p-19f;
+
+// Steps of a sum or maximum over the lanes below top_k (the others hold nothing).
+template <typename Op>
+__device__ __forceinline__ float over_chosen(const RouteParams &p, float v, Op op)
+{
+    for (int d = 16; d; d >>= 1)
+        if (d < p.top_k) v = op(v, __shfl_xor_sync(kFull, v, d));
+    return __shfl_sync(kFull, v, 0);
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_logits(const RouteParams &p, int64_t t, int lane, float (&l)[VPL])
+{
+    const float ninf = __uint_as_float(0xff800000u);
+    if (p.bf16) {
+        const uint16_t *row = static_cast<const uint16_t *>(p.logits) + t * p.stride + lane;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = i * 32 + lane < p.E ? __uint_as_float(uint32_t(row[i * 32]) << 16) : ninf;
+    } else {
+        const float *row = static_cast<const float *>(p.logits) + t * p.stride + lane;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = i * 32 + lane < p.E ? row[i * 32] : ninf;
+    }
+}
+
+// The experts of token t: lane j < top_k gets the j-th, and of it the logit, or
+// where the softmax is not renormalised the score.
+//
+// A first pass finds candidates by packed keys of scores from approximate
+// instructions; then the scores of the candidates alone are computed in FP32, one
+// a lane.  Where those are further apart than FP32's error, and the last chosen
+// from all that the candidate after it may stand for, the choice is certain; else
+// it is made again by whole keys.  (All scores in FP32 and whole keys, of which each
+// round takes a maximum and a minimum of indices, took 50 us for 16384 x 256.)
+template <int VPL>
+__device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int lane, const float (&l)[VPL], float *of_it)
+{
+    using Keys = Packed<VPL * 32>;
+    const bool softmax = p.score == CAKE_GG_SCORE_SOFTMAX, by_score = p.bias || (p.pair && p.groups > 1);
+    const float ninf = __uint_as_float(0xff800000u);
+    uint32_t key[VPL];
+    float most = 0.0f, sum = 1.0f;
+    if (softmax && (by_score || !p.renormalize)) {
+        float m = l[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+        most = warp_max(m);
+        float e[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) e[i] = exp2_fast((l[i] - most) * kLog2e);
+        sum = warp_sum(tree_sum(e));
+    }
+    // the score of a logit in FP32, of a candidate
+    auto score_of = [&](float v) { return softmax ? expf(v - most) / sum : sigmoid(v); };
+    const float error = softmax ? kSoftmaxError : kSigmoidError;
+    bool open = false;
+    if (by_score) {
+        const float over = softmax ? rcp_fast(sum) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int32_t e = i * 32 + lane;
+            const float s = softmax ? exp2_fast((l[i] - most) * kLog2e) * over : rcp_fast(1.0f + exp2_fast(l[i] * -kLog2e));
+            key[i] = e < p.E ? Keys::of(p.bias ? s + p.bias[e] : s, e) : 0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = i * 32 + lane < p.E ? Keys::of(l[i], i * 32 + lane) : 0;
+    }
+    unsigned kept = kFull;
+    if (p.groups > 1) {
+        // each group's largest two
+        const int32_t size = p.E / p.groups;
+        uint32_t first = 0, second = 0;                          // lane g: those of group g
+        auto group = [&](int g, uint32_t a, uint32_t b) {        // from each lane's largest two
+            const uint32_t m1 = __reduce_max_sync(kFull, a);
+            if (lane == g) first = m1;
+            if (p.pair) {
+                const uint32_t m2 = __reduce_max_sync(kFull, a == m1 ? b : a);
+                if (lane == g) second = m2;
+            }
+        };
+        if (size % 32 == 0) {                                    // whole registers
+            const int per = size / 32;
+            uint32_t a = 0, b = 0;
+            int in = 0, g = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                b = max(b, min(a, key[i]));
+                a = max(a, key[i]);
+                if (++in == per && g < p.groups) {
+                    group(g++, a, b);
+                    a = b = 0, in = 0;
+                }
+            }
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                uint32_t a = 0, b = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    const int32_t e = i * 32 + lane;
+                    const uint32_t k = e >= g * size && e < (g + 1) * size ? key[i] : 0;
+                    b = max(b, min(a, k));
+                    a = max(a, k);
+                }
+                group(g, a, b);
+            }
+        }
+        // a group's score: of the experts found, in FP32 (which are its largest for certain
+        // unless another comes as near as the line below allows)
+        float v = ninf, m = 0.0f, slack = 0.0f;
+        if (lane < p.groups) {
+            const int32_t e1 = Keys::expert(first), e2 = Keys::expert(second);
+            const float l1 = load_logit(p, t, e1);
+            float k1 = by_score ? score_of(l1) : l1;
+            if (p.bias) k1 += p.bias[e1];
+            v = k1, m = fabsf(k1), slack = Keys::most(first) - k1;
+            if (p.pair) {
+                float k2 = score_of(load_logit(p, t, e2));
+                if (p.bias) k2 += p.bias[e2];
+                v += k2, m += fabsf(k2), slack += Keys::most(second) - k2;
+            }
+            // (how much more than v the group's score may be: a packed key's lower bits)
+            slack = fmaxf(slack, 0.0f);
+        }
+        // a group's rank: how many are larger, or as large and before it
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const float o = __shfl_sync(kFull, v, g);
+            rank += o > v || (o == v && g < lane);
+        }
+        kept = __ballot_sync(kFull, lane < p.groups && rank < p.top_groups);
+        // certain where every group that stays is above every one that does not
+        const bool in = kept >> lane & 1u, out = lane < p.groups && !in;
+        const float worst = __uint_as_float(0x7f800000u);
+        float low = in ? v : worst, high = out ? v + slack : ninf, size_of = m;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            low = fminf(low, __shfl_xor_sync(kFull, low, d));
+            high = fmaxf(high, __shfl_xor_sync(kFull, high, d));
+            size_of = fmaxf(size_of, __shfl_xor_sync(kFull, size_of, d));
+        }
+        const bool nan = __any_sync(kFull, lane < p.groups && !(v - v == 0.0f));   // (NaNs and infinities go the long way)
+        open = nan || (p.top_groups < p.groups && !(low - high > (by_score ? 4.0f * (error + kFastError) : 0.0f) + size_of * 0x1p-21f));
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const uint32_t e = uint32_t(i * 32 + lane);
+            if (!(kept >> (e * p.div_group >> 20) & 1u)) key[i] = 0;
+        }
+        if (by_score && !p.bias) {
+            // (within the groups that stay by the logits)
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (key[i]) key[i] = Keys::of(l[i], i * 32 + lane);
+        }
+    }
+    // the chosen, and the one after them: the largest of the lanes' first, whose lane
+    // goes on to its next
+    sort_down(key);
+    uint32_t mine_key = 0, after = 0;
+    for (int j = 0; j <= p.top_k; ++j) {
+        after = __reduce_max_sync(kFull, key[0]);
+        if (lane == j && j < p.top_k) mine_key = after;
+        const bool own = key[0] == after;
+#pragma unroll
+        for (int i = 0; i + 1 < VPL; ++i) key[i] = own ? key[i + 1] : key[i];
+        if (own) key[VPL - 1] = 0;
+    }
+    const bool in = lane < p.top_k;
+    int32_t mine = Keys::expert(in ? mine_key : Keys::kMask);
+    float ml = in ? load_logit(p, t, mine) : ninf, s = 0.0f;
+    // certain?
+    {
+        float k = ml, tol = 0.0f, past = 0.0f;
+        if (p.bias) {
+            const float b = in ? p.bias[mine] : 0.0f;
+            s = score_of(ml);
+            k = s + b;
+            tol = error * s + 0x1p-22f * (fabsf(k) + fabsf(b)) + (softmax ? error * 0.03f : 0.0f);
+            past = 2.0f * (error + kFastError) + 0x1p-21f * (fabsf(k) + fabsf(b) + 1.0f);
+        }
+        const float k1 = __shfl_down_sync(kFull, k, 1), tol1 = __shfl_down_sync(kFull, tol, 1);
+        const int32_t e1 = __shfl_down_sync(kFull, mine, 1);
+        bool sure = true;
+        if (lane + 1 < p.top_k) sure = k - k1 > tol + tol1 || (!p.bias && k == k1 && mine < e1);
+        else if (lane + 1 == p.top_k) sure = after == 0 ? k == k : k - Keys::most(after) > past;
+        // (a NaN comes first, or its sum is one)
+        if (lane == 0) sure = sure && k == k && sum == sum && mine_key <= (0xff800000u | Keys::kMask);
+        open = open || !__all_sync(kFull, sure);
+    }
+    if (open) {
+        mine = choose_by_keys<VPL>(p, t, lane);
+        ml = in ? load_logit(p, t, mine) : ninf;
+    }
+    *of_it = !in ? 0.0f : softmax && !p.renormalize ? expf(ml - most) / sum : ml;
     return mine;
 }
 
@@ -351,21 +593,26 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
 __device__ __forceinline__ float finish(const RouteParams &p, float v, int lane)
 {
     const bool in = lane < p.top_k;
-    if (p.score == CAKE_GG_SCORE_SOFTMAX) {
-        if (!p.renormalize) return v * p.scale;
-        // the softmax over the chosen; where all of them are -inf, nothing
-        const float m = warp_max(in ? v : __uint_as_float(0xff800000u));
-        const float e = in && m > __uint_as_float(0xff800000u) ? expf(v - m) : in && v != v ? v : 0.0f;
-        const float sum = warp_sum(e);
-        return sum == 0.0f ? 0.0f : e / sum * p.scale;
+    const float ninf = __uint_as_float(0xff800000u);
+    auto largest = [](float a, float b) { return fmaxf(a, b); };
+    auto plus = [](float a, float b) { return a + b; };
+    if (!p.renormalize) {
+        if (p.score == CAKE_GG_SCORE_SOFTMAX) return v * p.scale;
+        return in ? sigmoid(v) * p.scale : 0.0f;
     }
-    if (!p.renormalize) return in ? sigmoid(v) * p.scale : 0.0f;
-    // where all chosen logits are far below zero their sigmoids vanish, not their
-    // ratios: e^(l - m) / (1 + e^l) with m the largest of them, if below zero
-    const float m = fminf(warp_max(in ? v : __uint_as_float(0xff800000u)), 0.0f);
+    // (by the logits the first is the largest; a NaN is the last, and found by the sum)
+    const float most = p.bias ? over_chosen(p, in ? v : ninf, largest) : fmaxf(__shfl_sync(kFull, v, 0), ninf);
     float s = 0.0f;
-    if (in) s = v > 0.0f || v != v ? sigmoid(v) : m > __uint_as_float(0xff800000u) ? expf(v - m) / (1.0f + expf(v)) : 0.0f;
-    const float sum = warp_sum(s);
+    if (p.score == CAKE_GG_SCORE_SOFTMAX) {
+        // the softmax over the chosen; where all of them are -inf, nothing
+        s = in && most > ninf ? expf(v - most) : in && v != v ? v : 0.0f;
+    } else {
+        // where all chosen logits are far below zero their sigmoids vanish, not their
+        // ratios: e^(l - m) / (1 + e^l) with m the largest of them, if below zero
+        const float m = fminf(most, 0.0f);
+        if (in) s = v > 0.0f || v != v ? sigmoid(v) : m > ninf ? expf(v - m) / (1.0f + expf(v)) : 0.0f;
+    }
+    const float sum = over_chosen(p, s, plus);
     return sum == 0.0f ? 0.0f : s / sum * p.scale;
 }
 
@@ -383,26 +630,29 @@ __device__ __forceinline__ Shared shared_of(uint8_t *raw, const RouteParams &p)
 {
     Shared s;
     s.bits = reinterpret_cast<uint32_t *>(raw);
-    s.counts = reinterpret_cast<int32_t *>(s.bits + p.E * bit_words(p.block_tokens));
+    s.counts = reinterpret_cast<int32_t *>(s.bits + p.E * bit_words(p.chunk));
     s.base = s.counts + p.E;
     s.chosen = reinterpret_cast<uint16_t *>(s.base + p.E);
     return s;
 }
-__host__ __device__ size_t shared_bytes(int32_t E, int32_t top_k, int block_tokens)
+size_t shared_bytes(int32_t E, int32_t top_k, int chunk)
 {
-    return size_t(E) * bit_words(block_tokens) * 4 + size_t(E) * 8 + (size_t(block_tokens) * top_k * 2 + 15) / 16 * 16;
+    return size_t(E) * bit_words(chunk) * 4 + size_t(E) * 8 + (size_t(chunk) * top_k * 2 + 15) / 16 * 16;
 }
 
 // The block's tokens [t0, t0 + n): their experts and weights, and who chose whom.
 template <int VPL>
 __device__ __forceinline__ void choose_all(const RouteParams &p, const Shared &s, int64_t t0, int n)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, words = bit_words(p.block_tokens);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, words = bit_words(p.chunk);
+    float l[VPL];
+    if (warp < n) load_logits(p, t0 + warp, lane, l);
     for (int i = threadIdx.x; i < p.E * words; i += kThreads) s.bits[i] = 0;
     __syncthreads();
     for (int i = warp; i < n; i += kWarps) {
         float v;
-        const int32_t e = choose<VPL>(p, t0 + i, lane, &v);
+        const int32_t e = choose<VPL>(p, t0 + i, lane, l, &v);
+        if (i + kWarps < n) load_logits(p, t0 + i + kWarps, lane, l);   // (while this token's is finished)
         const float w = finish(p, v, lane);
         if (lane < p.top_k) {
             const int64_t at = (t0 + i) * p.top_k + lane;
@@ -420,7 +670,10 @@ __device__ __forceinline__ void choose_all(const RouteParams &p, const Shared &s
     }
 }
 
-// A token's place among those of the block that chose the same expert.
+// The token of the i-th choice of a chunk.
+__device__ __forceinline__ int token_of(const RouteParams &p, int i) { return p.top_k == 1 ? i : int(__umulhi(uint32_t(i), p.div_top)); }
+
+// A token's place among those of the chunk that chose the same expert.
 __device__ __forceinline__ int32_t place(const Shared &s, int words, int32_t e, int i)
 {
     const uint32_t *b = s.bits + e * words;
@@ -461,7 +714,7 @@ __global__ void __launch_bounds__(kThreads)
     const Shared s = shared_of(raw, p);
     grid_dependency_wait();
     grid_launch_dependents();
-    const int rank = int(blockIdx.x), blocks = int(gridDim.x), e = threadIdx.x, words = bit_words(p.block_tokens);
+    const int rank = int(blockIdx.x), blocks = int(gridDim.x), e = threadIdx.x, words = bit_words(p.chunk);
     const int64_t t0 = int64_t(rank) * p.block_tokens;
     const int n = int(t0 >= p.T ? 0 : p.T - t0 < p.block_tokens ? p.T - t0 : p.block_tokens);
     choose_all<VPL>(p, s, t0, n);
@@ -487,91 +740,84 @@ __global__ void __launch_bounds__(kThreads)
     if (rank == 0 && e == 0) p.offsets[p.E] = total;
     __syncthreads();
     for (int i = threadIdx.x; i < n * p.top_k; i += kThreads) {
-        const int32_t x = s.chosen[i], token = i / p.top_k, row = s.base[x] + place(s, words, x, token);
+        const int32_t x = s.chosen[i], token = token_of(p, i), row = s.base[x] + place(s, words, x, token);
         p.position[t0 * p.top_k + i] = row;
         p.rows[row] = int32_t(t0) + token;
     }
     if (blocks > 1) cluster_sync_all();                          // the others may still read this one's counts
 }
 
-// Experts, weights and places within the block (to `position`); the last block
-// turns the blocks' counts into where their rows of an expert begin.
+// Experts, weights and places within the block (to `position`), a chunk of its
+// tokens after the other, and its counts.
 template <int VPL>
 __global__ void __launch_bounds__(kThreads)
     route_count_kernel(const RouteParams p)
 {
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ bool last;
     const Shared s = shared_of(raw, p);
     grid_dependency_wait();
     grid_launch_dependents();
-    const int words = bit_words(p.block_tokens), blocks = int(gridDim.x);
-    const int64_t t0 = int64_t(blockIdx.x) * p.block_tokens;
-    const int n = int(p.T - t0 < p.block_tokens ? p.T - t0 : p.block_tokens);
-    choose_all<VPL>(p, s, t0, n);
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[int64_t(blockIdx.x) * p.E + e] = s.counts[e];
-    for (int i = threadIdx.x; i < n * p.top_k; i += kThreads)
-        p.position[t0 * p.top_k + i] = place(s, words, s.chosen[i], i / p.top_k);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.ticket, 1u) + 1u == gridDim.x;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    // `parts` threads an expert, each a run of blocks: their sums, then the runs of
-    // each expert and the experts before it
+    const int words = bit_words(p.chunk);
+    const int64_t begin = int64_t(blockIdx.x) * p.block_tokens, end = min(p.T, begin + p.block_tokens);
+    for (int e = threadIdx.x; e < p.E; e += kThreads) s.base[e] = 0;
+    for (int64_t t0 = begin; t0 < end; t0 += p.chunk) {
+        const int n = int(min(int64_t(p.chunk), end - t0));
+        choose_all<VPL>(p, s, t0, n);
+        for (int i = threadIdx.x; i < n * p.top_k; i += kThreads) {
+            const int32_t x = s.chosen[i];
+            p.position[t0 * p.top_k + i] = s.base[x] + place(s, words, x, token_of(p, i));
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kThreads) s.base[e] += s.counts[e];
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[int64_t(blockIdx.x) * p.E + e] = s.base[e];
+}
+
+// Places within a block to rows: each block sums the counts of all blocks and of
+// those before it (at most 152 of them; one block that does it for all while the
+// others wait took 6 us for 256 experts, this 2), `parts` threads an expert.
+__global__ void __launch_bounds__(kThreads)
+    route_number_kernel(const RouteParams p)
+{
+    __shared__ int32_t sums[kThreads], before[kThreads], base[kMaxExperts];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int blocks = int(gridDim.x), me = int(blockIdx.x);
     int parts = 1;
     while (parts * 2 * p.E <= kThreads) parts *= 2;
     const int e = int(threadIdx.x) % p.E, part = int(threadIdx.x) / p.E, run = (blocks + parts - 1) / parts;
-    const int b0 = part * run, b1 = min(b0 + run, blocks);
-    const bool mine = part < parts;
-    int32_t sum = 0;
-    if (mine) {
+    int32_t all = 0, mine = 0;
+    if (part < parts) {
+        const int b0 = part * run, b1 = min(b0 + run, blocks);
 #pragma unroll 8
-        for (int b = b0; b < b1; ++b) sum += __ldcg(&p.counts[int64_t(b) * p.E + e]);
-    }
-    int32_t *sums = reinterpret_cast<int32_t *>(raw + shared_bytes(p.E, p.top_k, p.block_tokens));   // [part][expert]
-    if (mine) sums[part * p.E + e] = sum;
-    __syncthreads();
-    int32_t all = 0, before = 0;
-    if (mine)
-        for (int q = 0; q < parts; ++q) {
-            const int32_t c = sums[q * p.E + e];
-            if (q < part) before += c;
+        for (int b = b0; b < b1; ++b) {
+            const int32_t c = p.counts[int64_t(b) * p.E + e];
             all += c;
+            mine += b < me ? c : 0;
         }
+        sums[threadIdx.x] = all;
+        before[threadIdx.x] = mine;
+    }
+    __syncthreads();
+    all = mine = 0;
+    if (part == 0)
+        for (int q = 0; q < parts; ++q) all += sums[q * p.E + e], mine += before[q * p.E + e];
     int32_t total;
     const int32_t first = block_scan(part == 0 ? all : 0, &total);
     if (part == 0) {
-        s.base[e] = first;
-        p.offsets[e] = first;
+        base[e] = first + mine;
+        if (me == 0) p.offsets[e] = first;
     }
-    if (threadIdx.x == 0) p.offsets[p.E] = total, *p.ticket = 0;
+    if (me == 0 && threadIdx.x == 0) p.offsets[p.E] = total;
     __syncthreads();
-    if (mine) {
-        int32_t at = s.base[e] + before;
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) {
-            int32_t *c = &p.counts[int64_t(b) * p.E + e];
-            const int32_t v = __ldcg(c);
-            __stcg(c, at);
-            at += v;
-        }
+    const int64_t t0 = int64_t(me) * p.block_tokens, n = min(int64_t(p.block_tokens), p.T - t0) * p.top_k;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+        const int64_t at = t0 * p.top_k + i;
+        const int32_t row = p.position[at] + base[p.expert[at]];
+        p.position[at] = row;
+        p.rows[row] = int32_t(t0) + int32_t(p.top_k == 1 ? i : i / p.top_k);
     }
-}
-
-__global__ void __launch_bounds__(256)
-    route_number_kernel(const RouteParams p)
-{
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.T * p.top_k) return;
-    const int32_t t = int32_t(i / p.top_k);
-    const int32_t row = p.position[i] + p.counts[int64_t(t / p.block_tokens) * p.E + p.expert[i]];
-    p.position[i] = row;
-    p.rows[row] = t;
 }
 
 // ---------------------------------------------------------------- backward
@@ -614,13 +860,24 @@ __global__ void __launch_bounds__(256)
         float l[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) l[i] = i * 32 + lane < p.E ? load_logit(r, t, i * 32 + lane) : ninf;
-        scores(r, l, s, lane, &most, &sum);
+        float m = l[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+        most = warp_max(m);
+        float x[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = x[i] = i * 32 + lane < p.E ? expf(l[i] - most) : 0.0f;
+        sum = warp_sum(tree_sum(x));
+        const float over = 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] *= over;
     }
     const float ml = e >= 0 ? load_logit(r, t, e) : ninf;
     float d = 0.0f, inner = 0.0f;
     if (whole) {
-        d = e >= 0 ? g * (expf(ml - most) / sum) : 0.0f;
-        inner = warp_sum(d);
+        const float q = e >= 0 ? expf(ml - most) / sum : 0.0f;
+        inner = warp_sum(g * q);
+        d = q * (g - inner);
     } else if (p.score == CAKE_GG_SCORE_SOFTMAX) {
         const float m = warp_max(ml);
         const float x = e >= 0 && m > ninf ? expf(ml - m) : 0.0f;
@@ -635,25 +892,16 @@ __global__ void __launch_bounds__(256)
         inner = warp_sum(g * w);
         d = w * sigmoid(-ml) * (g - inner);
     } else if (e >= 0) d = g * sigmoid(ml) * sigmoid(-ml);
-    // the lane's experts of the row, and what the lanes of the chosen have for them
-    float out[VPL];
+    // the row, then over it the chosen
+    auto put = [&](int32_t x, float v) {
+        if (p.bf16) static_cast<uint16_t *>(p.d_logits)[t * p.E + x] = uint16_t(pack_bf16x2(v, 0.0f) & 0xffffu);
+        else static_cast<float *>(p.d_logits)[t * p.E + x] = v;
+    };
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = whole ? -s[i] * inner : 0.0f;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int32_t x = __shfl_sync(kFull, e, j);
-        const float v = __shfl_sync(kFull, d, j);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (x == i * 32 + lane) out[i] += v;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int32_t x = i * 32 + lane;
-        if (x < p.E) {
-            if (p.bf16) static_cast<uint16_t *>(p.d_logits)[t * p.E + x] = uint16_t(pack_bf16x2(out[i], 0.0f) & 0xffffu);
-            else static_cast<float *>(p.d_logits)[t * p.E + x] = out[i];
-        }
-    }
+    for (int i = 0; i < VPL; ++i)
+        if (i * 32 + lane < p.E) put(i * 32 + lane, whole ? -s[i] * inner : 0.0f);
+    __syncwarp();
+    if (e >= 0) put(e, d);
 }
 
 // ---------------------------------------------------------------- host
@@ -722,7 +970,7 @@ int check_scores(int logits_dtype, int64_t stride, int32_t E, int score)
 }
 
 // Blocks and their tokens: as few blocks of one cluster as have a warp for a token,
-// or one for each multiprocessor.
+// or one for each multiprocessor, which holds the bits of a chunk of its tokens.
 void choose_blocks(cake_gg_route_plan_t *pl)
 {
     const int64_t T = pl->T;
@@ -730,9 +978,7 @@ void choose_blocks(cake_gg_route_plan_t *pl)
     int64_t blocks = pl->cluster ? (T + kWarps - 1) / kWarps : kSms;
     if (pl->cluster && blocks > kClusterBlocks) blocks = kClusterBlocks;
     if (blocks < 1) blocks = 1;
-    int64_t per = (T + blocks - 1) / blocks;
-    if (per > kBlockTokens) per = kBlockTokens;
-    if (per < 1) per = 1;
+    const int64_t per = T == 0 ? 1 : (T + blocks - 1) / blocks;
     pl->block_tokens = int32_t(per);
     pl->blocks = int32_t(T == 0 ? 1 : (T + per - 1) / per);
 }
@@ -792,7 +1038,6 @@ int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_
     p.rows = rows;
     p.position = position;
     p.weight = weight;
-    p.ticket = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + 4);
     p.counts = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kHeader);
     p.T = pl.T;
     p.stride = row_stride;
@@ -806,15 +1051,17 @@ int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_
     p.renormalize = op.renormalize != 0;
     p.scale = op.scale;
     p.block_tokens = pl.block_tokens;
+    p.chunk = pl.block_tokens < kChunk ? pl.block_tokens : kChunk;
+    p.div_top = uint32_t((uint64_t(1) << 32) / uint32_t(pl.top_k) + ((uint64_t(1) << 32) % uint32_t(pl.top_k) != 0));
     const int32_t size = pl.E / op.groups;
     p.div_group = uint32_t(((1 << 20) + size - 1) / size);
-    const size_t shared = shared_bytes(pl.E, pl.top_k, pl.block_tokens);
+    const size_t shared = shared_bytes(pl.E, pl.top_k, p.chunk);
     cudaError_t err = with_experts(pl.E, [&](auto vpl) {
         constexpr int VPL = decltype(vpl)::value;
         return pl.cluster ? launch(route_cluster_kernel<VPL>, p, pl.blocks, kThreads, shared, pl.blocks, s)
-                          : launch(route_count_kernel<VPL>, p, pl.blocks, kThreads, shared + kThreads * 4, 1, s);
+                          : launch(route_count_kernel<VPL>, p, pl.blocks, kThreads, shared, 1, s);
     });
-    if (err == cudaSuccess && !pl.cluster) err = launch(route_number_kernel, p, (pl.T * pl.top_k + 255) / 256, 256, 0, 1, s);
+    if (err == cudaSuccess && !pl.cluster) err = launch(route_number_kernel, p, pl.blocks, kThreads, 0, 1, s);
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 

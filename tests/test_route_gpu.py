@@ -80,7 +80,7 @@ def make(T, E, seed, dtype="fp32", spread=2.0):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,top_k", [
     (1, 1, 1), (1, 8, 2), (1, 32, 4), (2, 5, 5), (3, 33, 8), (31, 64, 6), (32, 32, 32), (33, 100, 3), (64, 256, 8), (65, 200, 31),
-    (257, 12, 1), (300, 1024, 32), (1023, 40, 4), (1024, 512, 8), (1025, 256, 8), (1500, 7, 3), (2049, 1000, 9), (5000, 64, 6),
+    (257, 12, 1), (300, 1024, 32), (1023, 40, 4), (1024, 512, 8), (1025, 256, 8), (1500, 7, 3), (2049, 1000, 9), (5000, 64, 6), (400001, 6, 2),
 ])
 def test_route(T, E, top_k, score, dtype):
     logits, bias = make(T, E, T + E, dtype)
