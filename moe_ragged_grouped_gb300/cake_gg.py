@@ -10,6 +10,7 @@ PyTorch is used only for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import typing
 
@@ -973,38 +974,71 @@ def empty_routing(T, E, top_k, device) -> Routing:
                    i32(T, top_k))
 
 
+_real_types = None
+
+
+def _real_torch():
+    """Names of the real types, torch's float32 and int32."""
+    global _real_types
+    if _real_types is None:
+        import torch
+        _real_types = {torch.bfloat16: "bf16", torch.float32: "fp32"}, torch.float32, torch.int32
+    return _real_types
+
+
 def _real_name(tensor, name):
     """ "bf16" or "fp32"."""
-    import torch
-    kind = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(tensor.dtype)
+    kind = _real_torch()[0].get(tensor.dtype)
     if kind is None:
         raise TypeError(f"{name} is {tensor.dtype}: bfloat16 or float32 are taken")
     return kind
 
 
 def _logits(logits):
-    """The type of router logits [T, E] whose rows are dense (they may lie apart)."""
+    """The type of router logits [T, E] whose rows are dense (they may lie apart), T, E and how far apart."""
     kind = _real_name(logits, "logits")
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits are [T, E]")
-    if (logits.shape[1] > 1 and logits.stride(1) != 1) or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):
+    T, E = shape
+    apart, step = logits.stride()
+    if (E > 1 and step != 1) or (T > 1 and apart < E):
         raise ValueError("the rows of logits are not dense")
-    return kind
+    return kind, T, E, apart if T > 1 else E
 
 
-def _row_stride(logits):
-    return int(logits.stride(0)) if logits.shape[0] > 1 else int(logits.shape[1])
+def _is(tensor, dtype, shape, on):
+    """Whether this is a dense tensor of this type and shape on CUDA device `on` (_need() says what is not)."""
+    return tensor.dtype is dtype and tensor.shape == shape and tensor.get_device() == on and tensor.is_contiguous()
 
 
 def _here(tensor):
-    if tensor.get_device() < 0 or tensor.get_device() != _current_device():
+    """The index of a tensor's device, which has to be the current one."""
+    on = tensor.get_device()
+    if on < 0 or on != _current_device():
         _refuse_device(tensor)
+    return on
+
+
+def _handle(stream, on):
+    """A stream's handle (none: the current one's)."""
+    if stream is None:
+        return _current_stream(on)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _score_code(score):
     if score not in SCORES:
         raise ValueError(f"score is 'softmax' or 'sigmoid', got {score!r}")
     return SCORES[score]
+
+
+@functools.lru_cache(maxsize=64)
+def _route_options(score, groups, top_groups, group_score, renormalize, scale):
+    if group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score is 'max' or 'top2', got {group_score!r}")
+    return CakeGGRouteOptions(_score_code(score), int(groups), int(groups if top_groups is None else top_groups),
+                              GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
 
 
 def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True,
@@ -1023,33 +1057,37 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     (cake_gg_route_plan), the workspace and the outputs (empty_routing) once.  All
     tensors are on the current CUDA device; stream as in int8_gemm.
     """
-    import torch
-    kind = _logits(logits)
-    T, E = int(logits.shape[0]), int(logits.shape[1])
-    if group_score not in GROUP_SCORES:
-        raise ValueError(f"group_score is 'max' or 'top2', got {group_score!r}")
-    options = CakeGGRouteOptions(_score_code(score), int(groups), int(groups if top_groups is None else top_groups),
-                                 GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
+    kind, T, E, apart = _logits(logits)
+    options = _route_options(score, groups, top_groups, group_score, renormalize, scale)
     if plan is None:
         plan = cake_gg_route_plan(T, E, top_k)
     elif (plan.T, plan.E, plan.top_k) != (T, E, top_k):
         raise ValueError("the plan is another problem's")
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E,), logits.device)
+    _, f32, i32 = _real_types
+    on, many = logits.get_device(), (T, top_k)
+    if bias is not None and not _is(bias, f32, (E,), on):
+        _need(bias, "bias", f32, (E,), logits.device)
     if out is not None:
-        for tensor, name, dtype, shape in zip(out, Routing._fields, (torch.int32, torch.float32) + 3 * (torch.int32,),
-                                              ((T, top_k), (T, top_k), (E + 1,), (T * top_k,), (T, top_k))):
-            _need(tensor, name, dtype, shape, logits.device)
+        expert, weight, offsets, rows, position = out
+        if not (_is(expert, i32, many, on) and _is(weight, f32, many, on) and _is(offsets, i32, (E + 1,), on)
+                and _is(rows, i32, (T * top_k,), on) and _is(position, i32, many, on)):
+            for tensor, name, dtype, shape in zip(out, Routing._fields, (i32, f32, i32, i32, i32),
+                                                  (many, many, (E + 1,), (T * top_k,), many)):
+                _need(tensor, name, dtype, shape, logits.device)
     _here(logits)
     if out is None:
-        i32, f32 = torch.int32, torch.float32
         out = Routing(*(_result(shape, dtype, logits.device, stream) for shape, dtype in
-                        (((T, top_k), i32), ((T, top_k), f32), ((E + 1,), i32), ((T * top_k,), i32), ((T, top_k), i32))))
+                        ((many, i32), (many, f32), ((E + 1,), i32), ((T * top_k,), i32), (many, i32))))
+        expert, weight, offsets, rows, position = out
     if workspace is None:
         workspace = _scratch(plan, logits.device, stream)
-    elif workspace.device != logits.device:
+    elif workspace.get_device() != on:
         raise ValueError(f"workspace is on {workspace.device}, not on {logits.device}")
-    rc = cake_gg_route(plan, options, logits, kind, _row_stride(logits), bias, *out, workspace, stream=stream)
+    # (the call of cake_gg_route() above, without its conversions: a few tokens' time is the host's)
+    rc = (_lib or load_library()).cake_gg_route(
+        ctypes.byref(plan), ctypes.byref(options), logits.data_ptr(), DTYPES[kind], apart,
+        None if bias is None else bias.data_ptr(), expert.data_ptr(), weight.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+        position.data_ptr(), workspace.data_ptr(), workspace.nbytes, _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_route")
     return out
@@ -1061,36 +1099,38 @@ def route_grad(logits, expert, d_weight, score="softmax", renormalize=True, scal
     expert, score, renormalize and scale are route()'s.  The choice of experts and
     the bias have no gradient.  All tensors are on the current CUDA device.
     """
-    import torch
-    kind = _logits(logits)
-    T, E = int(logits.shape[0]), int(logits.shape[1])
-    _score_code(score)
+    kind, T, E, apart = _logits(logits)
+    code = _score_code(score)
     if expert.dim() != 2:
         raise ValueError("expert is [T, top_k]")
-    top_k = int(expert.shape[1])
-    _need(expert, "expert", torch.int32, (T, top_k), logits.device)
-    _need(d_weight, "d_weight", torch.float32, (T, top_k), logits.device)
-    if out is not None:
+    _, f32, i32 = _real_types
+    on, top_k = logits.get_device(), expert.shape[1]
+    if not (_is(expert, i32, (T, top_k), on) and _is(d_weight, f32, (T, top_k), on)):
+        _need(expert, "expert", i32, (T, top_k), logits.device)
+        _need(d_weight, "d_weight", f32, (T, top_k), logits.device)
+    if out is not None and not _is(out, logits.dtype, (T, E), on):
         _need(out, "out", logits.dtype, (T, E), logits.device)
     _here(logits)
     if out is None:
         out = _result((T, E), logits.dtype, logits.device, stream)
-    rc = cake_gg_route_grad(T, E, top_k, score, renormalize, scale, logits, kind, _row_stride(logits), expert, d_weight, out,
-                            stream)
+    rc = (_lib or load_library()).cake_gg_route_grad(T, E, top_k, code, bool(renormalize), scale, logits.data_ptr(), DTYPES[kind],
+                                                     apart, expert.data_ptr(), d_weight.data_ptr(), out.data_ptr(),
+                                                     _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_route_grad")
     return out
 
 
-def _need_position(position, weight, device):
-    """T and top_k of int32 [T, top_k] positions and their float32 weights."""
-    import torch
-    if position.dim() != 2:
+def _need_position(position, weight, like, on):
+    """T and top_k of int32 [T, top_k] positions and their float32 weights, on the device of `like`."""
+    _, f32, i32 = _real_types
+    shape = position.shape
+    if len(shape) != 2:
         raise ValueError("position is [T, top_k]")
-    shape = tuple(position.shape)
-    _need(position, "position", torch.int32, shape, device)
-    if weight is not None:
-        _need(weight, "weight", torch.float32, shape, device)
+    if not (_is(position, i32, shape, on) and (weight is None or _is(weight, f32, shape, on))):
+        _need(position, "position", i32, tuple(shape), like.device)
+        if weight is not None:
+            _need(weight, "weight", f32, tuple(shape), like.device)
     return shape
 
 
@@ -1105,16 +1145,20 @@ def combine_rows(rows, position, weight=None, out_dtype="bf16", out=None, stream
     kind = _real_name(rows, "rows")
     if rows.dim() != 2:
         raise ValueError("rows are [M, K]")
-    M, K = int(rows.shape[0]), int(rows.shape[1])
-    _need(rows, "rows", rows.dtype, (M, K), rows.device)
-    T, top_k = _need_position(position, weight, rows.device)
-    out_type = _torch_out_dtype(out_dtype)
-    if out is not None:
+    (M, K), on = rows.shape, rows.get_device()
+    if not rows.is_contiguous():
+        raise ValueError("rows is not contiguous")
+    T, top_k = _need_position(position, weight, rows, on)
+    code = _dtype_code(out_dtype)
+    out_type = (_i8_types or _i8_torch())[4][code == CAKE_GG_FP32]
+    if out is not None and not _is(out, out_type, (T, K), on):
         _need(out, "out", out_type, (T, K), rows.device)
     _here(rows)
     if out is None:
         out = _result((T, K), out_type, rows.device, stream)
-    rc = cake_gg_combine_rows(T, M, top_k, K, rows, kind, position, weight, out, out_dtype, stream)
+    rc = (_lib or load_library()).cake_gg_combine_rows(T, M, top_k, K, rows.data_ptr(), DTYPES[kind], position.data_ptr(),
+                                                       None if weight is None else weight.data_ptr(), out.data_ptr(), code,
+                                                       _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_rows")
     return out
@@ -1127,25 +1171,28 @@ def combine_grad(d_out, rows, position, weight, out=None, stream=None):
     of another number are refused; rows that it does not name keep what `out`, or
     fresh memory, holds).
     """
-    import torch
     kind, out_kind = _real_name(rows, "rows"), _real_name(d_out, "d_out")
     if rows.dim() != 2 or d_out.dim() != 2:
         raise ValueError("rows are [M, K], d_out is [T, K]")
     if weight is None:
         raise ValueError("without weights the rows' gradient is gather_rows(d_out, position)")
-    M, K = int(rows.shape[0]), int(rows.shape[1])
-    _need(rows, "rows", rows.dtype, (M, K), rows.device)
-    T, top_k = _need_position(position, weight, rows.device)
-    _need(d_out, "d_out", d_out.dtype, (T, K), rows.device)
+    (M, K), on = rows.shape, rows.get_device()
+    if not rows.is_contiguous():
+        raise ValueError("rows is not contiguous")
+    T, top_k = _need_position(position, weight, rows, on)
+    if not _is(d_out, d_out.dtype, (T, K), on):
+        _need(d_out, "d_out", d_out.dtype, (T, K), rows.device)
     if M != T * top_k:
         raise ValueError(f"{M} rows for {T} x {top_k} positions")
-    if out is not None:
+    if out is not None and not _is(out, rows.dtype, (M, K), on):
         _need(out, "out", rows.dtype, (M, K), rows.device)
     _here(rows)
     if out is None:
         out = _result((M, K), rows.dtype, rows.device, stream)
-    d_weight = _result((T, top_k), torch.float32, rows.device, stream)
-    rc = cake_gg_combine_grad(T, M, top_k, K, d_out, out_kind, rows, kind, position, weight, out, d_weight, stream)
+    d_weight = _result((T, top_k), weight.dtype, rows.device, stream)
+    rc = (_lib or load_library()).cake_gg_combine_grad(T, M, top_k, K, d_out.data_ptr(), DTYPES[out_kind], rows.data_ptr(),
+                                                       DTYPES[kind], position.data_ptr(), weight.data_ptr(), out.data_ptr(),
+                                                       d_weight.data_ptr(), _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_grad")
     return out, d_weight
@@ -1159,17 +1206,20 @@ def gather_rows(X, position, out=None, stream=None):
     kind = _real_name(X, "X")
     if X.dim() != 2:
         raise ValueError("X is [T, K]")
-    _need(X, "X", X.dtype, tuple(X.shape), X.device)
-    T, top_k = _need_position(position, None, X.device)
-    if X.shape[0] != T:
-        raise ValueError(f"{X.shape[0]} tokens for {T} positions")
-    M, K = T * top_k, int(X.shape[1])
-    if out is not None:
+    (tokens, K), on = X.shape, X.get_device()
+    if not X.is_contiguous():
+        raise ValueError("X is not contiguous")
+    T, top_k = _need_position(position, None, X, on)
+    if tokens != T:
+        raise ValueError(f"{tokens} tokens for {T} positions")
+    M = T * top_k
+    if out is not None and not _is(out, X.dtype, (M, K), on):
         _need(out, "out", X.dtype, (M, K), X.device)
     _here(X)
     if out is None:
         out = _result((M, K), X.dtype, X.device, stream)
-    rc = cake_gg_combine_grad(T, M, top_k, K, X, kind, None, kind, position, None, out, None, stream)
+    rc = (_lib or load_library()).cake_gg_combine_grad(T, M, top_k, K, X.data_ptr(), DTYPES[kind], None, DTYPES[kind],
+                                                       position.data_ptr(), None, out.data_ptr(), None, _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_grad")
     return out
