@@ -506,7 +506,7 @@ typedef struct cake_gg_route_options {
 typedef struct cake_gg_route_plan {
     int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
     int32_t E;               /* experts, 1 .. 1024                                  */
-    int64_t T;               /* tokens, 0 .. 2^24                                   */
+    int64_t T;               /* tokens, 0 .. 2^23                                   */
     int32_t top_k;           /* experts of a token, 1 .. min(E, 32)                 */
     /* chosen by cake_gg_route_plan() */
     int32_t cluster;         /* 1: one cluster of blocks, in one launch             */
@@ -515,7 +515,7 @@ typedef struct cake_gg_route_plan {
 } cake_gg_route_plan_t;
 
 /* Fill *plan.  Pure host arithmetic.  CAKE_GG_ERR_INVALID_ARG for sizes out of
- * range, CAKE_GG_ERR_OVERFLOW for T > 2^24 or T top_k >= 2^31. */
+ * range, CAKE_GG_ERR_OVERFLOW for T > 2^23 or T top_k >= 2^31. */
 int cake_gg_route_plan(cake_gg_route_plan_t *plan, int64_t T, int32_t E, int32_t top_k);
 
 /* Route.  Device pointers, aligned to their elements (bias null: none); the

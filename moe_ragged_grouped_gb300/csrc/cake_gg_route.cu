@@ -39,8 +39,8 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int32_t kMaxExperts = 1024, kMaxTop = 32, kMaxGroups = 32;
-constexpr int64_t kMaxTokens = 1 << 24;
-constexpr int64_t kClusterTokens = 1024;       // what one cluster serves
+constexpr int64_t kMaxTokens = 1 << 23;        // (a block's tokens are below 2^16)
+constexpr int64_t kClusterTokens = 256;        // what one cluster serves
 constexpr int kClusterBlocks = 8;
 constexpr int kChunk = 1024;                   // tokens that a block numbers at a time, at most
 constexpr int kSms = 152;
@@ -52,7 +52,7 @@ struct RouteParams {
     const float *bias;
     int32_t *expert, *offsets, *rows, *position;
     float *weight;
-    int32_t *counts;          // [block][E]
+    uint16_t *counts;         // [block][E rounded up to 8]
     int64_t T, stride;
     int32_t E, top_k, bf16, score, groups, top_groups, pair, renormalize, block_tokens, chunk;
     uint32_t div_top;         // 2^32 / top_k, rounded up
@@ -423,7 +423,9 @@ __device__ __forceinline__ void load_logits(const RouteParams &p, int64_t t, int
 // instructions; then the scores of the candidates alone are computed in FP32, one
 // a lane.  Where those are further apart than FP32's error, and the last chosen
 // from all that the candidate after it may stand for, the choice is certain; else
-// it is made again by whole keys.  (All scores in FP32 and whole keys, of which each
+// all that may be among the chosen are compared in 64 bits, one a lane, and where
+// these are more than a warp has lanes, or groups are as near, or NaNs are among
+// them, it is made again by whole keys.  (All scores in FP32 and whole keys, of which each
 // round takes a maximum and a minimum of indices, took 50 us for 16384 x 256.)
 template <int VPL>
 __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int lane, const float (&l)[VPL], float *of_it)
@@ -549,36 +551,70 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
     // the chosen, and the one after them: the largest of the lanes' first, whose lane
     // goes on to its next
     sort_down(key);
-    uint32_t mine_key = 0, after = 0;
-    for (int j = 0; j <= p.top_k; ++j) {
-        after = __reduce_max_sync(kFull, key[0]);
-        if (lane == j && j < p.top_k) mine_key = after;
-        const bool own = key[0] == after;
+    auto next = [&] {
+        const uint32_t m = __reduce_max_sync(kFull, key[0]);
+        const bool own = key[0] == m;
 #pragma unroll
         for (int i = 0; i + 1 < VPL; ++i) key[i] = own ? key[i + 1] : key[i];
         if (own) key[VPL - 1] = 0;
+        return m;
+    };
+    uint32_t mine_key = 0, after = 0;
+    for (int j = 0; j <= p.top_k; ++j) {
+        after = next();
+        if (lane == j && j < p.top_k) mine_key = after;
     }
     const bool in = lane < p.top_k;
     int32_t mine = Keys::expert(in ? mine_key : Keys::kMask);
-    float ml = in ? load_logit(p, t, mine) : ninf, s = 0.0f;
+    float ml = in ? load_logit(p, t, mine) : ninf, k = ml, past = 0.0f;
     // certain?
+    bool sure = true;
     {
-        float k = ml, tol = 0.0f, past = 0.0f;
+        float tol = 0.0f;
         if (p.bias) {
-            const float b = in ? p.bias[mine] : 0.0f;
-            s = score_of(ml);
+            const float b = in ? p.bias[mine] : 0.0f, s = score_of(ml);
             k = s + b;
             tol = error * s + 0x1p-22f * (fabsf(k) + fabsf(b)) + (softmax ? error * 0.03f : 0.0f);
             past = 2.0f * (error + kFastError) + 0x1p-21f * (fabsf(k) + fabsf(b) + 1.0f);
         }
         const float k1 = __shfl_down_sync(kFull, k, 1), tol1 = __shfl_down_sync(kFull, tol, 1);
         const int32_t e1 = __shfl_down_sync(kFull, mine, 1);
-        bool sure = true;
         if (lane + 1 < p.top_k) sure = k - k1 > tol + tol1 || (!p.bias && k == k1 && mine < e1);
         else if (lane + 1 == p.top_k) sure = after == 0 ? k == k : k - Keys::most(after) > past;
-        // (a NaN comes first, or its sum is one)
-        if (lane == 0) sure = sure && k == k && sum == sum && mine_key <= (0xff800000u | Keys::kMask);
-        open = open || !__all_sync(kFull, sure);
+        // (a NaN comes first, or the sum is one; then nothing is certain)
+        if (lane == 0 && !(k == k && sum == sum && mine_key <= (0xff800000u | Keys::kMask))) open = true;
+        open = __any_sync(kFull, open);
+    }
+    if (!open && !__all_sync(kFull, sure)) {
+        // All that may be among the chosen, one a lane, compared in 64 bits.
+        float line = in ? k - past : __uint_as_float(0x7f800000u);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) line = fminf(line, __shfl_xor_sync(kFull, line, d));
+        int n = p.top_k;
+        while (n < 32 && after != 0 && !(Keys::most(after) < line)) {
+            if (lane == n) mine_key = after;
+            ++n;
+            after = next();
+        }
+        // (a softmax needs its sum in 64 bits, and NaNs and infinities their order)
+        open = (p.bias && softmax) || (after != 0 && !(Keys::most(after) < line)) || !(line - line == 0.0f);
+        if (!open) {
+            const int32_t e = Keys::expert(lane < n ? mine_key : Keys::kMask);
+            double by = double(load_logit(p, t, e));
+            if (p.bias) by = sigmoid(by) + double(p.bias[e]);
+            int rank = 0;
+            for (int i = 0; i < n; ++i) {
+                const double o = __shfl_sync(kFull, by, i);
+                const int32_t oe = __shfl_sync(kFull, e, i);
+                rank += o > by || (o == by && oe < e);
+            }
+            for (int i = 0; i < n; ++i) {
+                const int to = __shfl_sync(kFull, rank, i);
+                const int32_t oe = __shfl_sync(kFull, e, i);
+                if (lane == to) mine = oe;
+            }
+            ml = in ? load_logit(p, t, mine) : ninf;
+        }
     }
     if (open) {
         mine = choose_by_keys<VPL>(p, t, lane);
@@ -747,6 +783,8 @@ __global__ void __launch_bounds__(kThreads)
     if (blocks > 1) cluster_sync_all();                          // the others may still read this one's counts
 }
 
+__host__ __device__ constexpr int32_t count_pitch(int32_t E) { return (E + 7) / 8 * 8; }
+
 // Experts, weights and places within the block (to `position`), a chunk of its
 // tokens after the other, and its counts.
 template <int VPL>
@@ -771,51 +809,62 @@ __global__ void __launch_bounds__(kThreads)
         for (int e = threadIdx.x; e < p.E; e += kThreads) s.base[e] += s.counts[e];
         __syncthreads();
     }
-    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[int64_t(blockIdx.x) * p.E + e] = s.base[e];
+    uint16_t *counts = p.counts + int64_t(blockIdx.x) * count_pitch(p.E);
+    for (int e = threadIdx.x; e < count_pitch(p.E); e += kThreads) counts[e] = e < p.E ? uint16_t(s.base[e]) : 0;
 }
 
 // Places within a block to rows: each block sums the counts of all blocks and of
-// those before it (at most 152 of them; one block that does it for all while the
-// others wait took 6 us for 256 experts, this 2), `parts` threads an expert.
+// those before it (at most 152 of them), eight experts a load, all threads.  (One
+// block that does it for all while the others wait took 6 us for 256 experts; all of
+// them, an expert a load, 7.)
 __global__ void __launch_bounds__(kThreads)
     route_number_kernel(const RouteParams p)
 {
-    __shared__ int32_t sums[kThreads], before[kThreads], base[kMaxExperts];
+    __shared__ int32_t sums[kMaxExperts], before[kMaxExperts];   // of expert 8 v + i at i * (vectors) + v
     grid_dependency_wait();
     grid_launch_dependents();
-    const int blocks = int(gridDim.x), me = int(blockIdx.x);
-    int parts = 1;
-    while (parts * 2 * p.E <= kThreads) parts *= 2;
-    const int e = int(threadIdx.x) % p.E, part = int(threadIdx.x) / p.E, run = (blocks + parts - 1) / parts;
-    int32_t all = 0, mine = 0;
+    const int blocks = int(gridDim.x), me = int(blockIdx.x), vectors = count_pitch(p.E) / 8;
+    const int64_t t0 = int64_t(me) * p.block_tokens, n = min(int64_t(p.block_tokens), p.T - t0) * p.top_k, at0 = t0 * p.top_k;
+    // (the first of the thread's choices, while the counts come)
+    int32_t position = 0, expert = 0;
+    if (threadIdx.x < n) position = p.position[at0 + threadIdx.x], expert = p.expert[at0 + threadIdx.x];
+    for (int e = threadIdx.x; e < vectors * 8; e += kThreads) sums[e] = before[e] = 0;
+    __syncthreads();
+    const int v = int(threadIdx.x) % vectors, part = int(threadIdx.x) / vectors, parts = kThreads / vectors;
     if (part < parts) {
-        const int b0 = part * run, b1 = min(b0 + run, blocks);
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) {
-            const int32_t c = p.counts[int64_t(b) * p.E + e];
-            all += c;
-            mine += b < me ? c : 0;
+        int32_t all[8] = {}, mine[8] = {};
+#pragma unroll 5
+        for (int b = part; b < blocks; b += parts) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(p.counts + int64_t(b) * (vectors * 8) + v * 8);
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t lo = int32_t(w[i] & 0xffffu), hi = int32_t(w[i] >> 16);
+                all[2 * i] += lo, all[2 * i + 1] += hi;
+                if (b < me) mine[2 * i] += lo, mine[2 * i + 1] += hi;
+            }
         }
-        sums[threadIdx.x] = all;
-        before[threadIdx.x] = mine;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            atomicAdd(&sums[i * vectors + v], all[i]);           // (whole numbers: their order changes nothing)
+            atomicAdd(&before[i * vectors + v], mine[i]);
+        }
     }
     __syncthreads();
-    all = mine = 0;
-    if (part == 0)
-        for (int q = 0; q < parts; ++q) all += sums[q * p.E + e], mine += before[q * p.E + e];
+    const int e = int(threadIdx.x), at = e % 8 * vectors + e / 8;
+    const int32_t all = e < p.E ? sums[at] : 0, mine = e < p.E ? before[at] : 0;
     int32_t total;
-    const int32_t first = block_scan(part == 0 ? all : 0, &total);
-    if (part == 0) {
-        base[e] = first + mine;
+    const int32_t first = block_scan(all, &total);               // (a barrier inside)
+    if (e < p.E) {
+        before[at] = first + mine;
         if (me == 0) p.offsets[e] = first;
     }
-    if (me == 0 && threadIdx.x == 0) p.offsets[p.E] = total;
+    if (me == 0 && e == 0) p.offsets[p.E] = total;
     __syncthreads();
-    const int64_t t0 = int64_t(me) * p.block_tokens, n = min(int64_t(p.block_tokens), p.T - t0) * p.top_k;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t at = t0 * p.top_k + i;
-        const int32_t row = p.position[at] + base[p.expert[at]];
-        p.position[at] = row;
+        if (i >= kThreads) position = p.position[at0 + i], expert = p.expert[at0 + i];
+        const int32_t row = position + before[expert % 8 * vectors + expert / 8];
+        p.position[at0 + i] = row;
         p.rows[row] = int32_t(t0) + int32_t(p.top_k == 1 ? i : i / p.top_k);
     }
 }
@@ -975,7 +1024,7 @@ void choose_blocks(cake_gg_route_plan_t *pl)
 {
     const int64_t T = pl->T;
     pl->cluster = T <= kClusterTokens;
-    int64_t blocks = pl->cluster ? (T + kWarps - 1) / kWarps : kSms;
+    int64_t blocks = pl->cluster ? (T + 3) / 4 : kSms;
     if (pl->cluster && blocks > kClusterBlocks) blocks = kClusterBlocks;
     if (blocks < 1) blocks = 1;
     const int64_t per = T == 0 ? 1 : (T + blocks - 1) / blocks;
@@ -983,7 +1032,7 @@ void choose_blocks(cake_gg_route_plan_t *pl)
     pl->blocks = int32_t(T == 0 ? 1 : (T + per - 1) / per);
 }
 
-uint64_t workspace_of(const cake_gg_route_plan_t &pl) { return kHeader + (pl.cluster ? 0 : uint64_t(pl.blocks) * uint64_t(pl.E) * 4); }
+uint64_t workspace_of(const cake_gg_route_plan_t &pl) { return kHeader + (pl.cluster ? 0 : uint64_t(pl.blocks) * uint64_t(count_pitch(pl.E)) * 2); }
 
 }  // namespace
 
@@ -1038,7 +1087,7 @@ int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_
     p.rows = rows;
     p.position = position;
     p.weight = weight;
-    p.counts = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kHeader);
+    p.counts = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + kHeader);
     p.T = pl.T;
     p.stride = row_stride;
     p.E = pl.E;
