@@ -19,6 +19,16 @@ forward's output is never read and its GEMM is not launched (the pages credit
 their earlier PR #8114 with skipping that recompute).  With early stop off
 the recompute runs the forward GEMM, as stock checkpointing does.
 
+Around the products of an expert layer in training:
+
+    r = route(logits, top_k, ...)              # a Routing; its weights have gradients
+    X = gather_rows(x, r.position)             # tokens to rows in expert order
+    y = combine_rows(Y, r.weight, r.position)  # rows back to tokens, weighted
+
+Their gradients are kernels as well: the rows' gradient of gather_rows is the sum
+that combine_rows makes, that of combine_rows the copy that gather_rows makes,
+weighted, so nothing is added by atomics and every run gives the same bits.
+
 This module only marshals arguments: every pass runs in libcake_gg.so.  Plans
 and workspaces are cached per (pass, shape, dtype, mode, device, stream) and
 reused across calls, as the workspace contract allows (zero-filled once,
@@ -149,3 +159,103 @@ def checkpointed_grouped_linear(X, W, offsets, early_stop=True, deterministic=Tr
     with set_checkpoint_early_stop(bool(early_stop)):
         return checkpoint(grouped_linear, X, W, offsets, deterministic, wgrad_dtype,
                           use_reentrant=False, context_fn=contexts)
+
+
+def _make_row_functions():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    names = {torch.bfloat16: "bf16", torch.float32: "fp32"}
+
+    def dense(G):
+        G = G.contiguous()
+        return G if G.dtype in names else G.float()
+
+    class Route(torch.autograd.Function):
+        """route(): the weights' gradient goes to the logits."""
+
+        @staticmethod
+        def forward(ctx, logits, top_k, bias, options):
+            out = gg.route(logits, top_k, bias=bias, **options)
+            ctx.save_for_backward(logits, out.expert)
+            ctx.options = {k: options[k] for k in ("score", "renormalize", "scale")}
+            ctx.mark_non_differentiable(out.expert, out.offsets, out.rows, out.position)
+            ctx.set_materialize_grads(False)
+            return tuple(out)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, _, d_weight, *__):
+            if d_weight is None:
+                return None, None, None, None
+            logits, expert = ctx.saved_tensors
+            return gg.route_grad(logits, expert, d_weight.contiguous().float(), **ctx.options), None, None, None
+
+    class Gather(torch.autograd.Function):
+        """gather_rows(): backwards each token takes the sum of its rows' gradients."""
+
+        @staticmethod
+        def forward(ctx, X, position):
+            ctx.save_for_backward(position)
+            ctx.dtype = X.dtype
+            return gg.gather_rows(X, position)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, G):
+            return gg.combine_rows(dense(G), ctx.saved_tensors[0], out_dtype=names[ctx.dtype]), None
+
+    class Combine(torch.autograd.Function):
+        """combine_rows(): backwards each row takes its weight's share, each weight a dot product."""
+
+        @staticmethod
+        def forward(ctx, rows, weight, position, out_dtype):
+            # (the rows' gradient has to cover every row)
+            if rows.shape[0] != position.numel():
+                raise ValueError(f"{rows.shape[0]} rows for {position.numel()} positions")
+            ctx.save_for_backward(rows, weight, position)
+            return gg.combine_rows(rows, position, weight, out_dtype=out_dtype)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, G):
+            rows, weight, position = ctx.saved_tensors
+            d_rows, d_weight = gg.combine_grad(dense(G), rows, position, weight)
+            return d_rows, d_weight, None, None
+
+    return Route, Gather, Combine
+
+
+_row_fns = None
+
+
+def _row_functions():
+    global _row_fns
+    if _row_fns is None:
+        _row_fns = _make_row_functions()
+    return _row_fns
+
+
+def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True, scale=1.0):
+    """cake_gg.route() whose weights are differentiable in the logits (bf16 or fp32).
+
+    The choice of experts has no gradient, and neither has the bias, which only
+    takes part in it.
+    """
+    options = dict(score=score, groups=groups, top_groups=top_groups, group_score=group_score, renormalize=renormalize,
+                   scale=scale)
+    return gg.Routing(*_row_functions()[0].apply(logits, top_k, bias, options))
+
+
+def gather_rows(X, position):
+    """Rows [T * top_k, K] in expert order of tokens X [T, K], differentiable in X; position is a Routing's."""
+    return _row_functions()[1].apply(X, position)
+
+
+def combine_rows(rows, weight, position, out_dtype="bf16"):
+    """Tokens [T, K] as weighted sums of their rows [T * top_k, K], differentiable in rows and weight.
+
+    weight float32 [T, top_k] and position are a Routing's, which names each row
+    once (rows of another number are refused).
+    """
+    return _row_functions()[2].apply(rows, weight, position, out_dtype)

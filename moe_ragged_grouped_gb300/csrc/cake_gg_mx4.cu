@@ -456,6 +456,12 @@ int64_t row_tiles(const cake_gg_mx4_plan_t &pl, int nt)
 // within one of the GPU's groups of them, whose sizes differ from part to part.
 int cluster_sms(int splits) { return splits <= 2 ? kSms : splits <= 6 ? 132 : 104; }
 
+// Whether a copy can number the scale tiles of a pair's rows.
+bool pair_fits(const cake_gg_mx4_plan_t &pl, int nt)
+{
+    return mx4_slots(pl.M_max, pl.E, nt) * ((pl.K + 127) / 128) * mx4_row_atoms(nt) <= INT32_MAX;
+}
+
 // The shape, from a model of its time in nanoseconds: waves of units over the
 // multiprocessors (152, or 76 pairs), the stages of a unit, or the reading of the
 // weights where that is longer; the storing of the last unit, the laying out of a
@@ -476,6 +482,7 @@ void choose(cake_gg_mx4_plan_t *pl)
     auto consider = [&](int pair, int nt, int splits) {
         const int64_t units = row_tiles(*pl, nt) * ((pl->N + 128 * pair - 1) / (128 * pair));
         if (splits > 1 && (units * splits > cluster_sms(splits) || n_kb < 2 * splits)) return;
+        if (pair == 2 && !pair_fits(*pl, nt)) return;
         const int64_t waves = (units * pair + kSms - 1) / kSms;
         int64_t ns = waves * ((n_kb + splits - 1) / splits) * (200 + nt * (pair == 2 ? 4 : 7) / 10);
         ns = (ns > weights ? ns : weights) + 12 * nt;
@@ -505,7 +512,7 @@ bool plan_ok(const cake_gg_mx4_plan_t &pl)
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= kMx4RowsMost && pl.tile_rows % 32 == 0 &&
            pl.stages >= kStagesLeast && pl.stages <= kMx4StagesMost && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 255) / 256 &&   // (a stage for every CTA)
-           (pl.pair == 1 || mx4_slots(pl.M_max, pl.E, pl.tile_rows) * ((pl.K + 127) / 128) <= INT32_MAX / 4) &&
+           (pl.pair == 1 || pair_fits(pl, pl.tile_rows)) &&
            mx4_mma_smem(pl.pair, pl.tile_rows, pl.stages, pl.splits, pl.E) <= kMx4SmemLimit;
 }
 

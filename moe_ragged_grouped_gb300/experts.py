@@ -1,4 +1,4 @@
-"""A mixture-of-experts layer in serving, with 8-bit weights and tokens.
+"""Mixture-of-experts layers in serving, with 8-bit or 4-bit weights and tokens.
 
     layer = Int8Experts(router, gate_up, down, top_k)
     y = layer(x)                               # x [T, K] bf16 -> y [T, K] bf16
@@ -18,6 +18,12 @@ largest size that it needed there and the two products' outputs of its last
 call, which the next call of as many tokens writes again; y is a new tensor each
 call.  Threads may call one layer at the same time, on one stream or several.
 A call that is being captured in a CUDA graph has buffers of the graph's own.
+
+    layer = Mx4Experts(router, gate_up, down, top_k, score="sigmoid", bias=bias, groups=8, top_groups=4)
+
+is the same layer in 4-bit floating point with a power of two for each block of
+32 values, in four calls of the library: the router's logits, the routing (with
+all of cake_gg.route's choices), the two products, the rows' way back.
 """
 from __future__ import annotations
 
@@ -53,8 +59,10 @@ class Int8Experts:
         self.down_q, self.down_s = self._quantise(down)
         self._keep_nothing()
 
+    _plans = staticmethod(_plans)
+
     def _keep_nothing(self):
-        self._planned = functools.lru_cache(maxsize=256)(functools.partial(_plans, self.E, self.K, self.F, self.top_k))
+        self._planned = functools.lru_cache(maxsize=256)(functools.partial(self._plans, self.E, self.K, self.F, self.top_k))
         self._mine = threading.local()   # a thread's calls may interleave with another's on one stream
 
     def __getstate__(self):
@@ -70,13 +78,18 @@ class Int8Experts:
         q, s = gg.quantize_rows(w.reshape(E * N, K).contiguous())
         return q.view(E, N, K), s.view(E, N)
 
+    def _kept(self, device):
+        """What the calling thread keeps for its current stream."""
+        if torch.cuda.is_current_stream_capturing():
+            return {}                      # (what is kept may be replaced while the graph still replays)
+        return self._mine.__dict__.setdefault((str(device), torch.cuda.current_stream(device).cuda_stream), {})
+
     def _for(self, T, device):
         """A call's plans, each with its workspace, and the two products' outputs."""
-        route, up, down = self._planned(T)
-        if torch.cuda.is_current_stream_capturing():
-            mine = {}                      # (what is kept may be replaced while the graph still replays)
-        else:
-            mine = self._mine.__dict__.setdefault((str(device), torch.cuda.current_stream(device).cuda_stream), {})
+        return self._buffers(T, device, self._kept(device))
+
+    def _buffers(self, T, device, mine):
+        route, up, down = self._planned(T)[:3]
         if "route" not in mine:
             mine["route"] = gg.make_workspace(route, device)         # (the same size for every T)
         # the products share a workspace: each call's kernels wait for those of the one before
@@ -97,6 +110,7 @@ class Int8Experts:
         return (route, mine["route"]), (up, work, h), (down, work, out)
 
     def _check(self, x):
+        """The layer's tokens, or a refusal that names what is wrong."""
         if x.dtype != torch.bfloat16:
             raise TypeError(f"x is {x.dtype}: torch.bfloat16 is needed")
         if x.dim() != 2 or x.shape[1] != self.K:
@@ -137,24 +151,95 @@ class Int8Experts:
         return (out[at].view(T, self.top_k, self.K) * weight[:, :, None]).sum(dim=1).to(x.dtype)
 
 
+def _mx4_plans(E, K, F, top_k, T):
+    """Plans of a 4-bit layer's call of T tokens: the router's, the two products' and the routing's."""
+    M = T * top_k
+    return (gg.cake_gg_router_plan(T, (E + 7) // 8 * 8, K), gg.cake_gg_mx4_plan(E, M, T, 2 * F, K, "bf16", None, "bf16"),
+            gg.cake_gg_mx4_plan(E, M, M, K, F, "bf16", "silu_mul", "fp32"), gg.cake_gg_route_plan(T, E, top_k))
+
+
+class Mx4Experts(Int8Experts):
+    """Experts in 4-bit floating point: router [E, K] fp32, gate_up [E, 2 F, K] and down [E, K, F] bf16 or fp32 (CUDA).
+
+    K and F are multiples of 32.  score, bias, groups, top_groups, group_score,
+    renormalize and scale are cake_gg.route's.
+    """
+
+    def __init__(self, router, gate_up, down, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max",
+                 renormalize=True, scale=1.0):
+        E, F2, K = gate_up.shape
+        if K % 32 or F2 % 64:
+            raise ValueError("K and F are multiples of 32")
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,)):
+            raise ValueError(f"bias is {bias.dtype} {tuple(bias.shape)}: float32 [{E}] is needed")
+        self.bias = bias
+        self.options = dict(score=score, groups=groups, top_groups=top_groups, group_score=group_score,
+                            renormalize=renormalize, scale=scale)
+        super().__init__(router, gate_up, down, top_k)
+
+    _plans = staticmethod(_mx4_plans)
+
+    @staticmethod
+    def _quantise(w):
+        return gg.quantize_mx4(w.contiguous())
+
+    def _for(self, T, device):
+        """A call's plans, each with its workspace, the two products' outputs, and the routing's."""
+        mine = self._kept(device)
+        products = self._buffers(T, device, mine)
+        plan = self._planned(T)[3]
+        if "choose" not in mine or mine["choose"].numel() < plan.workspace_bytes:
+            mine["choose"] = gg.make_workspace(plan, device)
+        if mine.get("routed") != T:
+            mine["routing"] = gg.empty_routing(T, self.E, self.top_k, device)
+            mine["routed"] = T
+        return (*products, (plan, mine["choose"], mine["routing"]))
+
+    def route(self, x):
+        """Experts [T, top_k] and weights [T, top_k] of each token."""
+        self._check(x)
+        if x.shape[0] == 0:
+            return gg.empty_routing(0, self.E, self.top_k, x.device)[:2]
+        route, _, _, choose = self._for(x.shape[0], x.device)
+        return tuple(t.clone() for t in self._routing(x, route, choose)[:2])
+
+    def _routing(self, x, route, choose):
+        logits = gg.router_gemm(x.float(), self.router, plan=route[0], workspace=route[1], check=False)
+        plan, work, out = choose
+        return gg.route(logits[:, :self.E], self.top_k, bias=self.bias, plan=plan, workspace=work, out=out, **self.options)
+
+    def __call__(self, x, check=False):
+        self._check(x)
+        if x.shape[0] == 0:
+            return torch.empty_like(x)
+        route, (up, work, h), (down, _, out), choose = self._for(x.shape[0], x.device)
+        r = self._routing(x, route, choose)
+        gg.mx4_gemm(x, self.up_q, self.up_s, offsets=r.offsets, rows=r.rows, out=h, plan=up, workspace=work, check=check)
+        gg.mx4_gemm(h, self.down_q, self.down_s, offsets=r.offsets, act="silu_mul", out_dtype="fp32", out=out, plan=down,
+                    workspace=work, check=check)
+        return gg.combine_rows(out, r.position, r.weight)
+
+
 def main():
-    """Run a small layer on the GPU and compare it with the same layer in FP32 on the quantised weights."""
+    """Run small layers on the GPU and compare each with the same layer in FP32 on the quantised weights."""
     g = torch.Generator(device="cuda").manual_seed(0)
     E, K, F, top_k = 8, 1024, 512, 2
     rand = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
-    layer = Int8Experts(rand(E, K) / K ** 0.5, rand(E, 2 * F, K) / K ** 0.5, rand(E, K, F) / F ** 0.5, top_k)
-    for T in (1, 16, 700):
-        x = rand(T, K).to(torch.bfloat16)
-        y = layer(x, check=True)
-        expert, weight = layer.route(x)
-        up, down = layer.up_q.float() * layer.up_s[..., None], layer.down_q.float() * layer.down_s[..., None]
-        want = torch.zeros(T, K, device="cuda")
-        for e in range(E):
-            t, j = (expert == e).nonzero(as_tuple=True)
-            gate, lin = (x[t].float() @ up[e].T).chunk(2, dim=1)
-            want[t] += weight[t, j, None] * ((torch.nn.functional.silu(gate) * lin) @ down[e].T)
-        err = float((y.float() - want).norm() / want.norm())
-        print(f"{T} tokens: relative difference from the unquantised activations {err:.4f}")
+    weights = rand(E, K) / K ** 0.5, rand(E, 2 * F, K) / K ** 0.5, rand(E, K, F) / F ** 0.5
+    for kind, values in ((Int8Experts, lambda q, s: q.float() * s[..., None]), (Mx4Experts, gg.mx4_values)):
+        layer = kind(*weights, top_k)
+        up, down = values(layer.up_q, layer.up_s), values(layer.down_q, layer.down_s)
+        for T in (1, 16, 700):
+            x = rand(T, K).to(torch.bfloat16)
+            y = layer(x, check=True)
+            expert, weight = layer.route(x)
+            want = torch.zeros(T, K, device="cuda")
+            for e in range(E):
+                t, j = (expert == e).nonzero(as_tuple=True)
+                gate, lin = (x[t].float() @ up[e].T).chunk(2, dim=1)
+                want[t] += weight[t, j, None] * ((torch.nn.functional.silu(gate) * lin) @ down[e].T)
+            err = float((y.float() - want).norm() / want.norm())
+            print(f"{kind.__name__}, {T} tokens: relative difference from the unquantised activations {err:.4f}")
 
 
 if __name__ == "__main__":

@@ -340,3 +340,101 @@ def test_no_rows():
     x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
     assert gg.mx4_gemm(x, q, s, offsets=offsets_of([0, 0])).shape == (0, 64)
     assert [t.shape[0] for t in gg.quantize_mx4(x)] == [0, 0]
+
+
+# ---------------------------------------------------------------- how a call behaves
+
+
+def test_every_shape_of_the_kernel(monkeypatch):
+    """Single CTAs, pairs, divided reductions, all tile sizes: ragged experts, routed and not, against 64 bits."""
+    import torch
+    sizes, N, K = [130, 0, 2, 257, 31], 392, 1056
+    E, M = len(sizes), sum(sizes)
+    q, s = weights(E, N, K, 4)
+    w = dense_values(q, s)
+    x, xs = gg.quantize_mx4(randn((M, K), 1))
+    rows = torch.from_numpy(np.random.default_rng(0).permutation(M).astype(np.int32)).cuda()
+    for pair, nt, splits in [(1, nt, 1) for nt in range(32, 193, 32)] + [(2, nt, 1) for nt in range(32, 193, 32)] + [(1, 32, 2), (1, 64, 3), (1, 32, 5)]:
+        for name, value in (("PAIR", pair), ("ROWS_PER_TILE", nt), ("SPLITS", splits)):
+            monkeypatch.setenv("CAKE_GG_MX4_" + name, str(value))
+        for out_dtype in ("bf16", "fp32"):
+            for r in (None, rows):
+                got = gg.mx4_gemm(x, q, s, xs=xs, offsets=offsets_of(sizes), rows=r, out_dtype=out_dtype)
+                check(got, values(x, xs), w, sizes, r, out_dtype)
+
+
+@pytest.mark.parametrize("pair", [1, 2])
+def test_same_bits_on_every_run_and_under_every_cap(pair, monkeypatch):
+    import torch
+    monkeypatch.setenv("CAKE_GG_MX4_PAIR", str(pair))
+    sizes, N, K = [40, 300, 0, 77], 520, 800
+    q, s = weights(4, N, K, 1)
+    x = randn((sum(sizes), K), 2)
+    first = gg.mx4_gemm(x, q, s, offsets=offsets_of(sizes), out_dtype="fp32")
+    for cap in [0] * 5 + [1, 2, 7, 100]:
+        assert torch.equal(first, gg.mx4_gemm(x, q, s, offsets=offsets_of(sizes), out_dtype="fp32", max_sms=cap))
+
+
+@pytest.mark.parametrize("pair,splits", [(1, 1), (1, 2), (2, 1)])
+def test_a_lost_copy_times_out(pair, splits, monkeypatch):
+    """Every wait ends, the status says so, and the next call is right."""
+    monkeypatch.setenv("CAKE_GG_MX4_PAIR", str(pair))
+    monkeypatch.setenv("CAKE_GG_MX4_ROWS_PER_TILE", "64")
+    monkeypatch.setenv("CAKE_GG_MX4_SPLITS", str(splits))
+    T, N, K = 50, 264, 1056
+    q, s = weights(1, N, K, 1)
+    x, xs = gg.quantize_mx4(randn((T, K), 2))
+    plan = gg.cake_gg_mx4_plan(1, T, T, N, K, "mx4", None, "fp32")
+    assert (plan.pair, plan.splits) == (pair, splits)
+    plan.timeout_ns = 100_000_000
+    work = gg.make_workspace(plan, "cuda")
+    plan.debug_flags = gg.CAKE_GG_DEBUG_DROP_FIRST_LOAD
+    with pytest.raises(gg.CakeGGError) as err:
+        gg.mx4_gemm(x, q[0], s[0], xs=xs, out_dtype="fp32", plan=plan, workspace=work)
+    assert err.value.code == gg.CAKE_GG_ERR_TIMEOUT
+    plan.debug_flags = 0
+    got = gg.mx4_gemm(x, q[0], s[0], xs=xs, out_dtype="fp32", plan=plan, workspace=work)
+    check(got, values(x, xs), dense_values(q, s), [T], None, "fp32")
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_captured_on_another_stream(T):
+    """A graph of quantising and product, replayed on new tokens and weights' rows."""
+    import torch
+    N, K = 264, 544
+    sizes = [T // 3, T - T // 3]
+    q, s = weights(2, N, K, 3)
+    xs = [randn((T, K), 5 + i) for i in range(3)]
+    want = [gg.mx4_gemm(x, q, s, offsets=offsets_of(sizes)) for x in xs]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        x, off, out = xs[0].clone(), offsets_of(sizes), torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+        plan = gg.cake_gg_mx4_plan(2, T, T, N, K)
+        work = gg.make_workspace(plan, "cuda")
+        run = lambda: gg.mx4_gemm(x, q, s, offsets=off, out=out, plan=plan, workspace=work, check=False)  # noqa: E731
+        run()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            run()
+            run()
+        for i in (1, 2, 0):
+            x.copy_(xs[i])
+            graph.replay()
+            stream.synchronize()
+            assert torch.equal(out, want[i])
+
+
+def test_weights_past_four_billion_values():
+    """Codes past 2^31 bytes: the last expert's, whose rows are the last."""
+    import torch
+    E, N, K = 70, 8192, 8192
+    q = torch.zeros((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((E, *gg._mx4_tiles(N, K)), dtype=torch.uint8, device="cuda")
+    q[-1], s[-1] = (t[0] for t in weights(1, N, K, 1))
+    x, xs = gg.quantize_mx4(randn((20, K), 2))
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[-1] = 20
+    got = gg.mx4_gemm(x, q, s, xs=xs, offsets=off.cuda(), out_dtype="fp32")
+    check(got, values(x, xs), dense_values(q[-1:], s[-1:]), [20], None, "fp32")
