@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -80,10 +81,35 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
 
 // ---------------------------------------------------------------- token pass
 
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Four pairs of values as E2M1 codes, to nearest, ties to even, held at 6; the
 // first of a pair in the low half of its byte.
 __device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv)
 {
+    float w[8];
+    const uint64_t by = pair2(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) unpair2(mul2(pair2(v[i], v[i + 1]), by), w[i], w[i + 1]);
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -92,8 +118,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv)
         "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
-        : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv), "f"(v[4] * inv), "f"(v[5] * inv),
-          "f"(v[6] * inv), "f"(v[7] * inv));
+        : "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "f"(w[4]), "f"(w[5]), "f"(w[6]), "f"(w[7]));
     return r;
 }
 
@@ -107,6 +132,25 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits)
 __device__ __forceinline__ float scale_inverse(uint32_t byte)
 {
     return byte == 255 ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+
+// The bits of the largest magnitude of eight values; a NaN's if there is one.
+__device__ __forceinline__ uint32_t largest8(const float (&v)[8])
+{
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(v[0]), "f"(v[1]), "f"(v[2]));
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[3]), "f"(v[4]));
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[5]), "f"(v[6]));
+    asm("max.NaN.abs.f32 %0, %0, %1, %1;" : "+f"(m) : "f"(v[7]));
+    return __float_as_uint(m);
+}
+__device__ __forceinline__ float least8(const float (&v)[8])
+{
+    float m;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(v[0]), "f"(v[1]), "f"(v[2]));
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[3]), "f"(v[4]));
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[5]), "f"(v[6]));
+    return fminf(m, v[7]);
 }
 
 __device__ __forceinline__ uint32_t block_max(uint32_t m)    // over the four lanes of a block
@@ -125,15 +169,17 @@ constexpr float kFastError = 0x1p-18f, kSlowError = 0x1p-20f, kFastFrom = -40.0f
 
 __device__ __forceinline__ void gate_fast(const float (&g)[8], const float (&u)[8], float (&h)[8])
 {
+    const uint64_t log2e = pair2(-1.44269504f, -1.44269504f), one = pair2(1.0f, 1.0f);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         float a, b, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g[j] * -1.44269504f));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(g[j + 1] * -1.44269504f));
-        a += 1.0f, b += 1.0f;
+        const uint64_t gg = pair2(g[j], g[j + 1]);
+        unpair2(mul2(gg, log2e), a, b);
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+        unpair2(add2(pair2(a, b), one), a, b);
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-        h[j] = g[j] * u[j] * (r * b);
-        h[j + 1] = g[j + 1] * u[j + 1] * (r * a);
+        unpair2(mul2(mul2(gg, pair2(u[j], u[j + 1])), mul2(pair2(b, a), pair2(r, r))), h[j], h[j + 1]);
     }
 }
 __device__ __forceinline__ double gate_exact(float g, float u) { return double(g) / (1.0 + exp(-double(g))) * double(u); }
@@ -145,12 +191,12 @@ __device__ __forceinline__ uint32_t code_of(double a)
            uint32_t(a >= 3.5) + uint32_t(a > 5.0);
 }
 
-// Codes of h, known to a relative `error`, under the scale of the block: those that
+// Codes of h, known to a relative `error`, under the scale of the block, whose
+// largest magnitude has the bits m: those that
 // the error decides are marked in `unsure`, a bit in each's place (all of them: the
 // scale is).
-__device__ __forceinline__ uint32_t codes8_known(const float (&h)[8], float error, uint32_t *byte, uint32_t *unsure)
+__device__ __forceinline__ uint32_t codes8_known(const float (&h)[8], uint32_t m, float error, uint32_t *byte, uint32_t *unsure)
 {
-    const uint32_t m = block_max(max_bits(h, 0));
     const float a = __uint_as_float(m);
     *byte = scale_byte(m);
     const float inv = scale_inverse(*byte);
@@ -173,7 +219,7 @@ __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (
         h[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
         least = fminf(least, g[j]);
     }
-    uint32_t unsure, w = codes8_known(h, kSlowError, byte, &unsure);
+    uint32_t unsure, w = codes8_known(h, block_max(largest8(h)), kSlowError, byte, &unsure);
     const bool whole = unsure == ~0u || (*byte != 255 && least < kSlowFrom);
     if (__any_sync(0xffffffffu, whole)) {
         double m = 0.0;
@@ -230,11 +276,14 @@ template <> struct Raw<float> {
 };
 
 // E matrices of R rows.  A lane has 8 values of a row at a time, four lanes a block,
-// a warp 256 values; it serves kRun such runs of one row, eight rows a block.
-constexpr int kRun = 4;
-
-template <typename XT, bool ACT>
-__global__ void __launch_bounds__(256)
+// a warp 256 values; it serves N such runs of one row, eight rows a block.  The runs
+// go through each step together, so that their waits for shuffles and exponentials
+// overlap: 32768 x 2048 gated takes 62 us (4.9 TB/s read and written), one run after
+// the other 96, two together 67; BF16 16384 x 4096 28 us (6.1), FP32 44 (6.9).  Gated
+// values are bound by their arithmetic, some 170 instructions for 8 of a lane, in
+// registers held down to what keeps three blocks resident (with two 71 us).
+template <typename XT, bool ACT, int N>
+__global__ void __launch_bounds__(256, ACT ? 3 : 1)
     mx4_quant_kernel(const XT *__restrict__ X, int64_t rows, int64_t R, int32_t K, uint8_t *__restrict__ Q, uint8_t *__restrict__ S)
 {
     grid_dependency_wait();
@@ -243,15 +292,11 @@ __global__ void __launch_bounds__(256)
     const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (t >= rows) return;
     const int32_t kt = (K + 127) / 128;
-    // (the scales of each matrix begin a tile of their own)
-    const int64_t e = rows == R ? 0 : t / R;
-    uint8_t *s = S + e * ((R + 127) / 128 * kt * kMx4Tile) + mx4_scale_at(t - e * R, 0, kt);
     const XT *row = X + t * (ACT ? 2 : 1) * int64_t(K);
-    uint8_t *q = Q + t * (int64_t(K) / 2);
-    const int k0 = int(blockIdx.y) * (256 * kRun) + lane * 8;
-    Raw<XT> raw[kRun], raw_u[ACT ? kRun : 1];
+    const int k0 = int(blockIdx.y) * (256 * N) + lane * 8;
+    Raw<XT> raw[N], raw_u[ACT ? N : 1];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int k = k0 + i * 256;
         if (k < K) {
             raw[i].load(row + k);
@@ -261,40 +306,78 @@ __global__ void __launch_bounds__(256)
             if (ACT) raw_u[ACT ? i : 0].zero();
         }
     }
+    // (the scales of each matrix begin a tile of their own)
+    const int64_t e = rows == R ? 0 : t / R;
+    uint8_t *s = S + e * ((R + 127) / 128 * kt * kMx4Tile) + mx4_scale_at(t - e * R, 0, kt);
+    uint8_t *q = Q + t * (int64_t(K) / 2);
+    uint32_t byte[N], w[N];
+    if constexpr (!ACT) {
+        uint32_t m[N];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        const int k = k0 + i * 256;
-        if (k - lane * 8 >= K) break;
-        float v[8];
-        raw[i].values(v);
-        uint32_t byte, w;
-        if constexpr (!ACT) {
-            byte = scale_byte(block_max(max_bits(v, 0)));
-            w = codes8(v, scale_inverse(byte));
-        } else {
-            float u[8], h[8], least = v[0];
-            raw_u[i].values(u);
-            gate_fast(v, u, h);
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            raw[i].values(v);
+            m[i] = largest8(v);
+        }
 #pragma unroll
-            for (int j = 1; j < 8; ++j) least = fminf(least, v[j]);
+        for (int i = 0; i < N; ++i) m[i] = block_max(m[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[8];
+            raw[i].values(v);
+            byte[i] = scale_byte(m[i]);
+            w[i] = codes8(v, scale_inverse(byte[i]));
+        }
+    } else {
+        float h[N][8], least[N];
+        uint32_t m[N], open = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float g[8], u[8];
+            raw[i].values(g);
+            raw_u[ACT ? i : 0].values(u);
+            gate_fast(g, u, h[i]);
+            m[i] = largest8(h[i]);
+            least[i] = least8(g);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = block_max(m[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
             uint32_t unsure;
-            w = codes8_known(h, kFastError, &byte, &unsure);
-            bool open = unsure != 0 || !(least > kFastFrom);
-            if (byte < 32 || byte == 255) {
-                // g u leaves FP32's range before h does; but zeros are zeros
+            w[i] = codes8_known(h[i], m[i], kFastError, &byte[i], &unsure);
+            // (a small block's g u may have left FP32's range before h does)
+            if (unsure != 0 || !(least[i] > kFastFrom) || byte[i] < 32 || byte[i] == 255) open |= 1u << i;
+        }
+        if (__any_sync(0xffffffffu, open != 0)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float g[8], u[8];
+                raw[i].values(g);
+                raw_u[ACT ? i : 0].values(u);
+                // zeros are zeros
                 bool zero = true;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) zero = zero && (v[j] == 0.0f || u[j] == 0.0f);
-                open = open || !zero;
+                for (int j = 0; j < 8; ++j) zero = zero && (g[j] == 0.0f || u[j] == 0.0f);
+                if (__any_sync(0xffffffffu, (open >> i & 1u) && !zero)) w[i] = codes8_gated(g, u, &byte[i]);
             }
-            if (__any_sync(0xffffffffu, open)) w = codes8_gated(v, u, &byte);
         }
-        if (byte == 255) w = 0;
-        if (k < K) *reinterpret_cast<uint32_t *>(q + k / 2) = w;
-        uint32_t word = byte << (8 * ((lane >> 2) & 3));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if ((lane & 15) == 0 && k < K) *reinterpret_cast<uint32_t *>(s + int64_t(k / 128) * kMx4Tile) = word;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int k = k0 + i * 256;
+        if (byte[i] == 255) w[i] = 0;
+        if (k < K) *reinterpret_cast<uint32_t *>(q + k / 2) = w[i];
+        byte[i] <<= 8 * ((lane >> 2) & 3);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) byte[i] |= __shfl_xor_sync(0xffffffffu, byte[i], 4);
+#pragma unroll
+    for (int i = 0; i < N; ++i) byte[i] |= __shfl_xor_sync(0xffffffffu, byte[i], 8);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int k = k0 + i * 256;
+        if ((lane & 15) == 0 && k < K) *reinterpret_cast<uint32_t *>(s + int64_t(k / 128) * kMx4Tile) = byte[i];
     }
 }
 
@@ -307,7 +390,9 @@ cudaError_t launch_quant_as(const void *X, int act, int64_t E, int64_t R, int32_
 {
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((E * R + 7) / 8), unsigned((K + 256 * kRun - 1) / (256 * kRun)), 1);
+    // (short rows: no runs past their end)
+    const int runs = K <= 256 ? 1 : K <= 512 ? 2 : 4;
+    cfg.gridDim = dim3(unsigned((E * R + 7) / 8), unsigned((K + 256 * runs - 1) / (256 * runs)), 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
     if (pdl_enabled()) {
@@ -317,8 +402,13 @@ cudaError_t launch_quant_as(const void *X, int act, int64_t E, int64_t R, int32_
         cfg.numAttrs = 1;
     }
     const XT *x = static_cast<const XT *>(X);
-    return act == CAKE_GG_ACT_SILU_MUL ? cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, true>, x, E * R, R, K, Q, S)
-                                       : cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, false>, x, E * R, R, K, Q, S);
+    auto run = [&](auto act_of) {
+        constexpr bool ACT = decltype(act_of)::value;
+        return runs == 1   ? cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, ACT, 1>, x, E * R, R, K, Q, S)
+               : runs == 2 ? cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, ACT, 2>, x, E * R, R, K, Q, S)
+                           : cudaLaunchKernelEx(&cfg, mx4_quant_kernel<XT, ACT, 4>, x, E * R, R, K, Q, S);
+    };
+    return act == CAKE_GG_ACT_SILU_MUL ? run(std::true_type()) : run(std::false_type());
 }
 
 int launch_quant(const void *X, int x_dtype, int act, int64_t E, int64_t R, int32_t K, uint8_t *Q, uint8_t *S, cudaStream_t stream)
