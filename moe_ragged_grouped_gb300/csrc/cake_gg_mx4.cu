@@ -249,11 +249,11 @@ __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (
     return w;
 }
 
-// Eight values of a row as they are in memory.
+// Eight values of a row as they are in memory, read once.
 template <typename XT> struct Raw;
 template <> struct Raw<uint16_t> {
     uint4 w;
-    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void load(const uint16_t *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void values(float (&v)[8]) const
     {
@@ -266,7 +266,7 @@ template <> struct Raw<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float *p)
     {
-        a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ void values(float (&v)[8]) const
