@@ -342,3 +342,78 @@ def test_no_tokens():
     assert gg.combine_rows(r, none, torch.empty((0, 4), device="cuda")).shape == (0, 64)
     d_rows, d_weight = gg.combine_grad(r, r, none, torch.empty((0, 4), device="cuda"))
     assert d_rows.shape == (0, 64) and d_weight.shape == (0, 4) and gg.gather_rows(r, none).shape == (0, 64)
+
+
+# ---------------------------------------------------------------- how a call behaves
+
+
+def test_chunks_of_many_experts():
+    """Blocks that go through several chunks of their tokens, with the most shared memory that takes."""
+    import torch
+    for T, E, top_k in ((120000, 520, 2), (160000, 24, 3)):
+        logits, _ = make(T, E, 1)
+        got = gg.route(logits, top_k)
+        expert = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :top_k]
+        by, order = torch.sort(expert.reshape(-1), stable=True)
+        position = torch.empty_like(order)
+        position[order] = torch.arange(order.numel(), device="cuda")
+        assert same(got.expert, expert) and same(got.position, position.view(T, top_k)) and same(got.rows, order // top_k)
+        assert same(got.offsets, torch.searchsorted(by, torch.arange(E + 1, device="cuda")))
+
+
+def test_same_bits_on_every_run():
+    import torch
+    logits, bias = make(3000, 200, 5)
+    o = dict(score="sigmoid", bias=bias, groups=8, top_groups=3, group_score="top2")
+    first = gg.route(logits, 6, **o)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, gg.route(logits, 6, **o)))
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_on_a_stream_that_is_not_the_current_one(T):
+    """Helpers given a stream: what they make belongs to it, and they wait for nothing else."""
+    import torch
+    logits, bias = make(T, 64, T)
+    position, r, w, _ = rows_case(T, 4, 264, "bf16", 1)
+    want = gg.route(logits, 4, bias=bias), gg.combine_rows(r, position, w)
+    grads = gg.route_grad(logits, want[0].expert, w), *gg.combine_grad(want[1], r, position, w), gg.gather_rows(want[1], position)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for s in (stream, stream.cuda_stream):
+        got = gg.route(logits, 4, bias=bias, stream=s), gg.combine_rows(r, position, w, stream=s)
+        back = (gg.route_grad(logits, got[0].expert, w, stream=s), *gg.combine_grad(got[1], r, position, w, stream=s),
+                gg.gather_rows(got[1], position, stream=s))
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[0], want[0])) and torch.equal(got[1], want[1])
+        assert all(torch.equal(a, b) for a, b in zip(back, grads))
+
+
+def test_captured():
+    """One graph of routing, its gradient and the rows' way, replayed on new logits."""
+    import torch
+    for T in (30, 2000):
+        ls = [make(T, 96, i)[0] for i in range(3)]
+        rows = torch.randn((T * 5, 64), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+        def step(l, **kept):
+            r = gg.route(l, 5, score="sigmoid", **kept)
+            y = gg.combine_rows(rows, r.position, r.weight, out_dtype="fp32")
+            d_rows, d_weight = gg.combine_grad(y, rows, r.position, r.weight)
+            return (*r, y, d_rows, gg.route_grad(l, r.expert, d_weight, score="sigmoid"))
+        want = [step(l) for l in ls]
+        torch.cuda.synchronize()
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            l = ls[0].clone()
+            plan = gg.cake_gg_route_plan(T, 96, 5)
+            kept = dict(plan=plan, workspace=gg.make_workspace(plan, "cuda"))
+            step(l, **kept)
+            stream.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                got = step(l, **kept)
+            for i in (1, 2, 0):
+                l.copy_(ls[i])
+                graph.replay()
+                stream.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
