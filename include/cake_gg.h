@@ -420,6 +420,11 @@ int cake_gg_i8_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, 
  * side of a border a gated value lies, 64 bits decide.  A block of zeros has s = 0; one
  * that holds a NaN or an infinity s = 255 and codes 0, so the products of its
  * row are NaN. */
+typedef enum {
+    CAKE_GG_MX4_MMA = 0,     /* tensor cores                                        */
+    CAKE_GG_MX4_ROWS = 1     /* few rows: integer dot products                      */
+} cake_gg_mx4_path_t;
+
 typedef struct cake_gg_mx4_plan {
     int32_t abi_version;     /* CAKE_GG_ABI_VERSION                                 */
     int32_t E;               /* experts, 1 .. 1024                                  */
@@ -438,7 +443,8 @@ typedef struct cake_gg_mx4_plan {
     int32_t stages;          /* shared-memory ring depth                            */
     int32_t splits;          /* CTAs of a cluster that share a tile's reduction     */
     int32_t debug_flags;     /* test-only fault injection; 0 in normal use          */
-    int32_t reserved;
+    int32_t path;            /* cake_gg_mx4_path_t; the shape above is the tensor
+                                cores'                                              */
     uint64_t timeout_ns;     /* limit of every in-kernel wait (default 2 s)         */
     uint64_t workspace_bytes;/* bytes of workspace the call needs                   */
 } cake_gg_mx4_plan_t;

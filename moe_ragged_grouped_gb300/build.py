@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(HERE, "libcake_gg.so")
 
 SOURCES = ["cake_gg_capi.cu", "cake_gg_fwd.cu", "cake_gg_dgrad.cu", "cake_gg_wgrad.cu", "cake_gg_router.cu",
            "cake_gg_int8.cu", "cake_gg_int8_rows.cu", "cake_gg_int8_mma.cu", "cake_gg_int8_warps.cu",
-           "cake_gg_mx4.cu", "cake_gg_mx4_mma.cu", "cake_gg_route.cu", "cake_gg_route_narrow.cu", "cake_gg_route_wide.cu",
+           "cake_gg_mx4.cu", "cake_gg_mx4_mma.cu", "cake_gg_mx4_rows.cu", "cake_gg_route.cu", "cake_gg_route_narrow.cu", "cake_gg_route_wide.cu",
            "cake_gg_route_widest.cu", "cake_gg_combine.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

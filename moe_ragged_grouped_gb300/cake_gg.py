@@ -35,6 +35,7 @@ CAKE_GG_NOALLOC_SCRATCH_BYTES = 32 << 20
 CAKE_GG_FWD, CAKE_GG_DGRAD, CAKE_GG_WGRAD = 0, 1, 2
 CAKE_GG_BF16, CAKE_GG_FP32, CAKE_GG_INT8, CAKE_GG_MX4 = 0, 1, 2, 3
 CAKE_GG_ACT_NONE, CAKE_GG_ACT_SILU_MUL = 0, 1
+CAKE_GG_MX4_MMA, CAKE_GG_MX4_ROWS = 0, 1
 CAKE_GG_DEBUG_DROP_FIRST_LOAD = 1
 CAKE_GG_SCORE_SOFTMAX, CAKE_GG_SCORE_SIGMOID = 0, 1
 CAKE_GG_GROUP_MAX, CAKE_GG_GROUP_TOP2 = 0, 1
@@ -151,13 +152,13 @@ class CakeGGMx4Plan(ctypes.Structure):
         ("stages", ctypes.c_int32),
         ("splits", ctypes.c_int32),
         ("debug_flags", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("path", ctypes.c_int32),
         ("timeout_ns", ctypes.c_uint64),
         ("workspace_bytes", ctypes.c_uint64),
     ]
 
     def as_dict(self):
-        return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
+        return {f[0]: getattr(self, f[0]) for f in self._fields_}
 
 
 class CakeGGRouteOptions(ctypes.Structure):

@@ -15,8 +15,8 @@
 
 #include <cuda_runtime.h>
 
-#include "cake_gg_int8_quant.cuh"
 #include "cake_gg_mx4.h"
+#include "cake_gg_mx4_quant.cuh"
 #include "cake_gg_ptx.cuh"
 
 using namespace cakegg;
@@ -70,7 +70,7 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
     L.arranged = L.tokens + align_up(T * uint64_t(pl.K) / 2, 256);
     L.rows = L.arranged;
     L.total = L.arranged;
-    if (pl.pair == 2) {
+    if (pl.pair == 2 && pl.path == CAKE_GG_MX4_MMA) {
         L.rows += uint64_t(mx4_slots(pl.M_max, pl.E, pl.tile_rows)) * uint64_t((pl.K + 127) / 128 * mx4_row_atoms(pl.tile_rows)) * kMx4Tile;
         // (whether a call routes is known with the call: T other than M_max says that it
         // does, and it may all the same)
@@ -80,84 +80,6 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
 }
 
 // ---------------------------------------------------------------- token pass
-
-// Two FP32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair2(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// Four pairs of values as E2M1 codes, to nearest, ties to even, held at 6; the
-// first of a pair in the low half of its byte.
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float inv)
-{
-    float w[8];
-    const uint64_t by = pair2(inv, inv);
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) unpair2(mul2(pair2(v[i], v[i + 1]), by), w[i], w[i + 1]);
-    uint32_t r;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-        "mov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(r)
-        : "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "f"(w[4]), "f"(w[5]), "f"(w[6]), "f"(w[7]));
-    return r;
-}
-
-// The scale's byte (exponent + 127; 255: a NaN) of a block's largest magnitude,
-// by its bits, and the reciprocal of the scale.  (Powers of two: exact.)
-__device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits)
-{
-    const int e = int(max_bits >> 23);
-    return e == 255 ? 255u : uint32_t(max(e - 2, 0));
-}
-__device__ __forceinline__ float scale_inverse(uint32_t byte)
-{
-    return byte == 255 ? 0.0f : __uint_as_float((254u - byte) << 23);
-}
-
-// The bits of the largest magnitude of eight values; a NaN's if there is one.
-__device__ __forceinline__ uint32_t largest8(const float (&v)[8])
-{
-    float m;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(v[0]), "f"(v[1]), "f"(v[2]));
-    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[3]), "f"(v[4]));
-    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[5]), "f"(v[6]));
-    asm("max.NaN.abs.f32 %0, %0, %1, %1;" : "+f"(m) : "f"(v[7]));
-    return __float_as_uint(m);
-}
-__device__ __forceinline__ float least8(const float (&v)[8])
-{
-    float m;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(v[0]), "f"(v[1]), "f"(v[2]));
-    asm("min.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[3]), "f"(v[4]));
-    asm("min.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[5]), "f"(v[6]));
-    return fminf(m, v[7]);
-}
-
-__device__ __forceinline__ uint32_t block_max(uint32_t m)    // over the four lanes of a block
-{
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
 
 // silu(g) * u, three ways.  By approximate instructions: the product g log2(e)
 // rounds to 2^-24 of it, which the exponential multiplies by at most 40 ln 2 / log2(e);
@@ -248,32 +170,6 @@ __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (
     }
     return w;
 }
-
-// Eight values of a row as they are in memory, read once.
-template <typename XT> struct Raw;
-template <> struct Raw<uint16_t> {
-    uint4 w;
-    __device__ __forceinline__ void load(const uint16_t *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void values(float (&v)[8]) const
-    {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-};
-template <> struct Raw<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p)
-    {
-        a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-    __device__ __forceinline__ void values(float (&v)[8]) const
-    {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-};
 
 // E matrices of R rows.  A lane has 8 values of a row at a time, four lanes a block,
 // a warp 256 values; it serves N such runs of one row, eight rows a block.  The runs
@@ -531,6 +427,22 @@ int stages_for(int pair, int nt, int splits, int E)
     return s;
 }
 
+// Whether a call of few rows takes the dot products, in runs of up to two rows: they need some
+// 2.5 us to begin with, and then their arithmetic, 4 million weights a microsecond; the
+// tensor cores 5 to 8 us, and then what HBM gives.  By dot products and by tensor cores,
+// BF16 rows: 1024 x 1024 2.7 and 5.9 us, 4096 x 4096 5.3 and 8.0, two rows of it 6.2 and
+// 8.0, 6144 x 4096 7.8 and 8.9, one token through 8 of 128 experts 2048 -> 768 6.1 and
+// 10.3; past the rule 4096 x 8192 10.0 and 8.4, 8192 x 8192 17 and 13.  Long rows leave few
+// blocks much to do one after another (8192 x 512 7.9 and 7.7), and blocks that are not all
+// resident begin anew: 9 rows of 256 x 4096 8.9 and 5.1, 64 of 256 x 1024 12.7 and 5.2.
+bool few_rows(const cake_gg_mx4_plan_t &pl)
+{
+    const int R = mx4_run_rows(pl.M_max, pl.E);
+    const int64_t runs = mx4_runs(pl.M_max, pl.E);
+    return pl.K <= 8192 && runs <= 8 * int64_t(pl.E) && runs * pl.N <= int64_t(28) * 1000 * 1000 / pl.K &&
+           runs * ((pl.N + 127) / 128 * 4) <= kSms * (R == 1 ? 3 : 2);
+}
+
 // Row tiles of nt rows that the call will have: exact for one expert; where E
 // share the rows, whole tiles and half a tile more for each expert that can have
 // rows, at least one each (the sizes are the device's).
@@ -588,6 +500,8 @@ void choose(cake_gg_mx4_plan_t *pl)
     for (int nt = kMx4RowsMost; nt >= 64; nt -= 32) consider(2, nt, 1);
     for (int nt = kMx4RowsMost; nt >= 32; nt -= 32)
         for (int sp = 1; sp <= (nt <= 64 ? 8 : 1); ++sp) consider(1, nt, sp);
+    const int path = env_int("CAKE_GG_MX4_PATH", few_rows(*pl) ? CAKE_GG_MX4_ROWS : CAKE_GG_MX4_MMA);
+    pl->path = path == CAKE_GG_MX4_ROWS && mx4_rows_fit(pl->M_max, pl->E, pl->K) ? CAKE_GG_MX4_ROWS : CAKE_GG_MX4_MMA;
     pl->pair = env_int("CAKE_GG_MX4_PAIR", pl->pair) == 2 ? 2 : 1;
     const int nt = env_int("CAKE_GG_MX4_ROWS_PER_TILE", pl->tile_rows);
     if (nt >= 32 && nt <= kMx4RowsMost && nt % 32 == 0) pl->tile_rows = nt;
@@ -599,6 +513,7 @@ void choose(cake_gg_mx4_plan_t *pl)
 // What the kernel can run.
 bool plan_ok(const cake_gg_mx4_plan_t &pl)
 {
+    if (pl.path != CAKE_GG_MX4_MMA && !(pl.path == CAKE_GG_MX4_ROWS && mx4_rows_fit(pl.M_max, pl.E, pl.K))) return false;
     return (pl.pair == 1 || pl.pair == 2) && pl.tile_rows >= 32 && pl.tile_rows <= kMx4RowsMost && pl.tile_rows % 32 == 0 &&
            pl.stages >= kStagesLeast && pl.stages <= kMx4StagesMost && pl.splits >= 1 && pl.splits <= 8 &&
            (pl.splits == 1 || pl.pair == 1) && pl.splits <= (pl.K + 255) / 256 &&   // (a stage for every CTA)
@@ -677,7 +592,8 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
     Mx4Params p{};
     p.offsets = offsets;
     // (a pair's rows are laid out before: for it row m is token m)
-    const bool pair = pl.pair == 2;
+    const bool few = pl.path == CAKE_GG_MX4_ROWS, pair = pl.pair == 2 && !few;
+    const bool pass = !ready && (!few || pl.act != CAKE_GG_ACT_NONE);   // (a few rows are quantised by the blocks)
     const uint8_t *scales = ready ? xs : base + L.scales, *x = ready ? static_cast<const uint8_t *>(X) : base + L.tokens;
     const uint8_t *x_rows = pair && rows ? base + L.rows : x;
     p.rows = pair ? nullptr : rows;
@@ -690,7 +606,7 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
     p.N = pl.N;
     p.K = pl.K;
     p.out_f32 = pl.out_dtype == CAKE_GG_FP32;
-    p.early = !ready || pair;
+    p.early = pass || pair;
     p.nt = pl.tile_rows;
     p.stages = pl.stages;
     p.splits = pl.splits;
@@ -699,9 +615,16 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
     const int cap = pl.max_sms > 0 && pl.max_sms < sms ? pl.max_sms : sms;
     // what cannot be launched is refused before anything is enqueued
     Mx4Launch product;
-    if ((rc = prepare_mx4_mma(&product, p, W, ws, x_rows, pl.pair, cap)) != CAKE_GG_OK) return rc;
-    if (!ready && (rc = launch_quant(X, pl.x_dtype, pl.act, 1, pl.T, pl.K, base + L.tokens, base + L.scales, s)) != CAKE_GG_OK)
+    if (!few && (rc = prepare_mx4_mma(&product, p, W, ws, x_rows, pl.pair, cap)) != CAKE_GG_OK) return rc;
+    if (pass && (rc = launch_quant(X, pl.x_dtype, pl.act, 1, pl.T, pl.K, base + L.tokens, base + L.scales, s)) != CAKE_GG_OK)
         return rc;
+    if (few) {
+        const bool codes = ready || pass;
+        return launch_mx4_rows(p, codes ? x : static_cast<const uint8_t *>(X), codes ? int(CAKE_GG_MX4) : pl.x_dtype, W, ws,
+                               pdl_enabled(), s) == cudaSuccess
+                   ? CAKE_GG_OK
+                   : CAKE_GG_ERR_CUDA;
+    }
     if (pair && launch_arrange(p, rows, pl.T, scales, x, base + L.arranged, base + L.rows, s) != cudaSuccess) return CAKE_GG_ERR_CUDA;
     return launch_mx4_mma(product, pdl_enabled(), s);
 }

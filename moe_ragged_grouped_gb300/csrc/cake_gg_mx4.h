@@ -67,6 +67,11 @@ struct Mx4Params {
     uint32_t div_nt;
 };
 
+// Few rows are taken in runs of an expert's: of one where there are no more rows than
+// experts, else of up to two; and as many runs as a call can have.
+__host__ __device__ __forceinline__ int mx4_run_rows(int64_t M, int32_t E) { return M > E ? 2 : 1; }
+__host__ __device__ __forceinline__ int64_t mx4_runs(int64_t M, int32_t E) { return M <= E ? M : E == 1 ? (M + 1) / 2 : (M + E) / 2; }
+
 constexpr size_t kMx4SmemLimit = 232448;   // opt-in dynamic shared memory per CTA (227 KB)
 constexpr int kMx4StagesMost = 12;
 
@@ -82,5 +87,11 @@ struct Mx4Launch {
 };
 int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p, const uint8_t *W, const uint8_t *ws, const uint8_t *x, int pair, int sms);
 int launch_mx4_mma(const Mx4Launch &l, bool pdl, cudaStream_t stream);
+
+// Few rows: integer dot products.  X: codes (x_dtype CAKE_GG_MX4, scales in p.xs), or
+// activations that the blocks quantise themselves.
+bool mx4_rows_fit(int64_t M, int32_t E, int32_t K);
+cudaError_t launch_mx4_rows(const Mx4Params &p, const void *X, int x_dtype, const uint8_t *W, const uint8_t *ws, bool pdl,
+                            cudaStream_t stream);
 
 }  // namespace cakegg

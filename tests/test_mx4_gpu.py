@@ -438,3 +438,81 @@ def test_weights_past_four_billion_values():
     off[-1] = 20
     got = gg.mx4_gemm(x, q, s, xs=xs, offsets=off.cuda(), out_dtype="fp32")
     check(got, values(x, xs), dense_values(q[-1:], s[-1:]), [20], None, "fp32")
+
+
+def test_on_a_stream_that_is_not_the_current_one():
+    """Helpers given a stream: what they make belongs to it."""
+    import torch
+    N, K, T = 264, 544, 300
+    q, s = weights(1, N, K, 3)
+    x = randn((T, K), 1)
+    want_q, want = gg.quantize_mx4(x), gg.mx4_gemm(x, q[0], s[0])
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for st in (stream, stream.cuda_stream):
+        got_q, got = gg.quantize_mx4(x, stream=st), gg.mx4_gemm(x, q[0], s[0], stream=st)
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got_q, want_q)) and torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- few rows
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("x_dtype", ["mx4", "bf16", "fp32"])
+@pytest.mark.parametrize("T,E,K,N,routed", [
+    (1, 1, 32, 8, False), (2, 1, 992, 136, False), (1, 1, 8192, 264, False), (3, 1, 1056, 1000, False), (15, 1, 1024, 1024, False),
+    (1, 40, 288, 520, True), (2, 9, 2880, 256, True), (7, 3, 64, 120, True), (9, 300, 96, 40, False),
+])
+def test_few_rows(T, E, K, N, routed, x_dtype, out_dtype):
+    """Dot products against 64 bits: one row and two a run, dense and by expert, codes and activations."""
+    import torch
+    rng = np.random.default_rng(T + K)
+    M = 2 * T if routed else T
+    sizes = [int(v) for v in rng.multinomial(M, [1 / E] * E)]
+    rows = torch.from_numpy(rng.integers(0, T, size=M).astype(np.int32)).cuda() if routed else None
+    plan = gg.cake_gg_mx4_plan(E, M, T, N, K, x_dtype, None, out_dtype)
+    assert plan.path == gg.CAKE_GG_MX4_ROWS
+    q, s = weights(E, N, K, T + N)
+    x = randn((T, K), T + K, "fp32" if x_dtype == "fp32" else "bf16")
+    xq, xs = gg.quantize_mx4(x)
+    scales = xs if x_dtype == "mx4" else None
+    got = gg.mx4_gemm(xq if scales is not None else x, q, s, xs=scales, offsets=offsets_of(sizes) if E > 1 else None, rows=rows,
+                      out_dtype=out_dtype)
+    check(got, values(xq, xs), dense_values(q, s), sizes, rows, out_dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_few_rows_of_every_scale(T):
+    """One block: its sum is exact, so the output is that sum rounded, whatever the two scales are."""
+    import torch
+    N = 1024
+    rng = np.random.default_rng(T)
+    codes = lambda r: torch.from_numpy(rng.integers(0, 256, size=(r, 16)).astype(np.uint8)).cuda()  # noqa: E731
+    tiles = lambda r: torch.from_numpy(rng.integers(0, 256, size=gg._mx4_tiles(r, 32)).astype(np.uint8)).cuda()  # noqa: E731
+    w, ws = codes(N), tiles(N)
+    ws[..., 1:] = 0                                              # (blocks that the rows do not have)
+    for byte in (0, 1, 2, 3, 64, 127, 128, 200, 253, 254, 255):
+        x, xs = codes(T), tiles(T)
+        xs[...] = 0
+        xs[..., 0] = byte
+        got = gg.mx4_gemm(x, w, ws, xs=xs, out_dtype="fp32")
+        want = (values(x, xs) @ values(w, ws).T).cpu().float()
+        assert torch.allclose(got.cpu(), want, rtol=0, atol=0, equal_nan=True), byte
+
+
+def test_few_rows_of_lost_tokens():
+    """A row whose token does not exist is reported and is zeros; the others are right."""
+    import torch
+    N, K, M = 128, 256, 3
+    q, s = weights(4, N, K, 1)
+    x = randn((M, K), 1)
+    rows = torch.tensor([0, 3, 2], dtype=torch.int32, device="cuda")
+    for tokens in (gg.quantize_mx4(x), (x, None)):
+        out = torch.empty((M, N), dtype=torch.float32, device="cuda")
+        with pytest.raises(gg.CakeGGError) as err:
+            gg.mx4_gemm(tokens[0], q, s, xs=tokens[1], offsets=offsets_of([1, 1, 0, 1]), rows=rows, out=out, out_dtype="fp32")
+        assert err.value.code == gg.CAKE_GG_ERR_BAD_ROWS
+        v, w = values(*gg.quantize_mx4(x)), dense_values(q, s)
+        assert not out[1].any()
+        check(out[0::2].contiguous(), v[0::2], w[0::3].contiguous(), [1, 1], None, "fp32")
