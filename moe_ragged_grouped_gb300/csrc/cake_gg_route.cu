@@ -12,7 +12,6 @@ namespace {
 constexpr int kThreads = kRouteThreads, kWarps = kThreads / 32;
 constexpr int32_t kMaxExperts = kRouteMaxExperts, kMaxTop = 32, kMaxGroups = 32;
 constexpr int64_t kMaxTokens = 1 << 23;        // (a block's tokens are below 2^16)
-constexpr int64_t kClusterTokens = 256;        // what one cluster serves
 constexpr int kClusterBlocks = 8;
 constexpr int kChunk = 1024;                   // tokens that a block numbers at a time, at most
 constexpr int kSms = 152;
@@ -92,12 +91,14 @@ int check_scores(int logits_dtype, int64_t stride, int32_t E, int score)
     return CAKE_GG_OK;
 }
 
-// Blocks and their tokens: as few blocks of one cluster as have a warp for a token,
-// or one for each multiprocessor, which holds the bits of a chunk of its tokens.
+// Blocks and their tokens: as few blocks of one cluster as have a warp for a token
+// (of 256 experts 256 tokens 12 us, 260 by two kernels 12; of 512 experts 128 10.3, and 256,
+// two for each warp, 15.1, by two kernels 10.6), or one for each multiprocessor, which
+// holds the bits of a chunk of its tokens.
 void choose_blocks(cake_gg_route_plan_t *pl)
 {
     const int64_t T = pl->T;
-    pl->cluster = T <= kClusterTokens;
+    pl->cluster = T <= kClusterBlocks * (pl->E <= kRouteNarrow ? kRouteThreads : kRouteThreads / 2) / 32;
     int64_t blocks = pl->cluster ? (T + 3) / 4 : kSms;
     if (pl->cluster && blocks > kClusterBlocks) blocks = kClusterBlocks;
     if (blocks < 1) blocks = 1;

@@ -17,7 +17,7 @@
 //
 // Rows are numbered by counting: for each expert a bit per token of the block says
 // who chose it, so a token's place among them is a population count, in the
-// order of the tokens and the same on every run.  Up to kClusterTokens one cluster of
+// order of the tokens and the same on every run.  Up to a token for each of its warps one cluster of
 // blocks does it all, counts read from one another's shared memory; more tokens
 // take a kernel that counts and one that numbers.
 //
@@ -30,7 +30,10 @@
 namespace cakegg {
 namespace {
 
-constexpr int kThreads = kRouteThreads, kWarps = kThreads / 32;
+// Threads of a block.  The keys and logits of a token of more than 256 experts do not
+// stay in the 64 registers that 1024 threads have each (8 of 384, 64 tokens 12.5 us, 8192
+// tokens 38; with 512 threads 10.5 and 34); of 256 either does (21 us for 16384 tokens).
+template <int VPL> constexpr int kThreadsOf = VPL * 32 <= kRouteNarrow ? kRouteThreads : kRouteThreads / 2;
 constexpr int32_t kMaxExperts = kRouteMaxExperts;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -669,6 +672,7 @@ __device__ __forceinline__ Shared shared_of(uint8_t *raw, const RouteParams &p)
 template <int VPL, Mode MODE>
 __device__ __forceinline__ void choose_all(const RouteParams &p, const Shared &s, int64_t t0, int n)
 {
+    constexpr int kThreads = kThreadsOf<VPL>, kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, words = bit_words(p.chunk);
     float l[VPL], bias[VPL];
     if (MODE != kByLogits && p.bias) load_row(p.bias, p.E, lane, bias);
@@ -712,37 +716,44 @@ __device__ __forceinline__ int32_t place(const Shared &s, int words, int32_t e, 
 }
 
 template <int VPL, Mode MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreadsOf<VPL>, 1)
     route_cluster_kernel(const RouteParams p)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     const Shared s = shared_of(raw, p);
     grid_dependency_wait();
     grid_launch_dependents();
-    const int rank = int(blockIdx.x), blocks = int(gridDim.x), e = threadIdx.x, words = bit_words(p.chunk);
+    constexpr int kThreads = kThreadsOf<VPL>;
+    const int rank = int(blockIdx.x), blocks = int(gridDim.x), words = bit_words(p.chunk);
     const int64_t t0 = int64_t(rank) * p.block_tokens;
     const int n = int(t0 >= p.T ? 0 : p.T - t0 < p.block_tokens ? p.T - t0 : p.block_tokens);
     choose_all<VPL, MODE>(p, s, t0, n);
     if (blocks > 1) cluster_sync_all();
     else __syncthreads();
-    int32_t all = 0, before = 0;
-    if (e < p.E) {
-        const uint32_t mine = smem_u32(&s.counts[e]);
-        for (int b = 0; b < blocks; ++b) {
-            int32_t c;
-            if (b == rank) c = s.counts[e];
-            else asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(map_to_cta(mine, uint32_t(b))) : "memory");
-            if (b < rank) before += c;
-            all += c;
+    int32_t total = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+        const int e = e0 + int(threadIdx.x);
+        int32_t all = 0, before = 0;
+        if (e < p.E) {
+            const uint32_t mine = smem_u32(&s.counts[e]);
+            for (int b = 0; b < blocks; ++b) {
+                int32_t c;
+                if (b == rank) c = s.counts[e];
+                else asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(map_to_cta(mine, uint32_t(b))) : "memory");
+                if (b < rank) before += c;
+                all += c;
+            }
+        }
+        int32_t sum;
+        if (e0) __syncthreads();
+        const int32_t first = total + block_scan(all, &sum);
+        total += sum;
+        if (e < p.E) {
+            s.base[e] = first + before;
+            if (rank == 0) p.offsets[e] = first;
         }
     }
-    int32_t total;
-    const int32_t first = block_scan(all, &total);
-    if (e < p.E) {
-        s.base[e] = first + before;
-        if (rank == 0) p.offsets[e] = first;
-    }
-    if (rank == 0 && e == 0) p.offsets[p.E] = total;
+    if (rank == 0 && threadIdx.x == 0) p.offsets[p.E] = total;
     __syncthreads();
     for (int i = threadIdx.x; i < n * p.top_k; i += kThreads) {
         const int32_t x = s.chosen[i], token = token_of(p, i), row = s.base[x] + place(s, words, x, token);
@@ -755,13 +766,14 @@ __global__ void __launch_bounds__(kThreads)
 // Experts, weights and places within the block (to `position`), a chunk of its
 // tokens after the other, and its counts.
 template <int VPL, Mode MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreadsOf<VPL>, 1)
     route_count_kernel(const RouteParams p)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     const Shared s = shared_of(raw, p);
     grid_dependency_wait();
     grid_launch_dependents();
+    constexpr int kThreads = kThreadsOf<VPL>;
     const int words = bit_words(p.chunk);
     const int64_t begin = int64_t(blockIdx.x) * p.block_tokens, end = min(p.T, begin + p.block_tokens);
     for (int e = threadIdx.x; e < p.E; e += kThreads) s.base[e] = 0;
@@ -892,8 +904,8 @@ cudaError_t launch_route(const RouteParams &p, int blocks, bool cluster, size_t 
 {
     auto with_mode = [&](auto mode) {
         constexpr Mode MODE = decltype(mode)::value;
-        return cluster ? route_launch(route_cluster_kernel<VPL, MODE>, p, blocks, kThreads, shared, blocks, stream)
-                       : route_launch(route_count_kernel<VPL, MODE>, p, blocks, kThreads, shared, 1, stream);
+        return cluster ? route_launch(route_cluster_kernel<VPL, MODE>, p, blocks, kThreadsOf<VPL>, shared, blocks, stream)
+                       : route_launch(route_count_kernel<VPL, MODE>, p, blocks, kThreadsOf<VPL>, shared, 1, stream);
     };
     if (!p.bias && !(p.pair && p.groups > 1)) return with_mode(std::integral_constant<Mode, kByLogits>());
     return p.score == CAKE_GG_SCORE_SOFTMAX ? with_mode(std::integral_constant<Mode, kBySoftmax>())

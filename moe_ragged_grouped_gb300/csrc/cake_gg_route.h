@@ -15,7 +15,8 @@ namespace cakegg {
 
 int device_sms(int *sms);   // (cake_gg_capi.cu)
 
-constexpr int kRouteThreads = 1024;
+constexpr int kRouteThreads = 1024;            // of a block that routes up to kRouteNarrow experts, half beyond
+constexpr int32_t kRouteNarrow = 256;
 constexpr int32_t kRouteMaxExperts = 1024;
 
 struct RouteParams {
@@ -53,7 +54,7 @@ inline size_t route_shared_bytes(int32_t E, int32_t top_k, int chunk)
 
 __host__ __device__ constexpr int32_t count_pitch(int32_t E) { return (E + 7) / 8 * 8; }
 
-// Exclusive sums over v of thread e (E <= kRouteThreads), in place of each; the total to all.
+// Exclusive sums over the threads' v (kRouteThreads of them at most), and the total to all.
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *total)
 {
     __shared__ int32_t sums[kRouteThreads / 32];
@@ -66,7 +67,7 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *total)
     }
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    int32_t w = sums[lane];
+    int32_t w = lane < int(blockDim.x >> 5) ? sums[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int32_t o = __shfl_up_sync(0xffffffffu, w, d);

@@ -417,3 +417,13 @@ def test_captured():
                 graph.replay()
                 stream.synchronize()
                 assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,top_k", [(97, 1024, 9), (128, 700, 5), (129, 700, 5), (128, 512, 8), (129, 512, 8), (200, 384, 8), (256, 256, 8),
+                                       (256, 130, 17), (257, 256, 8)])
+def test_around_one_cluster(T, E, top_k, score):
+    """As many tokens as one cluster of blocks takes, and one more; more experts than a block has threads."""
+    logits, bias = make(T, E, T + E)
+    for b in (None, bias):
+        check(gg.route(logits, top_k, score=score, bias=b), reference(logits, top_k, score=score, bias=b))
