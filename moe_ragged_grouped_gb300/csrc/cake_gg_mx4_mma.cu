@@ -13,14 +13,21 @@
 // bytes of every channel and row, two scale tiles of 128 channels x 4 blocks, and
 // the same of the rows.  The scales of the channels lie in memory as the tensor
 // cores take them and come by TMA; those of the rows, which begin anywhere in a
-// scale tile, or are routed, are put together by warps.  Both go from shared to
-// tensor memory by tcgen05.cp, which the MMAs of the stage follow in the pipe.
+// scale tile, or are routed, are put together by warps of a single CTA, two stages at a
+// time; a pair has them (and routed rows' codes) laid out before it starts, so that all
+// that its MMAs read comes by TMA.  Both go from shared to tensor memory by tcgen05.cp,
+// which the MMAs of the stage follow in the pipe.
 //
-// Roles of a CTA: warp 0 copies weights and their scales, warp 1 issues copies to
-// tensor memory and MMAs, warps 2-9 store (two groups on alternate 32 rows of a
-// tile), warps 10-13 put the rows' scales together, every fourth stage each, warp
-// 14 copies rows, or, where they are routed, warps 14-17 gather them, two on every
-// other stage.
+// Roles of a CTA: warp 0 copies weights and their scales, warp 1 issues MMAs, warps
+// 2-9 store (two groups on alternate 32 rows of a tile), warps 10-13 put the rows' scales
+// together where they do not come by TMA, warp 14 copies scales to tensor memory, warp 15
+// copies rows, or, where they are routed, warps 15-18 gather them, two on every other stage.
+//
+// Bound: long calls by the MMA loop (16384 x 4096 -> 4096 86 us, 6.3 PFLOP/s: the tensor
+// pipe has 384 of some 490 clocks of a stage, four times BF16's rate; with rows in 192 and
+// pairs, since a wider B takes the same hand-over), decoding by HBM (64 tokens through 4 of
+// 32 experts 6144 -> 4096: 70 us, 6.1 TB/s), a single token by what 128 units draw on 152
+// multiprocessors (15.2 us).
 #include <type_traits>
 
 #include "cake_gg_mx4.h"
