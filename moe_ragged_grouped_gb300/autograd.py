@@ -28,6 +28,8 @@ Around the products of an expert layer in training:
 Their gradients are kernels as well: the rows' gradient of gather_rows is the sum
 that combine_rows makes, that of combine_rows the copy that gather_rows makes,
 weighted, so nothing is added by atomics and every run gives the same bits.
+A backward pass can be captured in a CUDA graph; as with any torch function, no
+autograd graph of an earlier pass over the same leaves may be alive then.
 
 This module only marshals arguments: every pass runs in libcake_gg.so.  Plans
 and workspaces are cached per (pass, shape, dtype, mode, device, stream) and

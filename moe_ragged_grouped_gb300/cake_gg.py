@@ -1038,8 +1038,8 @@ def _score_code(score):
 def _route_options(score, groups, top_groups, group_score, renormalize, scale):
     if group_score not in GROUP_SCORES:
         raise ValueError(f"group_score is 'max' or 'top2', got {group_score!r}")
-    return CakeGGRouteOptions(_score_code(score), int(groups), int(groups if top_groups is None else top_groups),
-                              GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
+    return CakeGGRouteOptions(_score_code(score), groups, groups if top_groups is None else top_groups,
+                              GROUP_SCORES[group_score], int(renormalize), scale)
 
 
 def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True,
@@ -1059,7 +1059,9 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     tensors are on the current CUDA device; stream as in int8_gemm.
     """
     kind, T, E, apart = _logits(logits)
-    options = _route_options(score, groups, top_groups, group_score, renormalize, scale)
+    # (plain numbers: a tensor's value may change, and it is its identity that a cache sees)
+    options = _route_options(score, int(groups), None if top_groups is None else int(top_groups), group_score, bool(renormalize),
+                             float(scale))
     if plan is None:
         plan = cake_gg_route_plan(T, E, top_k)
     elif (plan.T, plan.E, plan.top_k) != (T, E, top_k):
@@ -1139,8 +1141,8 @@ def combine_rows(rows, position, weight=None, out_dtype="bf16", out=None, stream
     """Tokens [T, K] as sums of their rows: out[t] = sum_j weight[t, j] * rows[position[t, j]].
 
     rows [M, K] are bf16 or fp32, position int32 [T, top_k] (a Routing's; outside
-    [0, M): no row), weight float32 [T, top_k] (none: ones).  FP32 sums over j in
-    order, rounded once.  All tensors are on the current CUDA device; stream as in
+    [0, M): no row), weight float32 [T, top_k] (none: ones); K is a multiple of 8.
+    FP32 sums over j in order, rounded once.  All tensors are on the current CUDA device; stream as in
     int8_gemm.
     """
     kind = _real_name(rows, "rows")
@@ -1202,7 +1204,7 @@ def combine_grad(d_out, rows, position, weight, out=None, stream=None):
 def gather_rows(X, position, out=None, stream=None):
     """Tokens X [T, K] (bf16 or fp32) as rows in expert order [T * top_k, K]: out[position[t, j]] = X[t].
 
-    position names each row once, as a Routing's does.
+    position names each row once, as a Routing's does; K is a multiple of 8.
     """
     kind = _real_name(X, "X")
     if X.dim() != 2:

@@ -427,3 +427,17 @@ def test_around_one_cluster(T, E, top_k, score):
     logits, bias = make(T, E, T + E)
     for b in (None, bias):
         check(gg.route(logits, top_k, score=score, bias=b), reference(logits, top_k, score=score, bias=b))
+
+
+def test_options_by_value():
+    """An option given as a tensor counts with the value that it has at the call."""
+    import torch
+    logits, _ = make(40, 16, 3)
+    scale, renormalize, groups = torch.tensor(1.0), torch.tensor(True), torch.tensor(1)
+    call = lambda: gg.route(logits, 2, scale=scale, renormalize=renormalize, groups=groups, top_groups=1)  # noqa: E731
+    first = call()
+    scale.fill_(2.0)
+    assert torch.equal(call().weight, 2.0 * first.weight)
+    renormalize.fill_(False)
+    groups.fill_(4)
+    check(call(), reference(logits, 2, scale=2.0, renormalize=False, groups=4, top_groups=1))
