@@ -441,3 +441,24 @@ def test_options_by_value():
     renormalize.fill_(False)
     groups.fill_(4)
     check(call(), reference(logits, 2, scale=2.0, renormalize=False, groups=4, top_groups=1))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_groups_that_are_close(with_bias, score):
+    """Groups whose scores differ in the last places of FP32, not at all, or by which of two near experts counts."""
+    import torch
+    T, E, groups = 600, 128, 8
+    logits, bias = make(T, E, 11)
+    l = logits.view(T, groups, E // groups)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    base = torch.rand((T, 1, 2), generator=g, device="cuda") + 2.0
+    steps = torch.randint(-2, 3, (T, groups, 2), generator=g, device="cuda")
+    l[:, :, 3:5] = base * (1 + steps * 2.0 ** -23)               # the two largest, some steps apart
+    l[:200, :, 7] = l[:200, :, 4] * (1 - 2.0 ** -20)             # a third beside the second
+    l[200:300, 1::2] = l[200:300, ::2]                           # groups that are the same
+    if with_bias:
+        bias = (torch.randint(0, 3, (E // groups,), generator=g, device="cuda").float() * 0.125).repeat(groups)
+    for group_score in ("max", "top2"):
+        o = dict(score=score, bias=bias if with_bias else None, groups=groups, top_groups=3, group_score=group_score)
+        check(gg.route(logits, 6, **o), reference(logits, 6, **o))
