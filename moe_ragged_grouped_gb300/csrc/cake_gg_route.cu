@@ -93,13 +93,14 @@ int check_scores(int logits_dtype, int64_t stride, int32_t E, int score)
 
 // Blocks and their tokens: as few blocks of one cluster as have a warp for a token
 // (of 256 experts 256 tokens 12 us, 260 by two kernels 12; of 512 experts 128 10.3, and 256,
-// two for each warp, 15.1, by two kernels 10.6), or one for each multiprocessor, which
-// holds the bits of a chunk of its tokens.
+// two for each warp, 15.1, by two kernels 10.6), or blocks of eight tokens (257 in groups 13.3
+// us, in blocks of two 14.0, of thirty-two 15.6) or of more, one for each multiprocessor,
+// which holds the bits of a chunk of its tokens.
 void choose_blocks(cake_gg_route_plan_t *pl)
 {
     const int64_t T = pl->T;
     pl->cluster = T <= kClusterBlocks * (pl->E <= kRouteNarrow ? kRouteThreads : kRouteThreads / 2) / 32;
-    int64_t blocks = pl->cluster ? (T + 3) / 4 : kSms;
+    int64_t blocks = pl->cluster ? (T + 3) / 4 : T < 8 * kSms ? (T + 7) / 8 : kSms;
     if (pl->cluster && blocks > kClusterBlocks) blocks = kClusterBlocks;
     if (blocks < 1) blocks = 1;
     const int64_t per = T == 0 ? 1 : (T + blocks - 1) / blocks;
