@@ -9,6 +9,7 @@
 // gets nothing.
 #include <cstdint>
 #include <cstdlib>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -93,53 +94,107 @@ __global__ void __launch_bounds__(256)
         if (h == 0 || t + h < p.T) store8(static_cast<OT *>(p.out) + (t + h) * p.K + k, sum[h]);
 }
 
-// A block has a token; dy stays in registers for its rows where one pass of the
-// block covers it.
-template <typename RT, typename OT>
-__global__ void __launch_bounds__(256)
-    combine_grad_kernel(const CombineParams p)
+// Four values, for tokens to FP32 rows.
+__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[8], int i)
 {
-    __shared__ float part[kMaxTop][8];
+    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+    v[i] = __uint_as_float(w.x << 16), v[i + 1] = __uint_as_float(w.x & 0xffff0000u);
+    v[i + 2] = __uint_as_float(w.y << 16), v[i + 3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float *p, float (&v)[8], int i)
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+    v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+}
+
+// A block's 256 threads are one token's or, of short rows, several tokens', G threads
+// each.  A thread has C vectors of 8 values of dy at a time, which stay in registers for
+// the token's rows, of which U are under way at once.  (DW: with the weights' gradients.)
+// With a token a block, of as many threads as its row has vectors, 100000 tokens of 2 x 256
+// took 101 us, their gradients 101 (26 and 49 so), 4096 of 8 x 7168 195 (166).  Of more U or
+// C hold registers that more blocks would have: 8191 x 2 x 4096 57 us, with U = 4 73.
+template <int C, int U, bool DW, typename RT, typename OT>
+__global__ void __launch_bounds__(256)
+    combine_grad_kernel(const CombineParams p, int G)
+{
+    // (FP32 rows that are only written: a warp's stores lie side by side, 16 bytes a lane)
+    constexpr bool kSplit = !DW && sizeof(RT) == 4;
+    __shared__ float part[DW ? kMaxTop : 1][8];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t t = blockIdx.x;
+    const int tokens = 256 / G, mine = __shfl_sync(kFull, int(threadIdx.x) / G, 0), thread = int(threadIdx.x) - mine * G;   // (uniform)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = G * 8;
+    const int64_t t0 = int64_t(blockIdx.x) * tokens, t = t0 + mine;
+    const int top_k = t < p.T ? p.top_k : 0;
     const int32_t *position = p.position + t * p.top_k;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = int(blockDim.x) * 8;
     const OT *dy = static_cast<const OT *>(p.d_out) + t * p.K;
-    float g[8] = {};
-    if (int(threadIdx.x) * 8 < p.K) load8(dy + threadIdx.x * 8, g);
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t m = position[j];
-        const bool row = m >= 0 && m < p.M;
-        const float w = p.weight ? p.weight[t * p.top_k + j] : 1.0f;
-        float dot = 0.0f;
-        if (row)
-            for (int k = int(threadIdx.x) * 8; k < p.K; k += step) {
-                float d[8];
-                if (k >= step) load8(dy + k, g);
-                if (p.d_weight) {
-                    float v[8];
-                    load8(static_cast<const RT *>(p.rows) + m * p.K + k, v);
+    for (int32_t k0 = 0; k0 < p.K; k0 += C * step) {
+        const int32_t k = k0 + thread * 8, ka = k0 + (thread & ~31) * 8 + lane * 4;
+        float g[C][8] = {};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = w * g[i];
-                store8(static_cast<RT *>(p.d_rows) + m * p.K + k, d);
+        for (int c = 0; c < C; ++c)
+            if constexpr (kSplit) {
+                if (top_k > 0 && ka + c * step < p.K) load4(dy + ka + c * step, g[c], 0);
+                if (top_k > 0 && ka + c * step + 128 < p.K) load4(dy + ka + c * step + 128, g[c], 4);
+            } else if (top_k > 0 && k + c * step < p.K) {
+                load8(dy + k + c * step, g[c]);
             }
-        if (p.K > step && int(threadIdx.x) * 8 < p.K) load8(dy + threadIdx.x * 8, g);
-        if (p.d_weight) {
+        for (int j0 = 0; j0 < top_k; j0 += U) {
+            int64_t m[U];
+            float dot[U] = {}, v[DW ? U : 1][DW ? C : 1][8] = {};
 #pragma unroll
-            for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(kFull, dot, s);
-            if (lane == 0) part[j][warp] = dot;
+            for (int u = 0; u < U; ++u) {
+                m[u] = j0 + u < top_k ? position[j0 + u] : -1;
+                if (m[u] >= p.M) m[u] = -1;
+                if constexpr (DW) {
+                    if (m[u] >= 0)
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+                            if (k + c * step < p.K) load8(static_cast<const RT *>(p.rows) + m[u] * p.K + k + c * step, v[u][c]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (m[u] < 0) continue;
+                const float w = p.weight ? p.weight[t * p.top_k + j0 + u] : 1.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float d[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if constexpr (DW) dot[u] = fmaf(g[c][i], v[u][c][i], dot[u]);
+                        d[i] = w * g[c][i];
+                    }
+                    RT *to = static_cast<RT *>(p.d_rows) + m[u] * p.K + c * step;
+                    if constexpr (kSplit) {
+                        if (ka + c * step < p.K) __stcs(reinterpret_cast<float4 *>(to + ka), make_float4(d[0], d[1], d[2], d[3]));
+                        if (ka + c * step + 128 < p.K) __stcs(reinterpret_cast<float4 *>(to + ka + 128), make_float4(d[4], d[5], d[6], d[7]));
+                    } else if (k + c * step < p.K) {
+                        store8(to + k, d);
+                    }
+                }
+            }
+            if constexpr (DW) {
+#pragma unroll
+                for (int s = 16; s; s >>= 1)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(kFull, dot[u], s);
+                if (lane == 0)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (j0 + u < top_k) part[j0 + u][warp] = k0 == 0 ? dot[u] : part[j0 + u][warp] + dot[u];
+            }
         }
     }
-    if (!p.d_weight) return;
-    __syncthreads();
-    if (int(threadIdx.x) < p.top_k) {
-        float sum = 0.0f;
-        for (int w = 0; w < int(blockDim.x) / 32; ++w) sum += part[threadIdx.x][w];
-        p.d_weight[t * p.top_k + threadIdx.x] = sum;
+    if constexpr (DW) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < tokens * p.top_k; i += 256) {
+            const int of = i / p.top_k, j = i % p.top_k;
+            if (t0 + of >= p.T) break;
+            float sum = 0.0f;
+            for (int w = 0; w < G / 32; ++w) sum += part[j][of * (G / 32) + w];
+            p.d_weight[t0 * p.top_k + i] = sum;
+        }
     }
 }
 
@@ -151,8 +206,8 @@ bool pdl_enabled()
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, int threads, cudaStream_t stream)
+template <typename Kernel, typename... More>
+cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, int threads, cudaStream_t stream, More... more)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
@@ -165,7 +220,7 @@ cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, 
     cfg.gridDim = dim3(unsigned(T), unsigned(parts), 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, more...);
 }
 
 int check(int64_t T, int64_t M, int32_t top_k, int32_t K, int rows_dtype, int out_dtype)
@@ -246,15 +301,30 @@ int cake_gg_combine_grad(int64_t T, int64_t M, int32_t top_k, int32_t K, const v
     p.M = M;
     p.top_k = top_k;
     p.K = K;
-    const int threads = threads_for(K);
+    int G = 32;
+    while (G < 256 && G * 8 < K) G *= 2;
+    const int vectors = (K / 8 + G - 1) / G;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t err;
-    if (rows_dtype == CAKE_GG_BF16)
-        err = out_dtype == CAKE_GG_BF16 ? launch(combine_grad_kernel<uint16_t, uint16_t>, p, T, 1, threads, s)
-                                        : launch(combine_grad_kernel<uint16_t, float>, p, T, 1, threads, s);
-    else
-        err = out_dtype == CAKE_GG_BF16 ? launch(combine_grad_kernel<float, uint16_t>, p, T, 1, threads, s)
-                                        : launch(combine_grad_kernel<float, float>, p, T, 1, threads, s);
+    const int64_t blocks = (T + 256 / G - 1) / (256 / G);
+    using one = std::integral_constant<int, 1>;
+    using two = std::integral_constant<int, 2>;
+    using four = std::integral_constant<int, 4>;
+    auto run = [&](auto rows_of, auto out_of) {
+        using RT = decltype(rows_of);
+        using OT = decltype(out_of);
+        auto go = [&](auto c, auto u, auto dw) {
+            return launch(combine_grad_kernel<decltype(c)::value, decltype(u)::value, decltype(dw)::value, RT, OT>, p, blocks, 1, 256, s, G);
+        };
+        // (8191 tokens to 2 rows x 4096: 31.5 us by one vector at a time, 30.6 by two; 16384 to
+        // 2 x 2048, where the second is past the row, 31.9 and 33.0)
+        if (!d_weight) return vectors == 1 ? go(one(), one(), std::false_type()) : go(two(), one(), std::false_type());
+        // (16384 x 1 x 4096 72 us, two rows at a time 85; 42 tokens of 8 x 3128 FP32 6.1 us four at a time, 6.9 two)
+        return top_k == 1       ? go(one(), one(), std::true_type())
+               : blocks <= 152 ? go(one(), four(), std::true_type())
+                               : go(one(), two(), std::true_type());
+    };
+    const bool r16 = rows_dtype == CAKE_GG_BF16, o16 = out_dtype == CAKE_GG_BF16;
+    const cudaError_t err = r16 ? (o16 ? run(uint16_t(), uint16_t()) : run(uint16_t(), float())) : (o16 ? run(float(), uint16_t()) : run(float(), float()));
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 

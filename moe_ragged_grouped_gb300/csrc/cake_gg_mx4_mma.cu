@@ -38,7 +38,7 @@ namespace cakegg {
 namespace {
 
 constexpr int kThreads = 512, kThreadsRouted = 608;
-constexpr int kStoreWarp0 = 2, kStoreWarps = 8, kStoreThreads = kStoreWarps * 32;
+constexpr int kStoreWarp0 = 2, kStoreWarps = 8;
 constexpr int kScaleWarp0 = 10, kScaleWarps = 4;
 constexpr int kCopyWarp = 14;
 constexpr int kRowsWarp0 = 15, kGatherWarps = 4;

@@ -9,7 +9,7 @@ using namespace cakegg;
 
 namespace {
 
-constexpr int kThreads = kRouteThreads, kWarps = kThreads / 32;
+constexpr int kThreads = kRouteThreads;
 constexpr int32_t kMaxExperts = kRouteMaxExperts, kMaxTop = 32, kMaxGroups = 32;
 constexpr int64_t kMaxTokens = 1 << 23;        // (a block's tokens are below 2^16)
 constexpr int kClusterBlocks = 8;
