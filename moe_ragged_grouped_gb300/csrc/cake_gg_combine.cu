@@ -52,6 +52,24 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
 
+// Four values, for tokens to FP32 rows.
+__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[8], int i)
+{
+    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+    v[i] = __uint_as_float(w.x << 16), v[i + 1] = __uint_as_float(w.x & 0xffff0000u);
+    v[i + 2] = __uint_as_float(w.y << 16), v[i + 3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float *p, float (&v)[8], int i)
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+    v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+}
+
+__device__ __forceinline__ void store4(float *p, const float (&v)[8], int i)
+{
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+}
+
 struct CombineParams {
     const void *rows;         // r [M, K]
     const int32_t *position;  // [T, top_k]
@@ -64,23 +82,31 @@ struct CombineParams {
     int32_t top_k, K;
 };
 
-// A block has N tokens and 8 values a thread of a part of their rows.  Bound by HBM
-// and by the loads in flight: two tokens where one has few rows or short ones.
-template <int N, typename RT, typename OT>
+// A block has N tokens and 8 values a thread of a part of their rows, or, of short rows,
+// N tokens for each G threads (100000 of 2 x 256 31 us, with blocks of 32 threads 51; but
+// 32768 of 4 x 512 35, with blocks of 64 threads 30).  Bound by HBM and by the loads in
+// flight: two tokens where one has few rows or short ones.
+template <int N, bool SHORT, typename RT, typename OT>
 __global__ void __launch_bounds__(256)
-    combine_kernel(const CombineParams p)
+    combine_kernel(const CombineParams p, int G)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t t = int64_t(blockIdx.x) * N;
-    const int32_t k = int32_t(blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    int64_t t = int64_t(blockIdx.x) * N;
+    int thread = int(threadIdx.x);
+    if (SHORT) {
+        const int mine = __shfl_sync(kFull, thread / G, 0);
+        t = (int64_t(blockIdx.x) * (256 / G) + mine) * N;
+        thread -= mine * G;
+    }
+    const int32_t k = int32_t(blockIdx.y * blockDim.x) * 8 + thread * 8;
     if (k >= p.K) return;
     float sum[N][8] = {};
 #pragma unroll 4
     for (int j = 0; j < p.top_k; ++j)
 #pragma unroll
         for (int h = 0; h < N; ++h) {
-            if (h > 0 && t + h >= p.T) continue;
+            if ((SHORT || h > 0) && t + h >= p.T) continue;
             const int64_t at = (t + h) * p.top_k + j, m = p.position[at];
             const float w = p.weight ? p.weight[at] : 1.0f;
             if (m < 0 || m >= p.M) continue;
@@ -91,20 +117,7 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
     for (int h = 0; h < N; ++h)
-        if (h == 0 || t + h < p.T) store8(static_cast<OT *>(p.out) + (t + h) * p.K + k, sum[h]);
-}
-
-// Four values, for tokens to FP32 rows.
-__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[8], int i)
-{
-    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
-    v[i] = __uint_as_float(w.x << 16), v[i + 1] = __uint_as_float(w.x & 0xffff0000u);
-    v[i + 2] = __uint_as_float(w.y << 16), v[i + 3] = __uint_as_float(w.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load4(const float *p, float (&v)[8], int i)
-{
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
-    v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+        if ((!SHORT && h == 0) || t + h < p.T) store8(static_cast<OT *>(p.out) + (t + h) * p.K + k, sum[h]);
 }
 
 // A block's 256 threads are one token's or, of short rows, several tokens', G threads
@@ -167,8 +180,8 @@ __global__ void __launch_bounds__(256)
                     }
                     RT *to = static_cast<RT *>(p.d_rows) + m[u] * p.K + c * step;
                     if constexpr (kSplit) {
-                        if (ka + c * step < p.K) __stcs(reinterpret_cast<float4 *>(to + ka), make_float4(d[0], d[1], d[2], d[3]));
-                        if (ka + c * step + 128 < p.K) __stcs(reinterpret_cast<float4 *>(to + ka + 128), make_float4(d[4], d[5], d[6], d[7]));
+                        if (ka + c * step < p.K) store4(to + ka, d, 0);
+                        if (ka + c * step + 128 < p.K) store4(to + ka + 128, d, 4);
                     } else if (k + c * step < p.K) {
                         store8(to + k, d);
                     }
@@ -207,7 +220,7 @@ bool pdl_enabled()
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <typename Kernel, typename... More>
-cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, int threads, cudaStream_t stream, More... more)
+cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t blocks, int parts, int threads, cudaStream_t stream, More... more)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
@@ -217,7 +230,7 @@ cudaError_t launch(Kernel kernel, const CombineParams &p, int64_t T, int parts, 
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
     }
-    cfg.gridDim = dim3(unsigned(T), unsigned(parts), 1);
+    cfg.gridDim = dim3(unsigned(blocks), unsigned(parts), 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, kernel, p, more...);
@@ -233,11 +246,12 @@ int check(int64_t T, int64_t M, int32_t top_k, int32_t K, int rows_dtype, int ou
     return CAKE_GG_OK;
 }
 
-// Threads of a block for rows of K values, 8 a thread: whole warps, up to 256.
+// Threads for a token's row of K values, 8 a thread, up to 256: a power of two, whole warps.
 int threads_for(int32_t K)
 {
-    const int n = (K / 8 + 31) / 32 * 32;
-    return n > 256 ? 256 : n;
+    int G = 32;
+    while (G < 256 && G * 8 < K) G *= 2;
+    return G;
 }
 
 }  // namespace
@@ -263,16 +277,19 @@ int cake_gg_combine_rows(int64_t T, int64_t M, int32_t top_k, int32_t K, const v
     p.M = M;
     p.top_k = top_k;
     p.K = K;
-    const int threads = threads_for(K), parts = (K / 8 + threads - 1) / threads;
+    const int warps = (K / 8 + 31) / 32, G = threads_for(K);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // (BF16 16384 tokens of 2 rows x 4096: 68 us with two tokens a block, 69 with one, 32768 of
     // 4 x 512 31 and 34, but 8192 of 4 x 6144 85 and 84)
-    const bool two = T > 1 && (top_k <= 2 || K <= 1024);
+    const bool two = T > 1 && (top_k <= 2 || K <= 1024), few = T > 1 && top_k * K <= 1024;
+    const int threads = few || warps >= 8 ? 256 : warps * 32, parts = (warps * 32 + threads - 1) / threads;
+    const int64_t tokens = (few ? 256 / G : 1) * (two ? 2 : 1), blocks = (T + tokens - 1) / tokens;
     auto run = [&](auto rows_of, auto out_of) {
         using RT = decltype(rows_of);
         using OT = decltype(out_of);
-        return two ? launch(combine_kernel<2, RT, OT>, p, (T + 1) / 2, parts, threads, s)
-                   : launch(combine_kernel<1, RT, OT>, p, T, parts, threads, s);
+        return few   ? launch(combine_kernel<2, true, RT, OT>, p, blocks, parts, threads, s, G)
+               : two ? launch(combine_kernel<2, false, RT, OT>, p, blocks, parts, threads, s, G)
+                     : launch(combine_kernel<1, false, RT, OT>, p, blocks, parts, threads, s, G);
     };
     const bool r16 = rows_dtype == CAKE_GG_BF16, o16 = out_dtype == CAKE_GG_BF16;
     const cudaError_t err = r16 ? (o16 ? run(uint16_t(), uint16_t()) : run(uint16_t(), float())) : (o16 ? run(float(), uint16_t()) : run(float(), float()));
@@ -301,8 +318,7 @@ int cake_gg_combine_grad(int64_t T, int64_t M, int32_t top_k, int32_t K, const v
     p.M = M;
     p.top_k = top_k;
     p.K = K;
-    int G = 32;
-    while (G < 256 && G * 8 < K) G *= 2;
+    const int G = threads_for(K);
     const int vectors = (K / 8 + G - 1) / G;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t blocks = (T + 256 / G - 1) / (256 / G);

@@ -462,3 +462,40 @@ def test_groups_that_are_close(with_bias, score):
     for group_score in ("max", "top2"):
         o = dict(score=score, bias=bias if with_bias else None, groups=groups, top_groups=3, group_score=group_score)
         check(gg.route(logits, 6, **o), reference(logits, 6, **o))
+
+
+SHORT = [(1000, 1, 8), (13, 2, 256), (1001, 4, 256), (9, 3, 264), (50, 5, 128), (77, 1, 520), (2, 1, 1024), (31, 2, 1032), (700, 6, 1000), (160, 3, 4104)]
+
+
+@pytest.mark.parametrize("rows_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,top_k,K", SHORT)
+def test_short_rows(T, top_k, K, out_dtype, rows_dtype):
+    """Several tokens a block, the last of them not there; and more blocks than multiprocessors."""
+    test_combine(T, top_k, K, True, out_dtype, rows_dtype)
+    test_combine_grad(T, top_k, K, out_dtype, rows_dtype)
+
+
+@pytest.mark.parametrize("T,top_k,K", [(7, 2, 128), (301, 4, 256), (11, 3, 2056)])
+def test_short_rows_and_what_is_beside_them(T, top_k, K):
+    """Positions that are no rows, and the memory around what is written, by every kernel."""
+    import torch
+    from gg_testutil import guarded_empty, guards_intact
+    position, r, w, _ = rows_case(T, top_k, K, "fp32", 1)
+    position[::2, -1], position[T - 1, 0] = -1, T * top_k
+    ok = (position >= 0) & (position < T * top_k)
+    at = position.clamp(0, T * top_k - 1).long()
+    buf, view, guard = guarded_empty((T, K), "fp32")
+    gg.combine_rows(r, position, w, out=view, out_dtype="fp32")
+    terms = r.double()[at] * (w * ok)[:, :, None].double()
+    assert guards_intact(buf, guard, T * K, "fp32")
+    assert bool(((view.double() - terms.sum(dim=1)).abs() <= top_k * 2.0 ** -24 * terms.abs().sum(dim=1)).all())
+    for give in (lambda out: gg.combine_grad(r[:T], r, position, w, out=out)[1], lambda out: gg.gather_rows(r[:T], position, out=out)):
+        buf, view, guard = guarded_empty((T * top_k, K), "fp32")
+        got = give(view)
+        assert guards_intact(buf, guard, T * top_k * K, "fp32")
+        named = torch.zeros(T * top_k, dtype=torch.bool, device="cuda")
+        named[position[ok].long()] = True
+        assert bool(torch.isnan(view[~named]).all()) and bool(torch.isfinite(view[named]).all())
+        if got.shape == (T, top_k):
+            assert not got[~ok].any()
