@@ -459,7 +459,7 @@ int cake_gg_mx4_plan(cake_gg_mx4_plan_t *plan, int32_t E, int64_t M_max, int64_t
 
 /* The product.  X, xs, W, ws, Y, workspace: device pointers, 16-byte aligned;
  * rows, offsets 4-byte aligned.  The workspace is plan->workspace_bytes,
- * zero-filled once after allocation.  Enqueues one or two kernels on `stream`;
+ * zero-filled once after allocation.  Enqueues one to three kernels on `stream`;
  * allocates nothing, never synchronises.  Errors as cake_gg_i8_gemm's. */
 int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_t *xs, const int32_t *rows,
                      const uint8_t *W, const uint8_t *ws, void *Y, const int32_t *offsets, void *workspace,
