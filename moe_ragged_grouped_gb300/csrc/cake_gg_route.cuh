@@ -17,9 +17,9 @@
 //
 // Rows are numbered by counting: for each expert a bit per token of the block says
 // who chose it, so a token's place among them is a population count, in the
-// order of the tokens and the same on every run.  Up to a token for each of its warps one cluster of
-// blocks does it all, counts read from one another's shared memory; more tokens
-// take a kernel that counts and one that numbers.
+// order of the tokens and the same on every run.  As many tokens as a cluster of blocks
+// has warps are that cluster's, counts read from one another's shared memory; more
+// tokens take a kernel that counts and one that numbers.
 //
 // Included by the translation units that hold the kernels of some experts a lane.
 #pragma once
