@@ -10,10 +10,9 @@ using namespace cakegg;
 namespace {
 
 constexpr int kThreads = kRouteThreads;
-constexpr int32_t kMaxExperts = kRouteMaxExperts, kMaxTop = 32, kMaxGroups = 32;
+constexpr int32_t kMaxExperts = kRouteMaxExperts, kMaxTop = kRouteMaxTop, kMaxGroups = 32;
 constexpr int64_t kMaxTokens = 1 << 23;        // (a block's tokens are below 2^16)
 constexpr int kClusterBlocks = 8;
-constexpr int kChunk = 1024;                   // tokens that a block numbers at a time, at most
 constexpr int kSms = 152;
 constexpr uint64_t kHeader = 256;              // (as in the products' workspaces; its status word stays 0)
 
@@ -176,7 +175,7 @@ int cake_gg_route(const cake_gg_route_plan_t *plan, const cake_gg_route_options_
     p.renormalize = op.renormalize != 0;
     p.scale = op.scale;
     p.block_tokens = pl.block_tokens;
-    p.chunk = pl.block_tokens < kChunk ? pl.block_tokens : kChunk;
+    p.chunk = pl.block_tokens < kRouteChunk ? pl.block_tokens : kRouteChunk;
     p.div_top = uint32_t((uint64_t(1) << 32) / uint32_t(pl.top_k) + ((uint64_t(1) << 32) % uint32_t(pl.top_k) != 0));
     const int32_t size = pl.E / op.groups;
     p.div_group = uint32_t(((1 << 20) + size - 1) / size);

@@ -26,6 +26,7 @@
 
 #include "cake_gg_ptx.cuh"
 #include "cake_gg_route.h"
+#include "cake_gg_shared_limit.h"
 
 namespace cakegg {
 namespace {
@@ -945,6 +946,11 @@ cudaError_t launch_route(const RouteParams &p, int blocks, bool cluster, size_t 
 {
     auto with_mode = [&](auto mode) {
         constexpr Mode MODE = decltype(mode)::value;
+        // (a cluster's blocks have a few tokens each)
+        if (!cluster && shared > kRouteSharedDefault) {
+            const cudaError_t err = raise_shared_limit<route_count_kernel<VPL, MODE>>(route_shared_bytes(VPL * 32, kRouteMaxTop, kRouteChunk));
+            if (err != cudaSuccess) return err;
+        }
         return cluster ? route_launch(route_cluster_kernel<VPL, MODE>, p, blocks, kThreadsOf<VPL>, shared, blocks, stream)
                        : route_launch(route_count_kernel<VPL, MODE>, p, blocks, kThreadsOf<VPL>, shared, 1, stream);
     };

@@ -18,6 +18,9 @@ int device_sms(int *sms);   // (cake_gg_capi.cu)
 constexpr int kRouteThreads = 1024;            // of a block that routes up to kRouteNarrow experts, half beyond
 constexpr int32_t kRouteNarrow = 256;
 constexpr int32_t kRouteMaxExperts = 1024;
+constexpr int32_t kRouteMaxTop = 32;
+constexpr int kRouteChunk = 1024;              // tokens that a block numbers at a time, at most
+constexpr size_t kRouteSharedDefault = 48 << 10;   // what a launch may take without asking
 
 struct RouteParams {
     const void *logits;
@@ -47,7 +50,7 @@ struct RouteGradParams {
 // experts' first words then lie in different banks.
 __host__ __device__ constexpr int bit_words(int tokens) { return ((tokens + 31) / 32) | 1; }
 // Shared memory of a block: bits, counts, where rows begin, what was chosen.
-inline size_t route_shared_bytes(int32_t E, int32_t top_k, int chunk)
+constexpr size_t route_shared_bytes(int32_t E, int32_t top_k, int chunk)
 {
     return size_t(E) * bit_words(chunk) * 4 + size_t(E) * 8 + (size_t(chunk) * top_k * 2 + 15) / 16 * 16;
 }
@@ -99,10 +102,6 @@ cudaError_t route_launch(Kernel kernel, const Params &p, int64_t blocks, int thr
     if (pdl_enabled()) {
         attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[na++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (shared > 48 << 10) {
-        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared));
-        if (err != cudaSuccess) return err;
     }
     cfg.gridDim = dim3(unsigned(blocks), 1, 1);
     cfg.blockDim = dim3(unsigned(threads), 1, 1);
