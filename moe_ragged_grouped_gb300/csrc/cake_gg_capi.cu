@@ -1183,13 +1183,7 @@ int cake_gg_corun_spinner(int32_t ctas, uint64_t ns, void *stream)
     DevInfo dev;
     int rc = device_info(&dev);
     if (rc != CAKE_GG_OK) return rc;
-    static bool attr = false;
-    if (!attr) {
-        if (cudaFuncSetAttribute(corun_spinner_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(kSmemOptInLimit)) != cudaSuccess)
-            return CAKE_GG_ERR_CUDA;
-        attr = true;
-    }
+    if (raise_shared_limit<corun_spinner_kernel>(kSmemOptInLimit) != cudaSuccess) return CAKE_GG_ERR_CUDA;
     corun_spinner_kernel<<<ctas, 32, kSmemOptInLimit, static_cast<cudaStream_t>(stream)>>>(ns);
     return cudaGetLastError() == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }

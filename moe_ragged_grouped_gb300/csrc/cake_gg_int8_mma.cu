@@ -31,10 +31,13 @@
 // groups on alternate stages), warp 18 copies rows, or, where they are routed,
 // warps 18-21 gather them, two on every other stage (the first issue of a batch
 // of copies takes a few hundred clocks: all four on every stage were late).
+#include <type_traits>
+
 #include "cake_gg_int8.h"
 #include "cake_gg_int8_widen.cuh"
 #include "cake_gg_ptx.cuh"
 #include "cake_gg_roles.cuh"
+#include "cake_gg_shared_limit.h"
 
 namespace cakegg {
 namespace {
@@ -568,23 +571,6 @@ __global__ void __maxnreg__(80)
     }
 }
 
-// The opt-in limit of shared memory, raised once per device.
-template <int PAIR, bool OUT_F32>
-cudaError_t raise_limit()
-{
-    static bool raised[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!raised[dev]) {
-        err = cudaFuncSetAttribute(i8_mma_kernel<PAIR, OUT_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kI8SmemLimit));
-        if (err != cudaSuccess) return err;
-        raised[dev] = true;
-    }
-    return cudaSuccess;
-}
-
 template <int PAIR, bool OUT_F32>
 cudaError_t launch(const I8MmaLaunch &l, bool pdl, cudaStream_t stream)
 {
@@ -655,8 +641,11 @@ int prepare_i8_mma(I8MmaLaunch *l, const I8MmaParams &p0, const uint16_t *q, int
     }
     l->pair = pair;
     l->grid = int32_t(grid);
-    const cudaError_t err = pair == 2 ? (p.b.out_f32 ? raise_limit<2, true>() : raise_limit<2, false>())
-                                      : (p.b.out_f32 ? raise_limit<1, true>() : raise_limit<1, false>());
+    auto raise = [&](auto f32) {
+        return pair == 2 ? raise_shared_limit<i8_mma_kernel<2, decltype(f32)::value>>(kI8SmemLimit)
+                         : raise_shared_limit<i8_mma_kernel<1, decltype(f32)::value>>(kI8SmemLimit);
+    };
+    const cudaError_t err = p.b.out_f32 ? raise(std::true_type()) : raise(std::false_type());
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 

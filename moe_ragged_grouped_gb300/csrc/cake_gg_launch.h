@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "cake_gg_kernel.cuh"
+#include "cake_gg_shared_limit.h"
 
 namespace cakegg {
 
@@ -23,19 +24,10 @@ template <int MODE, bool SWAP, bool OUT_F32, int PAIR>
 cudaError_t launch_one(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o, const KParams &p,
                        int grid, size_t smem, cudaStream_t stream)
 {
-    auto kern = cake_gg_kernel<MODE, SWAP, OUT_F32, PAIR>;
-    // the opt-in shared-memory limit is raised once per device to the maximum,
-    // so later calls (including ones under stream capture) skip the attribute call
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    constexpr auto kern = cake_gg_kernel<MODE, SWAP, OUT_F32, PAIR>;
+    // (later calls, ones under stream capture among them, skip the attribute call)
+    cudaError_t err = raise_shared_limit<kern>(kSmemOptInLimit);
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemOptInLimit));
-        if (err != cudaSuccess) return err;
-        attr_set[dev] = true;
-    }
     if (smem > kSmemOptInLimit) return cudaErrorInvalidValue;
     // clusters: a CTA pair, the CTAs of a cluster split, or its pairs
     const int cluster = PAIR * (p.csplit > 0 ? p.csplit : 1);

@@ -33,6 +33,7 @@
 #include "cake_gg_mx4.h"
 #include "cake_gg_ptx.cuh"
 #include "cake_gg_roles.cuh"
+#include "cake_gg_shared_limit.h"
 
 namespace cakegg {
 namespace {
@@ -698,23 +699,6 @@ __global__ void __maxnreg__(96)
     }
 }
 
-// The opt-in limit of shared memory, raised once per device.
-template <int PAIR, bool OUT_F32>
-cudaError_t raise_limit()
-{
-    static bool raised[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!raised[dev]) {
-        err = cudaFuncSetAttribute(mx4_mma_kernel<PAIR, OUT_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMx4SmemLimit));
-        if (err != cudaSuccess) return err;
-        raised[dev] = true;
-    }
-    return cudaSuccess;
-}
-
 template <int PAIR, bool OUT_F32>
 cudaError_t launch(const Mx4Launch &l, bool pdl, cudaStream_t stream)
 {
@@ -800,8 +784,11 @@ int prepare_mx4_mma(Mx4Launch *l, const Mx4Params &p0, const uint8_t *W, const u
     }
     l->pair = pair;
     l->grid = int32_t(grid);
-    const cudaError_t err = pair == 2 ? (p.out_f32 ? raise_limit<2, true>() : raise_limit<2, false>())
-                                      : (p.out_f32 ? raise_limit<1, true>() : raise_limit<1, false>());
+    auto raise = [&](auto f32) {
+        return pair == 2 ? raise_shared_limit<mx4_mma_kernel<2, decltype(f32)::value>>(kMx4SmemLimit)
+                         : raise_shared_limit<mx4_mma_kernel<1, decltype(f32)::value>>(kMx4SmemLimit);
+    };
+    const cudaError_t err = p.out_f32 ? raise(std::true_type()) : raise(std::false_type());
     return err == cudaSuccess ? CAKE_GG_OK : CAKE_GG_ERR_CUDA;
 }
 

@@ -23,6 +23,7 @@
 #include "cake_gg_mx4.h"
 #include "cake_gg_mx4_quant.cuh"
 #include "cake_gg_ptx.cuh"
+#include "cake_gg_shared_limit.h"
 
 namespace cakegg {
 namespace {
@@ -222,16 +223,8 @@ size_t rows_smem(int R, int32_t K) { return size_t(R) * K + size_t(R) * (K / 32)
 template <int R, typename XT>
 cudaError_t launch(const Mx4Params &p, const void *X, const uint8_t *W, const uint8_t *ws, bool pdl, cudaStream_t stream)
 {
-    static bool raised[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    const cudaError_t err = raise_shared_limit<mx4_rows_kernel<R, XT>>(kMx4SmemLimit);
     if (err != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!raised[dev]) {
-        err = cudaFuncSetAttribute(mx4_rows_kernel<R, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMx4SmemLimit));
-        if (err != cudaSuccess) return err;
-        raised[dev] = true;
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     if (pdl) {

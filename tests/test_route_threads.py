@@ -42,3 +42,41 @@ def test_two_threads_route_other_sizes(E, sizes):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["mx4", "i8"])
+def test_threads_multiply_at_once(kind):
+    """Products of sizes that take every kernel, each thread's on a stream of its own: as by one thread."""
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    gg_build.build()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N, K = 520, 1024
+    w = torch.randn((N, K), generator=g, device="cuda")
+    q, s = gg.quantize_mx4(w) if kind == "mx4" else gg.quantize_rows(w)
+    multiply = gg.mx4_gemm if kind == "mx4" else gg.int8_gemm
+    xs = [torch.randn((T, K), generator=g, device="cuda").to(torch.bfloat16) for T in (1, 2, 40, 700, 3000)]
+    torch.cuda.synchronize()
+    got, failed = [None] * len(xs), []
+    start = threading.Barrier(len(xs))
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                start.wait(60)
+                got[i] = [multiply(xs[i], q, s, out_dtype=kind, check=False) for kind in ("bf16", "fp32") * 20][-2:]
+                stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for x, (a, b) in zip(xs, got):
+        assert torch.equal(a, multiply(x, q, s)) and torch.equal(b, multiply(x, q, s, out_dtype="fp32"))
