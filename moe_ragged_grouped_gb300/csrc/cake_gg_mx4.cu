@@ -88,6 +88,10 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
 // (a b).)  In FP32: two units in the last place of the exponential, a half each of the
 // sum, the quotient and the product: below 2^-20.  And in 64 bits.
 constexpr float kFastError = 0x1p-18f, kSlowError = 0x1p-20f, kFastFrom = -40.0f, kSlowFrom = -80.0f;
+// FP32's is of the normal range: half of a gate below kSlowGate may not be in it, whatever u
+// makes of it, nor a value that a block of a scale below kSlowScale tells from its neighbours.
+constexpr float kSlowGate = 0x1p-120f;
+constexpr uint32_t kSlowScale = 8;
 
 __device__ __forceinline__ void gate_fast(const float (&g)[8], const float (&u)[8], float (&h)[8])
 {
@@ -131,18 +135,22 @@ __device__ __forceinline__ uint32_t codes8_known(const float (&h)[8], uint32_t m
 
 // What the approximate instructions leave open (one block of some thousand): FP32,
 // and where that cannot tell either on which side of a border between two codes,
-// or between two scales, a value lies, 64 bits; and where a negative g's exponential
-// leaves FP32's range.
+// or between two scales, a value lies, 64 bits; and where a negative g's exponential, or
+// what FP32 makes of a small value, leaves its range.
 __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (&u)[8], uint32_t *byte)
 {
     float h[8], least = 0.0f;
+    bool tiny = false, some = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         h[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
         least = fminf(least, g[j]);
+        const bool counts = g[j] != 0.0f && u[j] != 0.0f;
+        some = some || counts;
+        tiny = tiny || (counts && fabsf(g[j]) < kSlowGate);
     }
     uint32_t unsure, w = codes8_known(h, block_max(largest8(h)), kSlowError, byte, &unsure);
-    const bool whole = unsure == ~0u || (*byte != 255 && least < kSlowFrom);
+    const bool whole = unsure == ~0u || (*byte != 255 && (least < kSlowFrom || tiny || (some && *byte < kSlowScale)));
     if (__any_sync(0xffffffffu, whole)) {
         double m = 0.0;
 #pragma unroll

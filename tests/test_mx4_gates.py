@@ -1,0 +1,56 @@
+"""Gated values at the ends of FP32's range: the codes are the rounding of silu(g) u itself."""
+import pytest
+
+from moe_ragged_grouped_gb300 import build as gg_build
+from moe_ragged_grouped_gb300 import cake_gg as gg
+from test_mx4_gpu import gated, quantised, same, unpacked
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    gg_build.build()
+
+
+def check(gate, u):
+    """Codes and scales, bit for bit."""
+    import torch
+    x = torch.cat([gate, u], dim=1).float().contiguous()
+    code, byte = unpacked(*gg.quantize_mx4(x, act="silu_mul"))
+    want = quantised(gated(x))
+    assert same(byte, want[1]), (byte - want[1]).nonzero()[:4]
+    assert same(code, want[0]), (code - want[0]).nonzero()[:4]
+
+
+@pytest.mark.parametrize("up", [40, 50, 100, 127])
+def test_subnormal_gates(up):
+    """A gate below the normal range, halved by the sigmoid, does not fit FP32; with a large u the product does."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(up)
+    whole = torch.randint(-64, 65, (512, 64), generator=g, device="cuda")
+    whole[0, :4] = torch.tensor([12, 1, 3, 5], device="cuda")
+    whole[0, 4:] = 0
+    gate = (whole.double() * 2.0 ** -149).float()
+    check(gate, torch.full_like(gate, 2.0 ** up))
+    check(gate, -torch.full_like(gate, 2.0 ** up) * (1 + torch.rand(gate.shape, generator=g, device="cuda")).clamp(max=1.9))
+
+
+@pytest.mark.parametrize("least", [-149, -130, -126, -120])
+def test_tiny_gates_beside_ordinary_ones(least):
+    """Rows in which some blocks have tiny gates and others lie on borders, so that all of a warp's are looked at again."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(-least)
+    gate = torch.randn((256, 256), generator=g, device="cuda")
+    tiny = torch.rand((256, 8), generator=g, device="cuda").repeat_interleave(32, dim=1) < 0.5
+    u = torch.randn((256, 256), generator=g, device="cuda")
+    power = torch.randint(least, least + 6, (256, 256), generator=g, device="cuda").double()
+    gate = torch.where(tiny, (torch.sign(gate).double() * (1 + torch.rand((256, 256), generator=g, device="cuda").double()) * 2.0 ** power).float(), gate)
+    u = torch.where(tiny, torch.sign(u) * 2.0 ** 126 * (1 + torch.rand((256, 256), generator=g, device="cuda")), u)
+    # (the first block of every other row: values on a border)
+    u[::2, :32] = (1.25 / (gate[::2, :32].double() / (1 + (-gate[::2, :32].double()).exp()))).clamp(-3e38, 3e38).float()
+    u[::2, 0] = (4.5 / (gate[::2, 0].double() / (1 + (-gate[::2, 0].double()).exp()))).clamp(-3e38, 3e38).float()
+    check(gate, u)
