@@ -140,7 +140,7 @@ __device__ __forceinline__ uint32_t codes8_known(const float (&h)[8], uint32_t m
 __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (&u)[8], uint32_t *byte)
 {
     float h[8], least = 0.0f;
-    bool tiny = false, some = false;
+    bool tiny = false, some = false, over = false;               // (over: FP32 has no such product, 64 bits may)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         h[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
@@ -148,20 +148,25 @@ __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (
         const bool counts = g[j] != 0.0f && u[j] != 0.0f;
         some = some || counts;
         tiny = tiny || (counts && fabsf(g[j]) < kSlowGate);
+        over = over || (isinf(h[j]) && isfinite(g[j]) && isfinite(u[j]));
     }
     uint32_t unsure, w = codes8_known(h, block_max(largest8(h)), kSlowError, byte, &unsure);
-    const bool whole = unsure == ~0u || (*byte != 255 && (least < kSlowFrom || tiny || (some && *byte < kSlowScale)));
+    const bool whole = unsure == ~0u || over || (*byte != 255 && (least < kSlowFrom || tiny || (some && *byte < kSlowScale)));
     if (__any_sync(0xffffffffu, whole)) {
+        // (an infinity is what rounds to one in FP32)
         double m = 0.0;
+        uint32_t lost = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmax(m, fabs(gate_exact(g[j], u[j])));
+        for (int j = 0; j < 8; ++j) {
+            const double v = gate_exact(g[j], u[j]);
+            m = fmax(m, fabs(v));
+            lost |= !isfinite(float(v));
+        }
         m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        if (*byte != 255) {
-            const int e = m > 0.0 ? ilogb(m) + 125 : 0;
-            *byte = uint32_t(max(e, 0));
-            unsure = ~0u;
-        }
+        lost = block_max(lost);
+        *byte = lost ? 255u : m > 0.0 ? uint32_t(max(ilogb(m) + 125, 0)) : 0u;
+        unsure = lost ? 0u : ~0u;
     }
     // (of a block that is unsure as a whole every value)
     if (unsure == ~0u) unsure = 0x11111111u;

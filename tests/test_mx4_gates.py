@@ -54,3 +54,19 @@ def test_tiny_gates_beside_ordinary_ones(least):
     u[::2, :32] = (1.25 / (gate[::2, :32].double() / (1 + (-gate[::2, :32].double()).exp()))).clamp(-3e38, 3e38).float()
     u[::2, 0] = (4.5 / (gate[::2, 0].double() / (1 + (-gate[::2, 0].double()).exp()))).clamp(-3e38, 3e38).float()
     check(gate, u)
+
+
+def test_at_the_largest_number():
+    """Products that FP32 just holds, or just does not: a block is a NaN where the rounded product is infinite."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    gate = torch.zeros((4096, 32), device="cuda")
+    u = torch.zeros((4096, 32), device="cuda")
+    gate[:, 0] = 1.5 + 3 * torch.rand(4096, generator=g, device="cuda")
+    largest = float(torch.finfo(torch.float32).max)
+    s = gate[:, 0].double() / (1 + (-gate[:, 0].double()).exp())
+    near = 1 + torch.randint(-8, 9, (4096,), generator=g, device="cuda").double() * 2.0 ** -25
+    u[:, 0] = (largest * near / s).float()
+    gate[:, 1:] = 1.0
+    u[:, 1:] = torch.randn((4096, 31), generator=g, device="cuda") * 1e38
+    check(gate, u)
