@@ -81,13 +81,16 @@ Layout layout(const cake_gg_mx4_plan_t &pl)
 
 // ---------------------------------------------------------------- token pass
 
-// silu(g) * u, three ways.  By approximate instructions: the product g log2(e)
-// rounds to 2^-24 of it, which the exponential multiplies by at most 40 ln 2 / log2(e);
-// the exponential is off by 2^-22, the reciprocal by 2^-23, four roundings by 2^-24
-// each: together below 2^-18 for g > -40.  (Two values share a reciprocal: 1 / a = b /
-// (a b).)  In FP32: two units in the last place of the exponential, a half each of the
-// sum, the quotient and the product: below 2^-20.  And in 64 bits.
-constexpr float kFastError = 0x1p-18f, kSlowError = 0x1p-20f, kFastFrom = -40.0f, kSlowFrom = -80.0f;
+// silu(g) * u, three ways.  By approximate instructions, for g > -32: the product g
+// log2(e) rounds to 2^-24 of itself and its constant is off by 2^-26, of which the
+// exponential makes |g| (2^-24 + 2^-26.2) <= 32 (7.3 x 10^-8) = 2.3 x 10^-6; the
+// instructions are off by 2^-22 (ex2) and 2^-23 (rcp); the sum, the product of the two
+// sums, g u, the quotient and the result round to 2^-24 each, and so does the result in
+// units of its scale: 3.1 x 10^-6 in all, below 2^-18 = 3.8 x 10^-6.  (Two values share a
+// reciprocal: 1 / a = b / (a b).)  In FP32: two units in the last place of the exponential
+// (2^-22), 2^-24 each of the sum, the quotient, the product and its scaling: 2^-21, below
+// 2^-20.  And in 64 bits.
+constexpr float kFastError = 0x1p-18f, kSlowError = 0x1p-20f, kFastFrom = -32.0f, kSlowFrom = -80.0f;
 // FP32's is of the normal range: half of a gate below kSlowGate may not be in it, whatever u
 // makes of it, nor a value that a block of a scale below kSlowScale tells from its neighbours.
 constexpr float kSlowGate = 0x1p-120f;

@@ -70,3 +70,17 @@ def test_at_the_largest_number():
     gate[:, 1:] = 1.0
     u[:, 1:] = torch.randn((4096, 31), generator=g, device="cuda") * 1e38
     check(gate, u)
+
+
+@pytest.mark.parametrize("steps", [0, 8, 64])
+def test_far_gates_on_borders(steps):
+    """Gates from -50 to -20, whose exponentials carry the most error, a few of FP32's steps from a border between codes."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(steps)
+    gate = -20 - 30 * torch.rand((8192, 32), generator=g, device="cuda")
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    want = mids[torch.randint(0, 7, (8192, 32), generator=g, device="cuda")].double()
+    want[:, 0] = 4.0 + 3 * torch.rand(8192, generator=g, device="cuda").double()
+    want[::7, 0] = 8.0
+    want *= 1 + torch.randint(-steps, steps + 1, (8192, 32), generator=g, device="cuda").double() * 2.0 ** -23
+    check(gate, (want / (gate.double() / (1 + (-gate.double()).exp()))).float())
