@@ -178,6 +178,8 @@ def _make_row_functions():
 
         @staticmethod
         def forward(ctx, logits, top_k, bias, options):
+            # (plain numbers: a tensor's value may change before the backward pass)
+            options = dict(options, renormalize=bool(options["renormalize"]), scale=float(options["scale"]))
             out = gg.route(logits, top_k, bias=bias, **options)
             ctx.save_for_backward(logits, out.expert)
             ctx.options = {k: options[k] for k in ("score", "renormalize", "scale")}
