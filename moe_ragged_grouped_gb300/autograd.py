@@ -217,13 +217,17 @@ def _make_row_functions():
             # (the rows' gradient has to cover every row)
             if rows.shape[0] != position.numel():
                 raise ValueError(f"{rows.shape[0]} rows for {position.numel()} positions")
-            ctx.save_for_backward(rows, weight, position)
+            # (without weights nothing of the rows is needed but their type)
+            ctx.save_for_backward(None if weight is None else rows, weight, position)
+            ctx.dtype = rows.dtype
             return gg.combine_rows(rows, position, weight, out_dtype=out_dtype)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, G):
             rows, weight, position = ctx.saved_tensors
+            if weight is None:
+                return gg.gather_rows(dense(G).to(ctx.dtype), position), None, None, None
             d_rows, d_weight = gg.combine_grad(dense(G), rows, position, weight)
             return d_rows, d_weight, None, None
 
@@ -259,7 +263,7 @@ def gather_rows(X, position):
 def combine_rows(rows, weight, position, out_dtype="bf16"):
     """Tokens [T, K] as weighted sums of their rows [T * top_k, K], differentiable in rows and weight.
 
-    weight float32 [T, top_k] and position are a Routing's, which names each row
-    once (rows of another number are refused).
+    weight float32 [T, top_k] (None: ones) and position are a Routing's, which names
+    each row once (rows of another number are refused).
     """
     return _row_functions()[2].apply(rows, weight, position, out_dtype)

@@ -20,6 +20,26 @@ def _rand(*shape, seed=0):
     return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
 
 
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_sums_without_weights(dtype, out_dtype):
+    """Each row's gradient is its token's, in the rows' type: one rounding."""
+    import torch
+    from moe_ragged_grouped_gb300 import autograd as ag
+    T, top, K = 21, 3, 72
+    kind = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    position = gg.route(_rand(T, 9), top).position
+    rows = _rand(T * top, K, seed=1).to(kind[dtype]).requires_grad_()
+    y = ag.combine_rows(rows, None, position, out_dtype=out_dtype)
+    v = rows.detach().double()[position.long()]
+    step = 2.0 ** -8 if out_dtype == "bf16" else 0.0
+    assert bool(((y.double() - v.sum(dim=1)).abs() <= step * v.sum(dim=1).abs() + top * 2.0 ** -24 * v.abs().sum(dim=1)).all())
+    G = _rand(T, K, seed=2).to(kind[out_dtype])
+    y.backward(G)
+    assert rows.grad.dtype == kind[dtype]
+    assert torch.equal(rows.grad[position.long()], G.to(kind[dtype])[:, None, :].expand(-1, top, -1))
+
+
 def test_options_are_the_forward_calls():
     """An option given as a tensor that changes afterwards: the gradient is that of the forward call."""
     import torch
