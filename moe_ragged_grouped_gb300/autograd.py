@@ -217,8 +217,8 @@ def _make_row_functions():
             # (the rows' gradient has to cover every row)
             if rows.shape[0] != position.numel():
                 raise ValueError(f"{rows.shape[0]} rows for {position.numel()} positions")
-            # (without weights nothing of the rows is needed but their type)
-            ctx.save_for_backward(None if weight is None else rows, weight, position)
+            # (the rows are the weights' gradient's only)
+            ctx.save_for_backward(rows if ctx.needs_input_grad[1] else None, weight, position)
             ctx.dtype = rows.dtype
             return gg.combine_rows(rows, position, weight, out_dtype=out_dtype)
 
@@ -226,10 +226,11 @@ def _make_row_functions():
         @once_differentiable
         def backward(ctx, G):
             rows, weight, position = ctx.saved_tensors
-            if weight is None:
-                return gg.gather_rows(dense(G).to(ctx.dtype), position), None, None, None
+            if not ctx.needs_input_grad[1]:
+                return gg.gather_rows(dense(G), position, weight=weight, out_dtype=names[ctx.dtype]), None, None, None
+            # (one pass makes both, so rows that want none cost their writing)
             d_rows, d_weight = gg.combine_grad(dense(G), rows, position, weight)
-            return d_rows, d_weight, None, None
+            return d_rows if ctx.needs_input_grad[0] else None, d_weight, None, None
 
     return Route, Gather, Combine
 

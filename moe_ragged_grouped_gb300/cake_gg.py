@@ -1201,10 +1201,13 @@ def combine_grad(d_out, rows, position, weight, out=None, stream=None):
     return out, d_weight
 
 
-def gather_rows(X, position, out=None, stream=None):
+def gather_rows(X, position, out=None, stream=None, weight=None, out_dtype=None):
     """Tokens X [T, K] (bf16 or fp32) as rows in expert order [T * top_k, K]: out[position[t, j]] = X[t].
 
-    position names each row once, as a Routing's does; K is a multiple of 8.
+    position names each row once, as a Routing's does; K is a multiple of 8.  With
+    weight (float32 [T, top_k]) a row is weight[t, j] X[t], an FP32 product;
+    out_dtype is "bf16" or "fp32" (none: X's type).  This is combine_grad's d_rows
+    without the rows.
     """
     kind = _real_name(X, "X")
     if X.dim() != 2:
@@ -1212,17 +1215,20 @@ def gather_rows(X, position, out=None, stream=None):
     (tokens, K), on = X.shape, X.get_device()
     if not X.is_contiguous():
         raise ValueError("X is not contiguous")
-    T, top_k = _need_position(position, None, X, on)
+    T, top_k = _need_position(position, weight, X, on)
     if tokens != T:
         raise ValueError(f"{tokens} tokens for {T} positions")
     M = T * top_k
-    if out is not None and not _is(out, X.dtype, (M, K), on):
-        _need(out, "out", X.dtype, (M, K), X.device)
+    code = DTYPES[kind] if out_dtype is None else _dtype_code(out_dtype)
+    out_type = (_i8_types or _i8_torch())[4][code == CAKE_GG_FP32]
+    if out is not None and not _is(out, out_type, (M, K), on):
+        _need(out, "out", out_type, (M, K), X.device)
     _here(X)
     if out is None:
-        out = _result((M, K), X.dtype, X.device, stream)
-    rc = (_lib or load_library()).cake_gg_combine_grad(T, M, top_k, K, X.data_ptr(), DTYPES[kind], None, DTYPES[kind],
-                                                       position.data_ptr(), None, out.data_ptr(), None, _handle(stream, on))
+        out = _result((M, K), out_type, X.device, stream)
+    rc = (_lib or load_library()).cake_gg_combine_grad(T, M, top_k, K, X.data_ptr(), DTYPES[kind], None, code, position.data_ptr(),
+                                                       None if weight is None else weight.data_ptr(), out.data_ptr(), None,
+                                                       _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_grad")
     return out

@@ -40,6 +40,48 @@ def test_sums_without_weights(dtype, out_dtype):
     assert torch.equal(rows.grad[position.long()], G.to(kind[dtype])[:, None, :].expand(-1, top, -1))
 
 
+class _Watched:
+    """The library, with the arguments of its gradient calls kept."""
+
+    def __init__(self, lib, calls):
+        self._lib, self._calls = lib, calls
+
+    def __getattr__(self, name):
+        f = getattr(self._lib, name)
+        if name != "cake_gg_combine_grad":
+            return f
+
+        def call(*args):
+            self._calls.append(args)
+            return f(*args)
+        return call
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_weights_that_are_frozen(dtype, monkeypatch):
+    """Without a gradient of the weights no row is read, and none is kept for the backward pass."""
+    import torch
+    from moe_ragged_grouped_gb300 import autograd as ag
+    T, top, K = 21, 3, 72
+    kind = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    r = gg.route(_rand(T, 9), top)
+    rows = _rand(T * top, K, seed=1).to(kind).requires_grad_()
+    G = _rand(T, K, seed=2)
+    calls = []
+    monkeypatch.setattr(gg, "_lib", _Watched(gg.load_library(), calls))
+    ag.combine_rows(rows, r.weight, r.position, out_dtype="fp32").backward(G)
+    (args,) = calls
+    assert args[6] is None and args[11] is None                  # (rows, d_weight)
+    want = (r.weight[:, :, None] * G[:, None, :]).to(kind)
+    assert torch.equal(rows.grad[r.position.long()], want)
+    # and with one as before
+    rows.grad, weight = None, r.weight.clone().requires_grad_()
+    ag.combine_rows(rows, weight, r.position, out_dtype="fp32").backward(G)
+    assert torch.equal(rows.grad[r.position.long()], want)
+    dots = G.double()[:, None, :] * rows.detach().double()[r.position.long()]
+    assert bool(((weight.grad.double() - dots.sum(dim=2)).abs() <= K * 2.0 ** -24 * dots.abs().sum(dim=2)).all())
+
+
 def test_options_are_the_forward_calls():
     """An option given as a tensor that changes afterwards: the gradient is that of the forward call."""
     import torch
