@@ -71,6 +71,12 @@ def _run(pass_, a, b, offsets, out_shape, out_dtype, det, E, M, N, K):
     return out
 
 
+def _dense(G):
+    """A gradient as the kernels take one: dense, from a 16-byte boundary on (part of a flat buffer may begin anywhere)."""
+    G = G.contiguous()
+    return G if G.data_ptr() % 16 == 0 else G.clone()
+
+
 def _make_function():
     import torch
 
@@ -99,9 +105,7 @@ def _make_function():
         @staticmethod
         def backward(ctx, G):
             X, W, offsets = ctx.saved_tensors
-            G = G.contiguous()
-            if G.dtype != torch.bfloat16:
-                G = G.to(torch.bfloat16)
+            G = _dense(G.to(torch.bfloat16))
             E, N, K = int(W.shape[0]), int(W.shape[1]), int(W.shape[2])
             M = int(X.shape[0])
             dX = dW = None
@@ -170,8 +174,7 @@ def _make_row_functions():
     names = {torch.bfloat16: "bf16", torch.float32: "fp32"}
 
     def dense(G):
-        G = G.contiguous()
-        return G if G.dtype in names else G.float()
+        return _dense(G if G.dtype in names else G.float())
 
     class Route(torch.autograd.Function):
         """route(): the weights' gradient goes to the logits."""

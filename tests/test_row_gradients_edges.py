@@ -82,6 +82,38 @@ def test_weights_that_are_frozen(dtype, monkeypatch):
     assert bool(((weight.grad.double() - dots.sum(dim=2)).abs() <= K * 2.0 ** -24 * dots.abs().sum(dim=2)).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_at_odd_places(dtype):
+    """A dense gradient that begins anywhere, as part of a flat buffer does."""
+    import torch
+    from moe_ragged_grouped_gb300 import autograd as ag
+    T, top, K, E = 8, 2, 64, 4
+    kind = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    r = gg.route(_rand(T, E), top)
+
+    def odd(f, *leaves):
+        """Gradients through y = f(leaves), whose own begins at the second value of a buffer, and those of an aligned one."""
+        both = []
+        for front in (1, 16):
+            xs = [t.detach().clone().requires_grad_() for t in leaves]
+            y = f(*xs)
+            buffer = _rand(front + y.numel(), seed=5)
+            buffer[front:] = _rand(y.numel(), seed=6)
+            flat = torch.cat([torch.zeros(front, dtype=y.dtype, device="cuda"), y.flatten()])
+            flat.backward(buffer.to(y.dtype))
+            both.append([t.grad for t in xs])
+        return both
+
+    rows, x = _rand(T * top, K, seed=1).to(kind), _rand(T, K, seed=2).to(kind)
+    cases = [(lambda a: ag.gather_rows(a, r.position), x), (lambda a, w: ag.combine_rows(a, w, r.position, out_dtype=dtype), rows, r.weight),
+             (lambda a: ag.combine_rows(a, r.weight, r.position, out_dtype=dtype), rows), (lambda a: ag.combine_rows(a, None, r.position, out_dtype=dtype), rows)]
+    if dtype == "bf16":
+        cases.append((lambda a, w: ag.grouped_linear(a, w, r.offsets), rows, _rand(E, 128, K, seed=3).to(kind)))
+    for case in cases:
+        a, b = odd(*case)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_options_are_the_forward_calls():
     """An option given as a tensor that changes afterwards: the gradient is that of the forward call."""
     import torch
