@@ -570,6 +570,13 @@ int cake_gg_combine_grad(int64_t T, int64_t M, int32_t top_k, int32_t K, const v
                          const void *rows, int rows_dtype, const int32_t *position, const float *weight,
                          void *d_rows, float *d_weight, void *stream);
 
+/* Zeros in the rows [M, K] that position [T, top_k] does not name (a position
+ * outside [0, M) names none); the others are left as they are.  named: M bytes of
+ * scratch.  After cake_gg_combine_grad every row then has its gradient.  One
+ * memset, two kernels. */
+int cake_gg_zero_unnamed_rows(int64_t T, int64_t M, int32_t top_k, int32_t K, const int32_t *position, void *rows,
+                              int rows_dtype, uint8_t *named, void *stream);
+
 /* Synchronise `stream`, return the status word of `workspace` (CAKE_GG_OK,
  * or the first _BAD_OFFSETS / _TIMEOUT / _BAD_ROWS recorded by a call since the last
  * check) and reset it to CAKE_GG_OK; CAKE_GG_ERR_CUDA if a CUDA call failed. */

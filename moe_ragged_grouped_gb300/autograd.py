@@ -230,9 +230,10 @@ def _make_row_functions():
         def backward(ctx, G):
             rows, weight, position = ctx.saved_tensors
             if not ctx.needs_input_grad[1]:
-                return gg.gather_rows(dense(G), position, weight=weight, out_dtype=names[ctx.dtype]), None, None, None
+                return gg.gather_rows(dense(G), position, weight=weight, out_dtype=names[ctx.dtype],
+                                      zero_rest=True), None, None, None
             # (one pass makes both, so rows that want none cost their writing)
-            d_rows, d_weight = gg.combine_grad(dense(G), rows, position, weight)
+            d_rows, d_weight = gg.combine_grad(dense(G), rows, position, weight, zero_rest=ctx.needs_input_grad[0])
             return d_rows if ctx.needs_input_grad[0] else None, d_weight, None, None
 
     return Route, Gather, Combine
@@ -268,6 +269,7 @@ def combine_rows(rows, weight, position, out_dtype="bf16"):
     """Tokens [T, K] as weighted sums of their rows [T * top_k, K], differentiable in rows and weight.
 
     weight float32 [T, top_k] (None: ones) and position are a Routing's, which names
-    each row once (rows of another number are refused).
+    each row once (rows of another number are refused).  A position outside the rows
+    names none: the token goes without, and a row that is left so has the gradient zero.
     """
     return _row_functions()[2].apply(rows, weight, position, out_dtype)

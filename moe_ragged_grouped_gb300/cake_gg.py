@@ -53,7 +53,8 @@ EXPORTED = ["cake_gg_plan", "cake_gg_fwd", "cake_gg_dgrad", "cake_gg_wgrad",
             "cake_gg_router_plan", "cake_gg_router_fp32",
             "cake_gg_i8_plan", "cake_gg_i8_gemm", "cake_gg_i8_quant",
             "cake_gg_mx4_plan", "cake_gg_mx4_gemm", "cake_gg_mx4_quant",
-            "cake_gg_route_plan", "cake_gg_route", "cake_gg_route_grad", "cake_gg_combine_rows", "cake_gg_combine_grad"]
+            "cake_gg_route_plan", "cake_gg_route", "cake_gg_route_grad", "cake_gg_combine_rows", "cake_gg_combine_grad",
+            "cake_gg_zero_unnamed_rows"]
 
 
 class CakeGGPlan(ctypes.Structure):
@@ -259,6 +260,8 @@ def load_library(path: str = LIB_PATH):
     lib.cake_gg_combine_rows.restype = ctypes.c_int
     lib.cake_gg_combine_grad.argtypes = [i64, i64, i32, i32, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp, vp, vp]
     lib.cake_gg_combine_grad.restype = ctypes.c_int
+    lib.cake_gg_zero_unnamed_rows.argtypes = [i64, i64, i32, i32, vp, vp, ctypes.c_int, vp, vp]
+    lib.cake_gg_zero_unnamed_rows.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -511,6 +514,12 @@ def cake_gg_combine_grad(T, M, top_k, K, d_out, out_dtype, rows, rows_dtype, pos
     return load_library().cake_gg_combine_grad(int(T), int(M), int(top_k), int(K), _ptr(d_out), _dtype_code(out_dtype),
                                                _ptr(rows), _dtype_code(rows_dtype), _ptr(position), _ptr(weight), _ptr(d_rows),
                                                _ptr(d_weight), _stream(stream, d_out))
+
+
+def cake_gg_zero_unnamed_rows(T, M, top_k, K, position, rows, rows_dtype, named, stream=None) -> int:
+    """cake_gg_zero_unnamed_rows(): zeros in the rows that position does not name; returns the status code."""
+    return load_library().cake_gg_zero_unnamed_rows(int(T), int(M), int(top_k), int(K), _ptr(position), _ptr(rows),
+                                                    _dtype_code(rows_dtype), _ptr(named), _stream(stream, rows))
 
 
 # ---------------------------------------------------------------- tensor-level helpers
@@ -1167,12 +1176,22 @@ def combine_rows(rows, position, weight=None, out_dtype="bf16", out=None, stream
     return out
 
 
-def combine_grad(d_out, rows, position, weight, out=None, stream=None):
+def _zero_rest(rows, position, stream):
+    """Zeros in the rows that position does not name."""
+    import torch
+    (T, top_k), (M, K) = position.shape, rows.shape
+    named = _result((M,), torch.uint8, rows.device, stream)
+    rc = cake_gg_zero_unnamed_rows(T, M, top_k, K, position, rows, _real_name(rows, "rows"), named, stream)
+    if rc != CAKE_GG_OK:
+        raise CakeGGError(rc, "cake_gg_zero_unnamed_rows")
+
+
+def combine_grad(d_out, rows, position, weight, out=None, stream=None, zero_rest=False):
     """Gradients of combine_rows: (d_rows [M, K] in the rows' type, d_weight float32 [T, top_k]), from d_out [T, K].
 
     position names each of the M = T * top_k rows once, as a Routing's does (rows
     of another number are refused; rows that it does not name keep what `out`, or
-    fresh memory, holds).
+    fresh memory, holds, or with zero_rest become zeros).
     """
     kind, out_kind = _real_name(rows, "rows"), _real_name(d_out, "d_out")
     if rows.dim() != 2 or d_out.dim() != 2:
@@ -1198,13 +1217,16 @@ def combine_grad(d_out, rows, position, weight, out=None, stream=None):
                                                        d_weight.data_ptr(), _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_grad")
+    if zero_rest:
+        _zero_rest(out, position, stream)
     return out, d_weight
 
 
-def gather_rows(X, position, out=None, stream=None, weight=None, out_dtype=None):
+def gather_rows(X, position, out=None, stream=None, weight=None, out_dtype=None, zero_rest=False):
     """Tokens X [T, K] (bf16 or fp32) as rows in expert order [T * top_k, K]: out[position[t, j]] = X[t].
 
-    position names each row once, as a Routing's does; K is a multiple of 8.  With
+    position names each row once, as a Routing's does (rows that it does not name keep what
+    `out`, or fresh memory, holds, or with zero_rest become zeros); K is a multiple of 8.  With
     weight (float32 [T, top_k]) a row is weight[t, j] X[t], an FP32 product;
     out_dtype is "bf16" or "fp32" (none: X's type).  This is combine_grad's d_rows
     without the rows.
@@ -1231,4 +1253,6 @@ def gather_rows(X, position, out=None, stream=None, weight=None, out_dtype=None)
                                                        _handle(stream, on))
     if rc != CAKE_GG_OK:
         raise CakeGGError(rc, "cake_gg_combine_grad")
+    if zero_rest:
+        _zero_rest(out, position, stream)
     return out

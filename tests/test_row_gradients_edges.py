@@ -131,3 +131,50 @@ def test_options_are_the_forward_calls():
         return logits.grad
 
     assert torch.equal(grad(True), grad(False))
+
+
+@pytest.mark.parametrize("weights", ["trained", "frozen", "none"])
+@pytest.mark.parametrize("T,top,K,dtype", [(5, 3, 8, "fp32"), (300, 2, 264, "bf16"), (40, 8, 4096, "fp32"), (70001, 2, 8, "bf16")])
+def test_rows_that_no_token_takes(T, top, K, dtype, weights):
+    """Positions outside the rows take none: the rows that are left have no part in the sums, so their gradient is zero."""
+    import torch
+    from moe_ragged_grouped_gb300 import autograd as ag
+    kind = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    M = T * top
+    g = torch.Generator(device="cuda").manual_seed(M)
+    position = torch.randperm(M, generator=g, device="cuda").view(T, top).to(torch.int32)
+    out = torch.rand((T, top), generator=g, device="cuda") < 0.3
+    out[0] = True
+    position[out] = torch.where(torch.rand((T, top), generator=g, device="cuda") < 0.5, -1, M).to(torch.int32)[out]
+    rows = _rand(M, K, seed=1).to(kind).requires_grad_()
+    w = _rand(T, top, seed=2).requires_grad_(weights == "trained")
+    G = _rand(T, K, seed=3)
+    # (what the allocator gives again is not zeros)
+    for _ in range(3):
+        torch.full((M, K), float("nan"), dtype=kind, device="cuda")
+    ag.combine_rows(rows, None if weights == "none" else w, position, out_dtype="fp32").backward(G)
+    want = torch.zeros_like(rows)
+    share = G[:, None, :] * (1.0 if weights == "none" else w.detach()[:, :, None])
+    want[position[~out].long()] = share.expand(-1, top, -1)[~out].to(kind)
+    assert torch.equal(rows.grad, want)
+    if weights == "trained":
+        assert not w.grad[out].any()
+
+
+def test_zeros_in_the_rows_left_alone():
+    """The named rows and the memory around stay as they were."""
+    import torch
+    from gg_testutil import guarded_empty, guards_intact
+    for M, K, kind in ((1, 8, "bf16"), (33, 24, "fp32"), (1000, 520, "bf16")):
+        position = torch.full((M, 1), -1, dtype=torch.int32, device="cuda")
+        position[::3, 0] = torch.arange(M - 1, -1, -1, dtype=torch.int32, device="cuda")[::3]
+        position[1::3, 0] = 2 ** 31 - 1
+        buf, view, guard = guarded_empty((M, K), kind)
+        bits = torch.int16 if kind == "bf16" else torch.int32
+        before = view.clone().view(bits)
+        work = torch.full((M,), 7, dtype=torch.uint8, device="cuda")
+        assert gg.cake_gg_zero_unnamed_rows(M, M, 1, K, position, view, kind, work) == gg.CAKE_GG_OK
+        named = torch.zeros(M, dtype=torch.bool, device="cuda")
+        named[position[::3, 0].long()] = True
+        assert guards_intact(buf, guard, M * K, kind) and not view[~named].any()
+        assert torch.equal(view.view(bits)[named], before[named])
