@@ -493,7 +493,7 @@ int cake_gg_i8_gemm(const cake_gg_i8_plan_t *plan, const void *X, const float *x
     const bool ready = pl.x_dtype == CAKE_GG_INT8;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))
         return CAKE_GG_ERR_INVALID_ARG;
-    if ((!offsets && pl.E != 1) || (!rows && pl.T != pl.M_max)) return CAKE_GG_ERR_INVALID_ARG;
+    if ((!offsets && pl.E != 1) || (!rows && pl.M_max > 0 && pl.T != pl.M_max)) return CAKE_GG_ERR_INVALID_ARG;
     if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(workspace, 16) || !aligned(xs, 4) ||
         !aligned(ws, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
         return CAKE_GG_ERR_ALIGNMENT;

@@ -593,7 +593,7 @@ int cake_gg_mx4_gemm(const cake_gg_mx4_plan_t *plan, const void *X, const uint8_
     const bool ready = pl.x_dtype == CAKE_GG_MX4;   // tokens come quantised
     if (!workspace || !W || !ws || (pl.M_max > 0 && (!X || !Y || (ready && !xs))) || (!ready && xs))
         return CAKE_GG_ERR_INVALID_ARG;
-    if ((!offsets && pl.E != 1) || (!rows && pl.T != pl.M_max)) return CAKE_GG_ERR_INVALID_ARG;
+    if ((!offsets && pl.E != 1) || (!rows && pl.M_max > 0 && pl.T != pl.M_max)) return CAKE_GG_ERR_INVALID_ARG;
     if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(workspace, 16) || !aligned(xs, 16) ||
         !aligned(ws, 16) || !aligned(rows, 4) || !aligned(offsets, 4))
         return CAKE_GG_ERR_ALIGNMENT;
