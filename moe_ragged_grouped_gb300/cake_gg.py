@@ -860,7 +860,7 @@ def mx4_values(q, scale):
     codes = torch.stack([q & 15, q >> 4], dim=-1).reshape(*q.shape[:-1], K).long()
     v = torch.where(codes < 8, sizes[codes & 7], -sizes[codes & 7])
     s = scale.transpose(-4, -2)                         # [.., tile, r % 128 / 32, r % 32, K / 128, block]
-    s = s.reshape(*scale.shape[:-5], scale.shape[-5] * 128, -1)[..., :R, :K // 32].to(torch.int32)
+    s = s.reshape(*scale.shape[:-5], scale.shape[-5] * 128, scale.shape[-4] * 4)[..., :R, :K // 32].to(torch.int32)
     # the power of two by its bits: 2^-127 is below the normal range
     power = torch.where(s == 0, torch.full_like(s, 1 << 22), s << 23).view(torch.float32)
     power = torch.where(s == 255, torch.full_like(power, float("nan")), power)

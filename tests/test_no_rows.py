@@ -1,4 +1,4 @@
-"""Calls of an expert-parallel rank to which nothing was routed."""
+"""Calls of an expert-parallel rank to which nothing was routed, and values of nothing."""
 import pytest
 
 from moe_ragged_grouped_gb300 import build as gg_build
@@ -18,6 +18,14 @@ def test_no_rows_of_some_tokens_is_not_refused(kind):
     # one with rows to compute does
     plan = getattr(gg, f"cake_gg_{kind}_plan")(4, 3, 5, 128, 256)
     assert call(plan, **{**a, "Y": AT, "workspace_bytes": plan.workspace_bytes}) == gg.CAKE_GG_ERR_INVALID_ARG
+
+
+def test_values_of_no_rows():
+    import torch
+    for lead in ((), (3,)):
+        q = torch.zeros((*lead, 0, 48), dtype=torch.uint8)
+        scale = torch.zeros((*lead, *gg._mx4_tiles(0, 96)), dtype=torch.uint8)
+        assert gg.mx4_values(q, scale).shape == (*lead, 0, 96)
 
 
 @pytest.mark.gpu
