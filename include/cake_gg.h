@@ -488,7 +488,9 @@ int cake_gg_mx4_quant(const void *X, int x_dtype, int act, int32_t E, int64_t R,
  * bias, or s), and only experts of the top_groups best are chosen; ties to the
  * lowest group.  The choice is that of 64-bit scores: where FP32 cannot tell,
  * they are computed.  Weights are s of the chosen (without the bias), divided by
- * their sum with `renormalize` (0 where none is above zero), times `scale`.
+ * their sum with `renormalize` (0 where none is above zero), times `scale`.  A token
+ * whose logits are all -inf has a softmax of zeros: its weights and its gradient
+ * are 0, its experts the first ones.
  *
  *   expert [T, top_k], weight [T, top_k]
  *   offsets [E + 1]: expert e's rows are [offsets[e], offsets[e + 1])

@@ -454,7 +454,8 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
         float m = l[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-        most = warp_max(m);
+        m = warp_max(m);
+        most = m == ninf ? 0.0f : m;                             // (nothing left: all exponentials are 0)
         float e[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) e[i] = exp2_fast((l[i] - most) * kLog2e);
@@ -661,7 +662,7 @@ __device__ __forceinline__ int32_t choose(const RouteParams &p, int64_t t, int l
         mine = choose_by_keys<VPL>(p, t, lane);
         ml = in ? load_logit(p, t, mine) : ninf;
     }
-    *of_it = !in ? 0.0f : softmax && !p.renormalize ? expf(ml - most) * reciprocal(sum) : ml;
+    *of_it = !in ? 0.0f : !softmax || p.renormalize ? ml : sum == 0.0f ? 0.0f : expf(ml - most) * reciprocal(sum);
     return mine;
 }
 
@@ -870,6 +871,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 1; i < VPL; ++i) m = fmaxf(m, s[i]);
     m = warp_max(m);
+    if (m == __uint_as_float(0xff800000u)) m = 0.0f;             // (nothing left: all exponentials are 0)
 #pragma unroll
     for (int i = 0; i < VPL; ++i) s[i] = x[i] = expf(s[i] - m);
     const float q = e >= 0 ? expf(l - m) : 0.0f;
@@ -880,7 +882,7 @@ __global__ void __launch_bounds__(256)
         sum += __shfl_xor_sync(kFull, sum, d);
         inner += __shfl_xor_sync(kFull, inner, d);
     }
-    const float over = reciprocal(sum);
+    const float over = sum == 0.0f ? 0.0f : reciprocal(sum);
     inner *= over;
     const float by = -inner * over;
     LT *out = static_cast<LT *>(p.d_logits) + t * p.E;
