@@ -1048,7 +1048,7 @@ def _route_options(score, groups, top_groups, group_score, renormalize, scale):
     if group_score not in GROUP_SCORES:
         raise ValueError(f"group_score is 'max' or 'top2', got {group_score!r}")
     return CakeGGRouteOptions(_score_code(score), groups, groups if top_groups is None else top_groups,
-                              GROUP_SCORES[group_score], int(renormalize), scale)
+                              GROUP_SCORES[group_score], int(renormalize), float.fromhex(scale))
 
 
 def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renormalize=True,
@@ -1068,9 +1068,9 @@ def route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=None, 
     tensors are on the current CUDA device; stream as in int8_gemm.
     """
     kind, T, E, apart = _logits(logits)
-    # (plain numbers: a tensor's value may change, and it is its identity that a cache sees)
+    # (plain values: a tensor's may change, and it is its identity that a cache sees, to which -0.0 is 0.0)
     options = _route_options(score, int(groups), None if top_groups is None else int(top_groups), group_score, bool(renormalize),
-                             float(scale))
+                             float(scale).hex())
     if plan is None:
         plan = cake_gg_route_plan(T, E, top_k)
     elif (plan.T, plan.E, plan.top_k) != (T, E, top_k):
