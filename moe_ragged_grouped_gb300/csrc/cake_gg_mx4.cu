@@ -190,7 +190,7 @@ __device__ __noinline__ uint32_t codes8_gated(const float (&g)[8], const float (
 // E matrices of R rows.  A lane has 8 values of a row at a time, four lanes a block,
 // a warp 256 values; it serves N such runs of one row, eight rows a block.  The runs
 // go through each step together, so that their waits for shuffles and exponentials
-// overlap: 32768 x 2048 gated takes 62 us (4.9 TB/s read and written), one run after
+// overlap: 32768 x 2048 gated takes 60 us (5.1 TB/s read and written), one run after
 // the other 96, two together 67; BF16 16384 x 4096 28 us (6.1), FP32 44 (6.9).  Gated
 // values are bound by their arithmetic, some 170 instructions for 8 of a lane, in
 // registers held down to what keeps three blocks resident (with two 71 us).

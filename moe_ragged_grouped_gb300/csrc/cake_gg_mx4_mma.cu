@@ -23,9 +23,9 @@
 // together where they do not come by TMA, warp 14 copies scales to tensor memory, warp 15
 // copies rows, or, where they are routed, warps 15-18 gather them, two on every other stage.
 //
-// Bound: long calls by the MMA loop (16384 x 4096 -> 4096 86 us, 6.3 PFLOP/s: the tensor
-// pipe has 384 of some 490 clocks of a stage, four times BF16's rate; with rows in 192 and
-// pairs, since a wider B takes the same hand-over), decoding by HBM (64 tokens through 4 of
+// Bound: long calls by the MMA loop (16384 x 4096 -> 4096 86 us, 6.3 PFLOP/s: a stage takes
+// 490 to 600 clocks with its hand-over, of which the tensor pipe is active some 410, at four
+// times BF16's rate; with rows in 192 and pairs, since a wider B takes the same hand-over), decoding by HBM (64 tokens through 4 of
 // 32 experts 6144 -> 4096: 70 us, 6.1 TB/s), a single token by what 128 units draw on 152
 // multiprocessors (15.2 us).
 #include <type_traits>

@@ -10,10 +10,11 @@
 //   w = s of the chosen, / their sum if asked, * scale
 //   rows by expert, then by token
 //
-// A warp has a token, a lane every 32nd expert; each round takes the largest key
-// and the lowest index among its equals by two warp reductions.  A choice by s + bias
-// is made in FP32 where that decides it; where two keys lie closer than FP32's error the
-// candidates are compared in 64 bits.
+// A warp has a token, a lane every 32nd expert.  A key packs the upper bits of a score
+// and the expert into one word, so that each round finds the largest and the lowest
+// index among its equals by one warp reduction over the lanes' sorted keys.  Scores of
+// the keys are approximate; those of the chosen, and of all that come near them, are
+// computed in FP32, and in 64 bits where two lie closer than FP32's error.
 //
 // Rows are numbered by counting: for each expert a bit per token of the block says
 // who chose it, so a token's place among them is a population count, in the
@@ -35,7 +36,6 @@ namespace {
 // stay in the 64 registers that 1024 threads have each (8 of 384, 64 tokens 12.5 us, 8192
 // tokens 38; with 512 threads 10.5 and 34); of 256 either does (21 us for 16384 tokens).
 template <int VPL> constexpr int kThreadsOf = VPL * 32 <= kRouteNarrow ? kRouteThreads : kRouteThreads / 2;
-constexpr int32_t kMaxExperts = kRouteMaxExperts;
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float load_logit(const RouteParams &p, int64_t t, int32_t e)
@@ -248,11 +248,17 @@ __device__ __noinline__ int32_t choose_in_64_bits(const RouteParams &p, int64_t 
     return mine;
 }
 
-// FP32's error of a score, relative to it: the exponential is off by two units in
-// its last place (2^-22), a sum or a quotient by 2^-24; the softmax's argument l - max
-// rounds to 2^-24 of itself (x e^-x <= 0.37 bounds what that is of the largest
-// score), its sum has ten roundings and its terms' 2^-22.  s + bias rounds by 2^-24 of
-// itself.
+// FP32's error of a score, relative to it.  A sigmoid: the exponential is off by two
+// units in its last place (2^-22), the sum rounds to 2^-24, its reciprocal is off by
+// 2^-23: below 2^-21.  A softmax, in units of 2^-24: its sum of up to 1024 terms rounds
+// ten times (10), each term is off by 4 (exponential), and of its argument x = l - max,
+// which rounds to |x| and, where the exponential is approximate, is multiplied by a
+// rounded constant (1.2 |x| more), the terms' mean counts, at most 4.5 (of n terms e^-x
+// beside the largest, n x e^-x / (1 + n e^-x)): 24 of the sum; the numerator 4, reciprocal
+// and product 3: 31, below 2^-19.  (A sum by exponentials in FP32 would be off by 19 in
+// place of 24, measured by the same 3 x 10^-7 of logits of deviation 1, and costs 0.5 us
+// of 21 for 16384 x 256.)  The numerator's own argument: x e^-x <= 0.37 bounds what it
+// is of the largest score.  s + bias rounds by 2^-24 of itself.
 constexpr float kSigmoidError = 0x1p-21f, kSoftmaxError = 0x1p-19f;
 
 // The experts of token t by whole FP32 keys: lane j < top_k gets the j-th.
