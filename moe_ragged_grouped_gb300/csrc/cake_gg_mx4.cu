@@ -267,11 +267,11 @@ __global__ void __launch_bounds__(256, ACT ? 3 : 1)
                 float g[8], u[8];
                 raw[i].values(g);
                 raw_u[ACT ? i : 0].values(u);
-                // zeros are zeros
+                // zeros are zeros, unless a far gate's exponential made a NaN of them
                 bool zero = true;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) zero = zero && (g[j] == 0.0f || u[j] == 0.0f);
-                if (__any_sync(0xffffffffu, (open >> i & 1u) && !zero)) w[i] = codes8_gated(g, u, &byte[i]);
+                if (__any_sync(0xffffffffu, (open >> i & 1u) && (!zero || byte[i] == 255))) w[i] = codes8_gated(g, u, &byte[i]);
             }
         }
     }

@@ -19,7 +19,7 @@ def cuda():
 def check(gate, u):
     """Codes and scales, bit for bit."""
     import torch
-    x = torch.cat([gate, u], dim=1).float().contiguous()
+    x = torch.cat([gate, u], dim=1).contiguous()
     code, byte = unpacked(*gg.quantize_mx4(x, act="silu_mul"))
     want = quantised(gated(x))
     assert same(byte, want[1]), (byte - want[1]).nonzero()[:4]
@@ -84,3 +84,26 @@ def test_far_gates_on_borders(steps):
     want[::7, 0] = 8.0
     want *= 1 + torch.randint(-steps, steps + 1, (8192, 32), generator=g, device="cuda").double() * 2.0 ** -23
     check(gate, (want / (gate.double() / (1 + (-gate.double()).exp()))).float())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_zeros_under_far_gates(dtype):
+    """Zeros whatever their gate is: blocks of them, alone in a row and beside others; an infinite gate's are NaNs."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(7)
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gate = torch.randn((60, 512), generator=g, device="cuda") * 10.0 ** torch.randint(0, 38, (60, 1), generator=g, device="cuda")
+    gate[:20] = -90 * torch.rand((20, 512), generator=g, device="cuda")
+    gate, u = gate.to(kind), torch.zeros((60, 512), dtype=kind, device="cuda")
+    u[:, ::3] = -0.0
+    u[1::4, :256] = torch.randn((15, 256), generator=g, device="cuda").to(kind)
+    u[2::4, 500] = 1.0
+    check(gate, u)
+    gate[::5, 70], gate[1::5, 300], gate[2::5, 100] = float("-inf"), float("inf"), float("nan")
+    check(gate, u)
+    u[3::5, 33] = float("inf")
+    gate[3::5, 33] = 0.0
+    check(gate, u)
+    x = torch.cat([torch.full((3, 64), -95.0, device="cuda"), torch.zeros((3, 64), device="cuda")], dim=1).to(kind)
+    w = gg.quantize_mx4(torch.randn((16, 64), generator=g, device="cuda"))
+    assert not gg.mx4_gemm(x, *w, act="silu_mul").any()
