@@ -418,8 +418,8 @@ int cake_gg_i8_quant(const void *X, int x_dtype, int act, int64_t T, int32_t K, 
  *
  * This is the rounding of h itself: where FP32 arithmetic cannot tell on which
  * side of a border a gated value lies, 64 bits decide.  A block of zeros has s = 0; one
- * that holds a NaN or an infinity s = 255 and codes 0, so the products of its
- * row are NaN. */
+ * that holds a NaN or an infinity (h as FP32 rounds it) s = 255 and codes 0, so the
+ * products of its row are NaN. */
 typedef enum {
     CAKE_GG_MX4_MMA = 0,     /* tensor cores                                        */
     CAKE_GG_MX4_ROWS = 1     /* few rows: integer dot products                      */
@@ -488,7 +488,8 @@ int cake_gg_mx4_quant(const void *X, int x_dtype, int act, int32_t E, int64_t R,
  * bias, or s), and only experts of the top_groups best are chosen; ties to the
  * lowest group.  The choice is that of 64-bit scores: where FP32 cannot tell,
  * they are computed.  Weights are s of the chosen (without the bias), divided by
- * their sum with `renormalize` (0 where none is above zero), times `scale`.  A token
+ * their sum with `renormalize` (0 where none is above zero; of a softmax that is the
+ * softmax over the chosen, in which the others take no part), times `scale`.  A token
  * whose logits are all -inf has a softmax of zeros: its weights and its gradient
  * are 0, its experts the first ones.
  *
