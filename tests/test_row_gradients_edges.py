@@ -178,3 +178,20 @@ def test_zeros_in_the_rows_left_alone():
         named[position[::3, 0].long()] = True
         assert guards_intact(buf, guard, M * K, kind) and not view[~named].any()
         assert torch.equal(view.view(bits)[named], before[named])
+
+
+def test_zeros_on_another_stream():
+    """The marks and the zeros go where the gradient goes."""
+    import torch
+    T, top, K = 3000, 2, 1024
+    position = torch.randperm(T * top, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").view(T, top).to(torch.int32)
+    position[::5] = -1
+    G, rows, w = _rand(T, K, seed=1), _rand(T * top, K, seed=2), _rand(T, top, seed=3)
+    want = gg.combine_grad(G, rows, position, w, zero_rest=True)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for st in (stream, stream.cuda_stream):
+        got = gg.combine_grad(G, rows, position, w, stream=st, zero_rest=True)
+        alone = gg.gather_rows(G, position, weight=w, stream=st, zero_rest=True)
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(alone, want[0])
